@@ -536,3 +536,11 @@ def qlora_linear_fwd_noalloc(X, W: NF4Weight, A=None, B=None, scale: float = 0.0
            lib.qlora_linear_fwd_noalloc(_ptr(X), M, ctypes.byref(st), _ptr(A), _ptr(B), r, float(scale),
                                         _ptr(out), _stream_ptr(X.device)))
     return out
+
+
+# the microscaled formats, RMSNorm and the microscaled products; the module
+# imports the names above, so it comes last
+from .mx import *  # noqa: E402,F401,F403
+from .mx import __all__ as _mx_all  # noqa: E402
+
+__all__ += _mx_all

@@ -25,7 +25,7 @@ LIB_NAME = "libqlora_nf4.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["api.cpp", "codebook.cpp", "profile.cpp", "nf4_quant.hip", "linear.hip", "gemv.hip", "merge.hip", "adamw.hip",
-           "noalloc.hip"]
+           "noalloc.hip", "api_mx.cpp", "mx_quant.hip", "rmsnorm.hip", "mx_linear.hip"]
 ARCH = os.environ.get("QLORA_OFFLOAD_ARCH", "gfx950")
 
 

@@ -8,6 +8,7 @@
 
 #include "../../include/qlora_nf4.h"
 #include "adamw.h"
+#include "error.h"
 #include "internal.h"
 
 namespace {
@@ -127,6 +128,24 @@ int linear_bwd_checked(const char *fn, const void *dY, const void *X, const void
 }
 
 }  // namespace
+
+namespace qnf4 {
+
+int api_fail(int status, const char *fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  std::vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  g_last_error = buf;
+  return status;
+}
+
+int api_ok() { return ok(); }
+
+int api_hip_status(hipError_t e, const char *where) { return hip_status(e, where); }
+
+}  // namespace qnf4
 
 extern "C" {
 

@@ -1,0 +1,178 @@
+// Microscaled quantization and dequantization: blocks of 32 elements of a row
+// share one power of two, elements are 4- or 8-bit floats.
+//
+// Both are one pass over memory. A lane holds eight consecutive elements, so
+// a block is a quad of lanes and its largest magnitude two lane exchanges
+// away; blocks never cross a row, so the matrix is walked as one run of
+// rows * cols / 32 blocks and only the address of the scale byte asks for the
+// row.
+#include "mx_device.h"
+
+namespace qnf4 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;                     // loads in flight per lane
+constexpr int kWaveBlocks = 16 * kUnroll;      // blocks per wave
+
+// Eight elements at p as fp32; amax: the bits of the largest magnitude.
+template <bool F32>
+__device__ __forceinline__ void load8(const void *src, int64_t at, mx_u32x4 (&r)[2]) {
+  if constexpr (F32) {
+    const mx_u32x4 *p = reinterpret_cast<const mx_u32x4 *>(static_cast<const float *>(src) + at);
+    r[0] = __builtin_nontemporal_load(p);
+    r[1] = __builtin_nontemporal_load(p + 1);
+  } else {
+    r[0] = __builtin_nontemporal_load(reinterpret_cast<const mx_u32x4 *>(static_cast<const __bf16 *>(src) + at));
+  }
+}
+
+template <int TYPE, bool F32>
+__global__ __launch_bounds__(kThreads) void k_mx_quant(const void *src, uint8_t *codes, uint8_t *scales,
+                                                       int64_t blocks, uint32_t nblk, uint32_t pitch) {
+  const int lane = threadIdx.x & 63;
+  const int64_t b0 = (static_cast<int64_t>(blockIdx.x) * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * kWaveBlocks;
+  if (b0 >= blocks) return;
+  mx_u32x4 in[kUnroll][2];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t b = b0 + 16 * u + (lane >> 2);
+    load8<F32>(src, 32 * min(b, blocks - 1) + 8 * (lane & 3), in[u]);
+  }
+  const MxRows rows(b0, nblk, kWaveBlocks);
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const uint32_t j = 16 * u + (lane >> 2);
+    const int64_t b = b0 + j;
+    if (b >= blocks) break;   // whole quads leave together
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t word = in[u][F32 ? i >> 2 : 0][F32 ? i & 3 : i >> 1];
+      if constexpr (F32) v[i] = __builtin_bit_cast(float, word);
+      else v[i] = (i & 1) ? bf16_hi(word) : bf16_lo(word);
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __builtin_bit_cast(uint32_t, v[i]) & 0x7fffffffu);
+    const uint32_t s = mx_scale_byte<TYPE>(quad_max(m));
+    const uint2 c = mx_encode8<TYPE>(v, mx_scale_value(s));
+    if constexpr (TYPE == QLORA_MX_FP4) {
+      __builtin_nontemporal_store(c.x, reinterpret_cast<uint32_t *>(codes + 16 * b) + (lane & 3));
+    } else {
+      const mx_u32x2 w = {c.x, c.y};
+      __builtin_nontemporal_store(w, reinterpret_cast<mx_u32x2 *>(codes + 32 * b) + (lane & 3));
+    }
+    if ((lane & 3) == 0) {
+      int64_t row;
+      uint32_t col;
+      rows.at(j, row, col);
+      uint8_t *p = scales + row * pitch;
+      p[col] = static_cast<uint8_t>(s);
+      if (col == nblk - 1)
+        for (uint32_t q = nblk; q < pitch; ++q) p[q] = 0;
+    }
+  }
+}
+
+template <int TYPE, bool F32>
+__global__ __launch_bounds__(kThreads) void k_mx_dequant(const uint8_t *codes, const uint8_t *scales, void *out,
+                                                         int64_t blocks, uint32_t nblk, uint32_t pitch) {
+  const int lane = threadIdx.x & 63;
+  const int64_t b0 = (static_cast<int64_t>(blockIdx.x) * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * kWaveBlocks;
+  if (b0 >= blocks) return;
+  const MxRows rows(b0, nblk, kWaveBlocks);
+  uint2 in[kUnroll];
+  uint32_t s[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t last = blocks - 1 - b0;
+    const uint32_t j = static_cast<uint32_t>(min(static_cast<int64_t>(16 * u + (lane >> 2)), last));
+    const int64_t b = b0 + j;
+    if constexpr (TYPE == QLORA_MX_FP4) in[u].x = reinterpret_cast<const uint32_t *>(codes + 16 * b)[lane & 3];
+    else in[u] = reinterpret_cast<const uint2 *>(codes + 32 * b)[lane & 3];
+    int64_t row;
+    uint32_t col;
+    rows.at(j, row, col);
+    s[u] = scales[row * pitch + col];
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t b = b0 + 16 * u + (lane >> 2);
+    if (b >= blocks) break;
+    const float scale = mx_scale_value(s[u]);
+    const int64_t at = 32 * b + 8 * (lane & 3);
+    if constexpr (F32) {
+      mx_float2 p[4];
+      if constexpr (TYPE == QLORA_MX_FP4) {
+        p[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(in[u].x, scale, 0);
+        p[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(in[u].x, scale, 1);
+        p[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(in[u].x, scale, 2);
+        p[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(in[u].x, scale, 3);
+      } else {
+        p[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(in[u].x, scale, 0);
+        p[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(in[u].x, scale, 1);
+        p[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(in[u].y, scale, 0);
+        p[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(in[u].y, scale, 1);
+      }
+      float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out) + at);
+      o[0] = make_float4(p[0][0], p[0][1], p[1][0], p[1][1]);
+      o[1] = make_float4(p[2][0], p[2][1], p[3][0], p[3][1]);
+    } else {
+      mx_bf16x2 p[4];
+      if constexpr (TYPE == QLORA_MX_FP4) {
+        p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(in[u].x, scale, 0);
+        p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(in[u].x, scale, 1);
+        p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(in[u].x, scale, 2);
+        p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(in[u].x, scale, 3);
+      } else {
+        p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(in[u].x, scale, 0);
+        p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(in[u].x, scale, 1);
+        p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(in[u].y, scale, 0);
+        p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(in[u].y, scale, 1);
+      }
+      mx_u32x4 w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __builtin_bit_cast(uint32_t, p[i]);
+      __builtin_nontemporal_store(w, reinterpret_cast<mx_u32x4 *>(static_cast<__bf16 *>(out) + at));
+    }
+  }
+}
+
+unsigned grid_of(int64_t blocks) {
+  return static_cast<unsigned>(ceil_div(blocks, static_cast<int64_t>(kThreads / 64) * kWaveBlocks));
+}
+
+}  // namespace
+
+hipError_t launch_mx_quantize(const void *X, bool x_bf16, int64_t rows, int64_t cols, int type, uint8_t *codes,
+                              uint8_t *scales, hipStream_t s) {
+  const int64_t blocks = rows * (cols / kMxBlock);
+  const uint32_t nblk = static_cast<uint32_t>(cols / kMxBlock), pitch = static_cast<uint32_t>(mx_pitch(cols));
+  const dim3 g(grid_of(blocks)), t(kThreads);
+  if (type == QLORA_MX_FP4) {
+    if (x_bf16) k_mx_quant<QLORA_MX_FP4, false><<<g, t, 0, s>>>(X, codes, scales, blocks, nblk, pitch);
+    else k_mx_quant<QLORA_MX_FP4, true><<<g, t, 0, s>>>(X, codes, scales, blocks, nblk, pitch);
+  } else {
+    if (x_bf16) k_mx_quant<QLORA_MX_FP8, false><<<g, t, 0, s>>>(X, codes, scales, blocks, nblk, pitch);
+    else k_mx_quant<QLORA_MX_FP8, true><<<g, t, 0, s>>>(X, codes, scales, blocks, nblk, pitch);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, int type,
+                                void *out, bool out_bf16, hipStream_t s) {
+  const int64_t blocks = rows * (cols / kMxBlock);
+  const uint32_t nblk = static_cast<uint32_t>(cols / kMxBlock), pitch = static_cast<uint32_t>(mx_pitch(cols));
+  const dim3 g(grid_of(blocks)), t(kThreads);
+  if (type == QLORA_MX_FP4) {
+    if (out_bf16) k_mx_dequant<QLORA_MX_FP4, false><<<g, t, 0, s>>>(codes, scales, out, blocks, nblk, pitch);
+    else k_mx_dequant<QLORA_MX_FP4, true><<<g, t, 0, s>>>(codes, scales, out, blocks, nblk, pitch);
+  } else {
+    if (out_bf16) k_mx_dequant<QLORA_MX_FP8, false><<<g, t, 0, s>>>(codes, scales, out, blocks, nblk, pitch);
+    else k_mx_dequant<QLORA_MX_FP8, true><<<g, t, 0, s>>>(codes, scales, out, blocks, nblk, pitch);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace qnf4

@@ -1,0 +1,361 @@
+// RMSNorm with the residual's addition, forward (bf16 or microscaled output)
+// and backward.
+//
+//   h = bf16(x + residual), rstd = 1 / sqrt(mean(h^2) + eps), y = h rstd w
+//   u = h rstd, g = dy w:  dx = rstd (g - u mean(g u)) + dh,  dw = sum dy u
+//
+// A row is read once: a lane keeps its elements in registers between the sum
+// and the scaling. It holds runs of eight elements, so a block of 32 of the
+// microscaled output lies in a quad of lanes.
+//
+// The forward computes in fp64. That costs two fp64 operations an element for
+// the sum and two for the scaling, at the fp32 rate of this card's vector
+// units, under a memory-bound kernel, and it decides every rounding to 8 or 4
+// bits as the definition does: with an fp32 sum, values within an ulp of a
+// rounding border land on either side.
+#include "mx_device.h"
+
+namespace qnf4 {
+namespace {
+
+constexpr int kOutBf16 = 2;   // besides the qlora_mx_type outputs
+
+struct FwdParams {
+  const __bf16 *x, *res;
+  const void *w;
+  __bf16 *y, *h;
+  uint8_t *codes, *scales;
+  float *rstd;
+  int64_t rows;
+  double eps, inv_cols;
+  uint32_t cols, pitch;
+  bool w_bf16;
+};
+
+// fp64 -> fp32 keeping 20 bits of mantissa, the last one set when anything
+// below it was: rounding the result to 8 or fewer bits of mantissa gives what
+// rounding the fp64 value gives.
+__device__ __forceinline__ float sticky_f32(double d) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, d);
+  const uint64_t hi = (b & 0xffffffff00000000ull) | (static_cast<uint32_t>(b) != 0 ? 0x100000000ull : 0ull);
+  return static_cast<float>(__builtin_bit_cast(double, hi));
+}
+
+__device__ __forceinline__ void unpack8(const mx_u32x4 &r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16_lo(r[i]);
+    v[2 * i + 1] = bf16_hi(r[i]);
+  }
+}
+
+__device__ __forceinline__ mx_u32x4 pack8(const float (&v)[8]) {
+  mx_u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    mx_bf16x2 p;
+    p[0] = static_cast<__bf16>(v[2 * i]);
+    p[1] = static_cast<__bf16>(v[2 * i + 1]);
+    r[i] = __builtin_bit_cast(uint32_t, p);
+  }
+  return r;
+}
+
+__device__ __forceinline__ mx_u32x4 load_row8(const __bf16 *p, int64_t at) {
+  return __builtin_nontemporal_load(reinterpret_cast<const mx_u32x4 *>(p + at));
+}
+
+__device__ __forceinline__ void load_weight8(const void *w, bool bf16, uint32_t col, float (&v)[8]) {
+  if (bf16) {
+    const mx_u32x4 r = *reinterpret_cast<const mx_u32x4 *>(static_cast<const __bf16 *>(w) + col);
+    unpack8(r, v);
+  } else {
+    const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(w) + col);
+    const float4 b = *reinterpret_cast<const float4 *>(static_cast<const float *>(w) + col + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+}
+
+// Sum over the T threads of a row, in every one of them. part: T / 64 slots of
+// shared memory (T > 64), free again when the next call follows a barrier.
+template <int T, class F>
+__device__ __forceinline__ F row_sum(F v, F *part) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  if constexpr (T > 64) {
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = part[0];
+#pragma unroll
+    for (int i = 1; i < T / 64; ++i) v += part[i];
+  }
+  return v;
+}
+
+// T threads to a row, up to NV runs of eight elements a thread. With T = 64 a
+// workgroup of four waves takes four rows.
+template <int T, int NV, int OUT>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void k_rms_fwd(const FwdParams p) {
+  __shared__ double part[T / 64];
+  const int t = T == 64 ? threadIdx.x & 63 : threadIdx.x;
+  const int64_t row = T == 64 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (row >= p.rows) return;   // whole waves (T = 64) or nobody
+  const int64_t base = row * p.cols;
+  mx_u32x4 x[NV], res[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const uint32_t col = 8u * (i * T + t);
+    if (col < p.cols) x[i] = load_row8(p.x, base + col);
+  }
+  if (p.res) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t col = 8u * (i * T + t);
+      if (col < p.cols) res[i] = load_row8(p.res, base + col);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t col = 8u * (i * T + t);
+      if (col < p.cols) {
+        // fp32 holds enough of the sum of two bf16 that rounding it again is
+        // rounding the exact sum
+        float a[8], b[8];
+        unpack8(x[i], a);
+        unpack8(res[i], b);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) a[k] += b[k];
+        x[i] = pack8(a);
+        __builtin_nontemporal_store(x[i], reinterpret_cast<mx_u32x4 *>(p.h + base + col));
+      }
+    }
+  }
+  double ss = 0.0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const uint32_t col = 8u * (i * T + t);
+    if (col < p.cols) {
+      float a[8];
+      unpack8(x[i], a);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) ss = __builtin_fma(static_cast<double>(a[k]), static_cast<double>(a[k]), ss);
+    }
+  }
+  ss = row_sum<T>(ss, part);
+  const double rstd = 1.0 / sqrt(ss * p.inv_cols + p.eps);
+  if (p.rstd && t == 0) p.rstd[row] = static_cast<float>(rstd);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const uint32_t col = 8u * (i * T + t);
+    if (col >= p.cols) continue;   // whole quads
+    float a[8], w[8], y[8];
+    unpack8(x[i], a);
+    load_weight8(p.w, p.w_bf16, col, w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = sticky_f32(static_cast<double>(a[k]) * rstd * static_cast<double>(w[k]));
+    if constexpr (OUT == kOutBf16) {
+      __builtin_nontemporal_store(pack8(y), reinterpret_cast<mx_u32x4 *>(p.y + base + col));
+    } else {
+      uint32_t m = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = max(m, __builtin_bit_cast(uint32_t, y[k]) & 0x7fffffffu);
+      const uint32_t s = mx_scale_byte<OUT>(quad_max(m));
+      const uint2 c = mx_encode8<OUT>(y, mx_scale_value(s));
+      if constexpr (OUT == QLORA_MX_FP4) {
+        *reinterpret_cast<uint32_t *>(p.codes + ((base + col) >> 1)) = c.x;
+      } else {
+        *reinterpret_cast<uint2 *>(p.codes + base + col) = c;
+      }
+      if ((t & 3) == 0) p.scales[row * p.pitch + (col >> 5)] = static_cast<uint8_t>(s);
+    }
+  }
+  if constexpr (OUT != kOutBf16) {
+    // the pad bytes behind the row's scales (at most 15)
+    const uint32_t at = (p.cols >> 5) + t;
+    if (at < p.pitch) p.scales[row * p.pitch + at] = 0;
+  }
+}
+
+struct BwdParams {
+  const __bf16 *dy, *h, *dh;
+  const void *w;
+  const float *rstd;
+  __bf16 *dx;
+  float *part;   // [groups][cols]
+  int64_t rows;
+  float inv_cols;
+  uint32_t cols;
+  bool w_bf16;
+};
+
+// Workgroup b (T > 64) or wave b (T = 64) of the launch takes rows b, b + G,
+// ...; its threads keep the sums of dy u of their columns over those rows.
+template <int T, int NV>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void k_rms_bwd(const BwdParams p) {
+  __shared__ float part[2][T / 64];
+  const int t = T == 64 ? threadIdx.x & 63 : threadIdx.x;
+  const int64_t groups = T == 64 ? static_cast<int64_t>(gridDim.x) * 4 : gridDim.x;
+  const int64_t group = T == 64 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  float dw[NV][8] = {};
+  int flip = 0;
+  for (int64_t row = group; row < p.rows; row += groups) {
+    const int64_t base = row * p.cols;
+    const float rstd = p.rstd[row];
+    mx_u32x4 dy[NV], h[NV], dh[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t col = 8u * (i * T + t);
+      if (col < p.cols) {
+        dy[i] = load_row8(p.dy, base + col);
+        h[i] = load_row8(p.h, base + col);
+        if (p.dh) dh[i] = load_row8(p.dh, base + col);
+      }
+    }
+    float c = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t col = 8u * (i * T + t);
+      if (col < p.cols) {
+        float a[8], b[8], w[8];
+        unpack8(dy[i], a);
+        unpack8(h[i], b);
+        load_weight8(p.w, p.w_bf16, col, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float u = b[k] * rstd;
+          const float du = a[k] * u;
+          dw[i][k] += du;
+          c = __builtin_fmaf(du, w[k], c);
+        }
+      }
+    }
+    c = row_sum<T>(c, part[flip]) * p.inv_cols;
+    flip ^= 1;   // the other slots: a row's sums are still read when the next row's are written
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t col = 8u * (i * T + t);
+      if (col < p.cols) {
+        float a[8], b[8], w[8], d[8];
+        unpack8(dy[i], a);
+        unpack8(h[i], b);
+        load_weight8(p.w, p.w_bf16, col, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) a[k] = rstd * (a[k] * w[k] - b[k] * rstd * c);
+        if (p.dh) {
+          unpack8(dh[i], d);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) a[k] += d[k];
+        }
+        __builtin_nontemporal_store(pack8(a), reinterpret_cast<mx_u32x4 *>(p.dx + base + col));
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const uint32_t col = 8u * (i * T + t);
+    if (col < p.cols) {
+      float4 *o = reinterpret_cast<float4 *>(p.part + group * p.cols + col);
+      o[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+      o[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+    }
+  }
+}
+
+// dw[c] = sum over the groups of part[g][c]: a workgroup takes 32 columns,
+// thread (lane c, slice s of 8) the groups s, s + 8, ...; slices are added in
+// order. fp64, so that the order over many groups costs no accuracy.
+__global__ __launch_bounds__(256) void k_rms_dw(const float *part, float *dw, int64_t groups, uint32_t cols) {
+  __shared__ double sum[8][32];
+  const int c = threadIdx.x & 31, s = threadIdx.x >> 5;
+  const uint32_t col = blockIdx.x * 32 + c;   // cols is a multiple of 32
+  double v = 0.0;
+#pragma unroll 8
+  for (int64_t g = s; g < groups; g += 8) v += part[g * cols + col];
+  sum[s][c] = v;
+  __syncthreads();
+  if (s == 0) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) v += sum[i][c];
+    dw[col] = static_cast<float>(v);
+  }
+}
+
+template <int T, int NV>
+hipError_t fwd_out(const FwdParams &p, int out, hipStream_t s) {
+  const dim3 g(static_cast<unsigned>(T == 64 ? ceil_div(p.rows, 4) : p.rows)), t(T < 256 ? 256 : T);
+  if (out == QLORA_MX_FP4) k_rms_fwd<T, NV, QLORA_MX_FP4><<<g, t, 0, s>>>(p);
+  else if (out == QLORA_MX_FP8) k_rms_fwd<T, NV, QLORA_MX_FP8><<<g, t, 0, s>>>(p);
+  else k_rms_fwd<T, NV, kOutBf16><<<g, t, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+// Rows of the partial dw sums: each thread group of the backward writes one.
+int64_t bwd_groups(int64_t rows, int64_t cols) {
+  const int64_t most = cols <= 4096 ? 2048 : cols <= 16384 ? 512 : 256;
+  return rows < most ? (cols <= 4096 ? ceil_div(rows, 4) * 4 : rows) : most;
+}
+
+template <int T, int NV>
+void bwd_run(const BwdParams &p, int64_t groups, hipStream_t s) {
+  k_rms_bwd<T, NV><<<static_cast<unsigned>(T == 64 ? groups / 4 : groups), T < 256 ? 256 : T, 0, s>>>(p);
+}
+
+}  // namespace
+
+hipError_t launch_rms_fwd(const RmsFwd &a, hipStream_t s) {
+  FwdParams p;
+  p.x = static_cast<const __bf16 *>(a.X);
+  p.res = static_cast<const __bf16 *>(a.residual);
+  p.w = a.weight;
+  p.w_bf16 = a.w_bf16;
+  p.y = static_cast<__bf16 *>(a.Y);
+  p.h = static_cast<__bf16 *>(a.H);
+  p.codes = a.codes;
+  p.scales = a.scales;
+  p.rstd = a.rstd;
+  p.rows = a.rows;
+  p.cols = static_cast<uint32_t>(a.cols);
+  p.pitch = static_cast<uint32_t>(mx_pitch(a.cols));
+  p.eps = a.eps;
+  p.inv_cols = 1.0 / static_cast<double>(a.cols);
+  const int out = a.codes ? a.type : kOutBf16;
+  // one workgroup a row: 256 threads while a thread's share is at most eight runs
+  if (a.cols <= 2048) return fwd_out<256, 1>(p, out, s);
+  if (a.cols <= 4096) return fwd_out<256, 2>(p, out, s);
+  if (a.cols <= 8192) return fwd_out<256, 4>(p, out, s);
+  if (a.cols <= 16384) return fwd_out<256, 8>(p, out, s);
+  return fwd_out<1024, 8>(p, out, s);
+}
+
+size_t rms_bwd_ws_bytes(int64_t rows, int64_t cols) {
+  return static_cast<size_t>(bwd_groups(rows, cols)) * static_cast<size_t>(cols) * sizeof(float);
+}
+
+hipError_t launch_rms_bwd(const void *dY, const void *H, const void *weight, bool w_bf16, const float *rstd,
+                          const void *dH, int64_t rows, int64_t cols, void *dX, float *dW, void *ws, hipStream_t s) {
+  BwdParams p;
+  p.dy = static_cast<const __bf16 *>(dY);
+  p.h = static_cast<const __bf16 *>(H);
+  p.dh = static_cast<const __bf16 *>(dH);
+  p.w = weight;
+  p.w_bf16 = w_bf16;
+  p.rstd = rstd;
+  p.dx = static_cast<__bf16 *>(dX);
+  p.part = static_cast<float *>(ws);
+  p.rows = rows;
+  p.cols = static_cast<uint32_t>(cols);
+  p.inv_cols = 1.0f / static_cast<float>(cols);
+  const int64_t groups = bwd_groups(rows, cols);
+  if (cols <= 1024) bwd_run<64, 2>(p, groups, s);
+  else if (cols <= 2048) bwd_run<64, 4>(p, groups, s);
+  else if (cols <= 4096) bwd_run<64, 8>(p, groups, s);
+  else if (cols <= 8192) bwd_run<256, 4>(p, groups, s);
+  else if (cols <= 16384) bwd_run<256, 8>(p, groups, s);
+  else bwd_run<1024, 8>(p, groups, s);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  k_rms_dw<<<static_cast<unsigned>(cols / 32), 256, 0, s>>>(p.part, dW, groups, p.cols);
+  return hipGetLastError();
+}
+
+}  // namespace qnf4

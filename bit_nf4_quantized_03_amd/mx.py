@@ -1,0 +1,313 @@
+"""Python binding of the microscaled formats, RMSNorm and the microscaled
+products (include/qlora_mx.h).
+
+As in the package itself, the functions carry the names of the C entry points
+and only marshal arguments: torch supplies device memory and the current
+stream of the tensors' device. They are re-exported by the package.
+"""
+from __future__ import annotations
+
+import ctypes
+import dataclasses
+from typing import Optional, Tuple
+
+import torch
+
+from . import QLORA_BF16, QLORA_F32, QloraError, lib, qlora_last_error
+
+__all__ = [
+    "MXMatrix", "QLORA_MX_FP4", "QLORA_MX_FP8", "MX_EXPORTED_SYMBOLS", "qlora_mx_scale_pitch",
+    "qlora_mx_storage_bytes", "qlora_mx_quantize", "qlora_mx_dequantize", "qlora_rmsnorm_fwd",
+    "qlora_rmsnorm_mx", "qlora_rmsnorm_bwd", "qlora_rmsnorm_bwd_workspace_bytes", "qlora_mx_linear",
+    "qlora_mx_linear_workspace_bytes", "qlora_mx_linear_grouped",
+]
+
+MX_EXPORTED_SYMBOLS = (
+    "qlora_mx_scale_pitch", "qlora_mx_storage_bytes", "qlora_mx_quantize", "qlora_mx_dequantize",
+    "qlora_rmsnorm_fwd", "qlora_rmsnorm_mx", "qlora_rmsnorm_bwd", "qlora_rmsnorm_bwd_workspace_bytes",
+    "qlora_mx_linear", "qlora_mx_linear_workspace_bytes", "qlora_mx_linear_grouped",
+)
+
+QLORA_MX_FP4 = 0   # sign, 2 exponent bits, 1 mantissa bit; two to a byte
+QLORA_MX_FP8 = 1   # sign, 4 exponent bits, 3 mantissa bits
+
+
+class _MX(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("type", ctypes.c_int32)]
+
+
+def _declare():
+    i64, sz, vp, i32, f64, ci = (ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_int32, ctypes.c_double,
+                                 ctypes.c_int)
+    mp = ctypes.POINTER(_MX)
+    sigs = {
+        "qlora_mx_scale_pitch": (i64, [i64]),
+        "qlora_mx_storage_bytes": (sz, [i64, i64, ci]),
+        "qlora_mx_quantize": (ci, [vp, ci, i64, i64, mp, vp]),
+        "qlora_mx_dequantize": (ci, [mp, vp, ci, vp]),
+        "qlora_rmsnorm_fwd": (ci, [vp, vp, vp, ci, i64, i64, f64, vp, vp, vp, vp]),
+        "qlora_rmsnorm_mx": (ci, [vp, vp, vp, ci, i64, i64, f64, mp, vp, vp]),
+        "qlora_rmsnorm_bwd_workspace_bytes": (sz, [i64, i64]),
+        "qlora_rmsnorm_bwd": (ci, [vp, vp, vp, ci, vp, vp, i64, i64, vp, vp, vp, sz, vp]),
+        "qlora_mx_linear_workspace_bytes": (sz, [i64, i64, i64]),
+        "qlora_mx_linear": (ci, [mp, mp, vp, vp, sz, vp]),
+        "qlora_mx_linear_grouped": (ci, [mp, mp, vp, i32, vp, vp]),
+    }
+    for name, (res, args) in sigs.items():
+        fn = getattr(lib, name)
+        fn.restype = res
+        fn.argtypes = args
+
+
+_declare()
+
+_DTYPES = {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}
+
+
+def _run(name: str, device, *args) -> None:
+    """Call the entry point on the current stream of ``device``, with that
+    device current (the library launches on the current one)."""
+    fn = getattr(lib, name)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if status != 0:
+        raise QloraError(name, status, qlora_last_error())
+
+
+def _dtype(name, dtype) -> int:
+    if dtype not in _DTYPES:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
+    return _DTYPES[dtype]
+
+
+def _tensor(name, t, dtype, shape, device=None):
+    """``t`` must be a contiguous CUDA tensor of this dtype (None: any) and
+    shape, on ``device``: the C ABI takes bare pointers."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _matrix_2d(name, t, dtype=None):
+    """Shape of a contiguous 2-D CUDA tensor with at least one row and column."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dim() != 2 or t.numel() == 0:
+        raise ValueError(f"{name} must be 2-D with at least one row and one column, got {tuple(t.shape)}")
+    _tensor(name, t, dtype, t.shape)
+    return t.shape
+
+
+def qlora_mx_scale_pitch(cols: int) -> int:
+    """Bytes between the scales of two rows of a matrix with ``cols`` columns (0 if cols is invalid)."""
+    return int(lib.qlora_mx_scale_pitch(cols))
+
+
+def qlora_mx_storage_bytes(rows: int, cols: int, mx: int) -> int:
+    return int(lib.qlora_mx_storage_bytes(rows, cols, mx))
+
+
+@dataclasses.dataclass
+class MXMatrix:
+    """Microscaled matrix [rows, cols] in device tensors: ``codes`` uint8
+    [rows, cols / 2] (4-bit elements) or [rows, cols] (8-bit), ``scales`` uint8
+    [rows, qlora_mx_scale_pitch(cols)], ``mx`` the element type."""
+    rows: int
+    cols: int
+    codes: torch.Tensor
+    scales: torch.Tensor
+    mx: int = QLORA_MX_FP4
+
+    @staticmethod
+    def empty(rows: int, cols: int, device, mx: int = QLORA_MX_FP4) -> "MXMatrix":
+        if mx not in (QLORA_MX_FP4, QLORA_MX_FP8):
+            raise ValueError(f"mx must be QLORA_MX_FP4 or QLORA_MX_FP8, got {mx}")
+        pitch = qlora_mx_scale_pitch(cols)
+        if rows < 1 or pitch == 0:
+            raise ValueError(f"{rows} x {cols}: needs rows >= 1 and cols a multiple of 32 up to 2^22")
+        return MXMatrix(rows, cols,
+                        torch.empty((rows, cols // 2 if mx == QLORA_MX_FP4 else cols), dtype=torch.uint8, device=device),
+                        torch.empty((rows, pitch), dtype=torch.uint8, device=device), mx)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def c_struct(self, name: str = "matrix", device=None) -> _MX:
+        """The C struct, after checking the buffers against rows and cols."""
+        if self.mx not in (QLORA_MX_FP4, QLORA_MX_FP8):
+            raise ValueError(f"{name}.mx must be QLORA_MX_FP4 or QLORA_MX_FP8, got {self.mx}")
+        rows, cols = self.rows, self.cols
+        device = self.codes.device if device is None else device
+        _tensor(f"{name}.codes", self.codes, torch.uint8, (rows, cols // 2 if self.mx == QLORA_MX_FP4 else cols), device)
+        _tensor(f"{name}.scales", self.scales, torch.uint8, (rows, 16 * -(-cols // 512)), device)
+        return _MX(rows, cols, self.codes.data_ptr(), self.scales.data_ptr(), self.mx)
+
+
+def qlora_mx_quantize(X, mx: Optional[int] = None, out: Optional[MXMatrix] = None) -> MXMatrix:
+    """Quantize a 2-D fp32 or bf16 CUDA tensor (columns a multiple of 32) to
+    microscaled floats of type ``mx`` (``out.mx`` when ``out`` is given, else
+    4 bits)."""
+    rows, cols = _matrix_2d("X", X)
+    dt = _dtype("X", X.dtype)
+    if out is None:
+        out = MXMatrix.empty(rows, cols, X.device, QLORA_MX_FP4 if mx is None else mx)
+    elif mx is not None and mx != out.mx:
+        raise ValueError(f"mx {mx} differs from out.mx {out.mx}")
+    st = out.c_struct("out", X.device)
+    _run("qlora_mx_quantize", X.device, X.data_ptr(), dt, rows, cols, ctypes.byref(st))
+    return out
+
+
+def qlora_mx_dequantize(q: MXMatrix, dtype=None, out=None):
+    """The values of ``q`` as a [rows, cols] tensor of ``dtype`` (float32 or bfloat16)."""
+    st = q.c_struct("q")
+    dtype = torch.float32 if dtype is None else dtype
+    dt = _dtype("dtype", dtype)
+    if out is None:
+        out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.device)
+    else:
+        _tensor("out", out, dtype, (q.rows, q.cols), q.device)
+    _run("qlora_mx_dequantize", q.device, ctypes.byref(st), out.data_ptr(), dt)
+    return out
+
+
+def _norm_inputs(X, weight, residual, h):
+    rows, cols = _matrix_2d("X", X, torch.bfloat16)
+    _tensor("weight", weight, None, (cols,), X.device)
+    dt = _dtype("weight", weight.dtype)
+    if residual is None:
+        if h is not None:
+            raise ValueError("h is only written with a residual")
+        return rows, cols, dt, None
+    _tensor("residual", residual, torch.bfloat16, (rows, cols), X.device)
+    if h is None:
+        h = torch.empty_like(X)
+    else:
+        _tensor("h", h, torch.bfloat16, (rows, cols), X.device)
+    return rows, cols, dt, h
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def qlora_rmsnorm_fwd(X, weight, eps: float = 1e-6, residual=None, out=None, h=None, rstd=None):
+    """(Y, H, rstd): Y = H * rstd * weight in bf16 with H = bf16(X + residual),
+    rstd = 1 / sqrt(mean(H^2) + eps) fp32 [rows]. Without a residual H is X
+    itself. ``h`` may be X or ``residual`` (in place)."""
+    rows, cols, dt, h = _norm_inputs(X, weight, residual, h)
+    if out is None:
+        out = torch.empty_like(X)
+    else:
+        _tensor("out", out, torch.bfloat16, (rows, cols), X.device)
+    if rstd is None:
+        rstd = torch.empty(rows, dtype=torch.float32, device=X.device)
+    else:
+        _tensor("rstd", rstd, torch.float32, (rows,), X.device)
+    _run("qlora_rmsnorm_fwd", X.device, X.data_ptr(), _at(residual), weight.data_ptr(), dt, rows, cols, float(eps),
+         out.data_ptr(), _at(h), rstd.data_ptr())
+    return out, X if h is None else h, rstd
+
+
+def qlora_rmsnorm_mx(X, weight, eps: float = 1e-6, residual=None, mx: Optional[int] = None,
+                     out: Optional[MXMatrix] = None, h=None) -> Tuple[MXMatrix, torch.Tensor]:
+    """(Y, H) of qlora_rmsnorm_fwd with Y in microscaled floats of type ``mx``
+    (``out.mx`` when ``out`` is given, else 8 bits)."""
+    rows, cols, dt, h = _norm_inputs(X, weight, residual, h)
+    if out is None:
+        out = MXMatrix.empty(rows, cols, X.device, QLORA_MX_FP8 if mx is None else mx)
+    elif mx is not None and mx != out.mx:
+        raise ValueError(f"mx {mx} differs from out.mx {out.mx}")
+    st = out.c_struct("out", X.device)
+    _run("qlora_rmsnorm_mx", X.device, X.data_ptr(), _at(residual), weight.data_ptr(), dt, rows, cols, float(eps),
+         ctypes.byref(st), _at(h))
+    return out, X if h is None else h
+
+
+def qlora_rmsnorm_bwd_workspace_bytes(rows: int, cols: int) -> int:
+    return int(lib.qlora_rmsnorm_bwd_workspace_bytes(rows, cols))
+
+
+def _workspace(ws, need: int, device):
+    """(address, bytes) of ``ws``, or of a new one when it is None."""
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    else:
+        _tensor("ws", ws, None, ws.shape, device)
+    return ws, _at(ws), 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def qlora_rmsnorm_bwd(dY, H, weight, rstd, dH=None, ws=None, outs: Optional[Tuple] = None):
+    """(dX, dW) of qlora_rmsnorm_fwd from its H and rstd. dX (bf16) is the
+    gradient of X and of the residual; ``dH`` is the gradient that reaches H
+    through the residual stream; dW is fp32 [cols]."""
+    rows, cols = _matrix_2d("H", H, torch.bfloat16)
+    device = H.device
+    _tensor("dY", dY, torch.bfloat16, (rows, cols), device)
+    _tensor("weight", weight, None, (cols,), device)
+    dt = _dtype("weight", weight.dtype)
+    _tensor("rstd", rstd, torch.float32, (rows,), device)
+    if dH is not None:
+        _tensor("dH", dH, torch.bfloat16, (rows, cols), device)
+    if outs is None:
+        dX, dW = torch.empty_like(dY), torch.empty(cols, dtype=torch.float32, device=device)
+    else:
+        dX, dW = outs
+        _tensor("dX", dX, torch.bfloat16, (rows, cols), device)
+        _tensor("dW", dW, torch.float32, (cols,), device)
+    ws, at, size = _workspace(ws, qlora_rmsnorm_bwd_workspace_bytes(rows, cols), device)
+    _run("qlora_rmsnorm_bwd", device, dY.data_ptr(), H.data_ptr(), weight.data_ptr(), dt, rstd.data_ptr(), _at(dH),
+         rows, cols, dX.data_ptr(), dW.data_ptr(), at, size)
+    return dX, dW
+
+
+def qlora_mx_linear_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(lib.qlora_mx_linear_workspace_bytes(M, N, K))
+
+
+def qlora_mx_linear(X: MXMatrix, W: MXMatrix, ws=None, out=None):
+    """Y = X W^T in bf16: X [M, K] in 8- or 4-bit, W [N, K] in 4-bit microscaled floats."""
+    device = X.device
+    sx, sw = X.c_struct("X"), W.c_struct("W", device)
+    if out is None:
+        out = torch.empty((X.rows, W.rows), dtype=torch.bfloat16, device=device)
+    else:
+        _tensor("out", out, torch.bfloat16, (X.rows, W.rows), device)
+    ws, at, size = _workspace(ws, lib.qlora_mx_linear_workspace_bytes(X.rows, W.rows, X.cols), device)
+    _run("qlora_mx_linear", device, ctypes.byref(sx), ctypes.byref(sw), out.data_ptr(), at, size)
+    return out
+
+
+def qlora_mx_linear_grouped(X: MXMatrix, W: MXMatrix, offsets, out=None):
+    """Y[i] = X[i] W_e^T for offsets[e] <= i < offsets[e + 1]: X [M, K] with its
+    rows sorted by expert, W [experts * N, K] the experts' weights one below the
+    other, offsets int32 [experts + 1] on the device. Rows that no expert has
+    are left as they were (zero in a new Y)."""
+    device = X.device
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("offsets must be a tensor [experts + 1]")
+    _tensor("offsets", offsets, torch.int32, offsets.shape, device)
+    experts = offsets.shape[0] - 1
+    sx, sw = X.c_struct("X"), W.c_struct("W", device)
+    if W.rows % experts:
+        raise ValueError(f"W has {W.rows} rows, not a multiple of {experts} experts")
+    shape = (X.rows, W.rows // experts)
+    if out is None:
+        out = torch.zeros(shape, dtype=torch.bfloat16, device=device)
+    else:
+        _tensor("out", out, torch.bfloat16, shape, device)
+    _run("qlora_mx_linear_grouped", device, ctypes.byref(sx), ctypes.byref(sw), offsets.data_ptr(), experts,
+         out.data_ptr())
+    return out

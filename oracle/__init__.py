@@ -18,6 +18,8 @@ Modules
   merge   merging an adapter into the dequantized base (fp64 rank sum,
           one rounding to fp32) and requantizing it.
   adamw   one AdamW step of the adapter parameters in fp32, op by op.
+  mx      microscaled formats (OCP Microscaling Formats specification 1.0),
+          RMSNorm forward and backward, and the products, in fp64.
 
 Sources (the pages the method is taken from):
   * Guanaco topic page (chipfoundryservices.com), "Technical Innovations":
@@ -38,4 +40,4 @@ Sources (the pages the method is taken from):
 Every function whose result is pinned only by its own self-consistency says
 "parity unpinned" in its docstring; at present none does.
 """
-from . import nf4, linear, merge, adamw  # noqa: F401
+from . import nf4, linear, merge, adamw, mx  # noqa: F401
