@@ -1,0 +1,281 @@
+// Tile engine of the large microscaled products: a BN x BM tile of Y^T (BN
+// rows of the 4-bit W, BM rows of X) per workgroup on
+// v_mfma_scale_f32_32x32x64_f8f6f4, fp32 accumulators in registers.
+//
+// W is the instruction's first operand, so a lane ends with four consecutive
+// columns of one row of Y (8-byte stores). Lane l (g = l / 32, l % 32 the row)
+// supplies, of the instruction's two blocks of 32, for a 4-bit operand the 16
+// bytes of block g, for an 8-bit one 16 bytes of each block (the half g), and
+// the scale byte of block g.
+//
+// The reduction runs in steps of 128 elements, two instructions deep. Codes
+// come by global_load_lds_dwordx4 into a ring of LDS stages, STAGES - 1 steps
+// ahead, one barrier a step; nothing is decoded. Scales come the same way, 16
+// bytes a row (512 elements) every four steps, into two buffers. The matrix
+// instructions of a step's second half run after the next step's
+// barrier: they cover its first LDS reads.
+//
+// LDS rows are 128 bytes (8-bit codes) or 64 (4-bit), unpadded, their 16-byte
+// chunks swapped by an exclusive or with the row so that the 32 rows that a
+// wave reads at one chunk fall on all banks; a copy fetches the chunk that
+// belongs at its lane's place.
+//
+// Behind the end of K the last step re-reads chunks of the same rows; their
+// scale bytes are the pad bytes 0 of both operands, 2^-254 together, which
+// vanishes in fp32 for every finite code. Rows past M or N are read from the
+// last row and not stored.
+#pragma once
+
+#include "gemm_core.h"
+#include "mx_device.h"
+
+namespace qnf4 {
+
+typedef int mx_v4i __attribute__((ext_vector_type(4)));
+typedef int mx_v8i __attribute__((ext_vector_type(8)));
+
+// The registers of one operand: 16 bytes (4-bit codes) or two times 16.
+__device__ __forceinline__ mx_v8i mx_operand(mx_v4i a) { return __builtin_shufflevector(a, mx_v4i{0, 0, 0, 0}, 0, 1, 2, 3, 4, 5, 6, 7); }
+__device__ __forceinline__ mx_v8i mx_operand(mx_v4i a, mx_v4i b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
+
+template <int XT_, int NF_, int MF_, int WN_, int WM_, int STAGES_>
+struct MxTile {
+  static constexpr int XT = XT_, NF = NF_, MF = MF_, WN = WN_, WM = WM_, STAGES = STAGES_;
+  static constexpr int kWaves = WN * WM, kThreads = 64 * kWaves;
+  static constexpr int BN = 32 * NF * WN, BM = 32 * MF * WM;
+  static constexpr int kXRow = XT == QLORA_MX_FP4 ? 64 : 128;   // bytes of a row and step
+  static constexpr int kW = BN * 64, kX = BM * kXRow, kStage = kW + kX;
+  static constexpr int kScale = (BN + BM) * 16;
+  static constexpr int kLds = STAGES * kStage + 2 * kScale;
+  static constexpr int kWCopies = kW / 1024 / kWaves, kXCopies = kX / 1024 / kWaves;
+  static constexpr int kCopies = kWCopies + kXCopies;
+  static_assert(kW % (1024 * kWaves) == 0 && kX % (1024 * kWaves) == 0, "whole copies per wave");
+  static_assert((BN + BM) / 64 <= kWaves && BN % 64 == 0 && BM % 64 == 0, "one scale copy per wave");
+  static_assert(kLds <= 160 * 1024, "LDS");
+  // a buffer of scales (four steps) is filled STAGES - 1 steps ahead: not before its readers are done
+  static_assert(STAGES == 3 || STAGES == 4, "ring");
+  static_assert(kCopies * (STAGES - 2) < 64, "vmcnt range");
+};
+
+// Byte offset of chunk c of row r in a tile of 64-byte rows / 128-byte rows.
+__device__ __forceinline__ uint32_t mx_off64(int r, int c) {
+  return static_cast<uint32_t>((r >> 1) * 128 + ((((r & 1) << 2 | c) ^ ((r >> 1) & 7)) << 4));
+}
+__device__ __forceinline__ uint32_t mx_off128(int r, int c) {
+  return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
+}
+
+// A value that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ int64_t mx_uniform(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(static_cast<uint64_t>(v) >> 32));
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+__device__ __forceinline__ const uint8_t *mx_uniform(const uint8_t *p) {
+  return reinterpret_cast<const uint8_t *>(mx_uniform(static_cast<int64_t>(reinterpret_cast<uintptr_t>(p))));
+}
+
+// 16 bytes per lane from base + off into LDS at dst + 16 lane. Returns nothing
+// into registers; waits are explicit (mx_wait).
+__device__ __forceinline__ void mx_copy(uint32_t dst, uint32_t off, const uint8_t *base) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" 
+               :
+               : "s"(dst), "v"(off), "s"(base)
+               : "memory", "m0");
+}
+
+// Until at most N vector-memory operations of the wave are in flight.
+template <int N>
+__device__ __forceinline__ void mx_wait() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+  asm volatile("" ::: "memory");
+}
+
+// Every LDS read of this wave is in registers, then the workgroup's barrier.
+__device__ __forceinline__ void mx_barrier() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// The copies of one operand: rows of ROWB bytes a step, lane's chunk and rows.
+template <int ROWB, int COPIES, int WAVES>
+struct MxCopies {
+  const uint8_t *base;
+  uint32_t row[COPIES];   // byte offset of the lane's row per copy
+  uint32_t chunk, last;   // byte of the lane's chunk in the step; the row's last chunk
+  __device__ MxCopies(const uint8_t *codes, int64_t row0, int64_t rows, int64_t ld) {
+    base = mx_uniform(codes + row0 * ld);
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int line = lane >> 3, p = lane & 7;
+    int r, c;
+    if constexpr (ROWB == 64) {
+      const int q = p ^ line;
+      r = 2 * line + (q >> 2);
+      c = q & 3;
+    } else {
+      r = line;
+      c = p ^ line;
+    }
+    const int64_t end = rows - 1 - row0;
+#pragma unroll
+    for (int i = 0; i < COPIES; ++i) {
+      const int64_t at = (w + WAVES * i) * (1024 / ROWB) + r;
+      row[i] = static_cast<uint32_t>((at < end ? at : end) * ld);
+    }
+    chunk = static_cast<uint32_t>(16 * c);
+    last = static_cast<uint32_t>(ld - 16);
+  }
+  // dst: LDS address of the wave's first block of the stage's tile
+  __device__ __forceinline__ void issue(int step, uint32_t dst) const {
+    const uint32_t k = min(static_cast<uint32_t>(step) * ROWB + chunk, last);
+#pragma unroll
+    for (int i = 0; i < COPIES; ++i) mx_copy(dst + 1024u * WAVES * i, row[i] + k, base);
+  }
+};
+
+template <class T>
+struct MxFrags {
+  mx_v8i w[T::NF], x[T::MF];
+};
+
+template <class T>
+struct MxAcc {
+  f32x16 v[T::NF][T::MF];
+};
+
+// One slice's matrix instructions, with the scale bytes 2 SLICE of the words.
+template <class T, int SLICE>
+__device__ __forceinline__ void mx_mma(MxAcc<T> &acc, const MxFrags<T> &f, const int (&sw)[T::NF], const int (&sx)[T::MF]) {
+#pragma unroll
+  for (int i = 0; i < T::NF; ++i)
+#pragma unroll
+    for (int j = 0; j < T::MF; ++j)
+      acc.v[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          f.w[i], f.x[j], acc.v[i][j], 4, T::XT == QLORA_MX_FP4 ? 4 : 0, 2 * SLICE, sw[i], 2 * SLICE, sx[j]);
+}
+
+struct MxOperands {
+  const uint8_t *x, *xs, *w, *ws;
+  int64_t x_rows, w_rows;      // rows that may be read
+  int64_t x_ld, w_ld;          // bytes of a row of codes
+  uint32_t pitch;
+};
+
+// acc += the tile at (n0, m0) over steps [s0, s1); s0 a multiple of four.
+template <class T>
+__device__ __forceinline__ void mx_mainloop(MxAcc<T> &acc, const MxOperands &p, int64_t n0, int64_t m0, int s0, int s1,
+                                            char *smem) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 31, g = lane >> 5;
+  const int wn = wave / T::WM, wm = wave % T::WM;
+  const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char *)smem));
+  const MxCopies<64, T::kWCopies, T::kWaves> cw(p.w, n0, p.w_rows, p.w_ld);
+  const MxCopies<T::kXRow, T::kXCopies, T::kWaves> cx(p.x, m0, p.x_rows, p.x_ld);
+  // scales: wave w < (BN + BM) / 64 copies those of 64 rows
+  const bool scales = wave < (T::BN + T::BM) / 64;
+  const bool of_w = 64 * wave < T::BN;
+  const uint8_t *sbase = mx_uniform(of_w ? p.ws + n0 * p.pitch : p.xs + m0 * p.pitch);
+  const int64_t send = of_w ? p.w_rows - 1 - n0 : p.x_rows - 1 - m0;
+  const int64_t sat = 64 * wave - (of_w ? 0 : T::BN) + lane;
+  const uint32_t srow = static_cast<uint32_t>((sat < send ? sat : send) * p.pitch);
+  const uint32_t sdst = lds + T::STAGES * T::kStage + 1024u * wave;
+
+  auto issue = [&](int step) {
+    const uint32_t stage = lds + static_cast<uint32_t>((step - s0) % T::STAGES) * T::kStage + 1024u * wave;
+    if ((step & 3) == 0 && scales)
+      mx_copy(sdst + static_cast<uint32_t>(step & 4) / 4 * T::kScale, srow + 4u * static_cast<uint32_t>(step), sbase);
+    cw.issue(step, stage);
+    cx.issue(step, stage + T::kW);
+  };
+
+  // the lane's LDS offsets within a stage, slices 0 and 1
+  uint32_t ow[2], oxa[2], oxb[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    ow[s] = mx_off64(32 * T::NF * wn + r, 2 * s + g);
+    if constexpr (T::XT == QLORA_MX_FP4) {
+      oxa[s] = T::kW + mx_off64(32 * T::MF * wm + r, 2 * s + g);
+    } else {
+      oxa[s] = T::kW + mx_off128(32 * T::MF * wm + r, 4 * s + g);
+      oxb[s] = T::kW + mx_off128(32 * T::MF * wm + r, 4 * s + 2 + g);
+    }
+  }
+  auto read = [&](MxFrags<T> &f, const char *stage, int s) {
+#pragma unroll
+    for (int i = 0; i < T::NF; ++i) f.w[i] = mx_operand(*reinterpret_cast<const mx_v4i *>(stage + ow[s] + 2048 * i));
+#pragma unroll
+    for (int j = 0; j < T::MF; ++j) {
+      const mx_v4i xa = *reinterpret_cast<const mx_v4i *>(stage + oxa[s] + 32 * T::kXRow * j);
+      if constexpr (T::XT == QLORA_MX_FP4) f.x[j] = mx_operand(xa);
+      else f.x[j] = mx_operand(xa, *reinterpret_cast<const mx_v4i *>(stage + oxb[s] + 32 * T::kXRow * j));
+    }
+  };
+
+  int sw[T::NF], sx[T::MF];       // scale words of this step, the lane's blocks in bytes 0 and 2
+  MxFrags<T> f0, f1;
+#pragma unroll
+  for (int i = 0; i < T::STAGES - 1; ++i)
+    if (s0 + i < s1) issue(s0 + i);
+
+  auto step = [&](auto jc, int i) {
+    constexpr int j = decltype(jc)::value;
+    if (i + T::STAGES - 1 <= s1) mx_wait<T::kCopies *(T::STAGES - 2)>();
+    else mx_wait<0>();
+    mx_barrier();
+    if (i + T::STAGES - 1 < s1) issue(i + T::STAGES - 1);
+    const char *stage = smem + static_cast<uint32_t>((i - s0) % T::STAGES) * T::kStage;
+    read(f0, stage, 0);
+    const char *sc = smem + T::STAGES * T::kStage + static_cast<uint32_t>(i & 4) / 4 * T::kScale + 4 * j + 16 * r;
+    uint32_t pw[T::NF], px[T::MF];
+#pragma unroll
+    for (int n = 0; n < T::NF; ++n) pw[n] = *reinterpret_cast<const uint32_t *>(sc + 512 * (T::NF * wn + n));
+#pragma unroll
+    for (int m = 0; m < T::MF; ++m) px[m] = *reinterpret_cast<const uint32_t *>(sc + 16 * T::BN + 512 * (T::MF * wm + m));
+    if (i > s0) mx_mma<T, 1>(acc, f1, sw, sx);   // the previous step's second half
+#pragma unroll
+    for (int n = 0; n < T::NF; ++n) sw[n] = static_cast<int>(pw[n] >> (8 * g));
+#pragma unroll
+    for (int m = 0; m < T::MF; ++m) sx[m] = static_cast<int>(px[m] >> (8 * g));
+    read(f1, stage, 1);
+    mx_mma<T, 0>(acc, f0, sw, sx);
+  };
+  for (int i = s0; i < s1; i += 4) {
+    step(std::integral_constant<int, 0>{}, i);
+    if (i + 1 < s1) step(std::integral_constant<int, 1>{}, i + 1);
+    if (i + 2 < s1) step(std::integral_constant<int, 2>{}, i + 2);
+    if (i + 3 < s1) step(std::integral_constant<int, 3>{}, i + 3);
+  }
+  if (s1 > s0) mx_mma<T, 1>(acc, f1, sw, sx);
+}
+
+// Y[m][n] = bf16(acc), m < m_end, n < N. Lane l holds row m = l % 32 of a
+// fragment, columns 8 q + 4 (l / 32) + 0 .. 3.
+template <class T>
+__device__ __forceinline__ void mx_store(const MxAcc<T> &acc, __bf16 *y, int64_t N, int64_t n0, int64_t m0, int64_t m_end) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wn = wave / T::WM, wm = wave % T::WM;
+#pragma unroll
+  for (int j = 0; j < T::MF; ++j) {
+    const int64_t m = m0 + 32 * (T::MF * wm + j) + (lane & 31);
+    if (m >= m_end) continue;
+#pragma unroll
+    for (int i = 0; i < T::NF; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t n = n0 + 32 * (T::NF * wn + i) + 8 * q + 4 * (lane >> 5);
+        __bf16 *o = y + m * N + n;
+        if ((N & 3) == 0) {
+          if (n < N)
+            *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16x2(acc.v[i][j][4 * q], acc.v[i][j][4 * q + 1]),
+                                                       pack_bf16x2(acc.v[i][j][4 * q + 2], acc.v[i][j][4 * q + 3]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < N) o[e] = static_cast<__bf16>(acc.v[i][j][4 * q + e]);
+        }
+      }
+  }
+}
+
+}  // namespace qnf4

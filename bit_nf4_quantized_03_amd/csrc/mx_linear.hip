@@ -11,7 +11,9 @@
 // of its scales) are taken in four steps, step i using blocks 4 b + i: a lane
 // then needs one 4-byte word of scales (blocks 4 g .. 4 g + 3, the selector
 // counting the steps) and 64 contiguous bytes of 4-bit codes.
-#include "mx_device.h"
+#include <type_traits>
+
+#include "mx_gemm.h"
 
 namespace qnf4 {
 namespace {
@@ -116,11 +118,141 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_gemv(const GemvParams p) {
   }
 }
 
+// ---------------------------------------------------------------- large tiles
+
+struct GemmParams {
+  MxOperands op;
+  const int32_t *offsets;
+  __bf16 *y;
+  int64_t M, N;
+  int steps, experts;
+};
+
+template <class T>
+__global__ __launch_bounds__(T::kThreads, 1) void k_mx_gemm(const GemmParams p) {
+  __shared__ __attribute__((aligned(16))) char smem[T::kLds];
+  const int tiles_m = static_cast<int>((p.M + T::BM - 1) / T::BM), tiles_n = static_cast<int>((p.N + T::BN - 1) / T::BN);
+  int tm, tn;
+  tile_of(static_cast<int>(blockIdx.x), tiles_m, tiles_n, tm, tn);
+  const int64_t n0 = static_cast<int64_t>(tn) * T::BN, m0 = static_cast<int64_t>(tm) * T::BM;
+  MxAcc<T> acc;
+#pragma unroll
+  for (int i = 0; i < T::NF; ++i)
+#pragma unroll
+    for (int j = 0; j < T::MF; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc.v[i][j][e] = 0.0f;
+  mx_mainloop<T>(acc, p.op, n0, m0, 0, p.steps, smem);
+  mx_store<T>(acc, p.y, p.N, n0, m0, p.M);
+}
+
+// Tile of a workgroup in the product by expert. Tiles are counted expert after
+// expert; each XCD takes a contiguous range of them (consecutive workgroups go
+// to the XCDs in turn). Every wave finds its tile by itself: the lanes count
+// the tiles of 64 experts at a time.
+struct GroupTile {
+  int expert, tm, tn;
+  int64_t m_begin, m_end;
+};
+
+__device__ __forceinline__ int expert_tiles(const GemmParams &p, int e, int bm, int tiles_n, int64_t &b, int64_t &end) {
+  b = end = 0;
+  if (e >= p.experts) return 0;
+  b = min(max(static_cast<int64_t>(p.offsets[e]), int64_t(0)), p.M);
+  end = min(max(static_cast<int64_t>(p.offsets[e + 1]), int64_t(0)), p.M);
+  return end > b ? static_cast<int>((end - b + bm - 1) / bm) * tiles_n : 0;
+}
+
+template <class T>
+__device__ __forceinline__ bool group_tile(const GemmParams &p, int bid, GroupTile &out) {
+  const int lane = threadIdx.x & 63;
+  const int tiles_n = static_cast<int>((p.N + T::BN - 1) / T::BN);
+  int64_t b, end;
+  int total = 0;
+  for (int e0 = 0; e0 < p.experts; e0 += 64) total += expert_tiles(p, e0 + lane, T::BM, tiles_n, b, end);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o);
+  if (bid >= total) return false;
+  const int base = total / 8, extra = total % 8, x = bid % 8;
+  int t = x * base + min(x, extra) + bid / 8;
+  for (int e0 = 0;; e0 += 64) {
+    const int n = expert_tiles(p, e0 + lane, T::BM, tiles_n, b, end);
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(upto, o);
+      if (lane >= o) upto += v;
+    }
+    const uint64_t here = __ballot(t < upto);
+    if (here == 0) {
+      t -= __shfl(upto, 63);
+      continue;   // ends: t is below the sum over all experts
+    }
+    const int l = __ffsll(static_cast<unsigned long long>(here)) - 1;
+    t -= __shfl(upto - n, l);
+    out.expert = __builtin_amdgcn_readfirstlane(e0 + l);
+    out.m_begin = mx_uniform(__shfl(b, l));
+    out.m_end = mx_uniform(__shfl(end, l));
+    break;
+  }
+  t = __builtin_amdgcn_readfirstlane(t);
+  // within the expert: groups of four tile rows, as tile_of
+  const int tiles_m = static_cast<int>((out.m_end - out.m_begin + T::BM - 1) / T::BM);
+  const int group = t / (4 * tiles_n), first = 4 * group, gm = min(tiles_m - first, 4), in = t - group * 4 * tiles_n;
+  out.tm = first + in % gm;
+  out.tn = in / gm;
+  return true;
+}
+
+template <class T>
+__global__ __launch_bounds__(T::kThreads, 1) void k_mx_gemm_grouped(const GemmParams p) {
+  __shared__ __attribute__((aligned(16))) char smem[T::kLds];
+  GroupTile t;
+  if (!group_tile<T>(p, static_cast<int>(blockIdx.x), t)) return;
+  const int64_t n0 = static_cast<int64_t>(t.tn) * T::BN;
+  const int64_t m0 = t.m_begin + static_cast<int64_t>(t.tm) * T::BM;
+  MxOperands op = p.op;
+  op.w += static_cast<int64_t>(t.expert) * p.N * op.w_ld;
+  op.ws += static_cast<int64_t>(t.expert) * p.N * op.pitch;
+  op.x_rows = t.m_end;
+  MxAcc<T> acc;
+#pragma unroll
+  for (int i = 0; i < T::NF; ++i)
+#pragma unroll
+    for (int j = 0; j < T::MF; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc.v[i][j][e] = 0.0f;
+  mx_mainloop<T>(acc, op, n0, m0, 0, p.steps, smem);
+  mx_store<T>(acc, p.y, p.N, n0, m0, t.m_end);
+}
+
 template <int XT>
 hipError_t run_gemv(const GemvParams &p, hipStream_t s) {
   const dim3 g(static_cast<unsigned>(ceil_div(p.N, 16)), p.experts ? p.experts : 1);
   k_mx_gemv<XT, 2, 4><<<g, 256, 0, s>>>(p);
   return hipGetLastError();
+}
+
+template <class T>
+hipError_t run_gemm(const GemmParams &p, hipStream_t s) {
+  const int64_t tiles_n = ceil_div(p.N, T::BN);
+  if (p.experts) {
+    // an expert's rows end in at most one partial tile
+    const int64_t most = (p.M / T::BM + p.experts) * tiles_n;
+    k_mx_gemm_grouped<T><<<static_cast<unsigned>(most), T::kThreads, 0, s>>>(p);
+  } else {
+    k_mx_gemm<T><<<static_cast<unsigned>(ceil_div(p.M, T::BM) * tiles_n), T::kThreads, 0, s>>>(p);
+  }
+  return hipGetLastError();
+}
+
+template <int XT>
+hipError_t run_gemm_any(const GemmParams &p, hipStream_t s) {
+  using Big = MxTile<XT, 4, 2, 2, 4, 3>;
+  using Mid = MxTile<XT, 2, 2, 2, 2, 3>;
+  const int64_t rows = p.experts ? p.M / p.experts : p.M;
+  if (rows >= 256) return run_gemm<Big>(p, s);
+  return run_gemm<Mid>(p, s);
 }
 
 }  // namespace
@@ -142,7 +274,17 @@ hipError_t launch_mx_linear(const MxLinear &a, void *, hipStream_t s) {
   p.nblk = static_cast<uint32_t>(a.K / kMxBlock);
   p.pitch = static_cast<uint32_t>(mx_pitch(a.K));
   p.experts = a.experts;
-  return a.x_type == QLORA_MX_FP4 ? run_gemv<QLORA_MX_FP4>(p, s) : run_gemv<QLORA_MX_FP8>(p, s);
+  const int64_t rows = a.experts ? a.M / a.experts : a.M;   // of one weight, on average
+  if (rows <= 32) return a.x_type == QLORA_MX_FP4 ? run_gemv<QLORA_MX_FP4>(p, s) : run_gemv<QLORA_MX_FP8>(p, s);
+  GemmParams q;
+  q.op = {a.x, a.xs, a.w, a.ws, a.M, a.N, p.xrow, p.wrow, p.pitch};
+  q.offsets = a.offsets;
+  q.y = p.y;
+  q.M = a.M;
+  q.N = a.N;
+  q.steps = static_cast<int>(ceil_div(a.K, 128));
+  q.experts = a.experts;
+  return a.x_type == QLORA_MX_FP4 ? run_gemm_any<QLORA_MX_FP4>(q, s) : run_gemm_any<QLORA_MX_FP8>(q, s);
 }
 
 }  // namespace qnf4
