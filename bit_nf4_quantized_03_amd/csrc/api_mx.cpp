@@ -213,13 +213,7 @@ int qlora_rmsnorm_bwd(const void *dY, const void *H, const void *weight, int w_d
                                                    ws, static_cast<hipStream_t>(stream)), fn);
 }
 
-size_t qlora_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (!valid_shape(M, K) || !valid_shape(N, K) || M > kMaxElems / N) return 0;
-  return qnf4::mx_linear_ws_bytes(M, N, K);
-}
-
-int qlora_mx_linear(const qlora_mx_matrix *X, const qlora_mx_matrix *W, void *Y, void *ws, size_t ws_bytes,
-                    void *stream) {
+int qlora_mx_linear(const qlora_mx_matrix *X, const qlora_mx_matrix *W, void *Y, void *stream) {
   const char *fn = "qlora_mx_linear";
   int st = check_matrix(fn, "X", X);
   if (st != QLORA_OK) return st;
@@ -227,12 +221,8 @@ int qlora_mx_linear(const qlora_mx_matrix *X, const qlora_mx_matrix *W, void *Y,
   if (st != QLORA_OK) return st;
   st = check_product(fn, X, W, W->rows, Y);
   if (st != QLORA_OK) return st;
-  const size_t need = qnf4::mx_linear_ws_bytes(X->rows, W->rows, X->cols);
-  if (need > 0 && (!ws || ws_bytes < need))
-    return api_fail(QLORA_ERR_WORKSPACE, "%s: workspace needs %zu bytes, got %zu", fn, need, ws ? ws_bytes : size_t(0));
-  if (need > 0 && !aligned16(ws)) return api_fail(QLORA_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
-  return qnf4::api_hip_status(qnf4::launch_mx_linear(product_args(X, W, W->rows, Y), need > 0 ? ws : nullptr,
-                                                     static_cast<hipStream_t>(stream)), fn);
+  return qnf4::api_hip_status(qnf4::launch_mx_linear(product_args(X, W, W->rows, Y), static_cast<hipStream_t>(stream)),
+                              fn);
 }
 
 int qlora_mx_linear_grouped(const qlora_mx_matrix *X, const qlora_mx_matrix *W, const int32_t *offsets,
@@ -256,7 +246,7 @@ int qlora_mx_linear_grouped(const qlora_mx_matrix *X, const qlora_mx_matrix *W, 
   qnf4::MxLinear a = product_args(X, W, W->rows / experts, Y);
   a.offsets = offsets;
   a.experts = experts;
-  return qnf4::api_hip_status(qnf4::launch_mx_linear(a, nullptr, static_cast<hipStream_t>(stream)), fn);
+  return qnf4::api_hip_status(qnf4::launch_mx_linear(a, static_cast<hipStream_t>(stream)), fn);
 }
 
 }  // extern "C"

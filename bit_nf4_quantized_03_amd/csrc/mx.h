@@ -50,7 +50,6 @@ struct MxLinear {
   void *Y;
 };
 constexpr int64_t kMxMaxK = int64_t(1) << 22;
-size_t mx_linear_ws_bytes(int64_t M, int64_t N, int64_t K);
-hipError_t launch_mx_linear(const MxLinear &a, void *ws, hipStream_t s);
+hipError_t launch_mx_linear(const MxLinear &a, hipStream_t s);
 
 }  // namespace qnf4

@@ -38,23 +38,26 @@ typedef int mx_v8i __attribute__((ext_vector_type(8)));
 __device__ __forceinline__ mx_v8i mx_operand(mx_v4i a) { return __builtin_shufflevector(a, mx_v4i{0, 0, 0, 0}, 0, 1, 2, 3, 4, 5, 6, 7); }
 __device__ __forceinline__ mx_v8i mx_operand(mx_v4i a, mx_v4i b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
 
-template <int XT_, int NF_, int MF_, int WN_, int WM_, int STAGES_>
+template <int XT_, int NF_, int MF_, int WN_, int WM_, int STAGES_, int KG_ = 1>
 struct MxTile {
-  static constexpr int XT = XT_, NF = NF_, MF = MF_, WN = WN_, WM = WM_, STAGES = STAGES_;
-  static constexpr int kWaves = WN * WM, kThreads = 64 * kWaves;
+  static constexpr int XT = XT_, NF = NF_, MF = MF_, WN = WN_, WM = WM_, STAGES = STAGES_, KG = KG_;
+  static constexpr int kWaves = WN * WM, kThreads = 64 * kWaves * KG;   // waves of one group
   static constexpr int BN = 32 * NF * WN, BM = 32 * MF * WM;
   static constexpr int kXRow = XT == QLORA_MX_FP4 ? 64 : 128;   // bytes of a row and step
   static constexpr int kW = BN * 64, kX = BM * kXRow, kStage = kW + kX;
   static constexpr int kScale = (BN + BM) * 16;
-  static constexpr int kLds = STAGES * kStage + 2 * kScale;
+  static constexpr int kRing = STAGES * kStage + 2 * kScale;   // of one group
+  static constexpr int kLds = KG * kRing;
   static constexpr int kWCopies = kW / 1024 / kWaves, kXCopies = kX / 1024 / kWaves;
   static constexpr int kCopies = kWCopies + kXCopies;
   static_assert(kW % (1024 * kWaves) == 0 && kX % (1024 * kWaves) == 0, "whole copies per wave");
-  static_assert((BN + BM) / 64 <= kWaves && BN % 64 == 0 && BM % 64 == 0, "one scale copy per wave");
+  static constexpr int kScaleBlocks = (BN + BM) / 64, kScaleCopies = (kScaleBlocks + kWaves - 1) / kWaves;
+  static_assert(BN % 64 == 0 && BM % 64 == 0, "whole scale copies");
   static_assert(kLds <= 160 * 1024, "LDS");
   // a buffer of scales (four steps) is filled STAGES - 1 steps ahead: not before its readers are done
   static_assert(STAGES == 3 || STAGES == 4, "ring");
   static_assert(kCopies * (STAGES - 2) < 64, "vmcnt range");
+  static_assert(KG == 1 || (KG - 1) * BN * BM * 4 <= kLds, "the groups' sums fit the ring");
 };
 
 // Byte offset of chunk c of row r in a tile of 64-byte rows / 128-byte rows.
@@ -104,9 +107,9 @@ struct MxCopies {
   const uint8_t *base;
   uint32_t row[COPIES];   // byte offset of the lane's row per copy
   uint32_t chunk, last;   // byte of the lane's chunk in the step; the row's last chunk
-  __device__ MxCopies(const uint8_t *codes, int64_t row0, int64_t rows, int64_t ld) {
+  __device__ MxCopies(const uint8_t *codes, int64_t row0, int64_t rows, int64_t ld, int w) {
     base = mx_uniform(codes + row0 * ld);
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
     const int line = lane >> 3, p = lane & 7;
     int r, c;
     if constexpr (ROWB == 64) {
@@ -162,29 +165,41 @@ struct MxOperands {
   uint32_t pitch;
 };
 
-// acc += the tile at (n0, m0) over steps [s0, s1); s0 a multiple of four.
+// acc += the tile at (n0, m0) over steps [s0, s1) of the wave's group; s0 a
+// multiple of four, `most` the longest group's number of steps (every wave
+// passes that many barriers).
 template <class T>
 __device__ __forceinline__ void mx_mainloop(MxAcc<T> &acc, const MxOperands &p, int64_t n0, int64_t m0, int s0, int s1,
-                                            char *smem) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+                                            int most, char *smem, int wave) {
+  const int lane = threadIdx.x & 63;
   const int r = lane & 31, g = lane >> 5;
   const int wn = wave / T::WM, wm = wave % T::WM;
   const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char *)smem));
-  const MxCopies<64, T::kWCopies, T::kWaves> cw(p.w, n0, p.w_rows, p.w_ld);
-  const MxCopies<T::kXRow, T::kXCopies, T::kWaves> cx(p.x, m0, p.x_rows, p.x_ld);
-  // scales: wave w < (BN + BM) / 64 copies those of 64 rows
-  const bool scales = wave < (T::BN + T::BM) / 64;
-  const bool of_w = 64 * wave < T::BN;
-  const uint8_t *sbase = mx_uniform(of_w ? p.ws + n0 * p.pitch : p.xs + m0 * p.pitch);
-  const int64_t send = of_w ? p.w_rows - 1 - n0 : p.x_rows - 1 - m0;
-  const int64_t sat = 64 * wave - (of_w ? 0 : T::BN) + lane;
-  const uint32_t srow = static_cast<uint32_t>((sat < send ? sat : send) * p.pitch);
+  const MxCopies<64, T::kWCopies, T::kWaves> cw(p.w, n0, p.w_rows, p.w_ld, wave);
+  const MxCopies<T::kXRow, T::kXCopies, T::kWaves> cx(p.x, m0, p.x_rows, p.x_ld, wave);
+  // scales: block b of 64 rows (W's rows, then X's) by wave b % kWaves
+  const uint8_t *sbase[T::kScaleCopies];
+  uint32_t srow[T::kScaleCopies];
+#pragma unroll
+  for (int c = 0; c < T::kScaleCopies; ++c) {
+    const int first = 64 * (wave + T::kWaves * c);
+    const bool of_w = first < T::BN;
+    sbase[c] = mx_uniform(of_w ? p.ws + n0 * p.pitch : p.xs + m0 * p.pitch);
+    const int64_t end = of_w ? p.w_rows - 1 - n0 : p.x_rows - 1 - m0;
+    const int64_t at = first - (of_w ? 0 : T::BN) + lane;
+    srow[c] = static_cast<uint32_t>((at < end ? at : end) * p.pitch);
+  }
   const uint32_t sdst = lds + T::STAGES * T::kStage + 1024u * wave;
 
   auto issue = [&](int step) {
     const uint32_t stage = lds + static_cast<uint32_t>((step - s0) % T::STAGES) * T::kStage + 1024u * wave;
-    if ((step & 3) == 0 && scales)
-      mx_copy(sdst + static_cast<uint32_t>(step & 4) / 4 * T::kScale, srow + 4u * static_cast<uint32_t>(step), sbase);
+    if ((step & 3) == 0) {
+#pragma unroll
+      for (int c = 0; c < T::kScaleCopies; ++c)
+        if (wave + T::kWaves * c < T::kScaleBlocks)
+          mx_copy(sdst + static_cast<uint32_t>(step & 4) / 4 * T::kScale + 1024u * T::kWaves * c,
+                  srow[c] + 4u * static_cast<uint32_t>(step), sbase[c]);
+    }
     cw.issue(step, stage);
     cx.issue(step, stage + T::kW);
   };
@@ -223,6 +238,7 @@ __device__ __forceinline__ void mx_mainloop(MxAcc<T> &acc, const MxOperands &p, 
     if (i + T::STAGES - 1 <= s1) mx_wait<T::kCopies *(T::STAGES - 2)>();
     else mx_wait<0>();
     mx_barrier();
+    if (T::KG > 1 && i >= s1) return;
     if (i + T::STAGES - 1 < s1) issue(i + T::STAGES - 1);
     const char *stage = smem + static_cast<uint32_t>((i - s0) % T::STAGES) * T::kStage;
     read(f0, stage, 0);
@@ -240,20 +256,66 @@ __device__ __forceinline__ void mx_mainloop(MxAcc<T> &acc, const MxOperands &p, 
     read(f1, stage, 1);
     mx_mma<T, 0>(acc, f0, sw, sx);
   };
-  for (int i = s0; i < s1; i += 4) {
+  const int end = T::KG > 1 ? s0 + most : s1;
+  for (int i = s0; i < end; i += 4) {
     step(std::integral_constant<int, 0>{}, i);
-    if (i + 1 < s1) step(std::integral_constant<int, 1>{}, i + 1);
-    if (i + 2 < s1) step(std::integral_constant<int, 2>{}, i + 2);
-    if (i + 3 < s1) step(std::integral_constant<int, 3>{}, i + 3);
+    if (i + 1 < end) step(std::integral_constant<int, 1>{}, i + 1);
+    if (i + 2 < end) step(std::integral_constant<int, 2>{}, i + 2);
+    if (i + 3 < end) step(std::integral_constant<int, 3>{}, i + 3);
   }
   if (s1 > s0) mx_mma<T, 1>(acc, f1, sw, sx);
 }
 
-// Y[m][n] = bf16(acc), m < m_end, n < N. Lane l holds row m = l % 32 of a
-// fragment, columns 8 q + 4 (l / 32) + 0 .. 3.
+// The whole product of a tile: the workgroup's KG groups of waves take a
+// contiguous part of the steps each, with a ring of their own, and the first
+// group gets the sums, added in group order. Returns whether the wave is of
+// that group; `wave` is its number in the group.
 template <class T>
-__device__ __forceinline__ void mx_store(const MxAcc<T> &acc, __bf16 *y, int64_t N, int64_t n0, int64_t m0, int64_t m_end) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+__device__ __forceinline__ bool mx_tile_product(MxAcc<T> &acc, const MxOperands &p, int64_t n0, int64_t m0, int steps,
+                                                char *smem, int &wave) {
+#pragma unroll
+  for (int i = 0; i < T::NF; ++i)
+#pragma unroll
+    for (int j = 0; j < T::MF; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc.v[i][j][e] = 0.0f;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), group = w / T::kWaves;
+  wave = w % T::kWaves;
+  const int per = T::KG > 1 ? (steps + 4 * T::KG - 1) / (4 * T::KG) * 4 : steps;
+  const int s0 = min(steps, group * per);
+  mx_mainloop<T>(acc, p, n0, m0, s0, min(steps, s0 + per), min(steps, per), smem + group * T::kRing, wave);
+  if constexpr (T::KG > 1) {
+    __syncthreads();   // the rings are free
+    float4 *sums = reinterpret_cast<float4 *>(smem);
+    constexpr int kRegs = T::NF * T::MF * 4;   // float4 a lane
+    if (group > 0) {
+#pragma unroll
+      for (int i = 0; i < kRegs; ++i) {
+        const f32x16 &v = acc.v[i / 4 / T::MF][i / 4 % T::MF];
+        const int q = 4 * (i % 4);
+        sums[((group - 1) * kRegs + i) * (64 * T::kWaves) + 64 * wave + (threadIdx.x & 63)] = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+      }
+    }
+    __syncthreads();
+    if (group > 0) return false;
+#pragma unroll
+    for (int k = 0; k < T::KG - 1; ++k)
+#pragma unroll
+      for (int i = 0; i < kRegs; ++i) {
+        f32x16 &v = acc.v[i / 4 / T::MF][i / 4 % T::MF];
+        const int q = 4 * (i % 4);
+        const float4 a = sums[(k * kRegs + i) * (64 * T::kWaves) + 64 * wave + (threadIdx.x & 63)];
+        v[q] += a.x, v[q + 1] += a.y, v[q + 2] += a.z, v[q + 3] += a.w;
+      }
+  }
+  return true;
+}
+
+// fn(m, n, v): the four sums v of row m, columns n .. n + 3. Lane l holds
+// row m = l % 32 of a fragment, columns 8 q + 4 (l / 32) + 0 .. 3.
+template <class T, class F>
+__device__ __forceinline__ void mx_each4(const MxAcc<T> &acc, int64_t n0, int64_t m0, int64_t m_end, int wave, F fn) {
+  const int lane = threadIdx.x & 63;
   const int wn = wave / T::WM, wm = wave % T::WM;
 #pragma unroll
   for (int j = 0; j < T::MF; ++j) {
@@ -263,18 +325,29 @@ __device__ __forceinline__ void mx_store(const MxAcc<T> &acc, __bf16 *y, int64_t
     for (int i = 0; i < T::NF; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int64_t n = n0 + 32 * (T::NF * wn + i) + 8 * q + 4 * (lane >> 5);
-        __bf16 *o = y + m * N + n;
-        if ((N & 3) == 0) {
-          if (n < N)
-            *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16x2(acc.v[i][j][4 * q], acc.v[i][j][4 * q + 1]),
-                                                       pack_bf16x2(acc.v[i][j][4 * q + 2], acc.v[i][j][4 * q + 3]));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (n + e < N) o[e] = static_cast<__bf16>(acc.v[i][j][4 * q + e]);
-        }
+        const f32x16 &v = acc.v[i][j];
+        fn(m, n0 + 32 * (T::NF * wn + i) + 8 * q + 4 * (lane >> 5),
+           make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
       }
+  }
+}
+
+// Y[m][n] = bf16(acc), m < m_end, n < N.
+template <class T>
+__device__ __forceinline__ void mx_store(const MxAcc<T> &acc, __bf16 *y, int64_t N, int64_t n0, int64_t m0,
+                                         int64_t m_end, int wave) {
+  if ((N & 3) == 0) {
+    mx_each4(acc, n0, m0, m_end, wave, [&](int64_t m, int64_t n, float4 v) {
+      if (n < N) *reinterpret_cast<uint2 *>(y + m * N + n) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    });
+  } else {
+    mx_each4(acc, n0, m0, m_end, wave, [&](int64_t m, int64_t n, float4 v) {
+      __bf16 *o = y + m * N + n;
+      if (n < N) o[0] = static_cast<__bf16>(v.x);
+      if (n + 1 < N) o[1] = static_cast<__bf16>(v.y);
+      if (n + 2 < N) o[2] = static_cast<__bf16>(v.z);
+      if (n + 3 < N) o[3] = static_cast<__bf16>(v.w);
+    });
   }
 }
 

@@ -1,16 +1,15 @@
 // Products of microscaled operands: Y = X W^T, W in 4-bit and X in 8- or 4-bit
 // floats, dense or one W per expert.
 //
-// The scaled matrix instruction v_mfma_scale_f32_16x16x128_f8f6f4 takes the
-// codes as they are stored. Its reduction of 128 is four blocks of 32; lane l
-// (g = l / 16, l % 16 the row) supplies for a 4-bit operand the 16 bytes of
-// block g, for an 8-bit one 16 bytes each of blocks g / 2 and 2 + g / 2 (the
-// half g % 2), and the scale byte of block g, picked from a register by a
-// selector that is the same for all lanes. The sum does not care which blocks
-// of the row an instruction takes, so 512 elements of a row (one 16-byte piece
-// of its scales) are taken in four steps, step i using blocks 4 b + i: a lane
-// then needs one 4-byte word of scales (blocks 4 g .. 4 g + 3, the selector
-// counting the steps) and 64 contiguous bytes of 4-bit codes.
+// The scaled matrix instructions take the codes as they are stored.
+// v_mfma_scale_f32_16x16x128_f8f6f4 (few rows; mx_gemm.h has the larger one)
+// reduces over four blocks of 32; lane l (g = l / 16, l % 16 the row) supplies
+// for a 4-bit operand the 16 bytes of block g, for an 8-bit one 16 bytes each
+// of blocks g / 2 and 2 + g / 2 (the half g % 2), and the scale byte of block
+// g. The four lanes of a row so read 64 contiguous bytes. A row's 16-byte piece
+// of scales serves four instructions, 512 elements.
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "mx_gemm.h"
@@ -18,7 +17,6 @@
 namespace qnf4 {
 namespace {
 
-typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 struct GemvParams {
@@ -31,27 +29,20 @@ struct GemvParams {
   int experts;        // 0: one weight, all rows
 };
 
-__device__ __forceinline__ uint4 load16(const uint8_t *p, bool ok) {
-  return ok ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
+// 16 bytes at p, zeros where the block lies behind the row's end.
+__device__ __forceinline__ mx_v4i load16(const uint8_t *p, bool ok) {
+  return ok ? *reinterpret_cast<const mx_v4i *>(p) : mx_v4i{0, 0, 0, 0};
 }
 
-template <int XT, int STEP>
-__device__ __forceinline__ v4f mma(const uint4 &w, const uint4 &xa, const uint4 &xb, v4f acc, int sw, int sx) {
-  v8i a = {static_cast<int>(w.x), static_cast<int>(w.y), static_cast<int>(w.z), static_cast<int>(w.w), 0, 0, 0, 0};
-  v8i b = {static_cast<int>(xa.x), static_cast<int>(xa.y), static_cast<int>(xa.z), static_cast<int>(xa.w),
-           static_cast<int>(xb.x), static_cast<int>(xb.y), static_cast<int>(xb.z), static_cast<int>(xb.w)};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, XT == QLORA_MX_FP4 ? 4 : 0, STEP, sw, STEP, sx);
-}
-
-// A workgroup takes 16 rows of W (of one expert) and all of the expert's rows
-// of X, 16 MT at a time; its WAVES waves take the 512-element pieces of the
-// reduction in turn and add their sums through LDS in wave order.
-template <int XT, int MT, int WAVES>
+// A workgroup takes 16 RT rows of W (of one expert) and all of the expert's
+// rows of X, 16 MT at a time; its WAVES waves take the 512-element pieces of
+// the reduction in turn and add their sums through LDS in wave order.
+template <int XT, int MT, int RT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_mx_gemv(const GemvParams p) {
-  __shared__ float part[WAVES][MT][16][17];
+  __shared__ float part[WAVES][MT][RT][16][17];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, g = lane >> 4;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (16 * RT);
   int64_t m_begin = 0, m_end = p.M;
   int64_t wbase = 0;
   if (p.experts) {
@@ -60,59 +51,69 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_gemv(const GemvParams p) {
     m_end = min(max(static_cast<int64_t>(p.offsets[e + 1]), int64_t(0)), p.M);
     wbase = static_cast<int64_t>(e) * p.N;
   }
-  const int64_t n = wbase + min(n0 + r, p.N - 1);
-  const uint8_t *wr = p.w + n * p.wrow;
-  const uint8_t *wsr = p.ws + n * p.pitch;
+  const uint8_t *wr[RT], *wsr[RT];
+#pragma unroll
+  for (int k = 0; k < RT; ++k) {
+    const int64_t n = wbase + min(n0 + 16 * k + r, p.N - 1);
+    wr[k] = p.w + n * p.wrow + 16 * g;
+    wsr[k] = p.ws + n * p.pitch;
+  }
   const uint32_t pieces = (p.nblk + 15) / 16;
   for (int64_t m0 = m_begin; m0 < m_end; m0 += 16 * MT) {
-    v4f acc[MT];
+    v4f acc[MT][RT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int k = 0; k < RT; ++k) acc[t][k] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     for (uint32_t q = wave; q < pieces; q += WAVES) {
-      uint4 w[4];
+      mx_v4i w[RT][4], sw[RT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t b = 16 * q + 4 * g + i;
-        w[i] = load16(wr + static_cast<int64_t>(b) * 16, b < p.nblk);
+      for (int k = 0; k < RT; ++k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[k][i] = load16(wr[k] + 256 * q + 64 * i, 16 * q + 4 * i + g < p.nblk);
+        sw[k] = *reinterpret_cast<const mx_v4i *>(wsr[k] + 16 * q);
       }
-      const int sw = *reinterpret_cast<const int *>(wsr + 16 * q + 4 * g);
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         const int64_t m = min(m0 + 16 * t + r, m_end - 1);
-        const uint8_t *xr = p.x + m * p.xrow;
-        uint4 xa[4], xb[4];
+        const uint8_t *xr = p.x + m * p.xrow + 16 * g;
+        mx_v8i x[4];
+        const mx_v4i sx = *reinterpret_cast<const mx_v4i *>(p.xs + m * p.pitch + 16 * q);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if constexpr (XT == QLORA_MX_FP4) {
-            const uint32_t b = 16 * q + 4 * g + i;
-            xa[i] = load16(xr + static_cast<int64_t>(b) * 16, b < p.nblk);
-            xb[i] = make_uint4(0, 0, 0, 0);
+            x[i] = mx_operand(load16(xr + 256 * q + 64 * i, 16 * q + 4 * i + g < p.nblk));
           } else {
-            const uint32_t b = 16 * q + 4 * (g >> 1) + i;
-            xa[i] = load16(xr + static_cast<int64_t>(b) * 32 + 16 * (g & 1), b < p.nblk);
-            xb[i] = load16(xr + static_cast<int64_t>(b + 8) * 32 + 16 * (g & 1), b + 8 < p.nblk);
+            const uint32_t b = 16 * q + 4 * i + (g >> 1);
+            x[i] = mx_operand(load16(xr + 512 * q + 128 * i, b < p.nblk), load16(xr + 512 * q + 128 * i + 64, b + 2 < p.nblk));
           }
         }
-        const int sx = *reinterpret_cast<const int *>(p.xs + m * p.pitch + 16 * q + 4 * g);
-        acc[t] = mma<XT, 0>(w[0], xa[0], xb[0], acc[t], sw, sx);
-        acc[t] = mma<XT, 1>(w[1], xa[1], xb[1], acc[t], sw, sx);
-        acc[t] = mma<XT, 2>(w[2], xa[2], xb[2], acc[t], sw, sx);
-        acc[t] = mma<XT, 3>(w[3], xa[3], xb[3], acc[t], sw, sx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int si = static_cast<int>(static_cast<uint32_t>(sx[i]) >> (8 * g));
+#pragma unroll
+          for (int k = 0; k < RT; ++k)
+            acc[t][k] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                mx_operand(w[k][i]), x[i], acc[t][k], 4, XT == QLORA_MX_FP4 ? 4 : 0, 0,
+                static_cast<int>(static_cast<uint32_t>(sw[k][i]) >> (8 * g)), 0, si);
+        }
       }
     }
     // lane l holds X row l % 16 of a tile, W rows 4 (l / 16) + 0 .. 3
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) part[wave][t][r][4 * g + v] = acc[t][v];
+      for (int k = 0; k < RT; ++k)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) part[wave][t][k][r][4 * g + v] = acc[t][k][v];
     __syncthreads();
-    for (int i = threadIdx.x; i < 256 * MT; i += 64 * WAVES) {
-      const int t = i >> 8, m = (i >> 4) & 15, c = i & 15;
+    for (int i = threadIdx.x; i < 256 * MT * RT; i += 64 * WAVES) {
+      const int c = i & 15, k = (i >> 4) % RT, m = (i >> 4) / RT & 15, t = (i >> 8) / RT;
       float sum = 0.0f;
 #pragma unroll
-      for (int k = 0; k < WAVES; ++k) sum += part[k][t][m][c];
-      const int64_t row = m0 + 16 * t + m;
-      if (row < m_end && n0 + c < p.N) p.y[row * p.N + n0 + c] = static_cast<__bf16>(sum);
+      for (int w = 0; w < WAVES; ++w) sum += part[w][t][k][m][c];
+      const int64_t row = m0 + 16 * t + m, n = n0 + 16 * k + c;
+      if (row < m_end && n < p.N) p.y[row * p.N + n] = static_cast<__bf16>(sum);
     }
     __syncthreads();
   }
@@ -125,25 +126,19 @@ struct GemmParams {
   const int32_t *offsets;
   __bf16 *y;
   int64_t M, N;
-  int steps, experts;
+  int steps;      // of 128 elements
+  int experts;
 };
 
 template <class T>
 __global__ __launch_bounds__(T::kThreads, 1) void k_mx_gemm(const GemmParams p) {
   __shared__ __attribute__((aligned(16))) char smem[T::kLds];
   const int tiles_m = static_cast<int>((p.M + T::BM - 1) / T::BM), tiles_n = static_cast<int>((p.N + T::BN - 1) / T::BN);
-  int tm, tn;
+  int tm, tn, wave;
   tile_of(static_cast<int>(blockIdx.x), tiles_m, tiles_n, tm, tn);
   const int64_t n0 = static_cast<int64_t>(tn) * T::BN, m0 = static_cast<int64_t>(tm) * T::BM;
   MxAcc<T> acc;
-#pragma unroll
-  for (int i = 0; i < T::NF; ++i)
-#pragma unroll
-    for (int j = 0; j < T::MF; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc.v[i][j][e] = 0.0f;
-  mx_mainloop<T>(acc, p.op, n0, m0, 0, p.steps, smem);
-  mx_store<T>(acc, p.y, p.N, n0, m0, p.M);
+  if (mx_tile_product<T>(acc, p.op, n0, m0, p.steps, smem, wave)) mx_store<T>(acc, p.y, p.N, n0, m0, p.M, wave);
 }
 
 // Tile of a workgroup in the product by expert. Tiles are counted expert after
@@ -216,20 +211,14 @@ __global__ __launch_bounds__(T::kThreads, 1) void k_mx_gemm_grouped(const GemmPa
   op.ws += static_cast<int64_t>(t.expert) * p.N * op.pitch;
   op.x_rows = t.m_end;
   MxAcc<T> acc;
-#pragma unroll
-  for (int i = 0; i < T::NF; ++i)
-#pragma unroll
-    for (int j = 0; j < T::MF; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc.v[i][j][e] = 0.0f;
-  mx_mainloop<T>(acc, op, n0, m0, 0, p.steps, smem);
-  mx_store<T>(acc, p.y, p.N, n0, m0, t.m_end);
+  int wave;
+  if (mx_tile_product<T>(acc, op, n0, m0, p.steps, smem, wave)) mx_store<T>(acc, p.y, p.N, n0, m0, t.m_end, wave);
 }
 
-template <int XT>
+template <int XT, int MT, int RT, int WAVES>
 hipError_t run_gemv(const GemvParams &p, hipStream_t s) {
-  const dim3 g(static_cast<unsigned>(ceil_div(p.N, 16)), p.experts ? p.experts : 1);
-  k_mx_gemv<XT, 2, 4><<<g, 256, 0, s>>>(p);
+  const dim3 g(static_cast<unsigned>(ceil_div(p.N, 16 * RT)), p.experts ? p.experts : 1);
+  k_mx_gemv<XT, MT, RT, WAVES><<<g, 64 * WAVES, 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -240,26 +229,90 @@ hipError_t run_gemm(const GemmParams &p, hipStream_t s) {
     // an expert's rows end in at most one partial tile
     const int64_t most = (p.M / T::BM + p.experts) * tiles_n;
     k_mx_gemm_grouped<T><<<static_cast<unsigned>(most), T::kThreads, 0, s>>>(p);
-  } else {
-    k_mx_gemm<T><<<static_cast<unsigned>(ceil_div(p.M, T::BM) * tiles_n), T::kThreads, 0, s>>>(p);
+    return hipGetLastError();
   }
+  k_mx_gemm<T><<<static_cast<unsigned>(ceil_div(p.M, T::BM) * tiles_n), T::kThreads, 0, s>>>(p);
   return hipGetLastError();
 }
 
+// The tiles, and what 128 steps of the reduction cost with them: us that a
+// compute unit takes for a workgroup's step of 128 elements, measured at sizes
+// that fill the GPU with that tile (8-bit X, K = 4096 and 11008). A product
+// takes about as many steps one after another as its fullest compute unit has
+// workgroups times steps, so the cheapest tile is the one with the smallest
+// cost times workgroups per compute unit: large tiles re-read their operands
+// less, small ones leave fewer compute units without work. Measured (us, 8-bit
+// X; the rule's choice first): 4096^3 256 x 256 62, 256 x 128 71, 128 x 128 71;
+// 2048 x 4096 x 4096 256 x 128 37, 128 x 128 39, 256 x 256 53; 301 x 4096 x
+// 11008 128 x 64 30, 64 x 64 34, 128 x 128 35, 256 x 256 119; 128 x 4096 x 4096
+// 64 x 64 10, 128 x 64 14, 128 x 128 19.
+constexpr int kTiles = 5;
+constexpr struct {
+  int bn, bm;
+  double cost;
+} kTile[kTiles] = {{256, 256, 1.68}, {256, 128, 0.92}, {128, 128, 0.50}, {128, 64, 0.28}, {64, 64, 0.18}};
+constexpr double kCus = 256;
+
+int choose_tile(int64_t M, int64_t N, int experts) {
+  int best = 0;
+  double least = 0;
+  for (int i = 0; i < kTiles; ++i) {
+    const double tiles_n = static_cast<double>(ceil_div(N, kTile[i].bn));
+    double full = tiles_n * static_cast<double>(ceil_div(M, kTile[i].bm)) / kCus;
+    // by expert: each one with rows ends in a partial tile, on average half of
+    // one; the counts are on the GPU, so the quarter allows for a few more
+    if (experts)
+      full = 0.25 + tiles_n * std::max(static_cast<double>(M) / kTile[i].bm + 0.5 * experts,
+                                       static_cast<double>(std::min<int64_t>(M, experts))) / kCus;
+    const double t = std::ceil(full) * kTile[i].cost;
+    if (i == 0 || t < least) least = t, best = i;
+  }
+  return best;
+}
+
 template <int XT>
-hipError_t run_gemm_any(const GemmParams &p, hipStream_t s) {
-  using Big = MxTile<XT, 4, 2, 2, 4, 3>;
-  using Mid = MxTile<XT, 2, 2, 2, 2, 3>;
-  const int64_t rows = p.experts ? p.M / p.experts : p.M;
-  if (rows >= 256) return run_gemm<Big>(p, s);
-  return run_gemm<Mid>(p, s);
+hipError_t run_tiles(const GemmParams &p, hipStream_t s) {
+  switch (choose_tile(p.M, p.N, p.experts)) {
+    case 0: return run_gemm<MxTile<XT, 4, 2, 2, 4, 3>>(p, s);
+    case 1: return run_gemm<MxTile<XT, 2, 2, 4, 2, 3>>(p, s);
+    case 2: return run_gemm<MxTile<XT, 2, 2, 2, 2, 3>>(p, s);
+    case 3: return run_gemm<MxTile<XT, 2, 1, 2, 2, 4>>(p, s);
+    default: return run_gemm<MxTile<XT, 1, 1, 2, 2, 3, 2>>(p, s);   // two groups of waves: 10 us where one takes 11.6
+  }
+}
+
+// Few rows: the matrix core's work does not matter, the weight's stream does.
+// X is read by every workgroup, so from 5 rows on, a workgroup takes 64 rows
+// of W where that leaves half of the compute units one (8 x 11008 x 4096: 8.8
+// us against 10.0 with 16 rows), else 16 (16 x 4096 x 4096: 6.1 against 7.9).
+// By expert 32 rows and half the waves (33 rows over eight 11008 x 4096: 41 us
+// against 50 and 54). Returns false where the tiles are faster: from 17 rows
+// on (32 x 11008 x 4096 10.1 us against 16) unless there are few of them (32 x
+// 4096 x 4096 9.4 us against 8.1), by expert from 9 rows on average on.
+template <int XT>
+bool run_few_rows(const GemvParams &p, hipStream_t s, hipError_t *e) {
+  if (p.experts) {
+    if (p.M > 8 * static_cast<int64_t>(p.experts)) return false;
+    *e = run_gemv<XT, 1, 2, 4>(p, s);
+    return true;
+  }
+  const bool many = p.N >= 64 * 128;
+  if (p.M > 32 || (p.M > 16 && many)) return false;
+  if (p.M > 16) *e = run_gemv<XT, 2, 1, 8>(p, s);
+  else if (p.M > 4 && many) *e = run_gemv<XT, 1, 4, 8>(p, s);
+  else *e = run_gemv<XT, 1, 1, 8>(p, s);
+  return true;
+}
+
+template <int XT>
+hipError_t run_product(const GemvParams &p, const GemmParams &q, hipStream_t s) {
+  hipError_t e;
+  return run_few_rows<XT>(p, s, &e) ? e : run_tiles<XT>(q, s);
 }
 
 }  // namespace
 
-size_t mx_linear_ws_bytes(int64_t, int64_t, int64_t) { return 0; }
-
-hipError_t launch_mx_linear(const MxLinear &a, void *, hipStream_t s) {
+hipError_t launch_mx_linear(const MxLinear &a, hipStream_t s) {
   GemvParams p;
   p.x = a.x;
   p.xs = a.xs;
@@ -274,8 +327,6 @@ hipError_t launch_mx_linear(const MxLinear &a, void *, hipStream_t s) {
   p.nblk = static_cast<uint32_t>(a.K / kMxBlock);
   p.pitch = static_cast<uint32_t>(mx_pitch(a.K));
   p.experts = a.experts;
-  const int64_t rows = a.experts ? a.M / a.experts : a.M;   // of one weight, on average
-  if (rows <= 32) return a.x_type == QLORA_MX_FP4 ? run_gemv<QLORA_MX_FP4>(p, s) : run_gemv<QLORA_MX_FP8>(p, s);
   GemmParams q;
   q.op = {a.x, a.xs, a.w, a.ws, a.M, a.N, p.xrow, p.wrow, p.pitch};
   q.offsets = a.offsets;
@@ -284,7 +335,7 @@ hipError_t launch_mx_linear(const MxLinear &a, void *, hipStream_t s) {
   q.N = a.N;
   q.steps = static_cast<int>(ceil_div(a.K, 128));
   q.experts = a.experts;
-  return a.x_type == QLORA_MX_FP4 ? run_gemm_any<QLORA_MX_FP4>(q, s) : run_gemm_any<QLORA_MX_FP8>(q, s);
+  return a.x_type == QLORA_MX_FP4 ? run_product<QLORA_MX_FP4>(p, q, s) : run_product<QLORA_MX_FP8>(p, q, s);
 }
 
 }  // namespace qnf4

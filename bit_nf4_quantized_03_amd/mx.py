@@ -19,13 +19,13 @@ __all__ = [
     "MXMatrix", "QLORA_MX_FP4", "QLORA_MX_FP8", "MX_EXPORTED_SYMBOLS", "qlora_mx_scale_pitch",
     "qlora_mx_storage_bytes", "qlora_mx_quantize", "qlora_mx_dequantize", "qlora_rmsnorm_fwd",
     "qlora_rmsnorm_mx", "qlora_rmsnorm_bwd", "qlora_rmsnorm_bwd_workspace_bytes", "qlora_mx_linear",
-    "qlora_mx_linear_workspace_bytes", "qlora_mx_linear_grouped",
+    "qlora_mx_linear_grouped",
 ]
 
 MX_EXPORTED_SYMBOLS = (
     "qlora_mx_scale_pitch", "qlora_mx_storage_bytes", "qlora_mx_quantize", "qlora_mx_dequantize",
     "qlora_rmsnorm_fwd", "qlora_rmsnorm_mx", "qlora_rmsnorm_bwd", "qlora_rmsnorm_bwd_workspace_bytes",
-    "qlora_mx_linear", "qlora_mx_linear_workspace_bytes", "qlora_mx_linear_grouped",
+    "qlora_mx_linear", "qlora_mx_linear_grouped",
 )
 
 QLORA_MX_FP4 = 0   # sign, 2 exponent bits, 1 mantissa bit; two to a byte
@@ -50,8 +50,7 @@ def _declare():
         "qlora_rmsnorm_mx": (ci, [vp, vp, vp, ci, i64, i64, f64, mp, vp, vp]),
         "qlora_rmsnorm_bwd_workspace_bytes": (sz, [i64, i64]),
         "qlora_rmsnorm_bwd": (ci, [vp, vp, vp, ci, vp, vp, i64, i64, vp, vp, vp, sz, vp]),
-        "qlora_mx_linear_workspace_bytes": (sz, [i64, i64, i64]),
-        "qlora_mx_linear": (ci, [mp, mp, vp, vp, sz, vp]),
+        "qlora_mx_linear": (ci, [mp, mp, vp, vp]),
         "qlora_mx_linear_grouped": (ci, [mp, mp, vp, i32, vp, vp]),
     }
     for name, (res, args) in sigs.items():
@@ -65,17 +64,28 @@ _declare()
 _DTYPES = {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}
 
 
-def _run(name: str, device, *args) -> None:
-    """Call the entry point on the current stream of ``device``, with that
-    device current (the library launches on the current one)."""
+def _entry(name: str):
+    """The entry point as a call (device, *arguments) on the current stream of
+    ``device``, with that device current (the library launches on the current
+    one)."""
     fn = getattr(lib, name)
-    if device.index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    if status != 0:
-        raise QloraError(name, status, qlora_last_error())
+    stream, current = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+
+    def call(device, *args):
+        index = device.index
+        if index == current():
+            status = fn(*args, stream(index))
+        else:
+            with torch.cuda.device(device):
+                status = fn(*args, stream(index))
+        if status != 0:
+            raise QloraError(name, status, qlora_last_error())
+    return call
+
+
+_quantize, _dequantize = _entry("qlora_mx_quantize"), _entry("qlora_mx_dequantize")
+_rmsnorm_fwd, _rmsnorm_mx, _rmsnorm_bwd = (_entry("qlora_rmsnorm_" + x) for x in ("fwd", "mx", "bwd"))
+_linear, _linear_grouped = _entry("qlora_mx_linear"), _entry("qlora_mx_linear_grouped")
 
 
 def _dtype(name, dtype) -> int:
@@ -166,7 +176,7 @@ def qlora_mx_quantize(X, mx: Optional[int] = None, out: Optional[MXMatrix] = Non
     elif mx is not None and mx != out.mx:
         raise ValueError(f"mx {mx} differs from out.mx {out.mx}")
     st = out.c_struct("out", X.device)
-    _run("qlora_mx_quantize", X.device, X.data_ptr(), dt, rows, cols, ctypes.byref(st))
+    _quantize(X.device, X.data_ptr(), dt, rows, cols, ctypes.byref(st))
     return out
 
 
@@ -179,7 +189,7 @@ def qlora_mx_dequantize(q: MXMatrix, dtype=None, out=None):
         out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.device)
     else:
         _tensor("out", out, dtype, (q.rows, q.cols), q.device)
-    _run("qlora_mx_dequantize", q.device, ctypes.byref(st), out.data_ptr(), dt)
+    _dequantize(q.device, ctypes.byref(st), out.data_ptr(), dt)
     return out
 
 
@@ -216,7 +226,7 @@ def qlora_rmsnorm_fwd(X, weight, eps: float = 1e-6, residual=None, out=None, h=N
         rstd = torch.empty(rows, dtype=torch.float32, device=X.device)
     else:
         _tensor("rstd", rstd, torch.float32, (rows,), X.device)
-    _run("qlora_rmsnorm_fwd", X.device, X.data_ptr(), _at(residual), weight.data_ptr(), dt, rows, cols, float(eps),
+    _rmsnorm_fwd(X.device, X.data_ptr(), _at(residual), weight.data_ptr(), dt, rows, cols, float(eps),
          out.data_ptr(), _at(h), rstd.data_ptr())
     return out, X if h is None else h, rstd
 
@@ -231,7 +241,7 @@ def qlora_rmsnorm_mx(X, weight, eps: float = 1e-6, residual=None, mx: Optional[i
     elif mx is not None and mx != out.mx:
         raise ValueError(f"mx {mx} differs from out.mx {out.mx}")
     st = out.c_struct("out", X.device)
-    _run("qlora_rmsnorm_mx", X.device, X.data_ptr(), _at(residual), weight.data_ptr(), dt, rows, cols, float(eps),
+    _rmsnorm_mx(X.device, X.data_ptr(), _at(residual), weight.data_ptr(), dt, rows, cols, float(eps),
          ctypes.byref(st), _at(h))
     return out, X if h is None else h
 
@@ -268,16 +278,12 @@ def qlora_rmsnorm_bwd(dY, H, weight, rstd, dH=None, ws=None, outs: Optional[Tupl
         _tensor("dX", dX, torch.bfloat16, (rows, cols), device)
         _tensor("dW", dW, torch.float32, (cols,), device)
     ws, at, size = _workspace(ws, qlora_rmsnorm_bwd_workspace_bytes(rows, cols), device)
-    _run("qlora_rmsnorm_bwd", device, dY.data_ptr(), H.data_ptr(), weight.data_ptr(), dt, rstd.data_ptr(), _at(dH),
+    _rmsnorm_bwd(device, dY.data_ptr(), H.data_ptr(), weight.data_ptr(), dt, rstd.data_ptr(), _at(dH),
          rows, cols, dX.data_ptr(), dW.data_ptr(), at, size)
     return dX, dW
 
 
-def qlora_mx_linear_workspace_bytes(M: int, N: int, K: int) -> int:
-    return int(lib.qlora_mx_linear_workspace_bytes(M, N, K))
-
-
-def qlora_mx_linear(X: MXMatrix, W: MXMatrix, ws=None, out=None):
+def qlora_mx_linear(X: MXMatrix, W: MXMatrix, out=None):
     """Y = X W^T in bf16: X [M, K] in 8- or 4-bit, W [N, K] in 4-bit microscaled floats."""
     device = X.device
     sx, sw = X.c_struct("X"), W.c_struct("W", device)
@@ -285,8 +291,7 @@ def qlora_mx_linear(X: MXMatrix, W: MXMatrix, ws=None, out=None):
         out = torch.empty((X.rows, W.rows), dtype=torch.bfloat16, device=device)
     else:
         _tensor("out", out, torch.bfloat16, (X.rows, W.rows), device)
-    ws, at, size = _workspace(ws, lib.qlora_mx_linear_workspace_bytes(X.rows, W.rows, X.cols), device)
-    _run("qlora_mx_linear", device, ctypes.byref(sx), ctypes.byref(sw), out.data_ptr(), at, size)
+    _linear(device, ctypes.byref(sx), ctypes.byref(sw), out.data_ptr())
     return out
 
 
@@ -308,6 +313,6 @@ def qlora_mx_linear_grouped(X: MXMatrix, W: MXMatrix, offsets, out=None):
         out = torch.zeros(shape, dtype=torch.bfloat16, device=device)
     else:
         _tensor("out", out, torch.bfloat16, shape, device)
-    _run("qlora_mx_linear_grouped", device, ctypes.byref(sx), ctypes.byref(sw), offsets.data_ptr(), experts,
+    _linear_grouped(device, ctypes.byref(sx), ctypes.byref(sw), offsets.data_ptr(), experts,
          out.data_ptr())
     return out

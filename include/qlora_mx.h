@@ -128,10 +128,6 @@ int qlora_rmsnorm_bwd(const void *dY, const void *H, const void *weight, int w_d
                       const void *dH, int64_t rows, int64_t cols, void *dX, float *dW, void *ws,
                       size_t ws_bytes, void *stream);
 
-/* Workspace bytes of qlora_mx_linear: 0 for many sizes (then ws may be NULL)
- * and for invalid ones. No contents are expected or kept. */
-size_t qlora_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
-
 /*
  * Y = X W^T: X [M, K] in microscaled 8- or 4-bit floats, W [N, K] in
  * microscaled 4-bit floats, Y bf16 [M, N]. Sums are fp32 in a fixed order
@@ -143,8 +139,7 @@ size_t qlora_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * are any sizes from 1. A NaN block (scale
  * 255) makes the row (X) or column (W) of Y that it enters NaN, and no other.
  */
-int qlora_mx_linear(const qlora_mx_matrix *X, const qlora_mx_matrix *W, void *Y, void *ws, size_t ws_bytes,
-                    void *stream);
+int qlora_mx_linear(const qlora_mx_matrix *X, const qlora_mx_matrix *W, void *Y, void *stream);
 
 /*
  * The product by expert: X [M, K] holds rows sorted by expert, W [experts *
@@ -156,7 +151,7 @@ int qlora_mx_linear(const qlora_mx_matrix *X, const qlora_mx_matrix *W, void *Y,
  *            below 0 or past M counts as 0 or M, and an expert whose end lies
  *            before its start has no rows.
  *   experts  1 .. QLORA_MX_EXPERTS, a divisor of W->rows
- * Types, sums and sizes as in qlora_mx_linear; no workspace.
+ * Types, sums and sizes as in qlora_mx_linear.
  */
 int qlora_mx_linear_grouped(const qlora_mx_matrix *X, const qlora_mx_matrix *W, const int32_t *offsets,
                             int32_t experts, void *Y, void *stream);

@@ -43,8 +43,6 @@ def test_sizes():
     assert qb.qlora_rmsnorm_bwd_workspace_bytes(1, 32) >= 128
     assert qb.qlora_rmsnorm_bwd_workspace_bytes(1, 65568) == qb.qlora_rmsnorm_bwd_workspace_bytes(0, 64) == 0
     assert qb.qlora_rmsnorm_bwd_workspace_bytes(1 << 31, 64) == 0
-    for bad in ((0, 64, 64), (64, 0, 64), (64, 64, 48), (64, 64, 1 << 23)):
-        assert qb.qlora_mx_linear_workspace_bytes(*bad) == 0
 
 
 def test_quantize_rejects():
@@ -117,11 +115,11 @@ def test_norm_rejects():
 def test_products_reject():
     f = lib.qlora_mx_linear
     x = M(4, 64, type=FP8)
-    assert f(None, ref(M()), FAKE, None, 0, None) == f(ref(x), None, FAKE, None, 0, None) == f(ref(x), ref(M()), None, None, 0, None) == -1
-    assert f(ref(x), ref(M(type=FP8)), FAKE, None, 0, None) == -7
-    assert f(ref(x), ref(M(cols=96)), FAKE, None, 0, None) == -2
-    assert f(ref(x), ref(M()), FAKE + 8, None, 0, None) == -6
-    assert f(ref(M(1 << 30, 64, type=FP8)), ref(M(1 << 30, 64)), FAKE, None, 0, None) == -2
+    assert f(None, ref(M()), FAKE, None) == f(ref(x), None, FAKE, None) == f(ref(x), ref(M()), None, None) == -1
+    assert f(ref(x), ref(M(type=FP8)), FAKE, None) == -7
+    assert f(ref(x), ref(M(cols=96)), FAKE, None) == -2
+    assert f(ref(x), ref(M()), FAKE + 8, None) == -6
+    assert f(ref(M(1 << 30, 64, type=FP8)), ref(M(1 << 30, 64)), FAKE, None) == -2
     g = lib.qlora_mx_linear_grouped
     assert g(ref(x), ref(M()), None, 2, FAKE, None) == -1
     for e in (0, -1, 3, 1025):
