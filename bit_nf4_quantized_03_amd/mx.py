@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+from ctypes import byref
 from typing import Optional, Tuple
 
 import torch
@@ -30,6 +31,8 @@ MX_EXPORTED_SYMBOLS = (
 
 QLORA_MX_FP4 = 0   # sign, 2 exponent bits, 1 mantissa bit; two to a byte
 QLORA_MX_FP8 = 1   # sign, 4 exponent bits, 3 mantissa bits
+_TYPES = (QLORA_MX_FP4, QLORA_MX_FP8)
+_MAX_COLS = 1 << 22
 
 
 class _MX(ctypes.Structure):
@@ -65,18 +68,17 @@ _DTYPES = {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}
 
 
 def _entry(name: str):
-    """The entry point as a call (device, *arguments) on the current stream of
-    ``device``, with that device current (the library launches on the current
+    """The entry point as a call (device index, *arguments) on that device's
+    current stream, with the device current (the library launches on the current
     one)."""
     fn = getattr(lib, name)
-    stream, current = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+    stream, current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
-    def call(device, *args):
-        index = device.index
+    def call(index, *args):
         if index == current():
             status = fn(*args, stream(index))
         else:
-            with torch.cuda.device(device):
+            with torch.cuda.device(index):
                 status = fn(*args, stream(index))
         if status != 0:
             raise QloraError(name, status, qlora_last_error())
@@ -94,9 +96,13 @@ def _dtype(name, dtype) -> int:
     return _DTYPES[dtype]
 
 
-def _tensor(name, t, dtype, shape, device=None):
+def _tensor(name, t, dtype, shape, index=None):
     """``t`` must be a contiguous CUDA tensor of this dtype (None: any) and
-    shape, on ``device``: the C ABI takes bare pointers."""
+    shape, on device ``index`` (None: any): the C ABI takes bare pointers.
+    Returns its address."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and (dtype is None or t.dtype is dtype) and t.shape == shape and \
+            t.is_contiguous() and (index is None or t.get_device() == index):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     if dtype is not None and t.dtype != dtype:
@@ -105,11 +111,10 @@ def _tensor(name, t, dtype, shape, device=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
-def _matrix_2d(name, t, dtype=None):
+def _rows_cols(name, t, dtype=None):
     """Shape of a contiguous 2-D CUDA tensor with at least one row and column."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
@@ -141,42 +146,40 @@ class MXMatrix:
 
     @staticmethod
     def empty(rows: int, cols: int, device, mx: int = QLORA_MX_FP4) -> "MXMatrix":
-        if mx not in (QLORA_MX_FP4, QLORA_MX_FP8):
+        if mx not in _TYPES:
             raise ValueError(f"mx must be QLORA_MX_FP4 or QLORA_MX_FP8, got {mx}")
-        pitch = qlora_mx_scale_pitch(cols)
-        if rows < 1 or pitch == 0:
+        if rows < 1 or cols < 32 or cols % 32 or cols > _MAX_COLS:
             raise ValueError(f"{rows} x {cols}: needs rows >= 1 and cols a multiple of 32 up to 2^22")
-        return MXMatrix(rows, cols,
-                        torch.empty((rows, cols // 2 if mx == QLORA_MX_FP4 else cols), dtype=torch.uint8, device=device),
-                        torch.empty((rows, pitch), dtype=torch.uint8, device=device), mx)
+        return MXMatrix(rows, cols, torch.empty((rows, cols // 2 if mx == QLORA_MX_FP4 else cols), dtype=torch.uint8, device=device),
+                        torch.empty((rows, -(-cols // 512) * 16), dtype=torch.uint8, device=device), mx)
 
     @property
     def device(self):
         return self.codes.device
 
-    def c_struct(self, name: str = "matrix", device=None) -> _MX:
-        """The C struct, after checking the buffers against rows and cols."""
-        if self.mx not in (QLORA_MX_FP4, QLORA_MX_FP8):
-            raise ValueError(f"{name}.mx must be QLORA_MX_FP4 or QLORA_MX_FP8, got {self.mx}")
-        rows, cols = self.rows, self.cols
-        device = self.codes.device if device is None else device
-        _tensor(f"{name}.codes", self.codes, torch.uint8, (rows, cols // 2 if self.mx == QLORA_MX_FP4 else cols), device)
-        _tensor(f"{name}.scales", self.scales, torch.uint8, (rows, 16 * -(-cols // 512)), device)
-        return _MX(rows, cols, self.codes.data_ptr(), self.scales.data_ptr(), self.mx)
+    def c_struct(self, name: str = "matrix", index=None) -> _MX:
+        """The C struct, after checking the buffers against rows and cols (on device ``index`` when given)."""
+        rows, cols, mx = self.rows, self.cols, self.mx
+        if mx not in _TYPES:
+            raise ValueError(f"{name}.mx must be QLORA_MX_FP4 or QLORA_MX_FP8, got {mx}")
+        codes = _tensor(f"{name}.codes", self.codes, torch.uint8, (rows, cols // 2 if mx == QLORA_MX_FP4 else cols), index)
+        scales = _tensor(f"{name}.scales", self.scales, torch.uint8, (rows, -(-cols // 512) * 16),
+                         self.codes.get_device() if index is None else index)
+        return _MX(rows, cols, codes, scales, mx)
 
 
 def qlora_mx_quantize(X, mx: Optional[int] = None, out: Optional[MXMatrix] = None) -> MXMatrix:
     """Quantize a 2-D fp32 or bf16 CUDA tensor (columns a multiple of 32) to
     microscaled floats of type ``mx`` (``out.mx`` when ``out`` is given, else
     4 bits)."""
-    rows, cols = _matrix_2d("X", X)
+    rows, cols = _rows_cols("X", X)
     dt = _dtype("X", X.dtype)
     if out is None:
         out = MXMatrix.empty(rows, cols, X.device, QLORA_MX_FP4 if mx is None else mx)
     elif mx is not None and mx != out.mx:
         raise ValueError(f"mx {mx} differs from out.mx {out.mx}")
-    st = out.c_struct("out", X.device)
-    _quantize(X.device, X.data_ptr(), dt, rows, cols, ctypes.byref(st))
+    index = X.get_device()
+    _quantize(index, X.data_ptr(), dt, rows, cols, byref(out.c_struct("out", index)))
     return out
 
 
@@ -185,49 +188,52 @@ def qlora_mx_dequantize(q: MXMatrix, dtype=None, out=None):
     st = q.c_struct("q")
     dtype = torch.float32 if dtype is None else dtype
     dt = _dtype("dtype", dtype)
+    index = q.codes.get_device()
     if out is None:
-        out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.device)
+        out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.codes.device)
+        at = out.data_ptr()
     else:
-        _tensor("out", out, dtype, (q.rows, q.cols), q.device)
-    _dequantize(q.device, ctypes.byref(st), out.data_ptr(), dt)
+        at = _tensor("out", out, dtype, (q.rows, q.cols), index)
+    _dequantize(index, byref(st), at, dt)
     return out
-
-
-def _norm_inputs(X, weight, residual, h):
-    rows, cols = _matrix_2d("X", X, torch.bfloat16)
-    _tensor("weight", weight, None, (cols,), X.device)
-    dt = _dtype("weight", weight.dtype)
-    if residual is None:
-        if h is not None:
-            raise ValueError("h is only written with a residual")
-        return rows, cols, dt, None
-    _tensor("residual", residual, torch.bfloat16, (rows, cols), X.device)
-    if h is None:
-        h = torch.empty_like(X)
-    else:
-        _tensor("h", h, torch.bfloat16, (rows, cols), X.device)
-    return rows, cols, dt, h
 
 
 def _at(t):
     return None if t is None else t.data_ptr()
 
 
+def _norm_inputs(X, weight, residual, h):
+    """(rows, cols, device index, addresses and weight type as the entry points take them, h)"""
+    rows, cols = _rows_cols("X", X, torch.bfloat16)
+    index = X.get_device()
+    w = _tensor("weight", weight, None, (cols,), index)
+    dt = _dtype("weight", weight.dtype)
+    if residual is None:
+        if h is not None:
+            raise ValueError("h is only written with a residual")
+        return rows, cols, index, (X.data_ptr(), None, w, dt, rows, cols), None
+    r = _tensor("residual", residual, torch.bfloat16, (rows, cols), index)
+    if h is None:
+        h = torch.empty_like(X)
+    else:
+        _tensor("h", h, torch.bfloat16, (rows, cols), index)
+    return rows, cols, index, (X.data_ptr(), r, w, dt, rows, cols), h
+
+
 def qlora_rmsnorm_fwd(X, weight, eps: float = 1e-6, residual=None, out=None, h=None, rstd=None):
     """(Y, H, rstd): Y = H * rstd * weight in bf16 with H = bf16(X + residual),
     rstd = 1 / sqrt(mean(H^2) + eps) fp32 [rows]. Without a residual H is X
     itself. ``h`` may be X or ``residual`` (in place)."""
-    rows, cols, dt, h = _norm_inputs(X, weight, residual, h)
+    rows, cols, index, args, h = _norm_inputs(X, weight, residual, h)
     if out is None:
         out = torch.empty_like(X)
     else:
-        _tensor("out", out, torch.bfloat16, (rows, cols), X.device)
+        _tensor("out", out, torch.bfloat16, (rows, cols), index)
     if rstd is None:
         rstd = torch.empty(rows, dtype=torch.float32, device=X.device)
     else:
-        _tensor("rstd", rstd, torch.float32, (rows,), X.device)
-    _rmsnorm_fwd(X.device, X.data_ptr(), _at(residual), weight.data_ptr(), dt, rows, cols, float(eps),
-         out.data_ptr(), _at(h), rstd.data_ptr())
+        _tensor("rstd", rstd, torch.float32, (rows,), index)
+    _rmsnorm_fwd(index, *args, float(eps), out.data_ptr(), _at(h), rstd.data_ptr())
     return out, X if h is None else h, rstd
 
 
@@ -235,14 +241,12 @@ def qlora_rmsnorm_mx(X, weight, eps: float = 1e-6, residual=None, mx: Optional[i
                      out: Optional[MXMatrix] = None, h=None) -> Tuple[MXMatrix, torch.Tensor]:
     """(Y, H) of qlora_rmsnorm_fwd with Y in microscaled floats of type ``mx``
     (``out.mx`` when ``out`` is given, else 8 bits)."""
-    rows, cols, dt, h = _norm_inputs(X, weight, residual, h)
+    rows, cols, index, args, h = _norm_inputs(X, weight, residual, h)
     if out is None:
         out = MXMatrix.empty(rows, cols, X.device, QLORA_MX_FP8 if mx is None else mx)
     elif mx is not None and mx != out.mx:
         raise ValueError(f"mx {mx} differs from out.mx {out.mx}")
-    st = out.c_struct("out", X.device)
-    _rmsnorm_mx(X.device, X.data_ptr(), _at(residual), weight.data_ptr(), dt, rows, cols, float(eps),
-         ctypes.byref(st), _at(h))
+    _rmsnorm_mx(index, *args, float(eps), byref(out.c_struct("out", index)), _at(h))
     return out, X if h is None else h
 
 
@@ -250,48 +254,43 @@ def qlora_rmsnorm_bwd_workspace_bytes(rows: int, cols: int) -> int:
     return int(lib.qlora_rmsnorm_bwd_workspace_bytes(rows, cols))
 
 
-def _workspace(ws, need: int, device):
-    """(address, bytes) of ``ws``, or of a new one when it is None."""
-    if ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    else:
-        _tensor("ws", ws, None, ws.shape, device)
-    return ws, _at(ws), 0 if ws is None else ws.numel() * ws.element_size()
-
-
 def qlora_rmsnorm_bwd(dY, H, weight, rstd, dH=None, ws=None, outs: Optional[Tuple] = None):
     """(dX, dW) of qlora_rmsnorm_fwd from its H and rstd. dX (bf16) is the
     gradient of X and of the residual; ``dH`` is the gradient that reaches H
     through the residual stream; dW is fp32 [cols]."""
-    rows, cols = _matrix_2d("H", H, torch.bfloat16)
-    device = H.device
-    _tensor("dY", dY, torch.bfloat16, (rows, cols), device)
-    _tensor("weight", weight, None, (cols,), device)
+    rows, cols = _rows_cols("H", H, torch.bfloat16)
+    index = H.get_device()
+    dy = _tensor("dY", dY, torch.bfloat16, (rows, cols), index)
+    w = _tensor("weight", weight, None, (cols,), index)
     dt = _dtype("weight", weight.dtype)
-    _tensor("rstd", rstd, torch.float32, (rows,), device)
-    if dH is not None:
-        _tensor("dH", dH, torch.bfloat16, (rows, cols), device)
+    rs = _tensor("rstd", rstd, torch.float32, (rows,), index)
+    dh = None if dH is None else _tensor("dH", dH, torch.bfloat16, (rows, cols), index)
     if outs is None:
-        dX, dW = torch.empty_like(dY), torch.empty(cols, dtype=torch.float32, device=device)
+        dX, dW = torch.empty_like(dY), torch.empty(cols, dtype=torch.float32, device=H.device)
     else:
         dX, dW = outs
-        _tensor("dX", dX, torch.bfloat16, (rows, cols), device)
-        _tensor("dW", dW, torch.float32, (cols,), device)
-    ws, at, size = _workspace(ws, qlora_rmsnorm_bwd_workspace_bytes(rows, cols), device)
-    _rmsnorm_bwd(device, dY.data_ptr(), H.data_ptr(), weight.data_ptr(), dt, rstd.data_ptr(), _at(dH),
-         rows, cols, dX.data_ptr(), dW.data_ptr(), at, size)
+        _tensor("dX", dX, torch.bfloat16, (rows, cols), index)
+        _tensor("dW", dW, torch.float32, (cols,), index)
+    if ws is None:
+        ws = torch.empty(lib.qlora_rmsnorm_bwd_workspace_bytes(rows, cols), dtype=torch.uint8, device=H.device)
+    else:
+        _tensor("ws", ws, None, ws.shape, index)
+    _rmsnorm_bwd(index, dy, H.data_ptr(), w, dt, rs, dh, rows, cols, dX.data_ptr(), dW.data_ptr(), ws.data_ptr(),
+                 ws.numel() * ws.element_size())
     return dX, dW
 
 
 def qlora_mx_linear(X: MXMatrix, W: MXMatrix, out=None):
     """Y = X W^T in bf16: X [M, K] in 8- or 4-bit, W [N, K] in 4-bit microscaled floats."""
-    device = X.device
-    sx, sw = X.c_struct("X"), W.c_struct("W", device)
+    sx = X.c_struct("X")
+    index = X.codes.get_device()
+    sw = W.c_struct("W", index)
     if out is None:
-        out = torch.empty((X.rows, W.rows), dtype=torch.bfloat16, device=device)
+        out = torch.empty((X.rows, W.rows), dtype=torch.bfloat16, device=X.codes.device)
+        at = out.data_ptr()
     else:
-        _tensor("out", out, torch.bfloat16, (X.rows, W.rows), device)
-    _linear(device, ctypes.byref(sx), ctypes.byref(sw), out.data_ptr())
+        at = _tensor("out", out, torch.bfloat16, (X.rows, W.rows), index)
+    _linear(index, byref(sx), byref(sw), at)
     return out
 
 
@@ -300,19 +299,20 @@ def qlora_mx_linear_grouped(X: MXMatrix, W: MXMatrix, offsets, out=None):
     rows sorted by expert, W [experts * N, K] the experts' weights one below the
     other, offsets int32 [experts + 1] on the device. Rows that no expert has
     are left as they were (zero in a new Y)."""
-    device = X.device
+    sx = X.c_struct("X")
+    index = X.codes.get_device()
+    sw = W.c_struct("W", index)
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
         raise ValueError("offsets must be a tensor [experts + 1]")
-    _tensor("offsets", offsets, torch.int32, offsets.shape, device)
+    off = _tensor("offsets", offsets, torch.int32, offsets.shape, index)
     experts = offsets.shape[0] - 1
-    sx, sw = X.c_struct("X"), W.c_struct("W", device)
     if W.rows % experts:
         raise ValueError(f"W has {W.rows} rows, not a multiple of {experts} experts")
     shape = (X.rows, W.rows // experts)
     if out is None:
-        out = torch.zeros(shape, dtype=torch.bfloat16, device=device)
+        out = torch.zeros(shape, dtype=torch.bfloat16, device=X.codes.device)
+        at = out.data_ptr()
     else:
-        _tensor("out", out, torch.bfloat16, shape, device)
-    _linear_grouped(device, ctypes.byref(sx), ctypes.byref(sw), offsets.data_ptr(), experts,
-         out.data_ptr())
+        at = _tensor("out", out, torch.bfloat16, shape, index)
+    _linear_grouped(index, byref(sx), byref(sw), off, experts, at)
     return out
