@@ -33,7 +33,7 @@ struct RmsFwd {
   void *H;
   float *rstd;
 };
-constexpr int64_t kRmsMaxCols = 65536;
+constexpr int64_t kRmsMaxCols = 32768;
 hipError_t launch_rms_fwd(const RmsFwd &a, hipStream_t s);
 size_t rms_bwd_ws_bytes(int64_t rows, int64_t cols);
 hipError_t launch_rms_bwd(const void *dY, const void *H, const void *weight, bool w_bf16, const float *rstd,

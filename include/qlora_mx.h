@@ -94,7 +94,7 @@ int qlora_mx_dequantize(const qlora_mx_matrix *q, void *out, int out_dtype, void
  *   H         bf16 [rows, cols], h: needed with a residual, NULL without; may
  *             be X or residual (in place)
  *   rstd      fp32 [rows] for the backward, or NULL
- * cols a multiple of 32, at most 65536. A row that holds a NaN or an Inf has
+ * cols a multiple of 32, at most 32768. A row that holds a NaN or an Inf has
  * NaN (or 0) outputs and leaves the other rows alone. A row of zeros with
  * eps = 0 is NaN.
  */

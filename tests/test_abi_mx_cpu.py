@@ -41,7 +41,7 @@ def test_sizes():
     assert qb.qlora_mx_storage_bytes(3, 64, 2) == qb.qlora_mx_storage_bytes(0, 64, 0) == qb.qlora_mx_storage_bytes(3, 65, 0) == 0
     assert qb.qlora_mx_storage_bytes(1 << 40, 64, 0) == 0
     assert qb.qlora_rmsnorm_bwd_workspace_bytes(1, 32) >= 128
-    assert qb.qlora_rmsnorm_bwd_workspace_bytes(1, 65568) == qb.qlora_rmsnorm_bwd_workspace_bytes(0, 64) == 0
+    assert qb.qlora_rmsnorm_bwd_workspace_bytes(1, 32800) == qb.qlora_rmsnorm_bwd_workspace_bytes(0, 64) == 0
     assert qb.qlora_rmsnorm_bwd_workspace_bytes(1 << 31, 64) == 0
 
 
@@ -80,7 +80,7 @@ def test_norm_rejects():
     assert call(X=None) == call(w=None) == call(Y=None) == call(H=None) == -1
     assert call(res=None) == -2                     # H without a residual
     assert call(wt=3) == -3
-    assert call(rows=0) == call(cols=0) == call(cols=40) == call(cols=65568) == call(rows=1 << 31) == -2
+    assert call(rows=0) == call(cols=0) == call(cols=40) == call(cols=32800) == call(rows=1 << 31) == -2
     assert call(eps=-1e-9) == call(eps=float("inf")) == call(eps=float("nan")) == -2
     assert call(Y=FAKE) == -2                       # Y is H
     for name in ("X", "res", "w", "Y", "H", "rstd"):

@@ -162,7 +162,7 @@ def norm_data(rows, cols, seed, residual, w_bf16):
 
 
 NORM_SHAPES = [(1, 32), (5, 96), (3, 1056), (2, 2048), (1, 4096), (70, 4096), (4, 4128), (3, 8192), (2, 11008), (2, 16416),
-               (1, 65536), (1100, 512), (1030, 2080)]
+               (1, 32768), (1100, 512), (1030, 2080)]
 
 
 @pytest.mark.parametrize("residual,w_bf16", [(True, False), (False, True), (True, True)])
