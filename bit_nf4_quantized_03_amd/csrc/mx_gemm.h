@@ -15,10 +15,12 @@
 // instructions of a step's second half run after the next step's
 // barrier: they cover its first LDS reads.
 //
-// LDS rows are 128 bytes (8-bit codes) or 64 (4-bit), unpadded, their 16-byte
-// chunks swapped by an exclusive or with the row so that the 32 rows that a
-// wave reads at one chunk fall on all banks; a copy fetches the chunk that
-// belongs at its lane's place.
+// LDS rows are 128 bytes (8-bit codes) or 64 (4-bit), unpadded. Sixteen lanes
+// of a 16-byte read go through the 64 banks at a time, so a row's chunks are
+// swapped by an exclusive or with row / 2 (128 bytes) or row / 4 (64 bytes):
+// sixteen consecutive rows read at one chunk then lie on all banks. (With the
+// row itself in the exclusive or, half of the LDS's cycles were conflicts.) A
+// copy fetches the chunk that belongs at its lane's place.
 //
 // Behind the end of K the last step re-reads chunks of the same rows; their
 // scale bytes are the pad bytes 0 of both operands, 2^-254 together, which
@@ -62,10 +64,10 @@ struct MxTile {
 
 // Byte offset of chunk c of row r in a tile of 64-byte rows / 128-byte rows.
 __device__ __forceinline__ uint32_t mx_off64(int r, int c) {
-  return static_cast<uint32_t>((r >> 1) * 128 + ((((r & 1) << 2 | c) ^ ((r >> 1) & 7)) << 4));
+  return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 2) & 3)) << 4));
 }
 __device__ __forceinline__ uint32_t mx_off128(int r, int c) {
-  return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
+  return static_cast<uint32_t>(r * 128 + ((c ^ ((r >> 1) & 7)) << 4));
 }
 
 // A value that is the same in all lanes, in scalar registers.
@@ -110,15 +112,14 @@ struct MxCopies {
   __device__ MxCopies(const uint8_t *codes, int64_t row0, int64_t rows, int64_t ld, int w) {
     base = mx_uniform(codes + row0 * ld);
     const int lane = threadIdx.x & 63;
-    const int line = lane >> 3, p = lane & 7;
-    int r, c;
+    int r, c;   // row of the wave's first block that the lane copies, chunk that belongs at its place
     if constexpr (ROWB == 64) {
-      const int q = p ^ line;
-      r = 2 * line + (q >> 2);
-      c = q & 3;
+      r = lane >> 2;
+      c = (lane & 3) ^ ((r >> 2) & 3);
     } else {
-      r = line;
-      c = p ^ line;
+      static_assert(WAVES % 2 == 0, "a wave's blocks of eight rows are all even or all odd");
+      r = lane >> 3;
+      c = (lane & 7) ^ (4 * (w & 1) + (r >> 1));
     }
     const int64_t end = rows - 1 - row0;
 #pragma unroll
