@@ -85,7 +85,7 @@ __device__ __forceinline__ const uint8_t *mx_uniform(const uint8_t *p) {
 __device__ __forceinline__ void mx_copy(uint32_t dst, uint32_t off, const uint8_t *base) {
   asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" 
                :
-               : "s"(dst), "v"(off), "s"(base)
+               : "s"(__builtin_amdgcn_readfirstlane(dst)), "v"(off), "s"(base)
                : "memory", "m0");
 }
 
@@ -130,11 +130,9 @@ struct MxCopies {
     chunk = static_cast<uint32_t>(16 * c);
     last = static_cast<uint32_t>(ld - 16);
   }
-  // dst: LDS address of the wave's first block of the stage's tile
-  __device__ __forceinline__ void issue(int step, uint32_t dst) const {
-    const uint32_t k = min(static_cast<uint32_t>(step) * ROWB + chunk, last);
-#pragma unroll
-    for (int i = 0; i < COPIES; ++i) mx_copy(dst + 1024u * WAVES * i, row[i] + k, base);
+  // Copy i of a step; dst: LDS address of the wave's first block of the tile.
+  __device__ __forceinline__ void issue(int i, int step, uint32_t dst) const {
+    mx_copy(dst + 1024u * WAVES * i, row[i] + min(static_cast<uint32_t>(step) * ROWB + chunk, last), base);
   }
 };
 
@@ -148,15 +146,19 @@ struct MxAcc {
   f32x16 v[T::NF][T::MF];
 };
 
-// One slice's matrix instructions, with the scale bytes 2 SLICE of the words.
-template <class T, int SLICE>
-__device__ __forceinline__ void mx_mma(MxAcc<T> &acc, const MxFrags<T> &f, const int (&sw)[T::NF], const int (&sx)[T::MF]) {
+// One slice's matrix instructions, with the scale bytes 2 SLICE of the words;
+// after(i) is called behind those of W fragment i.
+template <class T, int SLICE, class F>
+__device__ __forceinline__ void mx_mma(MxAcc<T> &acc, const MxFrags<T> &f, const int (&sw)[T::NF], const int (&sx)[T::MF],
+                                       F after) {
 #pragma unroll
-  for (int i = 0; i < T::NF; ++i)
+  for (int i = 0; i < T::NF; ++i) {
 #pragma unroll
     for (int j = 0; j < T::MF; ++j)
       acc.v[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
           f.w[i], f.x[j], acc.v[i][j], 4, T::XT == QLORA_MX_FP4 ? 4 : 0, 2 * SLICE, sw[i], 2 * SLICE, sx[j]);
+    after(i);
+  }
 }
 
 struct MxOperands {
@@ -192,17 +194,25 @@ __device__ __forceinline__ void mx_mainloop(MxAcc<T> &acc, const MxOperands &p, 
   }
   const uint32_t sdst = lds + T::STAGES * T::kStage + 1024u * wave;
 
-  auto issue = [&](int step) {
+  // Copies of step `step`, part `part` of `parts`. Steps past the end copy the
+  // last one again, into a stage that is not read any more: every step has the
+  // same copies, and one wait count serves them all.
+  auto issue = [&](int step, int part, int parts) {
     const uint32_t stage = lds + static_cast<uint32_t>((step - s0) % T::STAGES) * T::kStage + 1024u * wave;
-    if ((step & 3) == 0) {
+    const int from = min(step, s1 - 1);
+    if ((step & 3) == 0 && part == 0) {
 #pragma unroll
       for (int c = 0; c < T::kScaleCopies; ++c)
         if (wave + T::kWaves * c < T::kScaleBlocks)
           mx_copy(sdst + static_cast<uint32_t>(step & 4) / 4 * T::kScale + 1024u * T::kWaves * c,
-                  srow[c] + 4u * static_cast<uint32_t>(step), sbase[c]);
+                  srow[c] + 4u * static_cast<uint32_t>(from & ~3), sbase[c]);
     }
-    cw.issue(step, stage);
-    cx.issue(step, stage + T::kW);
+#pragma unroll
+    for (int c = 0; c < T::kCopies; ++c)
+      if (c * parts / T::kCopies == part) {
+        if (c < T::kWCopies) cw.issue(c, from, stage);
+        else cx.issue(c - T::kWCopies, from, stage + T::kW);
+      }
   };
 
   // the lane's LDS offsets within a stage, slices 0 and 1
@@ -217,45 +227,63 @@ __device__ __forceinline__ void mx_mainloop(MxAcc<T> &acc, const MxOperands &p, 
       oxb[s] = T::kW + mx_off128(32 * T::MF * wm + r, 4 * s + 2 + g);
     }
   }
-  auto read = [&](MxFrags<T> &f, const char *stage, int s) {
-#pragma unroll
-    for (int i = 0; i < T::NF; ++i) f.w[i] = mx_operand(*reinterpret_cast<const mx_v4i *>(stage + ow[s] + 2048 * i));
+  // part `part` of NF of a slice's fragments
+  auto read = [&](MxFrags<T> &f, const char *stage, int s, int part) {
 #pragma unroll
     for (int j = 0; j < T::MF; ++j) {
+      if (j * T::NF / T::MF != part) continue;
       const mx_v4i xa = *reinterpret_cast<const mx_v4i *>(stage + oxa[s] + 32 * T::kXRow * j);
       if constexpr (T::XT == QLORA_MX_FP4) f.x[j] = mx_operand(xa);
       else f.x[j] = mx_operand(xa, *reinterpret_cast<const mx_v4i *>(stage + oxb[s] + 32 * T::kXRow * j));
     }
+    f.w[part] = mx_operand(*reinterpret_cast<const mx_v4i *>(stage + ow[s] + 2048 * part));
   };
 
   int sw[T::NF], sx[T::MF];       // scale words of this step, the lane's blocks in bytes 0 and 2
   MxFrags<T> f0, f1;
+  if (s1 > s0) {
 #pragma unroll
-  for (int i = 0; i < T::STAGES - 1; ++i)
-    if (s0 + i < s1) issue(s0 + i);
+    for (int i = 0; i < T::STAGES - 1; ++i) issue(s0 + i, 0, 1);
+  }
 
   auto step = [&](auto jc, int i) {
     constexpr int j = decltype(jc)::value;
-    if (i + T::STAGES - 1 <= s1) mx_wait<T::kCopies *(T::STAGES - 2)>();
-    else mx_wait<0>();
+    mx_wait<T::kCopies *(T::STAGES - 2)>();
     mx_barrier();
     if (T::KG > 1 && i >= s1) return;
-    if (i + T::STAGES - 1 < s1) issue(i + T::STAGES - 1);
     const char *stage = smem + static_cast<uint32_t>((i - s0) % T::STAGES) * T::kStage;
-    read(f0, stage, 0);
     const char *sc = smem + T::STAGES * T::kStage + static_cast<uint32_t>(i & 4) / 4 * T::kScale + 4 * j + 16 * r;
     uint32_t pw[T::NF], px[T::MF];
+    // The LDS reads of the next half and the copies of a later step go out
+    // between the matrix instructions. With the copies in front of them every
+    // wave waited for the others' (the compute unit takes 16 cycles for 1 KB),
+    // and the matrix cores stood still for a third of the step.
+    const auto first = [&](int n) {
+      read(f0, stage, 0, n);
+      if (n == T::NF - 1) {
 #pragma unroll
-    for (int n = 0; n < T::NF; ++n) pw[n] = *reinterpret_cast<const uint32_t *>(sc + 512 * (T::NF * wn + n));
+        for (int k = 0; k < T::NF; ++k) pw[k] = *reinterpret_cast<const uint32_t *>(sc + 512 * (T::NF * wn + k));
 #pragma unroll
-    for (int m = 0; m < T::MF; ++m) px[m] = *reinterpret_cast<const uint32_t *>(sc + 16 * T::BN + 512 * (T::MF * wm + m));
-    if (i > s0) mx_mma<T, 1>(acc, f1, sw, sx);   // the previous step's second half
+        for (int m = 0; m < T::MF; ++m) px[m] = *reinterpret_cast<const uint32_t *>(sc + 16 * T::BN + 512 * (T::MF * wm + m));
+      }
+      issue(i + T::STAGES - 1, n, 2 * T::NF);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    if (j > 0 || i > s0) {   // the previous step's second half
+      mx_mma<T, 1>(acc, f1, sw, sx, first);
+    } else {
+#pragma unroll
+      for (int n = 0; n < T::NF; ++n) first(n);
+    }
 #pragma unroll
     for (int n = 0; n < T::NF; ++n) sw[n] = static_cast<int>(pw[n] >> (8 * g));
 #pragma unroll
     for (int m = 0; m < T::MF; ++m) sx[m] = static_cast<int>(px[m] >> (8 * g));
-    read(f1, stage, 1);
-    mx_mma<T, 0>(acc, f0, sw, sx);
+    mx_mma<T, 0>(acc, f0, sw, sx, [&](int n) {
+      read(f1, stage, 1, n);
+      issue(i + T::STAGES - 1, T::NF + n, 2 * T::NF);
+      __builtin_amdgcn_sched_barrier(0);
+    });
   };
   const int end = T::KG > 1 ? s0 + most : s1;
   for (int i = s0; i < end; i += 4) {
@@ -264,7 +292,8 @@ __device__ __forceinline__ void mx_mainloop(MxAcc<T> &acc, const MxOperands &p, 
     if (i + 2 < end) step(std::integral_constant<int, 2>{}, i + 2);
     if (i + 3 < end) step(std::integral_constant<int, 3>{}, i + 3);
   }
-  if (s1 > s0) mx_mma<T, 1>(acc, f1, sw, sx);
+  if (s1 > s0) mx_mma<T, 1>(acc, f1, sw, sx, [](int) {});
+  mx_wait<0>();   // no copy may land in LDS that somebody else has by then
 }
 
 // The whole product of a tile: the workgroup's KG groups of waves take a
