@@ -138,7 +138,7 @@ __global__ __launch_bounds__(T::kThreads, 1) void k_mx_gemm(const GemmParams p) 
   tile_of(static_cast<int>(blockIdx.x), tiles_m, tiles_n, tm, tn);
   const int64_t n0 = static_cast<int64_t>(tn) * T::BN, m0 = static_cast<int64_t>(tm) * T::BM;
   MxAcc<T> acc;
-  if (mx_tile_product<T>(acc, p.op, n0, m0, p.steps, smem, wave)) mx_store<T>(acc, p.y, p.N, n0, m0, p.M, wave);
+  if (mx_tile_product<T>(acc, p.op, n0, m0, p.steps, smem, wave)) mx_store<T>(acc, p.y, p.N, n0, m0, p.M, wave, smem);
 }
 
 // Tile of a workgroup in the product by expert. Tiles are counted expert after
@@ -212,7 +212,7 @@ __global__ __launch_bounds__(T::kThreads, 1) void k_mx_gemm_grouped(const GemmPa
   op.x_rows = t.m_end;
   MxAcc<T> acc;
   int wave;
-  if (mx_tile_product<T>(acc, op, n0, m0, p.steps, smem, wave)) mx_store<T>(acc, p.y, p.N, n0, m0, t.m_end, wave);
+  if (mx_tile_product<T>(acc, op, n0, m0, p.steps, smem, wave)) mx_store<T>(acc, p.y, p.N, n0, m0, t.m_end, wave, smem);
 }
 
 template <int XT, int MT, int RT, int WAVES>
