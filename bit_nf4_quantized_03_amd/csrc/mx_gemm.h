@@ -9,8 +9,12 @@
 // the scale byte of block g.
 //
 // The reduction runs in steps of 128 elements, two instructions deep. Codes
-// come by global_load_lds_dwordx4 into a ring of LDS stages, STAGES - 1 steps
-// ahead, one barrier a step; nothing is decoded. Scales come the same way, 16
+// come by global_load_lds_dwordx4 into a ring of LDS stages, two or three steps
+// ahead, one barrier a step; nothing is decoded. With a 4-bit X the larger tiles
+// copy two steps together and have one barrier for them: 64 bytes of a row are
+// half a cache line, and both halves cross to the compute unit for each (2048 x
+// 22016 x 8192 210 us without it, 201 with; 301 x 4096 x 11008, where few
+// workgroups wait for each other's copies, 25 without, 31 with). Scales come the same way, 16
 // bytes a row (512 elements) every four steps, into two buffers. The matrix
 // instructions of a step's second half run after the next step's
 // barrier: they cover its first LDS reads.
@@ -40,7 +44,7 @@ typedef int mx_v8i __attribute__((ext_vector_type(8)));
 __device__ __forceinline__ mx_v8i mx_operand(mx_v4i a) { return __builtin_shufflevector(a, mx_v4i{0, 0, 0, 0}, 0, 1, 2, 3, 4, 5, 6, 7); }
 __device__ __forceinline__ mx_v8i mx_operand(mx_v4i a, mx_v4i b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
 
-template <int XT_, int NF_, int MF_, int WN_, int WM_, int STAGES_, int KG_ = 1>
+template <int XT_, int NF_, int MF_, int WN_, int WM_, int STAGES_, int KG_ = 1, bool PAIR_ = false>
 struct MxTile {
   static constexpr int XT = XT_, NF = NF_, MF = MF_, WN = WN_, WM = WM_, STAGES = STAGES_, KG = KG_;
   static constexpr int kWaves = WN * WM, kThreads = 64 * kWaves * KG;   // waves of one group
@@ -56,9 +60,13 @@ struct MxTile {
   static constexpr int kScaleBlocks = (BN + BM) / 64, kScaleCopies = (kScaleBlocks + kWaves - 1) / kWaves;
   static_assert(BN % 64 == 0 && BM % 64 == 0, "whole scale copies");
   static_assert(kLds <= 160 * 1024, "LDS");
-  // a buffer of scales (four steps) is filled STAGES - 1 steps ahead: not before its readers are done
-  static_assert(STAGES == 3 || STAGES == 4, "ring");
-  static_assert(kCopies * (STAGES - 2) < 64, "vmcnt range");
+  // the steps go in pairs, copied together, two steps ahead
+  static constexpr bool kPair = PAIR_;
+  static constexpr int kAhead = kPair ? 2 : STAGES - 1;
+  static constexpr int kNewer = kPair ? 0 : kCopies * (STAGES - 2);   // copies in flight behind a step's own
+  // a buffer of scales (four steps) is filled kAhead steps ahead: not before its readers are done
+  static_assert(kPair ? STAGES == 4 && XT == QLORA_MX_FP4 : STAGES == 3 || STAGES == 4, "ring");
+  static_assert(kNewer < 64, "vmcnt range");
   // after the main loop: the groups' sums, then 32 rows of bf16 for each wave of the first group
   static constexpr int kSums = (KG - 1) * BN * BM * 4, kStoreRow = 64 * NF + 16, kStore = 32 * kStoreRow;
   static_assert(kSums + kWaves * kStore <= kLds, "sums and rows fit the rings");
@@ -196,24 +204,28 @@ __device__ __forceinline__ void mx_mainloop(MxAcc<T> &acc, const MxOperands &p, 
   }
   const uint32_t sdst = lds + T::STAGES * T::kStage + 1024u * wave;
 
-  // Copies of step `step`, part `part` of `parts`. Steps past the end copy the
-  // last one again, into a stage that is not read any more: every step has the
-  // same copies, and one wait count serves them all.
+  // Copies of step `step` (and the next one, where they go in pairs), part
+  // `part` of `parts`. Steps past the end copy the last one again, into a stage
+  // that is not read any more: every step has the same copies, and one wait
+  // count serves them all.
   auto issue = [&](int step, int part, int parts) {
-    const uint32_t stage = lds + static_cast<uint32_t>((step - s0) % T::STAGES) * T::kStage + 1024u * wave;
-    const int from = min(step, s1 - 1);
     if ((step & 3) == 0 && part == 0) {
+      const uint32_t at = 4u * static_cast<uint32_t>(min(step, s1 - 1) & ~3);
 #pragma unroll
       for (int c = 0; c < T::kScaleCopies; ++c)
         if (wave + T::kWaves * c < T::kScaleBlocks)
-          mx_copy(sdst + static_cast<uint32_t>(step & 4) / 4 * T::kScale + 1024u * T::kWaves * c,
-                  srow[c] + 4u * static_cast<uint32_t>(from & ~3), sbase[c]);
+          mx_copy(sdst + static_cast<uint32_t>(step & 4) / 4 * T::kScale + 1024u * T::kWaves * c, srow[c] + at, sbase[c]);
     }
 #pragma unroll
     for (int c = 0; c < T::kCopies; ++c)
       if (c * parts / T::kCopies == part) {
-        if (c < T::kWCopies) cw.issue(c, from, stage);
-        else cx.issue(c - T::kWCopies, from, stage + T::kW);
+#pragma unroll
+        for (int k = 0; k < (T::kPair ? 2 : 1); ++k) {
+          const uint32_t stage = lds + static_cast<uint32_t>((step + k - s0) % T::STAGES) * T::kStage + 1024u * wave;
+          const int from = min(step + k, s1 - 1);
+          if (c < T::kWCopies) cw.issue(c, from, stage);
+          else cx.issue(c - T::kWCopies, from, stage + T::kW);
+        }
       }
   };
 
@@ -245,13 +257,16 @@ __device__ __forceinline__ void mx_mainloop(MxAcc<T> &acc, const MxOperands &p, 
   MxFrags<T> f0, f1;
   if (s1 > s0) {
 #pragma unroll
-    for (int i = 0; i < T::STAGES - 1; ++i) issue(s0 + i, 0, 1);
+    for (int i = 0; i < T::kAhead; i += T::kPair ? 2 : 1) issue(s0 + i, 0, 1);
   }
 
   auto step = [&](auto jc, int i) {
     constexpr int j = decltype(jc)::value;
-    mx_wait<T::kCopies *(T::STAGES - 2)>();
-    mx_barrier();
+    constexpr bool kCopying = !T::kPair || j % 2 == 0;
+    if (kCopying) {
+      mx_wait<T::kNewer>();
+      mx_barrier();
+    }
     if (T::KG > 1 && i >= s1) return;
     const char *stage = smem + static_cast<uint32_t>((i - s0) % T::STAGES) * T::kStage;
     const char *sc = smem + T::STAGES * T::kStage + static_cast<uint32_t>(i & 4) / 4 * T::kScale + 4 * j + 16 * r;
@@ -268,7 +283,7 @@ __device__ __forceinline__ void mx_mainloop(MxAcc<T> &acc, const MxOperands &p, 
 #pragma unroll
         for (int m = 0; m < T::MF; ++m) px[m] = *reinterpret_cast<const uint32_t *>(sc + 16 * T::BN + 512 * (T::MF * wm + m));
       }
-      issue(i + T::STAGES - 1, n, 2 * T::NF);
+      if (kCopying) issue(i + T::kAhead, n, 2 * T::NF);
       __builtin_amdgcn_sched_barrier(0);
     };
     if (j > 0 || i > s0) {   // the previous step's second half
@@ -283,7 +298,7 @@ __device__ __forceinline__ void mx_mainloop(MxAcc<T> &acc, const MxOperands &p, 
     for (int m = 0; m < T::MF; ++m) sx[m] = static_cast<int>(px[m] >> (8 * g));
     mx_mma<T, 0>(acc, f0, sw, sx, [&](int n) {
       read(f1, stage, 1, n);
-      issue(i + T::STAGES - 1, T::NF + n, 2 * T::NF);
+      if (kCopying) issue(i + T::kAhead, T::NF + n, 2 * T::NF);
       __builtin_amdgcn_sched_barrier(0);
     });
   };

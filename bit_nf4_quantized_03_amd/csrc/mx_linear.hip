@@ -235,36 +235,49 @@ hipError_t run_gemm(const GemmParams &p, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The tiles, and what 128 steps of the reduction cost with them: us that a
-// compute unit takes for a workgroup's step of 128 elements, measured at sizes
-// that fill the GPU with that tile (8-bit X, K = 4096 and 11008). A product
-// takes about as many steps one after another as its fullest compute unit has
-// workgroups times steps, so the cheapest tile is the one with the smallest
-// cost times workgroups per compute unit: large tiles re-read their operands
-// less, small ones leave fewer compute units without work. Measured (us, 8-bit
-// X; the rule's choice first): 4096^3 256 x 256 62, 256 x 128 71, 128 x 128 71;
-// 2048 x 4096 x 4096 256 x 128 37, 128 x 128 39, 256 x 256 53; 301 x 4096 x
-// 11008 128 x 64 30, 64 x 64 34, 128 x 128 35, 256 x 256 119; 128 x 4096 x 4096
-// 64 x 64 10, 128 x 64 14, 128 x 128 19.
+// The tiles, and what a step of 128 elements costs with them in us: `light` for
+// a workgroup while few compute units work, `full` on every compute unit (there
+// per workgroup). `shared`: a compute unit holds two workgroups or more. All
+// measured at K = 4096, N = 4096 (first an 8-bit X, then 4 bits).
+//
+// Large tiles re-read their operands less, small ones leave fewer compute units
+// without work, so the tile is chosen by the time that these figures give.
+// Times behind the rule (us, 8-bit X, N = K = 4096; its choice first): 4096
+// rows 256 x 256 54, 256 x 128 61, 128 x 128 66; 2048 rows 256 x 128 32, 128 x
+// 128 35, 256 x 256 43; 1000 rows 128 x 128 20, 128 x 64 24, 256 x 128 24; 301
+// rows 128 x 64 13, 64 x 64 15, 128 x 128 16; 128 rows 64 x 64 10, 128 x 64 12.
 constexpr int kTiles = 5;
 constexpr struct {
   int bn, bm;
-  double cost;
-} kTile[kTiles] = {{256, 256, 1.68}, {256, 128, 0.92}, {128, 128, 0.50}, {128, 64, 0.28}, {64, 64, 0.18}};
+  bool shared;
+  struct {
+    double light, full;
+  } cost[2];
+} kTile[kTiles] = {{256, 256, false, {{1.03, 1.53}, {0.61, 1.05}}},
+                   {256, 128, false, {{0.54, 0.88}, {0.41, 0.64}}},
+                   {128, 128, true, {{0.33, 0.47}, {0.29, 0.36}}},
+                   {128, 64, true, {{0.205, 0.305}, {0.19, 0.25}}},
+                   {64, 64, true, {{0.15, 0.20}, {0.13, 0.18}}}};
 constexpr double kCus = 256;
 
-int choose_tile(int64_t M, int64_t N, int experts) {
+int choose_tile(int64_t M, int64_t N, int experts, bool fp4) {
   int best = 0;
   double least = 0;
   for (int i = 0; i < kTiles; ++i) {
     const double tiles_n = static_cast<double>(ceil_div(N, kTile[i].bn));
-    double full = tiles_n * static_cast<double>(ceil_div(M, kTile[i].bm)) / kCus;
-    // by expert: each one with rows ends in a partial tile, on average half of
-    // one; the counts are on the GPU, so the quarter allows for a few more
-    if (experts)
-      full = 0.25 + tiles_n * std::max(static_cast<double>(M) / kTile[i].bm + 0.5 * experts,
-                                       static_cast<double>(std::min<int64_t>(M, experts))) / kCus;
-    const double t = std::ceil(full) * kTile[i].cost;
+    double tiles_m = static_cast<double>(ceil_div(M, kTile[i].bm)), spare = 0;
+    if (experts) {
+      // an expert's rows end in a partial tile, on average half of one; the
+      // counts are on the GPU, and `spare` allows for a few more
+      tiles_m = std::max(static_cast<double>(M) / kTile[i].bm + 0.5 * experts,
+                         static_cast<double>(std::min<int64_t>(M, experts)));
+      spare = 0.1;
+    }
+    const double load = tiles_m * tiles_n / kCus + spare;   // workgroups per compute unit
+    const double light = kTile[i].cost[fp4].light, full = kTile[i].cost[fp4].full;
+    double t;
+    if (load <= 1) t = light + (full - light) * load;
+    else t = full * (kTile[i].shared ? (load + std::ceil(load)) / 2 : std::ceil(load));
     if (i == 0 || t < least) least = t, best = i;
   }
   return best;
@@ -272,10 +285,12 @@ int choose_tile(int64_t M, int64_t N, int experts) {
 
 template <int XT>
 hipError_t run_tiles(const GemmParams &p, hipStream_t s) {
-  switch (choose_tile(p.M, p.N, p.experts)) {
-    case 0: return run_gemm<MxTile<XT, 4, 2, 2, 4, 3>>(p, s);
-    case 1: return run_gemm<MxTile<XT, 2, 2, 4, 2, 3>>(p, s);
-    case 2: return run_gemm<MxTile<XT, 2, 2, 2, 2, 3>>(p, s);
+  constexpr bool kPair = XT == QLORA_MX_FP4;
+  constexpr int kDeep = kPair ? 4 : 3;   // stages
+  switch (choose_tile(p.M, p.N, p.experts, XT == QLORA_MX_FP4)) {
+    case 0: return run_gemm<MxTile<XT, 4, 2, 2, 4, kDeep, 1, kPair>>(p, s);
+    case 1: return run_gemm<MxTile<XT, 2, 2, 4, 2, kDeep, 1, kPair>>(p, s);
+    case 2: return run_gemm<MxTile<XT, 2, 2, 2, 2, kDeep, 1, kPair>>(p, s);
     case 3: return run_gemm<MxTile<XT, 2, 1, 2, 2, 4>>(p, s);
     default: return run_gemm<MxTile<XT, 1, 1, 2, 2, 3, 2>>(p, s);   // two groups of waves: 10 us where one takes 11.6
   }
