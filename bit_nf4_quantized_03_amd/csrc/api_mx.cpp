@@ -206,7 +206,7 @@ int qlora_rmsnorm_bwd(const void *dY, const void *H, const void *weight, int w_d
       !aligned16(dW))
     return api_fail(QLORA_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
   const size_t need = qnf4::rms_bwd_ws_bytes(rows, cols);
-  if (!ws || ws_bytes < need)
+  if (need > 0 && (!ws || ws_bytes < need))
     return api_fail(QLORA_ERR_WORKSPACE, "%s: workspace needs %zu bytes, got %zu", fn, need, ws ? ws_bytes : size_t(0));
   if (!aligned16(ws)) return api_fail(QLORA_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
   return qnf4::api_hip_status(qnf4::launch_rms_bwd(dY, H, weight, w_dtype == QLORA_BF16, rstd, dH, rows, cols, dX, dW,

@@ -368,7 +368,8 @@ hipError_t launch_rms_fwd(const RmsFwd &a, hipStream_t s) {
 }
 
 size_t rms_bwd_ws_bytes(int64_t rows, int64_t cols) {
-  return static_cast<size_t>(bwd_groups(rows, cols)) * static_cast<size_t>(cols) * sizeof(float);
+  const unsigned groups = bwd_groups(rows, cols);
+  return groups > 1 ? static_cast<size_t>(groups) * static_cast<size_t>(cols) * sizeof(float) : 0;
 }
 
 hipError_t launch_rms_bwd(const void *dY, const void *H, const void *weight, bool w_bf16, const float *rstd,
@@ -381,11 +382,11 @@ hipError_t launch_rms_bwd(const void *dY, const void *H, const void *weight, boo
   p.w_bf16 = w_bf16;
   p.rstd = rstd;
   p.dx = static_cast<__bf16 *>(dX);
-  p.part = static_cast<float *>(ws);
   p.rows = rows;
   p.cols = static_cast<uint32_t>(cols);
   p.inv_cols = 1.0f / static_cast<float>(cols);
   const unsigned groups = bwd_groups(rows, cols);
+  p.part = groups > 1 ? static_cast<float *>(ws) : dW;   // one workgroup: its sums are dW
   if (cols <= 512) bwd_run<64, 1>(p, groups, s);
   else if (cols <= 1024) bwd_run<128, 1>(p, groups, s);
   else if (cols <= 2048) bwd_run<256, 1>(p, groups, s);
@@ -394,7 +395,7 @@ hipError_t launch_rms_bwd(const void *dY, const void *H, const void *weight, boo
   else if (cols <= 16384) bwd_run<1024, 2>(p, groups, s);
   else bwd_run<1024, 4>(p, groups, s);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || groups == 1) return e;
   k_rms_dw<<<static_cast<unsigned>(cols / 32), 256, 0, s>>>(p.part, dW, groups, p.cols);
   return hipGetLastError();
 }

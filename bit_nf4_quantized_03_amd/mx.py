@@ -114,19 +114,27 @@ def _tensor(name, t, dtype, shape, index=None):
     raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
+# torch.empty by another name: 1.3 us a call instead of 1.7
 def _empty(rows, cols, dtype, device):
-    # torch.empty by another name: 1.3 us a call instead of 1.7
     return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
+def _empty_1d(n, dtype, device):
+    return torch.empty_strided((n,), (1,), dtype=dtype, device=device)
 
 
 def _rows_cols(name, t, dtype=None):
     """Shape of a contiguous 2-D CUDA tensor with at least one row and column."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2 and (dtype is None or t.dtype is dtype) and \
+            t.is_contiguous():
+        rows, cols = t.shape
+        if rows and cols:
+            return rows, cols
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     if t.dim() != 2 or t.numel() == 0:
         raise ValueError(f"{name} must be 2-D with at least one row and one column, got {tuple(t.shape)}")
-    _tensor(name, t, dtype, t.shape)
-    return t.shape
+    _tensor(name, t, dtype, t.shape)   # raises
 
 
 def qlora_mx_scale_pitch(cols: int) -> int:
@@ -240,7 +248,7 @@ def qlora_rmsnorm_fwd(X, weight, eps: float = 1e-6, residual=None, out=None, h=N
     else:
         _tensor("out", out, torch.bfloat16, (rows, cols), index)
     if rstd is None:
-        rstd = torch.empty(rows, dtype=torch.float32, device=X.device)
+        rstd = _empty_1d(rows, torch.float32, X.device)
     else:
         _tensor("rstd", rstd, torch.float32, (rows,), index)
     _rmsnorm_fwd(index, *args, float(eps), out.data_ptr(), _at(h), rstd.data_ptr())
@@ -276,17 +284,18 @@ def qlora_rmsnorm_bwd(dY, H, weight, rstd, dH=None, ws=None, outs: Optional[Tupl
     rs = _tensor("rstd", rstd, torch.float32, (rows,), index)
     dh = None if dH is None else _tensor("dH", dH, torch.bfloat16, (rows, cols), index)
     if outs is None:
-        dX, dW = torch.empty_like(dY), torch.empty(cols, dtype=torch.float32, device=H.device)
+        dX, dW = torch.empty_like(dY), _empty_1d(cols, torch.float32, H.device)
     else:
         dX, dW = outs
         _tensor("dX", dX, torch.bfloat16, (rows, cols), index)
         _tensor("dW", dW, torch.float32, (cols,), index)
     if ws is None:
-        ws = torch.empty(lib.qlora_rmsnorm_bwd_workspace_bytes(rows, cols), dtype=torch.uint8, device=H.device)
+        size = lib.qlora_rmsnorm_bwd_workspace_bytes(rows, cols)
+        ws = _empty_1d(size, torch.uint8, H.device) if size else None
     else:
         _tensor("ws", ws, None, ws.shape, index)
-    _rmsnorm_bwd(index, dy, H.data_ptr(), w, dt, rs, dh, rows, cols, dX.data_ptr(), dW.data_ptr(), ws.data_ptr(),
-                 ws.numel() * ws.element_size())
+        size = ws.numel() * ws.element_size()
+    _rmsnorm_bwd(index, dy, H.data_ptr(), w, dt, rs, dh, rows, cols, dX.data_ptr(), dW.data_ptr(), _at(ws), size)
     return dX, dW
 
 

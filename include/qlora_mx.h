@@ -109,7 +109,8 @@ int qlora_rmsnorm_fwd(const void *X, const void *residual, const void *weight, i
 int qlora_rmsnorm_mx(const void *X, const void *residual, const void *weight, int w_dtype, int64_t rows,
                      int64_t cols, double eps, const qlora_mx_matrix *Y, void *H, void *stream);
 
-/* Workspace bytes of qlora_rmsnorm_bwd (0 for an invalid shape). */
+/* Workspace bytes of qlora_rmsnorm_bwd: 0 for a few rows (ws may then be NULL)
+ * and for an invalid shape. No contents are expected or kept. */
 size_t qlora_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t cols);
 
 /*

@@ -40,7 +40,7 @@ def test_sizes():
     assert qb.qlora_mx_storage_bytes(3, 64, FP8) == 3 * (64 + 16)
     assert qb.qlora_mx_storage_bytes(3, 64, 2) == qb.qlora_mx_storage_bytes(0, 64, 0) == qb.qlora_mx_storage_bytes(3, 65, 0) == 0
     assert qb.qlora_mx_storage_bytes(1 << 40, 64, 0) == 0
-    assert qb.qlora_rmsnorm_bwd_workspace_bytes(1, 32) >= 128
+    assert qb.qlora_rmsnorm_bwd_workspace_bytes(1, 32) == 0 and qb.qlora_rmsnorm_bwd_workspace_bytes(100, 64) >= 512
     assert qb.qlora_rmsnorm_bwd_workspace_bytes(1, 32800) == qb.qlora_rmsnorm_bwd_workspace_bytes(0, 64) == 0
     assert qb.qlora_rmsnorm_bwd_workspace_bytes(1 << 31, 64) == 0
 
@@ -91,8 +91,8 @@ def test_norm_rejects():
     assert g(FAKE, FAKE, FAKE, F32, 4, 64, 1e-6, ref(M(4, 64, type=9)), FAKE, None) == -7
     assert g(FAKE, None, FAKE, F32, 4, 64, 1e-6, ref(M(4, 64)), FAKE, None) == -2
     b = lib.qlora_rmsnorm_bwd
-    need = qb.qlora_rmsnorm_bwd_workspace_bytes(4, 64)
-    args = [FAKE, FAKE, FAKE, F32, FAKE, None, 4, 64, 2 * FAKE, FAKE, FAKE, need, None]
+    need = qb.qlora_rmsnorm_bwd_workspace_bytes(100, 64)
+    args = [FAKE, FAKE, FAKE, F32, FAKE, None, 100, 64, 2 * FAKE, FAKE, FAKE, need, None]
     for i in (0, 1, 2, 4, 8, 9):
         bad = list(args)
         bad[i] = None

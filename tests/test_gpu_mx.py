@@ -535,7 +535,8 @@ def test_refusals_with_tensors(qb):
     with pytest.raises(qb.QloraError):
         qb.qlora_rmsnorm_fwd(b, w, eps=float("nan"))
     y, h, r = qb.qlora_rmsnorm_fwd(b, w)
+    many = torch.randn(100, 64, device="cuda").to(torch.bfloat16)
     with pytest.raises(qb.QloraError):
-        qb.qlora_rmsnorm_bwd(b, h, w, r, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        qb.qlora_rmsnorm_bwd(many, many, w, torch.ones(100, device="cuda"), ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(qb.QloraError):
         qb.qlora_rmsnorm_bwd(b, h, w, r, outs=(h, torch.empty(64, device="cuda")))
