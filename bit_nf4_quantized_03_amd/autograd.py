@@ -1,4 +1,4 @@
-"""torch.autograd wrapper of the QLoRA linear layer.
+"""torch.autograd wrappers of the QLoRA linear layer and of RMSNorm.
 
 Marshalling only: the forward is one ``qlora_linear_fwd_save`` call, which
 also keeps the adapter activations bf16(scale X A^T) [M, r], and the backward
@@ -12,12 +12,16 @@ projections into a larger model with autograd, recompute them under
 
 Tensors: X bf16 [M, K] (any leading shape, flattened to M rows), A fp32
 [r, K], B fp32 [N, r], on the weight's device. The output is bf16 [..., N].
+
+``rmsnorm`` is the norm in front of the projections, with the residual's
+addition: one ``qlora_rmsnorm_fwd`` call and one ``qlora_rmsnorm_bwd`` call.
 """
 from __future__ import annotations
 
 import torch
 
-from . import NF4Weight, qlora_linear_bwd, qlora_linear_bwd_saved, qlora_linear_fwd, qlora_linear_fwd_save
+from . import (NF4Weight, qlora_linear_bwd, qlora_linear_bwd_saved, qlora_linear_fwd, qlora_linear_fwd_save,
+               qlora_rmsnorm_bwd, qlora_rmsnorm_fwd)
 
 
 class QLoRALinearFn(torch.autograd.Function):
@@ -47,3 +51,37 @@ class QLoRALinearFn(torch.autograd.Function):
 def qlora_linear(X, W: NF4Weight, A=None, B=None, scale: float = 0.0):
     """Y = X W-hat^T + scale (X A^T) B^T with autograd to X, A and B."""
     return QLoRALinearFn.apply(X, A, B, W, float(scale))
+
+
+class RMSNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, weight, residual, eps: float):
+        flat = X.reshape(-1, X.shape[-1]).contiguous()
+        res = None if residual is None else residual.reshape(flat.shape).contiguous()
+        Y, H, rstd = qlora_rmsnorm_fwd(flat, weight, eps, residual=res)
+        ctx.save_for_backward(H, weight, rstd)
+        ctx.set_materialize_grads(False)
+        if residual is None:
+            return Y.reshape(X.shape)
+        return Y.reshape(X.shape), H.reshape(X.shape)
+
+    @staticmethod
+    def backward(ctx, dY, dH=None):
+        H, weight, rstd = ctx.saved_tensors
+        with_residual = ctx.needs_input_grad[2]
+        if dY is None:   # only H went on, X and the residual take its gradient
+            return dH, None, dH if with_residual else None, None
+        shape = dY.shape
+        dY = dY.reshape(H.shape).contiguous()
+        if dH is not None:
+            dH = dH.reshape(H.shape).contiguous()
+        dX, dW = qlora_rmsnorm_bwd(dY, H, weight, rstd, dH=dH)
+        dX = dX.reshape(shape)
+        return dX, dW.to(weight.dtype), dX if with_residual else None, None
+
+
+def rmsnorm(X, weight, residual=None, eps: float = 1e-6):
+    """RMSNorm of bf16 X [..., D] with autograd to X, weight [D] (fp32 or bf16)
+    and residual. Without a residual the result is Y; with one it is (Y, H), H =
+    bf16(X + residual) being the residual stream that goes on."""
+    return RMSNormFn.apply(X, weight, residual, float(eps))

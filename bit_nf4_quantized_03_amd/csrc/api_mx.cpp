@@ -14,7 +14,6 @@ using qnf4::api_fail;
 
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 constexpr int64_t kMaxCols = qnf4::kMxMaxK;
-constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;   // workgroups of a launch
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -56,8 +55,6 @@ int check_norm_shape(const char *fn, int64_t rows, int64_t cols) {
   if (cols > qnf4::kRmsMaxCols)
     return api_fail(QLORA_ERR_SHAPE, "%s: cols = %lld past %lld", fn, static_cast<long long>(cols),
                     static_cast<long long>(qnf4::kRmsMaxCols));
-  if (rows > kMaxGrid) return api_fail(QLORA_ERR_SHAPE, "%s: rows = %lld past %lld", fn, static_cast<long long>(rows),
-                                       static_cast<long long>(kMaxGrid));
   return QLORA_OK;
 }
 
@@ -94,8 +91,9 @@ int check_product(const char *fn, const qlora_mx_matrix *X, const qlora_mx_matri
   if (X->cols != W->cols)
     return api_fail(QLORA_ERR_SHAPE, "%s: X has %lld columns but W has %lld", fn, static_cast<long long>(X->cols),
                     static_cast<long long>(W->cols));
-  if (X->rows > kMaxElems / n) return api_fail(QLORA_ERR_SHAPE, "%s: Y of %lld x %lld is too large", fn,
-                                               static_cast<long long>(X->rows), static_cast<long long>(n));
+  if (X->rows > qnf4::kMxMaxRows || n > qnf4::kMxMaxRows || X->rows > qnf4::kMxMaxOut / n)
+    return api_fail(QLORA_ERR_SHAPE, "%s: Y of %lld x %lld is too large", fn, static_cast<long long>(X->rows),
+                    static_cast<long long>(n));
   return QLORA_OK;
 }
 
@@ -187,7 +185,7 @@ int qlora_rmsnorm_mx(const void *X, const void *residual, const void *weight, in
 }
 
 size_t qlora_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t cols) {
-  if (!valid_shape(rows, cols) || cols > qnf4::kRmsMaxCols || rows > kMaxGrid) return 0;
+  if (!valid_shape(rows, cols) || cols > qnf4::kRmsMaxCols) return 0;
   return qnf4::rms_bwd_ws_bytes(rows, cols);
 }
 
@@ -238,9 +236,9 @@ int qlora_mx_linear_grouped(const qlora_mx_matrix *X, const qlora_mx_matrix *W, 
   if (!offsets) return api_fail(QLORA_ERR_NULL, "%s: offsets must not be NULL", fn);
   if ((reinterpret_cast<uintptr_t>(offsets) & 3u) != 0)
     return api_fail(QLORA_ERR_ALIGN, "%s: offsets must be 4-byte aligned", fn);
-  if (X->rows > INT32_MAX)
-    return api_fail(QLORA_ERR_SHAPE, "%s: X has %lld rows, past what int32 offsets reach", fn,
-                    static_cast<long long>(X->rows));
+  if (W->rows > qnf4::kMxMaxExpertRows)
+    return api_fail(QLORA_ERR_SHAPE, "%s: W has %lld rows, more than %lld", fn, static_cast<long long>(W->rows),
+                    static_cast<long long>(qnf4::kMxMaxExpertRows));
   st = check_product(fn, X, W, W->rows / experts, Y);
   if (st != QLORA_OK) return st;
   qnf4::MxLinear a = product_args(X, W, W->rows / experts, Y);

@@ -13,6 +13,10 @@ namespace qnf4 {
 
 constexpr int kMxBlock = QLORA_MX_BLOCK;
 
+// A launch holds fewer than 2^32 threads: longer runs go out in pieces of this
+// many workgroups (of at most 1024 threads).
+constexpr int64_t kMaxGroups = int64_t(1) << 21;
+
 inline int64_t mx_pitch(int64_t cols) { return 16 * ceil_div(cols, 512); }
 inline int64_t mx_row_bytes(int64_t cols, int type) { return type == QLORA_MX_FP4 ? cols / 2 : cols; }
 
@@ -50,6 +54,8 @@ struct MxLinear {
   void *Y;
 };
 constexpr int64_t kMxMaxK = int64_t(1) << 22;
+// What keeps a product's launch below 2^32 threads with every tile.
+constexpr int64_t kMxMaxRows = int64_t(1) << 24, kMxMaxExpertRows = int64_t(1) << 28, kMxMaxOut = int64_t(1) << 37;
 hipError_t launch_mx_linear(const MxLinear &a, hipStream_t s);
 
 }  // namespace qnf4

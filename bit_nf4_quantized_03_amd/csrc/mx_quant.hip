@@ -29,9 +29,9 @@ __device__ __forceinline__ void load8(const void *src, int64_t at, mx_u32x4 (&r)
 
 template <int TYPE, bool F32>
 __global__ __launch_bounds__(kThreads) void k_mx_quant(const void *src, uint8_t *codes, uint8_t *scales,
-                                                       int64_t blocks, uint32_t nblk, uint32_t pitch) {
+                                                       int64_t blocks, uint32_t nblk, uint32_t pitch, int64_t group0) {
   const int lane = threadIdx.x & 63;
-  const int64_t b0 = (static_cast<int64_t>(blockIdx.x) * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * kWaveBlocks;
+  const int64_t b0 = ((group0 + blockIdx.x) * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * kWaveBlocks;
   if (b0 >= blocks) return;
   mx_u32x4 in[kUnroll][2];
 #pragma unroll
@@ -77,9 +77,9 @@ __global__ __launch_bounds__(kThreads) void k_mx_quant(const void *src, uint8_t 
 
 template <int TYPE, bool F32>
 __global__ __launch_bounds__(kThreads) void k_mx_dequant(const uint8_t *codes, const uint8_t *scales, void *out,
-                                                         int64_t blocks, uint32_t nblk, uint32_t pitch) {
+                                                         int64_t blocks, uint32_t nblk, uint32_t pitch, int64_t group0) {
   const int lane = threadIdx.x & 63;
-  const int64_t b0 = (static_cast<int64_t>(blockIdx.x) * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * kWaveBlocks;
+  const int64_t b0 = ((group0 + blockIdx.x) * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * kWaveBlocks;
   if (b0 >= blocks) return;
   const MxRows rows(b0, nblk, kWaveBlocks);
   uint2 in[kUnroll];
@@ -139,8 +139,16 @@ __global__ __launch_bounds__(kThreads) void k_mx_dequant(const uint8_t *codes, c
   }
 }
 
-unsigned grid_of(int64_t blocks) {
-  return static_cast<unsigned>(ceil_div(blocks, static_cast<int64_t>(kThreads / 64) * kWaveBlocks));
+// run(workgroups, first workgroup) for all blocks
+template <class F>
+hipError_t in_pieces(int64_t blocks, F run) {
+  const int64_t groups = ceil_div(blocks, static_cast<int64_t>(kThreads / 64) * kWaveBlocks);
+  for (int64_t g = 0; g < groups; g += kMaxGroups) {
+    run(dim3(static_cast<unsigned>(groups - g < kMaxGroups ? groups - g : kMaxGroups)), g);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
@@ -149,30 +157,30 @@ hipError_t launch_mx_quantize(const void *X, bool x_bf16, int64_t rows, int64_t 
                               uint8_t *scales, hipStream_t s) {
   const int64_t blocks = rows * (cols / kMxBlock);
   const uint32_t nblk = static_cast<uint32_t>(cols / kMxBlock), pitch = static_cast<uint32_t>(mx_pitch(cols));
-  const dim3 g(grid_of(blocks)), t(kThreads);
-  if (type == QLORA_MX_FP4) {
-    if (x_bf16) k_mx_quant<QLORA_MX_FP4, false><<<g, t, 0, s>>>(X, codes, scales, blocks, nblk, pitch);
-    else k_mx_quant<QLORA_MX_FP4, true><<<g, t, 0, s>>>(X, codes, scales, blocks, nblk, pitch);
-  } else {
-    if (x_bf16) k_mx_quant<QLORA_MX_FP8, false><<<g, t, 0, s>>>(X, codes, scales, blocks, nblk, pitch);
-    else k_mx_quant<QLORA_MX_FP8, true><<<g, t, 0, s>>>(X, codes, scales, blocks, nblk, pitch);
-  }
-  return hipGetLastError();
+  return in_pieces(blocks, [&](dim3 g, int64_t first) {
+    if (type == QLORA_MX_FP4) {
+      if (x_bf16) k_mx_quant<QLORA_MX_FP4, false><<<g, kThreads, 0, s>>>(X, codes, scales, blocks, nblk, pitch, first);
+      else k_mx_quant<QLORA_MX_FP4, true><<<g, kThreads, 0, s>>>(X, codes, scales, blocks, nblk, pitch, first);
+    } else {
+      if (x_bf16) k_mx_quant<QLORA_MX_FP8, false><<<g, kThreads, 0, s>>>(X, codes, scales, blocks, nblk, pitch, first);
+      else k_mx_quant<QLORA_MX_FP8, true><<<g, kThreads, 0, s>>>(X, codes, scales, blocks, nblk, pitch, first);
+    }
+  });
 }
 
 hipError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, int type,
                                 void *out, bool out_bf16, hipStream_t s) {
   const int64_t blocks = rows * (cols / kMxBlock);
   const uint32_t nblk = static_cast<uint32_t>(cols / kMxBlock), pitch = static_cast<uint32_t>(mx_pitch(cols));
-  const dim3 g(grid_of(blocks)), t(kThreads);
-  if (type == QLORA_MX_FP4) {
-    if (out_bf16) k_mx_dequant<QLORA_MX_FP4, false><<<g, t, 0, s>>>(codes, scales, out, blocks, nblk, pitch);
-    else k_mx_dequant<QLORA_MX_FP4, true><<<g, t, 0, s>>>(codes, scales, out, blocks, nblk, pitch);
-  } else {
-    if (out_bf16) k_mx_dequant<QLORA_MX_FP8, false><<<g, t, 0, s>>>(codes, scales, out, blocks, nblk, pitch);
-    else k_mx_dequant<QLORA_MX_FP8, true><<<g, t, 0, s>>>(codes, scales, out, blocks, nblk, pitch);
-  }
-  return hipGetLastError();
+  return in_pieces(blocks, [&](dim3 g, int64_t first) {
+    if (type == QLORA_MX_FP4) {
+      if (out_bf16) k_mx_dequant<QLORA_MX_FP4, false><<<g, kThreads, 0, s>>>(codes, scales, out, blocks, nblk, pitch, first);
+      else k_mx_dequant<QLORA_MX_FP4, true><<<g, kThreads, 0, s>>>(codes, scales, out, blocks, nblk, pitch, first);
+    } else {
+      if (out_bf16) k_mx_dequant<QLORA_MX_FP8, false><<<g, kThreads, 0, s>>>(codes, scales, out, blocks, nblk, pitch, first);
+      else k_mx_dequant<QLORA_MX_FP8, true><<<g, kThreads, 0, s>>>(codes, scales, out, blocks, nblk, pitch, first);
+    }
+  });
 }
 
 }  // namespace qnf4

@@ -28,7 +28,7 @@ struct FwdParams {
   __bf16 *y, *h;
   uint8_t *codes, *scales;
   float *rstd;
-  int64_t rows;
+  int64_t rows, group0;   // group0: the launch's first workgroup
   double eps, inv_cols;
   uint32_t cols, pitch;
   bool w_bf16;
@@ -115,7 +115,7 @@ template <int T, int THREADS, int NV, int OUT>
 __global__ __launch_bounds__(THREADS) void k_rms_fwd(const FwdParams p) {
   __shared__ double part[THREADS / 64];
   const int t = threadIdx.x % T, sub = threadIdx.x / T;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (THREADS / T) + sub;
+  const int64_t row = (p.group0 + blockIdx.x) * (THREADS / T) + sub;
   const bool live = row < p.rows;
   // rows past the end are read from the last one and stored nowhere
   const int64_t base = min(row, p.rows - 1) * p.cols;
@@ -312,12 +312,17 @@ __global__ __launch_bounds__(256) void k_rms_dw(const float *part, float *dw, in
 }
 
 template <int T, int THREADS, int NV>
-hipError_t fwd_run(const FwdParams &p, int out, hipStream_t s) {
-  const unsigned g = static_cast<unsigned>(ceil_div(p.rows, THREADS / T));
-  if (out == QLORA_MX_FP4) k_rms_fwd<T, THREADS, NV, QLORA_MX_FP4><<<g, THREADS, 0, s>>>(p);
-  else if (out == QLORA_MX_FP8) k_rms_fwd<T, THREADS, NV, QLORA_MX_FP8><<<g, THREADS, 0, s>>>(p);
-  else k_rms_fwd<T, THREADS, NV, kOutBf16><<<g, THREADS, 0, s>>>(p);
-  return hipGetLastError();
+hipError_t fwd_run(FwdParams p, int out, hipStream_t s) {
+  const int64_t groups = ceil_div(p.rows, THREADS / T);
+  for (p.group0 = 0; p.group0 < groups; p.group0 += kMaxGroups) {
+    const unsigned g = static_cast<unsigned>(std::min(groups - p.group0, kMaxGroups));
+    if (out == QLORA_MX_FP4) k_rms_fwd<T, THREADS, NV, QLORA_MX_FP4><<<g, THREADS, 0, s>>>(p);
+    else if (out == QLORA_MX_FP8) k_rms_fwd<T, THREADS, NV, QLORA_MX_FP8><<<g, THREADS, 0, s>>>(p);
+    else k_rms_fwd<T, THREADS, NV, kOutBf16><<<g, THREADS, 0, s>>>(p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // Rows of a backward workgroup at a time (1024 threads).

@@ -177,8 +177,8 @@ class MXMatrix:
             raise ValueError(f"{name}.mx must be QLORA_MX_FP4 or QLORA_MX_FP8, got {mx}")
         shape, pitch = (rows, cols if mx else cols // 2), (rows, -(-cols // 512) * 16)
         if index is None:
-            index = codes.get_device()
-        if not (codes.is_cuda and codes.dtype is torch.uint8 and codes.shape == shape and codes.is_contiguous() and
+            index = codes.get_device() if isinstance(codes, torch.Tensor) else -1
+        if not (isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor) and codes.is_cuda and codes.dtype is torch.uint8 and codes.shape == shape and codes.is_contiguous() and
                 scales.is_cuda and scales.dtype is torch.uint8 and scales.shape == pitch and scales.is_contiguous() and
                 codes.get_device() == scales.get_device() == index):
             _tensor(f"{name}.codes", codes, torch.uint8, shape, index)

@@ -136,9 +136,9 @@ int qlora_rmsnorm_bwd(const void *dY, const void *H, const void *weight, int w_d
  * exactly, with one reservation that is the matrix instruction's: with an
  * 8-bit X it adds eight neighbouring products of a row at a time and cuts them
  * off 13 binades below the largest of the eight (only products 10 or more
- * binades smaller than it lose anything). M and N
- * are any sizes from 1. A NaN block (scale
- * 255) makes the row (X) or column (W) of Y that it enters NaN, and no other.
+ * binades smaller than it lose anything). M and N are any sizes from 1 to 2^24
+ * with M N at most 2^37. A NaN block (scale 255) makes the row (X) or column
+ * (W) of Y that it enters NaN, and no other.
  */
 int qlora_mx_linear(const qlora_mx_matrix *X, const qlora_mx_matrix *W, void *Y, void *stream);
 
@@ -151,7 +151,7 @@ int qlora_mx_linear(const qlora_mx_matrix *X, const qlora_mx_matrix *W, void *Y,
  *            on are left as they were. Offsets are read on the GPU only: one
  *            below 0 or past M counts as 0 or M, and an expert whose end lies
  *            before its start has no rows.
- *   experts  1 .. QLORA_MX_EXPERTS, a divisor of W->rows
+ *   experts  1 .. QLORA_MX_EXPERTS, a divisor of W->rows (at most 2^28)
  * Types, sums and sizes as in qlora_mx_linear.
  */
 int qlora_mx_linear_grouped(const qlora_mx_matrix *X, const qlora_mx_matrix *W, const int32_t *offsets,

@@ -44,7 +44,8 @@ def nearest_codes(x: np.ndarray, mx: int) -> np.ndarray:
 
 def quantize(x: np.ndarray, mx: int):
     """(codes, scales) of x [rows, cols]. Blocks with a NaN or an Inf: scale 255, codes 0."""
-    x = np.asarray(x, dtype=np.float64)
+    with np.errstate(invalid="ignore"):           # signalling NaN among every bf16 pattern
+        x = np.asarray(x, dtype=np.float64)
     rows, cols = x.shape
     b = x.reshape(rows, cols // BLOCK, BLOCK)
     bad = ~np.isfinite(b).all(-1)

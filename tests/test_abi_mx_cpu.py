@@ -42,7 +42,7 @@ def test_sizes():
     assert qb.qlora_mx_storage_bytes(1 << 40, 64, 0) == 0
     assert qb.qlora_rmsnorm_bwd_workspace_bytes(1, 32) == 0 and qb.qlora_rmsnorm_bwd_workspace_bytes(100, 64) >= 512
     assert qb.qlora_rmsnorm_bwd_workspace_bytes(1, 32800) == qb.qlora_rmsnorm_bwd_workspace_bytes(0, 64) == 0
-    assert qb.qlora_rmsnorm_bwd_workspace_bytes(1 << 31, 64) == 0
+    assert qb.qlora_rmsnorm_bwd_workspace_bytes(1 << 35, 64) == 0
 
 
 def test_quantize_rejects():
@@ -80,7 +80,7 @@ def test_norm_rejects():
     assert call(X=None) == call(w=None) == call(Y=None) == call(H=None) == -1
     assert call(res=None) == -2                     # H without a residual
     assert call(wt=3) == -3
-    assert call(rows=0) == call(cols=0) == call(cols=40) == call(cols=32800) == call(rows=1 << 31) == -2
+    assert call(rows=0) == call(cols=0) == call(cols=40) == call(cols=32800) == call(rows=1 << 35) == -2
     assert call(eps=-1e-9) == call(eps=float("inf")) == call(eps=float("nan")) == -2
     assert call(Y=FAKE) == -2                       # Y is H
     for name in ("X", "res", "w", "Y", "H", "rstd"):
@@ -119,13 +119,15 @@ def test_products_reject():
     assert f(ref(x), ref(M(type=FP8)), FAKE, None) == -7
     assert f(ref(x), ref(M(cols=96)), FAKE, None) == -2
     assert f(ref(x), ref(M()), FAKE + 8, None) == -6
-    assert f(ref(M(1 << 30, 64, type=FP8)), ref(M(1 << 30, 64)), FAKE, None) == -2
+    for m, n in ((1 << 25, 1), (1, 1 << 25), (1 << 19, 1 << 19)):
+        assert f(ref(M(m, 64, type=FP8)), ref(M(n, 64)), FAKE, None) == -2
     g = lib.qlora_mx_linear_grouped
     assert g(ref(x), ref(M()), None, 2, FAKE, None) == -1
     for e in (0, -1, 3, 1025):
         assert g(ref(x), ref(M()), FAKE, e, FAKE, None) == -2, e
     assert g(ref(x), ref(M()), FAKE + 2, 2, FAKE, None) == -6
-    assert g(ref(M(1 << 31, 64, type=FP8)), ref(M()), FAKE, 2, FAKE, None) == -2
+    assert g(ref(M(1 << 25, 64, type=FP8)), ref(M()), FAKE, 2, FAKE, None) == -2
+    assert g(ref(x), ref(M(1 << 29, 64)), FAKE, 1024, FAKE, None) == -2
     assert g(ref(x), ref(M(type=FP8)), FAKE, 2, FAKE, None) == -7
 
 

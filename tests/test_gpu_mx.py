@@ -275,6 +275,8 @@ def check_sharply(got, xc, wc, t, seed, rows_of=None):
     """A sample of the outputs against the cut's own bound, group by group (tens of times sharper than
     product_bound): xc, wc are the oracle's (codes, scales); rows_of maps an output row to its first row of W."""
     M, N = got.shape
+    if M == 0:
+        return
     rng = np.random.default_rng(seed)
     m, n = rng.integers(0, M, 600), rng.integers(0, N, 600)
     wn = n if rows_of is None else rows_of[m] + n
@@ -319,8 +321,23 @@ def test_linear(qb, M, N, K, t):
     assert qb.qlora_mx_linear(X, W, out=out) is out and torch.equal(out, Y)
 
 
+# sizes at which each of the larger tiles is chosen, with whole and ragged rows of Y, one step and several pieces
 @pytest.mark.parametrize("t", TYPES)
-@pytest.mark.parametrize("M,N,K", [(1, 272, 4096), (20, 80, 1056), (40, 80, 96), (150, 270, 640), (700, 600, 2048), (300, 300, 8192)])
+@pytest.mark.parametrize("M,N,K", [(4000, 4090, 160), (4096, 4096, 544), (3900, 4096, 1056), (2040, 4090, 1056), (2048, 4096, 96),
+                                   (1000, 4090, 544), (990, 4096, 2080), (310, 4090, 544), (320, 4096, 32), (5000, 2056, 1504)])
+def test_linear_large_tiles(qb, M, N, K, t):
+    gu.announce(f"mx linear {M}x{N}x{K} type {t}")
+    X, xv, W, wv, xc, wc = product_data(qb, M, N, K, t, M + N + K)
+    Y = qb.qlora_mx_linear(X, W)
+    ref, size = mx.linear(xv, wv)
+    got = gu.host_bf16_f32(Y).astype(np.float64)
+    check_product(got, ref, size, K, t)
+    check_sharply(got, xc, wc, t, K)
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("M,N,K", [(1, 272, 4096), (20, 80, 1056), (40, 80, 96), (150, 270, 640), (700, 600, 2048), (300, 300, 8192),
+                                   (4096, 4096, 1056), (2048, 4096, 320), (1000, 4096, 544)])
 def test_linear_exact_on_whole_numbers(qb, M, N, K, t):
     """One nonzero of X per row and block column: every sum is exact, so Y must be bit for bit."""
     gu.announce(f"mx linear exact {M}x{N}x{K} type {t}")
@@ -358,6 +375,9 @@ def test_linear_nan_blocks_stay_in_their_row_and_column(qb, M):
     (256, 544, [0, 0, 0, 17, 17, 50, 51, 51, 64], 64),
     (128, 2048, [0, 300, 301, 301, 570, 600], 600),
     (300, 1024, [0, 16, 32, 48, 1100], 1103),
+    (72, 64, [0, 0, 0, 0], 5),                # no expert has a row
+    (2050, 544, [0, 1500, 1500, 4000], 4001),
+    (4096, 160, [0, 700, 2100, 2101, 4096], 4096),
     (64, 256, [-5, 4, 2, 9, 40], 12),         # out of range and not ascending: clamped, expert 1 has no rows
 ])
 def test_grouped(qb, N, K, offsets, M, t):
@@ -386,6 +406,21 @@ def test_grouped(qb, N, K, offsets, M, t):
     new = qb.qlora_mx_linear_grouped(X, W, off)
     if none.any():
         assert (gu.host_bf16_f32(new)[:none.size][none] == 0).all() or offsets != sorted(offsets)
+
+
+@pytest.mark.parametrize("E,M", [(130, 300), (70, 900), (1024, 64), (1024, 20000)])
+def test_grouped_many_experts(qb, E, M):
+    """More experts than lanes, most of them with a few rows or none."""
+    import torch
+    gu.announce(f"mx grouped {E} experts {M} rows")
+    N, K = 64, 64
+    rng = np.random.default_rng(E + M)
+    X, xv, W, wv, xc, wc = product_data(qb, M, N * E, K, mx.FP8, E)
+    counts = np.bincount((E * rng.random(M) ** 3).astype(int), minlength=E)
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    Y = qb.qlora_mx_linear_grouped(X, W, torch.tensor(offsets, dtype=torch.int32, device="cuda"))
+    ref, size = mx.grouped(xv, wv.reshape(E, N, K), offsets)
+    check_product(gu.host_bf16_f32(Y).astype(np.float64), ref, size, K, mx.FP8)
 
 
 def test_grouped_equals_dense_by_expert(qb):
@@ -490,6 +525,118 @@ def test_two_streams_at_once(qb):
     for runs in got:
         for outs in runs:
             assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("t", TYPES)
+def test_offsets_past_32_bits(qb, t):
+    """Elements, codes and outputs behind 2^32: the last rows against the same rows on their own."""
+    import torch
+    gu.announce(f"mx past 32 bits type {t}")
+    rows, cols = (1 << 17) + 5, 1 << 15
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = torch.randn(3, cols, device="cuda")
+    q = qb.qlora_mx_quantize(x, t)
+    last = qb.qlora_mx_quantize(x[-3:].contiguous(), t)
+    assert torch.equal(q.codes[-3:], last.codes) and torch.equal(q.scales[-3:], last.scales)
+    assert not q.codes[:7].any() and not q.scales[rows // 2].any()
+    y = qb.qlora_mx_dequantize(q, torch.bfloat16)
+    assert torch.equal(y[-3:], qb.qlora_mx_dequantize(last, torch.bfloat16)) and not y[rows // 2].any()
+    w = torch.ones(cols, device="cuda")
+    n, h, rstd = qb.qlora_rmsnorm_fwd(x, w, out=y)
+    few = qb.qlora_rmsnorm_fwd(x[-3:].contiguous(), w)
+    assert torch.equal(n[-3:], few[0]) and torch.equal(rstd[-3:], few[2])
+    del q, n, y
+    X = qb.qlora_mx_quantize(x[:, :64].contiguous(), t)
+    W = qb.qlora_mx_quantize(torch.randn(cols + 8, 64, device="cuda"))
+    Y = qb.qlora_mx_linear(X, W)                      # 131077 x 32776 outputs
+    tail = qb.MXMatrix(3, 64, X.codes[-3:].clone(), X.scales[-3:].clone(), t)
+    assert torch.equal(Y[-3:], qb.qlora_mx_linear(tail, W)) and not Y[rows // 2].any()
+
+
+def test_many_short_rows(qb):
+    """More workgroups than one launch takes (norm), and short rows by the million (quantize)."""
+    import torch
+    gu.announce("mx many short rows")
+    rows = 4 * (1 << 21) + 6
+    x = torch.zeros(rows, 32, dtype=torch.bfloat16, device="cuda")
+    x[-7:] = torch.randn(7, 32, device="cuda")
+    w = torch.ones(32, device="cuda")
+    y, _, rstd = qb.qlora_rmsnorm_fwd(x, w, eps=1.0)
+    few = qb.qlora_rmsnorm_fwd(x[-7:].contiguous(), w, eps=1.0)
+    assert torch.equal(y[-7:], few[0]) and torch.equal(rstd[-7:], few[2]) and (rstd[:-7] == 1.0).all()
+    q, _ = qb.qlora_rmsnorm_mx(x, w, eps=1.0)
+    p = qb.qlora_mx_quantize(y)
+    assert torch.equal(p.codes[-7:], qb.qlora_mx_quantize(y[-7:].contiguous()).codes) and not q.codes[:-7].any()
+
+
+def test_norm_and_projection_with_autograd(qb):
+    """The norm with its residual in front of a QLoRA projection, through autograd, against the oracle in fp64;
+    and the paths on which one of the two gradients does not arrive."""
+    import torch
+    from bit_nf4_quantized_03_amd.autograd import qlora_linear, rmsnorm
+    from oracle import linear, nf4
+    gu.announce("norm and projection with autograd")
+    rng = np.random.default_rng(1)
+    D, N, r, s = 128, 192, 8, 0.5
+    wq = rng.normal(size=(N, D)).astype(np.float32) * 0.05
+    base = qb.qlora_nf4_quantize(gu.dev_f32(wq))
+    wv = nf4.dequantize(nf4.quantize(wq, nf4.nf4_codebook()), nf4.nf4_codebook())
+    a, b = (rng.normal(size=z).astype(np.float32) * 0.1 for z in ((r, D), (N, r)))
+    xd, x = bf16(rng.normal(size=(6, D)))
+    rd, res = bf16(rng.normal(size=(6, D)))
+    g = (1 + 0.1 * rng.normal(size=D)).astype(np.float32)
+    X, R, G, A, B = (v.requires_grad_(True) for v in (xd.view(2, 3, D), rd.view(2, 3, D), gu.dev_f32(g), gu.dev_f32(a), gu.dev_f32(b)))
+    y, h = rmsnorm(X, G, R)
+    z = qlora_linear(y, base, A, B, s)
+    zd, zg = bf16(rng.normal(size=(6, N)))
+    hd, hg = bf16(rng.normal(size=(6, D)))
+    torch.autograd.backward([z, h], [zd.view(2, 3, N), hd.view(2, 3, D)])
+    yn, hv, _ = mx.rmsnorm(x, g, 1e-6, res)
+    dy, da, db = linear.backward(zg, mx.round_bf16(yn), wv, a, b, s)
+    dx, dg = mx.rmsnorm_backward(dy, hv, g.astype(np.float64), 1e-6, hg)
+    assert torch.equal(X.grad, R.grad)
+    # dy is rounded to bf16 once and formed from bf16 factors (2^-8 each at most), dx once more
+    assert gu.rel_fro(gu.host_bf16_f32(X.grad.reshape(6, D)), dx) <= 2e-2
+    assert gu.rel_fro(gu.host(G.grad), dg) <= 2e-2 and gu.rel_fro(gu.host(A.grad), da) <= 2e-2 and gu.rel_fro(gu.host(B.grad), db) <= 2e-2
+
+    X2, G2 = xd.detach().clone().requires_grad_(True), gu.dev_bf16(synth.f32_to_bf16(g)).requires_grad_(True)
+    rmsnorm(X2, G2).backward(hd)                      # no residual, bf16 weight
+    gb = synth.bf16_to_f32(synth.f32_to_bf16(g)).astype(np.float64)
+    dx, dg = mx.rmsnorm_backward(hg, x, gb, 1e-6)
+    assert X2.grad.dtype == torch.bfloat16 and G2.grad.dtype == torch.bfloat16
+    assert gu.rel_fro(gu.host_bf16_f32(X2.grad), dx) <= 2.0 ** -8 and gu.rel_fro(gu.host_bf16_f32(G2.grad), dg) <= 2.0 ** -8
+    X3, R3 = xd.detach().clone().requires_grad_(True), rd.detach().clone().requires_grad_(True)
+    rmsnorm(X3, G2.detach(), R3)[1].backward(hd)      # only the residual stream goes on
+    assert torch.equal(X3.grad, hd) and torch.equal(R3.grad, hd)
+    X4 = xd.detach().clone().requires_grad_(True)
+    rmsnorm(X4, G2.detach(), rd.detach())[0].backward(hd)   # only y goes on, the residual has no gradient
+    dx, _ = mx.rmsnorm_backward(hg, hv, gb, 1e-6)
+    assert gu.rel_fro(gu.host_bf16_f32(X4.grad), dx) <= 2.0 ** -8
+
+
+def test_backward_captured_beside_an_eager_graph(qb):
+    """A captured backward of the same leaves as a live eager graph, replayed with new gradients."""
+    import torch
+    gu.announce("rmsnorm backward captured")
+    xd, _, rd, _, wd, _ = norm_data(300, 1024, 3, True, False)
+    dy, dh = torch.randn_like(xd), torch.randn_like(xd)
+    _, H, R = qb.qlora_rmsnorm_fwd(xd, wd, residual=rd)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        qb.qlora_rmsnorm_bwd(dy, H, wd, R, dH=dh)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, h, r = qb.qlora_rmsnorm_fwd(xd, wd, residual=rd)
+        dx, dw = qb.qlora_rmsnorm_bwd(dy, h, wd, r, dH=dh)
+    for i in range(3):
+        dy.copy_(torch.randn_like(xd))
+        graph.replay()
+        torch.cuda.synchronize()
+        a, b = dx.clone(), dw.clone()
+        want = qb.qlora_rmsnorm_bwd(dy, H, wd, R, dH=dh)
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1]), f"replay {i}"
 
 
 def test_refusals_with_tensors(qb):
