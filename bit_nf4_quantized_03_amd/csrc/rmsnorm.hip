@@ -293,20 +293,20 @@ __global__ __launch_bounds__(THREADS) void k_rms_bwd(const BwdParams p) {
 }
 
 // dw[c] = sum over the groups of part[g][c]: a workgroup takes 32 columns,
-// thread (lane c, slice s of 8) the groups s, s + 8, ...; slices are added in
-// order. fp64, so that the order over many groups costs no accuracy.
-__global__ __launch_bounds__(256) void k_rms_dw(const float *part, float *dw, int64_t groups, uint32_t cols) {
-  __shared__ double sum[8][32];
+// thread (column c, slice s of 32) the groups s, s + 32, ...; slices are added
+// in order. fp64, so that the order over many groups costs no accuracy.
+__global__ __launch_bounds__(1024) void k_rms_dw(const float *part, float *dw, int groups, uint32_t cols) {
+  __shared__ double sum[32][32];
   const int c = threadIdx.x & 31, s = threadIdx.x >> 5;
   const uint32_t col = blockIdx.x * 32 + c;   // cols is a multiple of 32
   double v = 0.0;
 #pragma unroll 8
-  for (int64_t g = s; g < groups; g += 8) v += part[g * cols + col];
+  for (int g = s; g < groups; g += 32) v += part[static_cast<int64_t>(g) * cols + col];
   sum[s][c] = v;
   __syncthreads();
   if (s == 0) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) v += sum[i][c];
+    for (int i = 1; i < 32; ++i) v += sum[i][c];
     dw[col] = static_cast<float>(v);
   }
 }
@@ -328,11 +328,13 @@ hipError_t fwd_run(FwdParams p, int out, hipStream_t s) {
 // Rows of a backward workgroup at a time (1024 threads).
 int bwd_rows(int64_t cols) { return cols <= 512 ? 16 : cols <= 1024 ? 8 : cols <= 2048 ? 4 : cols <= 8192 ? 2 : 1; }
 
-// Workgroups of the backward, and rows of partial dw sums: one per compute
-// unit, so that the sums stay small beside the rows (two: 4096 x 4096 35 us
-// instead of 32, 4096 x 8192 62 instead of 57).
+// Workgroups of the backward, and rows of partial dw sums: at most one per
+// compute unit, so that the sums stay small beside the rows (two: 4096 x 4096
+// 35 us instead of 32, 4096 x 8192 62 instead of 57), and no more than are
+// needed to have the rows done in as many turns.
 unsigned bwd_groups(int64_t rows, int64_t cols) {
-  return static_cast<unsigned>(std::min<int64_t>(ceil_div(rows, bwd_rows(cols)), 256));
+  const int64_t turns = ceil_div(rows, bwd_rows(cols));
+  return static_cast<unsigned>(ceil_div(turns, ceil_div(turns, 256)));
 }
 
 template <int T, int NV>
@@ -401,7 +403,7 @@ hipError_t launch_rms_bwd(const void *dY, const void *H, const void *weight, boo
   else bwd_run<1024, 4>(p, groups, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || groups == 1) return e;
-  k_rms_dw<<<static_cast<unsigned>(cols / 32), 256, 0, s>>>(p.part, dW, groups, p.cols);
+  k_rms_dw<<<static_cast<unsigned>(cols / 32), 1024, 0, s>>>(p.part, dW, static_cast<int>(groups), p.cols);
   return hipGetLastError();
 }
 
