@@ -75,6 +75,9 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_gemv(const GemvParams p) {
       }
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
+        // lanes of rows that are not there load nothing: with one row a
+        // sixteenth of a load's addresses (1 x 4096 x 11008 7.7 -> 7.0 us)
+        const bool on = m0 + 16 * t + r < m_end;
         const int64_t m = min(m0 + 16 * t + r, m_end - 1);
         const uint8_t *xr = p.x + m * p.xrow + 16 * g;
         mx_v8i x[4];
@@ -82,10 +85,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_gemv(const GemvParams p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if constexpr (XT == QLORA_MX_FP4) {
-            x[i] = mx_operand(load16(xr + 256 * q + 64 * i, 16 * q + 4 * i + g < p.nblk));
+            x[i] = mx_operand(load16(xr + 256 * q + 64 * i, on && 16 * q + 4 * i + g < p.nblk));
           } else {
             const uint32_t b = 16 * q + 4 * i + (g >> 1);
-            x[i] = mx_operand(load16(xr + 512 * q + 128 * i, b < p.nblk), load16(xr + 512 * q + 128 * i + 64, b + 2 < p.nblk));
+            x[i] = mx_operand(load16(xr + 512 * q + 128 * i, on && b < p.nblk),
+                              load16(xr + 512 * q + 128 * i + 64, on && b + 2 < p.nblk));
           }
         }
 #pragma unroll
