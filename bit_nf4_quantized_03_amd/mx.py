@@ -16,6 +16,11 @@ import torch
 
 from . import QLORA_BF16, QLORA_F32, QloraError, lib, qlora_last_error
 
+try:
+    from . import _fastcall as _fast   # whole calls with new outputs; None where the call is not that simple
+except ImportError as e:
+    raise ImportError("_fastcall.so is missing: build it with `python bit_nf4_quantized_03_amd/build.py`") from e
+
 __all__ = [
     "MXMatrix", "QLORA_MX_FP4", "QLORA_MX_FP8", "MX_EXPORTED_SYMBOLS", "qlora_mx_scale_pitch",
     "qlora_mx_storage_bytes", "qlora_mx_quantize", "qlora_mx_dequantize", "qlora_rmsnorm_fwd",
@@ -65,6 +70,20 @@ def _declare():
 _declare()
 
 _DTYPES = {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}
+_DTYPES_OR_NONE = (None, torch.float32, torch.bfloat16)
+
+
+_stream, _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
+def _fast_on(t):
+    """(device index, stream) for a whole call on the current device when ``t``
+    lies there, else None."""
+    if isinstance(t, torch.Tensor) and t.is_cuda:
+        index = t.get_device()
+        if index == _current():
+            return index, _stream(index)
+    return None
 
 
 def _entry(name: str):
@@ -72,14 +91,13 @@ def _entry(name: str):
     current stream, with the device current (the library launches on the current
     one)."""
     fn = getattr(lib, name)
-    stream, current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
     def call(index, *args):
-        if index == current():
-            status = fn(*args, stream(index))
+        if index == _current():
+            status = fn(*args, _stream(index))
         else:
             with torch.cuda.device(index):
-                status = fn(*args, stream(index))
+                status = fn(*args, _stream(index))
         if status != 0:
             raise QloraError(name, status, qlora_last_error())
     return call
@@ -190,6 +208,10 @@ def qlora_mx_quantize(X, mx: Optional[int] = None, out: Optional[MXMatrix] = Non
     """Quantize a 2-D fp32 or bf16 CUDA tensor (columns a multiple of 32) to
     microscaled floats of type ``mx`` (``out.mx`` when ``out`` is given, else
     4 bits)."""
+    if out is None and (at := _fast_on(X)):
+        new = _fast.quantize(*at, X, QLORA_MX_FP4 if mx is None else mx)
+        if new is not None:
+            return MXMatrix(*X.shape, *new, QLORA_MX_FP4 if mx is None else mx)
     rows, cols = _rows_cols("X", X)
     dt = _dtype("X", X.dtype)
     if out is None:
@@ -203,6 +225,10 @@ def qlora_mx_quantize(X, mx: Optional[int] = None, out: Optional[MXMatrix] = Non
 
 def qlora_mx_dequantize(q: MXMatrix, dtype=None, out=None):
     """The values of ``q`` as a [rows, cols] tensor of ``dtype`` (float32 or bfloat16)."""
+    if out is None and dtype in _DTYPES_OR_NONE and (at := _fast_on(q.codes)):
+        new = _fast.dequantize(*at, q.codes, q.scales, q.rows, q.cols, q.mx, dtype is torch.bfloat16)
+        if new is not None:
+            return new
     st = q.c_struct("q")
     dtype = torch.float32 if dtype is None else dtype
     dt = _dtype("dtype", dtype)
@@ -242,6 +268,10 @@ def qlora_rmsnorm_fwd(X, weight, eps: float = 1e-6, residual=None, out=None, h=N
     """(Y, H, rstd): Y = H * rstd * weight in bf16 with H = bf16(X + residual),
     rstd = 1 / sqrt(mean(H^2) + eps) fp32 [rows]. Without a residual H is X
     itself. ``h`` may be X or ``residual`` (in place)."""
+    if out is None and h is None and rstd is None and (at := _fast_on(X)):
+        new = _fast.norm_fwd(*at, X, weight, eps, residual)
+        if new is not None:
+            return new
     rows, cols, index, args, h = _norm_inputs(X, weight, residual, h)
     if out is None:
         out = torch.empty_like(X)
@@ -259,6 +289,10 @@ def qlora_rmsnorm_mx(X, weight, eps: float = 1e-6, residual=None, mx: Optional[i
                      out: Optional[MXMatrix] = None, h=None) -> Tuple[MXMatrix, torch.Tensor]:
     """(Y, H) of qlora_rmsnorm_fwd with Y in microscaled floats of type ``mx``
     (``out.mx`` when ``out`` is given, else 8 bits)."""
+    if out is None and h is None and (at := _fast_on(X)):
+        new = _fast.norm_mx(*at, X, weight, eps, residual, QLORA_MX_FP8 if mx is None else mx)
+        if new is not None:
+            return MXMatrix(*X.shape, new[0], new[1], QLORA_MX_FP8 if mx is None else mx), new[2]
     rows, cols, index, args, h = _norm_inputs(X, weight, residual, h)
     if out is None:
         out = MXMatrix.empty(rows, cols, X.device, QLORA_MX_FP8 if mx is None else mx)
@@ -276,6 +310,10 @@ def qlora_rmsnorm_bwd(dY, H, weight, rstd, dH=None, ws=None, outs: Optional[Tupl
     """(dX, dW) of qlora_rmsnorm_fwd from its H and rstd. dX (bf16) is the
     gradient of X and of the residual; ``dH`` is the gradient that reaches H
     through the residual stream; dW is fp32 [cols]."""
+    if ws is None and outs is None and (at := _fast_on(H)):
+        new = _fast.norm_bwd(*at, dY, H, weight, rstd, dH)
+        if new is not None:
+            return new
     rows, cols = _rows_cols("H", H, torch.bfloat16)
     index = H.get_device()
     dy = _tensor("dY", dY, torch.bfloat16, (rows, cols), index)
@@ -301,6 +339,10 @@ def qlora_rmsnorm_bwd(dY, H, weight, rstd, dH=None, ws=None, outs: Optional[Tupl
 
 def qlora_mx_linear(X: MXMatrix, W: MXMatrix, out=None):
     """Y = X W^T in bf16: X [M, K] in 8- or 4-bit, W [N, K] in 4-bit microscaled floats."""
+    if out is None and (at := _fast_on(X.codes)):
+        new = _fast.linear(*at, X.codes, X.scales, X.rows, X.cols, X.mx, W.codes, W.scales, W.rows, W.cols, W.mx)
+        if new is not None:
+            return new
     sx = X.c_struct("X")
     index = X.codes.get_device()
     sw = W.c_struct("W", index)
