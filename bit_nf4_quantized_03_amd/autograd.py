@@ -19,6 +19,7 @@ addition: one ``qlora_rmsnorm_fwd`` call and one ``qlora_rmsnorm_bwd`` call.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (NF4Weight, qlora_linear_bwd, qlora_linear_bwd_saved, qlora_linear_fwd, qlora_linear_fwd_save,
                qlora_rmsnorm_bwd, qlora_rmsnorm_fwd)
@@ -66,6 +67,7 @@ class RMSNormFn(torch.autograd.Function):
         return Y.reshape(X.shape), H.reshape(X.shape)
 
     @staticmethod
+    @once_differentiable   # a second derivative is refused, not taken for zero
     def backward(ctx, dY, dH=None):
         H, weight, rstd = ctx.saved_tensors
         with_residual = ctx.needs_input_grad[2]

@@ -614,6 +614,26 @@ def test_norm_and_projection_with_autograd(qb):
     assert gu.rel_fro(gu.host_bf16_f32(X4.grad), dx) <= 2.0 ** -8
 
 
+def test_autograd_norm_gradients_are_their_own(qb):
+    """X and the residual have equal gradients in memory of their own; a second derivative is refused."""
+    import torch
+    from bit_nf4_quantized_03_amd.autograd import rmsnorm
+    gu.announce("autograd norm gradients")
+    x, r = (torch.randn(4, 64, device="cuda").bfloat16().requires_grad_(True) for _ in range(2))
+    g = torch.ones(64, device="cuda")
+    for turn in (1, 2):   # the second turn adds to what the first left
+        y, h = rmsnorm(x, g, r)
+        (y.float().square().sum() + h.float().sum()).backward()
+        assert x.grad.data_ptr() != r.grad.data_ptr() and torch.equal(x.grad, r.grad)
+        if turn == 1:
+            first = x.grad.clone()
+    assert torch.equal(x.grad, 2 * first)
+    y, h = rmsnorm(x, g, r)
+    (d,) = torch.autograd.grad(y.float().square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        d.float().sum().backward()
+
+
 def test_backward_captured_beside_an_eager_graph(qb):
     """A captured backward of the same leaves as a live eager graph, replayed with new gradients."""
     import torch
