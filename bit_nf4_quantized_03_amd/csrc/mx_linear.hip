@@ -34,21 +34,79 @@ __device__ __forceinline__ mx_v4i load16(const uint8_t *p, bool ok) {
   return ok ? *reinterpret_cast<const mx_v4i *>(p) : mx_v4i{0, 0, 0, 0};
 }
 
-// A workgroup takes 16 RT rows of W (of one expert) and all of the expert's
-// rows of X, 16 MT at a time; its WAVES waves take the 512-element pieces of
-// the reduction in turn and add their sums through LDS in wave order.
+// Rows of X of expert e, clamped to X; none where its end lies before its start.
+__device__ __forceinline__ void expert_rows(const int32_t *offsets, int experts, int64_t M, int e, int64_t &b, int64_t &end) {
+  b = end = 0;
+  if (e >= experts) return;
+  b = min(max(static_cast<int64_t>(offsets[e]), int64_t(0)), M);
+  end = max(min(max(static_cast<int64_t>(offsets[e + 1]), int64_t(0)), M), b);
+}
+
+// Finds number `t` among the pieces that `count(b, end)` gives each expert's
+// rows, expert after expert: the expert, its rows and the number within it.
+// False where there are fewer. The lanes count 64 experts at a time.
+template <class F>
+__device__ __forceinline__ bool find_piece(const int32_t *offsets, int experts, int64_t M, int &t, int &expert, int64_t &b,
+                                           int64_t &end, F count) {
+  const int lane = threadIdx.x & 63;
+  for (int e0 = 0; e0 < experts; e0 += 64) {
+    int64_t lb, lend;
+    expert_rows(offsets, experts, M, e0 + lane, lb, lend);
+    const int n = count(lb, lend);
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(upto, o);
+      if (lane >= o) upto += v;
+    }
+    const uint64_t here = __ballot(t < upto);
+    if (here == 0) {
+      t = __builtin_amdgcn_readfirstlane(t - __shfl(upto, 63));
+      continue;
+    }
+    const int l = __ffsll(static_cast<unsigned long long>(here)) - 1;
+    t = __builtin_amdgcn_readfirstlane(t - __shfl(upto - n, l));
+    expert = __builtin_amdgcn_readfirstlane(e0 + l);
+    b = mx_uniform(__shfl(lb, l));
+    end = mx_uniform(__shfl(lend, l));
+    return true;
+  }
+  return false;
+}
+
+// A workgroup takes 16 RT rows of W and up to 16 MT rows of X: all of them,
+// or by expert 16 of the expert's. Its WAVES waves take the 512-element pieces
+// of the reduction in turn and add their sums through LDS in wave order.
+//
+// By expert blockIdx.y < experts is an expert and its first 16 rows; the
+// numbers behind them are the further runs of 16 of the experts that have
+// them, found from the offsets: an expert with many rows has as many
+// workgroups (512 rows of one expert among 64: 57 us; by the workgroups of its
+// first 16 rows in turn 160).
+//
+// Bound by the weight's bytes: 1 x 11008 x 4096 8.5 us (2.8 TB/s: one load's
+// round trip for each wave, then the sums), 33 rows over eight 11008 x 4096
+// 39 us (4.6 TB/s), 64 over 64 4096 x 4096 98 us (5.8 TB/s).
 template <int XT, int MT, int RT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_mx_gemv(const GemvParams p) {
   __shared__ float part[WAVES][MT][RT][16][17];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, g = lane >> 4;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (16 * RT);
-  int64_t m_begin = 0, m_end = p.M;
+  int64_t m0 = 0, m_end = p.M;
   int64_t wbase = 0;
   if (p.experts) {
-    const int e = blockIdx.y;
-    m_begin = min(max(static_cast<int64_t>(p.offsets[e]), int64_t(0)), p.M);
-    m_end = min(max(static_cast<int64_t>(p.offsets[e + 1]), int64_t(0)), p.M);
+    int e = blockIdx.y;
+    if (e < p.experts) {
+      expert_rows(p.offsets, p.experts, p.M, e, m0, m_end);
+    } else {
+      int piece = e - p.experts;
+      const auto further = [](int64_t b, int64_t end) { return end > b ? static_cast<int>((end - b - 1) >> 4) : 0; };
+      if (!find_piece(p.offsets, p.experts, p.M, piece, e, m0, m_end, further)) return;
+      m0 += 16 * (piece + 1);
+    }
+    if (m0 >= m_end) return;
+    m_end = min(m_end, m0 + 16);
     wbase = static_cast<int64_t>(e) * p.N;
   }
   const uint8_t *wr[RT], *wsr[RT];
@@ -59,67 +117,64 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_gemv(const GemvParams p) {
     wsr[k] = p.ws + n * p.pitch;
   }
   const uint32_t pieces = (p.nblk + 15) / 16;
-  for (int64_t m0 = m_begin; m0 < m_end; m0 += 16 * MT) {
-    v4f acc[MT][RT];
+  v4f acc[MT][RT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+  for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int k = 0; k < RT; ++k) acc[t][k] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    for (uint32_t q = wave; q < pieces; q += WAVES) {
-      mx_v4i w[RT][4], sw[RT];
+    for (int k = 0; k < RT; ++k) acc[t][k] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  for (uint32_t q = wave; q < pieces; q += WAVES) {
+    mx_v4i w[RT][4], sw[RT];
 #pragma unroll
-      for (int k = 0; k < RT; ++k) {
+    for (int k = 0; k < RT; ++k) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[k][i] = load16(wr[k] + 256 * q + 64 * i, 16 * q + 4 * i + g < p.nblk);
-        sw[k] = *reinterpret_cast<const mx_v4i *>(wsr[k] + 16 * q);
-      }
+      for (int i = 0; i < 4; ++i) w[k][i] = load16(wr[k] + 256 * q + 64 * i, 16 * q + 4 * i + g < p.nblk);
+      sw[k] = *reinterpret_cast<const mx_v4i *>(wsr[k] + 16 * q);
+    }
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        // lanes of rows that are not there load nothing: with one row a
-        // sixteenth of a load's addresses (1 x 4096 x 11008 7.7 -> 7.0 us)
-        const bool on = m0 + 16 * t + r < m_end;
-        const int64_t m = min(m0 + 16 * t + r, m_end - 1);
-        const uint8_t *xr = p.x + m * p.xrow + 16 * g;
-        mx_v8i x[4];
-        const mx_v4i sx = *reinterpret_cast<const mx_v4i *>(p.xs + m * p.pitch + 16 * q);
+    for (int t = 0; t < MT; ++t) {
+      // lanes of rows that are not there load nothing: with one row a
+      // sixteenth of a load's addresses (1 x 4096 x 11008 7.7 -> 7.0 us)
+      const bool on = m0 + 16 * t + r < m_end;
+      const int64_t m = min(m0 + 16 * t + r, m_end - 1);
+      const uint8_t *xr = p.x + m * p.xrow + 16 * g;
+      mx_v8i x[4];
+      const mx_v4i sx = *reinterpret_cast<const mx_v4i *>(p.xs + m * p.pitch + 16 * q);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (XT == QLORA_MX_FP4) {
-            x[i] = mx_operand(load16(xr + 256 * q + 64 * i, on && 16 * q + 4 * i + g < p.nblk));
-          } else {
-            const uint32_t b = 16 * q + 4 * i + (g >> 1);
-            x[i] = mx_operand(load16(xr + 512 * q + 128 * i, on && b < p.nblk),
-                              load16(xr + 512 * q + 128 * i + 64, on && b + 2 < p.nblk));
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int si = static_cast<int>(static_cast<uint32_t>(sx[i]) >> (8 * g));
-#pragma unroll
-          for (int k = 0; k < RT; ++k)
-            acc[t][k] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                mx_operand(w[k][i]), x[i], acc[t][k], 4, XT == QLORA_MX_FP4 ? 4 : 0, 0,
-                static_cast<int>(static_cast<uint32_t>(sw[k][i]) >> (8 * g)), 0, si);
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (XT == QLORA_MX_FP4) {
+          x[i] = mx_operand(load16(xr + 256 * q + 64 * i, on && 16 * q + 4 * i + g < p.nblk));
+        } else {
+          const uint32_t b = 16 * q + 4 * i + (g >> 1);
+          x[i] = mx_operand(load16(xr + 512 * q + 128 * i, on && b < p.nblk),
+                            load16(xr + 512 * q + 128 * i + 64, on && b + 2 < p.nblk));
         }
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int si = static_cast<int>(static_cast<uint32_t>(sx[i]) >> (8 * g));
+#pragma unroll
+        for (int k = 0; k < RT; ++k)
+          acc[t][k] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              mx_operand(w[k][i]), x[i], acc[t][k], 4, XT == QLORA_MX_FP4 ? 4 : 0, 0,
+              static_cast<int>(static_cast<uint32_t>(sw[k][i]) >> (8 * g)), 0, si);
+      }
     }
-    // lane l holds X row l % 16 of a tile, W rows 4 (l / 16) + 0 .. 3
+  }
+  // lane l holds X row l % 16 of a tile, W rows 4 (l / 16) + 0 .. 3
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+  for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int k = 0; k < RT; ++k)
+    for (int k = 0; k < RT; ++k)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) part[wave][t][k][r][4 * g + v] = acc[t][k][v];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 256 * MT * RT; i += 64 * WAVES) {
-      const int c = i & 15, k = (i >> 4) % RT, m = (i >> 4) / RT & 15, t = (i >> 8) / RT;
-      float sum = 0.0f;
+      for (int v = 0; v < 4; ++v) part[wave][t][k][r][4 * g + v] = acc[t][k][v];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 256 * MT * RT; i += 64 * WAVES) {
+    const int c = i & 15, k = (i >> 4) % RT, m = (i >> 4) / RT & 15, t = (i >> 8) / RT;
+    float sum = 0.0f;
 #pragma unroll
-      for (int w = 0; w < WAVES; ++w) sum += part[w][t][k][m][c];
-      const int64_t row = m0 + 16 * t + m, n = n0 + 16 * k + c;
-      if (row < m_end && n < p.N) p.y[row * p.N + n] = static_cast<__bf16>(sum);
-    }
-    __syncthreads();
+    for (int w = 0; w < WAVES; ++w) sum += part[w][t][k][m][c];
+    const int64_t row = m0 + 16 * t + m, n = n0 + 16 * k + c;
+    if (row < m_end && n < p.N) p.y[row * p.N + n] = static_cast<__bf16>(sum);
   }
 }
 
@@ -147,54 +202,29 @@ __global__ __launch_bounds__(T::kThreads, 1) void k_mx_gemm(const GemmParams p) 
 
 // Tile of a workgroup in the product by expert. Tiles are counted expert after
 // expert; each XCD takes a contiguous range of them (consecutive workgroups go
-// to the XCDs in turn). Every wave finds its tile by itself: the lanes count
-// the tiles of 64 experts at a time.
+// to the XCDs in turn). Every wave finds its tile by itself.
 struct GroupTile {
   int expert, tm, tn;
   int64_t m_begin, m_end;
 };
 
-__device__ __forceinline__ int expert_tiles(const GemmParams &p, int e, int bm, int tiles_n, int64_t &b, int64_t &end) {
-  b = end = 0;
-  if (e >= p.experts) return 0;
-  b = min(max(static_cast<int64_t>(p.offsets[e]), int64_t(0)), p.M);
-  end = min(max(static_cast<int64_t>(p.offsets[e + 1]), int64_t(0)), p.M);
-  return end > b ? static_cast<int>((end - b + bm - 1) / bm) * tiles_n : 0;
-}
-
 template <class T>
 __device__ __forceinline__ bool group_tile(const GemmParams &p, int bid, GroupTile &out) {
   const int lane = threadIdx.x & 63;
   const int tiles_n = static_cast<int>((p.N + T::BN - 1) / T::BN);
-  int64_t b, end;
+  const auto tiles = [=](int64_t b, int64_t end) { return static_cast<int>((end - b + T::BM - 1) / T::BM) * tiles_n; };
   int total = 0;
-  for (int e0 = 0; e0 < p.experts; e0 += 64) total += expert_tiles(p, e0 + lane, T::BM, tiles_n, b, end);
+  for (int e0 = 0; e0 < p.experts; e0 += 64) {
+    int64_t b, end;
+    expert_rows(p.offsets, p.experts, p.M, e0 + lane, b, end);
+    total += tiles(b, end);
+  }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o);
   if (bid >= total) return false;
   const int base = total / 8, extra = total % 8, x = bid % 8;
   int t = x * base + min(x, extra) + bid / 8;
-  for (int e0 = 0;; e0 += 64) {
-    const int n = expert_tiles(p, e0 + lane, T::BM, tiles_n, b, end);
-    int upto = n;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(upto, o);
-      if (lane >= o) upto += v;
-    }
-    const uint64_t here = __ballot(t < upto);
-    if (here == 0) {
-      t -= __shfl(upto, 63);
-      continue;   // ends: t is below the sum over all experts
-    }
-    const int l = __ffsll(static_cast<unsigned long long>(here)) - 1;
-    t -= __shfl(upto - n, l);
-    out.expert = __builtin_amdgcn_readfirstlane(e0 + l);
-    out.m_begin = mx_uniform(__shfl(b, l));
-    out.m_end = mx_uniform(__shfl(end, l));
-    break;
-  }
-  t = __builtin_amdgcn_readfirstlane(t);
+  if (!find_piece(p.offsets, p.experts, p.M, t, out.expert, out.m_begin, out.m_end, tiles)) return false;
   // within the expert: groups of four tile rows, as tile_of
   const int tiles_m = static_cast<int>((out.m_end - out.m_begin + T::BM - 1) / T::BM);
   const int group = t / (4 * tiles_n), first = 4 * group, gm = min(tiles_m - first, 4), in = t - group * 4 * tiles_n;
@@ -221,7 +251,8 @@ __global__ __launch_bounds__(T::kThreads, 1) void k_mx_gemm_grouped(const GemmPa
 
 template <int XT, int MT, int RT, int WAVES>
 hipError_t run_gemv(const GemvParams &p, hipStream_t s) {
-  const dim3 g(static_cast<unsigned>(ceil_div(p.N, 16 * RT)), p.experts ? p.experts : 1);
+  // by expert: every run of 16 rows but an expert's first is a whole one or follows one
+  const dim3 g(static_cast<unsigned>(ceil_div(p.N, 16 * RT)), p.experts ? p.experts + static_cast<unsigned>(p.M / 16) : 1);
   k_mx_gemv<XT, MT, RT, WAVES><<<g, 64 * WAVES, 0, s>>>(p);
   return hipGetLastError();
 }
@@ -248,8 +279,12 @@ hipError_t run_gemm(const GemmParams &p, hipStream_t s) {
 // without work, so the tile is chosen by the time that these figures give.
 // Times behind the rule (us, 8-bit X, N = K = 4096; its choice first): 4096
 // rows 256 x 256 54, 256 x 128 61, 128 x 128 66; 2048 rows 256 x 128 32, 128 x
-// 128 35, 256 x 256 43; 1000 rows 128 x 128 20, 128 x 64 24, 256 x 128 24; 301
-// rows 128 x 64 13, 64 x 64 15, 128 x 128 16; 128 rows 64 x 64 10, 128 x 64 12.
+// 128 35, 256 x 256 43; 1000 rows 128 x 128 19, 128 x 64 23, 256 x 128 24; 301
+// rows 128 x 64 12.3, 128 x 128 15.7, 64 x 64 17.3; 128 rows 64 x 64 9.6, 128 x
+// 64 11.8. The 64 x 64 tile has two groups of waves with half the steps each
+// and four stages: one workgroup fills a compute unit, but it is chosen where
+// there is no second (with three stages, two to a unit, 128 rows 10.3; one
+// group 11.6; 128 x 64 in two groups 12.2).
 constexpr int kTiles = 5;
 constexpr struct {
   int bn, bm;
@@ -261,7 +296,7 @@ constexpr struct {
                    {256, 128, false, {{0.54, 0.88}, {0.41, 0.64}}},
                    {128, 128, true, {{0.33, 0.47}, {0.29, 0.36}}},
                    {128, 64, true, {{0.205, 0.305}, {0.19, 0.25}}},
-                   {64, 64, true, {{0.15, 0.20}, {0.13, 0.18}}}};
+                   {64, 64, false, {{0.14, 0.185}, {0.12, 0.165}}}};
 constexpr double kCus = 256;
 
 int choose_tile(int64_t M, int64_t N, int experts, bool fp4) {
@@ -296,7 +331,7 @@ hipError_t run_tiles(const GemmParams &p, hipStream_t s) {
     case 1: return run_gemm<MxTile<XT, 2, 2, 4, 2, kDeep, 1, kPair>>(p, s);
     case 2: return run_gemm<MxTile<XT, 2, 2, 2, 2, kDeep, 1, kPair>>(p, s);
     case 3: return run_gemm<MxTile<XT, 2, 1, 2, 2, 4>>(p, s);
-    default: return run_gemm<MxTile<XT, 1, 1, 2, 2, 3, 2>>(p, s);   // two groups of waves: 10 us where one takes 11.6
+    default: return run_gemm<MxTile<XT, 1, 1, 2, 2, 4, 2>>(p, s);
   }
 }
 
@@ -304,15 +339,20 @@ hipError_t run_tiles(const GemmParams &p, hipStream_t s) {
 // X is read by every workgroup, so from 5 rows on, a workgroup takes 64 rows
 // of W where that leaves half of the compute units one (8 x 11008 x 4096: 8.8
 // us against 10.0 with 16 rows), else 16 (16 x 4096 x 4096: 6.1 against 7.9).
-// By expert 32 rows and half the waves (33 rows over eight 11008 x 4096: 41 us
-// against 50 and 54). Returns false where the tiles are faster: from 17 rows
-// on (32 x 11008 x 4096 10.1 us against 16) unless there are few of them (32 x
-// 4096 x 4096 9.4 us against 8.1), by expert from 9 rows on average on.
+// By expert 64 rows and half the waves (one row for each of 64 4096 x 4096: 98
+// us, 5.8 TB/s, against 104 with 32 rows of W and 107 with 128; four for each
+// of eight 11008 x 4096: 39.5, 40.4 and 48), a quarter of them where the
+// reduction has no more than two pieces (4096 x 1024, 16 experts of 4 rows: 9.9
+// against 11.2). Returns false where the tiles are faster: from 17 rows on (32
+// x 11008 x 4096 9.3 us against 16) unless there are few of them (32 x 4096 x
+// 4096 9.4 us against 8.1), by expert from 9 rows on average on (64 4096 x 4096:
+// 8 rows 108 to 113 us against 118 with 128 x 64 tiles, 16 rows 126 to 162
+// against 120 to 124).
 template <int XT>
 bool run_few_rows(const GemvParams &p, hipStream_t s, hipError_t *e) {
   if (p.experts) {
     if (p.M > 8 * static_cast<int64_t>(p.experts)) return false;
-    *e = run_gemv<XT, 1, 2, 4>(p, s);
+    *e = p.nblk <= 32 ? run_gemv<XT, 1, 4, 2>(p, s) : run_gemv<XT, 1, 4, 4>(p, s);
     return true;
   }
   const bool many = p.N >= 64 * 128;

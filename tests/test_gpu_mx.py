@@ -423,6 +423,27 @@ def test_grouped_many_experts(qb, E, M):
     check_product(gu.host_bf16_f32(Y).astype(np.float64), ref, size, K, mx.FP8)
 
 
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("E,offsets,M", [
+    (16, [0] + [64] * 16, 64),                                   # one expert has every row
+    (16, [0] * 15 + [3, 60], 64),                                # the last two, rows behind them
+    (20, [1, 17, 34, 34, 67] + [67 + i for i in range(16)], 83),  # 16, 17, none, 33 and one each
+    (200, [0] * 100 + [100] * 66 + [300] * 35, 400),             # runs of one expert behind the first 64
+])
+def test_grouped_few_rows_uneven(qb, E, offsets, M, t):
+    """Few rows on average, but some experts with many."""
+    import torch
+    gu.announce(f"mx grouped uneven {E} experts {M} rows type {t}")
+    N, K = 80, 544
+    X, xv, W, wv, xc, wc = product_data(qb, M, N * E, K, t, E + M)
+    out = torch.full((M, N), 9.0, dtype=torch.bfloat16, device="cuda")
+    got = gu.host_bf16_f32(qb.qlora_mx_linear_grouped(X, W, torch.tensor(offsets, dtype=torch.int32, device="cuda"), out=out))
+    ref, size = mx.grouped(xv, wv.reshape(E, N, K), offsets)
+    none = np.isnan(ref[:, 0])
+    assert (got[none] == 9.0).all()
+    check_product(got[~none].astype(np.float64), ref[~none], size[~none], K, t)
+
+
 def test_grouped_equals_dense_by_expert(qb):
     """Each expert's rows through the dense product: the same sums up to their order."""
     import torch
