@@ -44,27 +44,28 @@ typedef int mx_v8i __attribute__((ext_vector_type(8)));
 __device__ __forceinline__ mx_v8i mx_operand(mx_v4i a) { return __builtin_shufflevector(a, mx_v4i{0, 0, 0, 0}, 0, 1, 2, 3, 4, 5, 6, 7); }
 __device__ __forceinline__ mx_v8i mx_operand(mx_v4i a, mx_v4i b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
 
-template <int XT_, int NF_, int MF_, int WN_, int WM_, int STAGES_, int KG_ = 1, bool PAIR_ = false>
+template <int XT_, int NF_, int MF_, int WN_, int WM_, int STAGES_, int SP_ = 1, int KG_ = 1, bool PAIR_ = false>
 struct MxTile {
-  static constexpr int XT = XT_, NF = NF_, MF = MF_, WN = WN_, WM = WM_, STAGES = STAGES_, KG = KG_;
+  static constexpr int XT = XT_, NF = NF_, MF = MF_, WN = WN_, WM = WM_, STAGES = STAGES_, SP = SP_, KG = KG_;
   static constexpr int kWaves = WN * WM, kThreads = 64 * kWaves * KG;   // waves of one group
   static constexpr int BN = 32 * NF * WN, BM = 32 * MF * WM;
   static constexpr int kXRow = XT == QLORA_MX_FP4 ? 64 : 128;   // bytes of a row and step
   static constexpr int kW = BN * 64, kX = BM * kXRow, kStage = kW + kX;
-  static constexpr int kScale = (BN + BM) * 16;
+  static constexpr int kScale = (BN + BM) * 16 * SP;             // SP pieces of 16 scales of a row, 4 SP steps
   static constexpr int kRing = STAGES * kStage + 2 * kScale;   // of one group
   static constexpr int kLds = KG * kRing;
   static constexpr int kWCopies = kW / 1024 / kWaves, kXCopies = kX / 1024 / kWaves;
   static constexpr int kCopies = kWCopies + kXCopies;
   static_assert(kW % (1024 * kWaves) == 0 && kX % (1024 * kWaves) == 0, "whole copies per wave");
-  static constexpr int kScaleBlocks = (BN + BM) / 64, kScaleCopies = (kScaleBlocks + kWaves - 1) / kWaves;
-  static_assert(BN % 64 == 0 && BM % 64 == 0, "whole scale copies");
+  static constexpr int kScaleRows = 64 / SP;   // rows of a scale copy
+  static constexpr int kScaleBlocks = kScale / 1024, kScaleCopies = (kScaleBlocks + kWaves - 1) / kWaves;
+  static_assert(BN % 64 == 0 && BM % 64 == 0 && (SP == 1 || SP == 2 || SP == 4), "whole scale copies");
   static_assert(kLds <= 160 * 1024, "LDS");
   // the steps go in pairs, copied together, two steps ahead
   static constexpr bool kPair = PAIR_;
   static constexpr int kAhead = kPair ? 2 : STAGES - 1;
   static constexpr int kNewer = kPair ? 0 : kCopies * (STAGES - 2);   // copies in flight behind a step's own
-  // a buffer of scales (four steps) is filled kAhead steps ahead: not before its readers are done
+  // a buffer of scales (4 SP steps) is filled kAhead steps ahead: not before its readers are done
   static_assert(kPair ? STAGES == 4 && XT == QLORA_MX_FP4 : STAGES == 3 || STAGES == 4, "ring");
   static_assert(kNewer < 64, "vmcnt range");
   // after the main loop: the groups' sums, then 32 rows of bf16 for each wave of the first group
@@ -190,16 +191,18 @@ __device__ __forceinline__ void mx_mainloop(MxAcc<T> &acc, const MxOperands &p, 
   const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char *)smem));
   const MxCopies<64, T::kWCopies, T::kWaves> cw(p.w, n0, p.w_rows, p.w_ld, wave);
   const MxCopies<T::kXRow, T::kXCopies, T::kWaves> cx(p.x, m0, p.x_rows, p.x_ld, wave);
-  // scales: block b of 64 rows (W's rows, then X's) by wave b % kWaves
+  // scales: block b of kScaleRows rows (W's rows, then X's) by wave b % kWaves,
+  // a row's SP pieces swapped so that 32 rows' reads of one lie on 16 banks
   const uint8_t *sbase[T::kScaleCopies];
   uint32_t srow[T::kScaleCopies];
+  const uint32_t spiece = 16u * ((lane ^ (lane >> 4)) & (T::SP - 1)), slast = p.pitch - 16;
 #pragma unroll
   for (int c = 0; c < T::kScaleCopies; ++c) {
-    const int first = 64 * (wave + T::kWaves * c);
+    const int first = T::kScaleRows * (wave + T::kWaves * c);
     const bool of_w = first < T::BN;
     sbase[c] = mx_uniform(of_w ? p.ws + n0 * p.pitch : p.xs + m0 * p.pitch);
     const int64_t end = of_w ? p.w_rows - 1 - n0 : p.x_rows - 1 - m0;
-    const int64_t at = first - (of_w ? 0 : T::BN) + lane;
+    const int64_t at = first - (of_w ? 0 : T::BN) + lane / T::SP;
     srow[c] = static_cast<uint32_t>((at < end ? at : end) * p.pitch);
   }
   const uint32_t sdst = lds + T::STAGES * T::kStage + 1024u * wave;
@@ -209,12 +212,14 @@ __device__ __forceinline__ void mx_mainloop(MxAcc<T> &acc, const MxOperands &p, 
   // that is not read any more: every step has the same copies, and one wait
   // count serves them all.
   auto issue = [&](int step, int part, int parts) {
-    if ((step & 3) == 0 && part == 0) {
-      const uint32_t at = 4u * static_cast<uint32_t>(min(step, s1 - 1) & ~3);
+    const uint32_t rel = static_cast<uint32_t>(step - s0);
+    if (rel % (4 * T::SP) == 0 && part == 0) {
+      // pieces behind a row's last one are not read: the last stands in for them
+      const uint32_t at = min(4u * static_cast<uint32_t>(step) + spiece, slast);
 #pragma unroll
       for (int c = 0; c < T::kScaleCopies; ++c)
         if (wave + T::kWaves * c < T::kScaleBlocks)
-          mx_copy(sdst + static_cast<uint32_t>(step & 4) / 4 * T::kScale + 1024u * T::kWaves * c, srow[c] + at, sbase[c]);
+          mx_copy(sdst + (rel / (4 * T::SP) & 1) * T::kScale + 1024u * T::kWaves * c, srow[c] + at, sbase[c]);
     }
 #pragma unroll
     for (int c = 0; c < T::kCopies; ++c)
@@ -253,6 +258,7 @@ __device__ __forceinline__ void mx_mainloop(MxAcc<T> &acc, const MxOperands &p, 
     f.w[part] = mx_operand(*reinterpret_cast<const mx_v4i *>(stage + ow[s] + 2048 * part));
   };
 
+  const uint32_t sswap = static_cast<uint32_t>(r) >> (T::SP == 4 ? 2 : 3);   // as the copies swap a row's pieces
   int sw[T::NF], sx[T::MF];       // scale words of this step, the lane's blocks in bytes 0 and 2
   MxFrags<T> f0, f1;
   if (s1 > s0) {
@@ -269,7 +275,9 @@ __device__ __forceinline__ void mx_mainloop(MxAcc<T> &acc, const MxOperands &p, 
     }
     if (T::KG > 1 && i >= s1) return;
     const char *stage = smem + static_cast<uint32_t>((i - s0) % T::STAGES) * T::kStage;
-    const char *sc = smem + T::STAGES * T::kStage + static_cast<uint32_t>(i & 4) / 4 * T::kScale + 4 * j + 16 * r;
+    const uint32_t rel = static_cast<uint32_t>(i - s0);
+    const char *sc = smem + T::STAGES * T::kStage + (rel / (4 * T::SP) & 1) * T::kScale + 16 * T::SP * r +
+                     16 * ((rel / 4 ^ sswap) & (T::SP - 1)) + 4 * j;
     uint32_t pw[T::NF], px[T::MF];
     // The LDS reads of the next half and the copies of a later step go out
     // between the matrix instructions. With the copies in front of them every
@@ -279,9 +287,9 @@ __device__ __forceinline__ void mx_mainloop(MxAcc<T> &acc, const MxOperands &p, 
       read(f0, stage, 0, n);
       if (n == T::NF - 1) {
 #pragma unroll
-        for (int k = 0; k < T::NF; ++k) pw[k] = *reinterpret_cast<const uint32_t *>(sc + 512 * (T::NF * wn + k));
+        for (int k = 0; k < T::NF; ++k) pw[k] = *reinterpret_cast<const uint32_t *>(sc + 512 * T::SP * (T::NF * wn + k));
 #pragma unroll
-        for (int m = 0; m < T::MF; ++m) px[m] = *reinterpret_cast<const uint32_t *>(sc + 16 * T::BN + 512 * (T::MF * wm + m));
+        for (int m = 0; m < T::MF; ++m) px[m] = *reinterpret_cast<const uint32_t *>(sc + T::SP * (16 * T::BN + 512 * (T::MF * wm + m)));
       }
       if (kCopying) issue(i + T::kAhead, n, 2 * T::NF);
       __builtin_amdgcn_sched_barrier(0);

@@ -327,11 +327,11 @@ hipError_t run_tiles(const GemmParams &p, hipStream_t s) {
   constexpr bool kPair = XT == QLORA_MX_FP4;
   constexpr int kDeep = kPair ? 4 : 3;   // stages
   switch (choose_tile(p.M, p.N, p.experts, XT == QLORA_MX_FP4)) {
-    case 0: return run_gemm<MxTile<XT, 4, 2, 2, 4, kDeep, 1, kPair>>(p, s);
-    case 1: return run_gemm<MxTile<XT, 2, 2, 4, 2, kDeep, 1, kPair>>(p, s);
-    case 2: return run_gemm<MxTile<XT, 2, 2, 2, 2, kDeep, 1, kPair>>(p, s);
-    case 3: return run_gemm<MxTile<XT, 2, 1, 2, 2, 4>>(p, s);
-    default: return run_gemm<MxTile<XT, 1, 1, 2, 2, 4, 2>>(p, s);
+    case 0: return run_gemm<MxTile<XT, 4, 2, 2, 4, kDeep, kPair ? 2 : 1, 1, kPair>>(p, s);
+    case 1: return run_gemm<MxTile<XT, 2, 2, 4, 2, kDeep, kPair ? 2 : 4, 1, kPair>>(p, s);
+    case 2: return run_gemm<MxTile<XT, 2, 2, 2, 2, kDeep, kPair ? 2 : 1, 1, kPair>>(p, s);
+    case 3: return run_gemm<MxTile<XT, 2, 1, 2, 2, 4, 2>>(p, s);
+    default: return run_gemm<MxTile<XT, 1, 1, 2, 2, 4, 4, 2>>(p, s);
   }
 }
 
