@@ -5,7 +5,9 @@
 // a block is a quad of lanes and its largest magnitude two lane exchanges
 // away; blocks never cross a row, so the matrix is walked as one run of
 // rows * cols / 32 blocks and only the address of the scale byte asks for the
-// row.
+// row. Four loads a lane are in flight. Bound by memory: 22016 x 8192 between
+// bf16 and 4 bits 74.8 us there and 70.7 back, 6.1 and 6.5 TB/s; 37 x 11008 and 8
+// bits 3.5 and 2.7 us, a launch and one round trip.
 #include "mx_device.h"
 
 namespace qnf4 {

@@ -110,7 +110,9 @@ __device__ __forceinline__ F row_sum(F v, F *part) {
 }
 
 // A workgroup of THREADS takes R = THREADS / T rows, T threads to a row with up
-// to NV runs of eight elements each.
+// to NV runs of eight elements each. Bound by memory for many rows (4096 x 4096
+// with residual 25.8 us into bf16, 5.2 TB/s, 27.8 into 8 bits, 4.2), by the
+// round trip of its loads and the sum for a few (1 x 4096 2.8 us).
 template <int T, int THREADS, int NV, int OUT>
 __global__ __launch_bounds__(THREADS) void k_rms_fwd(const FwdParams p) {
   __shared__ double part[THREADS / 64];
@@ -193,15 +195,21 @@ struct BwdParams {
 // R rows at a time as in the forward, rows b R .. for workgroup b, then G R
 // further on for a grid of G. A thread keeps the sums of dy u of its columns
 // over its rows; the R sums of a column are added in order through LDS, so that
-// a workgroup writes one row of partial sums. The next rows' loads are under
-// way while the current ones are worked on, where the registers are there.
+// a workgroup writes one row of partial sums. Bound by memory: 4096 x 4096 with
+// dh 28 us with the sums of k_rms_dw, 6.0 TB/s of the 168 MB that the rows
+// are. Where the registers are there, the next rows' loads are under way while
+// the current ones are worked on, and the weights stay in registers (loaded
+// again twice a row they were more bytes than the row: 4096 x 4096 32 us, 4096
+// x 8192 58 against 49).
 template <int T, int THREADS, int NV>
 __global__ __launch_bounds__(THREADS) void k_rms_bwd(const BwdParams p) {
   constexpr int R = THREADS / T;
   constexpr bool kAhead = NV == 1;
+  constexpr bool kKeep = NV <= 2;   // weights in registers
   __shared__ float part[2][THREADS / 64];
   __shared__ float4 sums[R > 1 ? NV * T * 2 : 1];
-  const int t = threadIdx.x % T, sub = threadIdx.x / T;
+  int t = threadIdx.x % T;
+  const int sub = threadIdx.x / T;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * R;
   int64_t first = static_cast<int64_t>(blockIdx.x) * R;
   const auto row_of = [&](int64_t f) { return min(f + sub, p.rows - 1); };
@@ -213,45 +221,64 @@ __global__ __launch_bounds__(THREADS) void k_rms_bwd(const BwdParams p) {
     next_rstd = p.rstd[row];
     load_runs<T>(next_dy, p.dy, row * p.cols, p.cols, t);
     load_runs<T>(next_h, p.h, row * p.cols, p.cols, t);
-    if (p.dh) load_runs<T>(next_dh, p.dh, row * p.cols, p.cols, t);
+    if (p.dh && kKeep) load_runs<T>(next_dh, p.dh, row * p.cols, p.cols, t);
   };
   if (kAhead) load(first);
+  float w[NV][8];
+  const auto weights = [&](int i) { load_weight8(p.w, p.w_bf16, 8u * (i * T + t), p.cols, w[i]); };
+  if (kKeep) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) weights(i);
+  }
   for (int flip = 0; first < p.rows; first += stride, flip ^= 1) {
-    const bool live = first + sub < p.rows;   // the same in a row's threads
+    const bool live = R == 1 || first + sub < p.rows;   // the same in a row's threads
     const int64_t base = row_of(first) * p.cols;
+    if (!kKeep) asm volatile("" : "+v"(t));   // the columns' addresses are formed again in each turn, not kept
     if (!kAhead) load(first);
     rstd = next_rstd;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) dy[i] = next_dy[i], h[i] = next_h[i], dh[i] = next_dh[i];
+    for (int i = 0; i < NV; ++i) {
+      dy[i] = next_dy[i], h[i] = next_h[i];
+      if (kKeep) dh[i] = next_dh[i];
+    }
     if (kAhead && first + stride < p.rows) load(first + stride);
     float c = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float a[8], b[8], w[8];
+      float a[8], b[8];
       unpack8(dy[i], a);
       unpack8(h[i], b);
-      load_weight8(p.w, p.w_bf16, 8u * (i * T + t), p.cols, w);
+      if (!kKeep) __builtin_amdgcn_sched_barrier(0), weights(i);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float du = a[k] * (b[k] * rstd);
         if (live) dw[i][k] += du;
-        c = __builtin_fmaf(du, w[k], c);
+        c = __builtin_fmaf(du, w[i][k], c);
       }
     }
     c = row_sum<T>(c, part[flip] + sub * (T / 64)) * p.inv_cols;
     if (!live) continue;
+    if (!kKeep) {
+      // the row stays packed: without this the compiler keeps it as fp32 for
+      // the second use and spills (300 x 24576 65 us)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) asm volatile("" : "+v"(dy[i]), "+v"(h[i]));
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const uint32_t col = 8u * (i * T + t);
       if (col < p.cols) {
-        float a[8], b[8], w[8], d[8];
+        float a[8], b[8], d[8];
         unpack8(dy[i], a);
         unpack8(h[i], b);
-        load_weight8(p.w, p.w_bf16, col, p.cols, w);
+        if (!kKeep) {
+          __builtin_amdgcn_sched_barrier(0);
+          weights(i);
+        }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) a[k] = rstd * (a[k] * w[k] - b[k] * rstd * c);
+        for (int k = 0; k < 8; ++k) a[k] = rstd * (a[k] * w[i][k] - b[k] * rstd * c);
         if (p.dh) {
-          unpack8(dh[i], d);
+          unpack8(kKeep ? dh[i] : load_row8(p.dh, base + col), d);
 #pragma unroll
           for (int k = 0; k < 8; ++k) a[k] += d[k];
         }
@@ -326,12 +353,13 @@ hipError_t fwd_run(FwdParams p, int out, hipStream_t s) {
 }
 
 // Rows of a backward workgroup at a time (1024 threads).
-int bwd_rows(int64_t cols) { return cols <= 512 ? 16 : cols <= 1024 ? 8 : cols <= 2048 ? 4 : cols <= 8192 ? 2 : 1; }
+int bwd_rows(int64_t cols) { return cols <= 512 ? 16 : cols <= 1024 ? 8 : cols <= 2048 ? 4 : cols <= 4096 ? 2 : 1; }
 
 // Workgroups of the backward, and rows of partial dw sums: at most one per
-// compute unit, so that the sums stay small beside the rows (two: 4096 x 4096
-// 35 us instead of 32, 4096 x 8192 62 instead of 57), and no more than are
-// needed to have the rows done in as many turns.
+// compute unit, so that the sums stay small beside the rows (two a unit cost
+// 4096 x 4096 three and 4096 x 8192 five us more), and no more than are needed
+// to have the rows done in as many turns. Up to 8192 columns a thread has one
+// run of a row (two, with two rows at a time: 4096 x 8192 52 us against 49).
 unsigned bwd_groups(int64_t rows, int64_t cols) {
   const int64_t turns = ceil_div(rows, bwd_rows(cols));
   return static_cast<unsigned>(ceil_div(turns, ceil_div(turns, 256)));
@@ -398,7 +426,7 @@ hipError_t launch_rms_bwd(const void *dY, const void *H, const void *weight, boo
   else if (cols <= 1024) bwd_run<128, 1>(p, groups, s);
   else if (cols <= 2048) bwd_run<256, 1>(p, groups, s);
   else if (cols <= 4096) bwd_run<512, 1>(p, groups, s);
-  else if (cols <= 8192) bwd_run<512, 2>(p, groups, s);
+  else if (cols <= 8192) bwd_run<1024, 1>(p, groups, s);
   else if (cols <= 16384) bwd_run<1024, 2>(p, groups, s);
   else bwd_run<1024, 4>(p, groups, s);
   hipError_t e = hipGetLastError();

@@ -104,7 +104,8 @@ int qlora_rmsnorm_fwd(const void *X, const void *residual, const void *weight, i
 /*
  * The same norm with its output in microscaled floats: Y (same rows and cols)
  * is exactly what qlora_mx_quantize would make of the unrounded Y, with no
- * bf16 rounding in between. Y's buffers overlap no input.
+ * bf16 rounding in between (a Y below fp32's normal range, 2^-126, is rounded to
+ * fp32 first, here and in qlora_rmsnorm_fwd). Y's buffers overlap no input.
  */
 int qlora_rmsnorm_mx(const void *X, const void *residual, const void *weight, int w_dtype, int64_t rows,
                      int64_t cols, double eps, const qlora_mx_matrix *Y, void *H, void *stream);

@@ -208,7 +208,7 @@ def test_rmsnorm_in_place_and_special_rows(qb):
 
 
 @pytest.mark.parametrize("residual,w_bf16", [(True, False), (False, True)])
-@pytest.mark.parametrize("rows,cols", NORM_SHAPES + [(2500, 96), (700, 8224)])
+@pytest.mark.parametrize("rows,cols", NORM_SHAPES + [(2500, 96), (700, 8224), (300, 4128), (600, 8160), (520, 20512)])
 def test_rmsnorm_backward(qb, rows, cols, residual, w_bf16):
     import torch
     gu.announce(f"rmsnorm backward {rows}x{cols} residual={residual}")
