@@ -14,10 +14,16 @@
 // copy two steps together and have one barrier for them: 64 bytes of a row are
 // half a cache line, and both halves cross to the compute unit for each (2048 x
 // 22016 x 8192 210 us without it, 201 with; 301 x 4096 x 11008, where few
-// workgroups wait for each other's copies, 25 without, 31 with). Scales come the same way, 16
-// bytes a row (512 elements) every four steps, into two buffers. The matrix
-// instructions of a step's second half run after the next step's
-// barrier: they cover its first LDS reads.
+// workgroups wait for each other's copies, 25 without, 31 with). Scales come
+// the same way into two buffers, SP pieces of 16 bytes of a row (512 elements
+// each) every 4 SP steps: a piece alone costs a whole cache line on its way, so
+// SP is 2 or 4 where the LDS is there (301 x 4096 x 11008 27.3 -> 26.0 us, with
+// a 4-bit X 25.5 -> 23.6). The matrix instructions of a step's second half run
+// after the next step's barrier: they cover its first LDS reads.
+//
+// Bound by the copies and the matrix cores together: 4096^3 with an 8-bit X 55
+// us (2.5 PFLOP/s, the cores 70 % busy; the copies alone 34), 2048 x 22016 x 8192
+// with a 4-bit one 197 us (3.8 PFLOP/s; the copies alone 162).
 //
 // LDS rows are 128 bytes (8-bit codes) or 64 (4-bit), unpadded. Sixteen lanes
 // of a 16-byte read go through the 64 banks at a time, so a row's chunks are

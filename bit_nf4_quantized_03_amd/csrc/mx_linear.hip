@@ -84,7 +84,7 @@ __device__ __forceinline__ bool find_piece(const int32_t *offsets, int experts, 
 // workgroups (512 rows of one expert among 64: 57 us; by the workgroups of its
 // first 16 rows in turn 160).
 //
-// Bound by the weight's bytes: 1 x 11008 x 4096 8.5 us (2.8 TB/s: one load's
+// Bound by the weight's bytes: 1 x 11008 x 4096 8.0 us (3.0 TB/s: one load's
 // round trip for each wave, then the sums), 33 rows over eight 11008 x 4096
 // 39 us (4.6 TB/s), 64 over 64 4096 x 4096 98 us (5.8 TB/s).
 template <int XT, int MT, int RT, int WAVES>
@@ -336,18 +336,26 @@ hipError_t run_tiles(const GemmParams &p, hipStream_t s) {
 }
 
 // Few rows: the matrix core's work does not matter, the weight's stream does.
-// X is read by every workgroup, so from 5 rows on, a workgroup takes 64 rows
-// of W where that leaves half of the compute units one (8 x 11008 x 4096: 8.8
-// us against 10.0 with 16 rows), else 16 (16 x 4096 x 4096: 6.1 against 7.9).
-// By expert 64 rows and half the waves (one row for each of 64 4096 x 4096: 98
-// us, 5.8 TB/s, against 104 with 32 rows of W and 107 with 128; four for each
-// of eight 11008 x 4096: 39.5, 40.4 and 48), a quarter of them where the
-// reduction has no more than two pieces (4096 x 1024, 16 experts of 4 rows: 9.9
-// against 11.2). Returns false where the tiles are faster: from 17 rows on (32
-// x 11008 x 4096 9.3 us against 16) unless there are few of them (32 x 4096 x
-// 4096 9.4 us against 8.1), by expert from 9 rows on average on (64 4096 x 4096:
-// 8 rows 108 to 113 us against 118 with 128 x 64 tiles, 16 rows 126 to 162
-// against 120 to 124).
+// X is read by every workgroup, so a workgroup takes as many rows of W, 64, 32
+// or 16, as leave the compute units about as evenly loaded as the next fewer
+// would (the factors are between what 40000 and 28672, 4096 and 18432 rows of W
+// ask for): `uneven` is the time of the fullest unit over the average (8 rows of X,
+// K = 4096, 64 / 32 / 16 rows of W: N = 4096 8.4, 6.2, 5.7 us; 6144 8.6, 6.5,
+// 7.6; 11008 8.8, 10.2, 10.5; 22016 16.5, 13.9, 17.9). Eight waves share the
+// reduction, four where units have two workgroups or more (32000 17.6 us
+// against 18.9).
+//
+// By expert 64 rows and four waves (one row for each of 64 4096 x 4096: 98 us,
+// 5.8 TB/s, against 104 with 32 rows of W and 107 with 128; four for each of
+// eight 11008 x 4096: 39.5, 40.4 and 48), two where the reduction has no more
+// than two pieces (4096 x 1024, 16 experts of 4 rows: 9.9 against 11.2).
+//
+// Returns false where the tiles are faster (K = 4096, stream against tiles): N
+// = 4096 from 25 rows on (24: 7.4 against 8.2 us, 32: 8.2 each), N = 8192 from
+// 17 (16: 7.5 against 8.4, 24: 9.1 against 8.5), more from 9 (8 x 22016 13.8
+// each, 16 x 22016 16.3 against 14.1), by expert from 9 on average on (64 4096 x
+// 4096: 8 rows 108 to 113 us against 118 with 128 x 64 tiles, 16 rows 126 to
+// 162 against 120 to 124).
 template <int XT>
 bool run_few_rows(const GemvParams &p, hipStream_t s, hipError_t *e) {
   if (p.experts) {
@@ -355,11 +363,15 @@ bool run_few_rows(const GemvParams &p, hipStream_t s, hipError_t *e) {
     *e = p.nblk <= 32 ? run_gemv<XT, 1, 4, 2>(p, s) : run_gemv<XT, 1, 4, 4>(p, s);
     return true;
   }
-  const bool many = p.N >= 64 * 128;
-  if (p.M > 32 || (p.M > 16 && many)) return false;
-  if (p.M > 16) *e = run_gemv<XT, 2, 1, 8>(p, s);
-  else if (p.M > 4 && many) *e = run_gemv<XT, 1, 4, 8>(p, s);
-  else *e = run_gemv<XT, 1, 1, 8>(p, s);
+  const auto uneven = [&](int rows) {
+    const double load = static_cast<double>(ceil_div(p.N, rows)) / kCus;
+    return std::ceil(load) / load;
+  };
+  if (p.M > (p.N <= 16 * kCus ? 24 : p.N <= 32 * kCus ? 16 : 8)) return false;
+  const int rows = p.M > 16 ? 16 : uneven(64) <= 1.15 * uneven(32) ? 64 : uneven(32) <= 1.25 * uneven(16) ? 32 : 16;
+  if (rows == 64) *e = p.N <= 64 * kCus ? run_gemv<XT, 1, 4, 8>(p, s) : run_gemv<XT, 1, 4, 4>(p, s);
+  else if (rows == 32) *e = run_gemv<XT, 1, 2, 8>(p, s);
+  else *e = p.M > 16 ? run_gemv<XT, 2, 1, 8>(p, s) : run_gemv<XT, 1, 1, 8>(p, s);
   return true;
 }
 

@@ -321,6 +321,19 @@ def test_linear(qb, M, N, K, t):
     assert qb.qlora_mx_linear(X, W, out=out) is out and torch.equal(out, Y)
 
 
+# sizes at which each form of the few rows' product is chosen, and their last ones before the tiles
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("M,N,K", [(24, 4096, 544), (25, 4090, 544), (16, 6150, 544), (17, 6150, 96), (5, 8200, 1056), (8, 11000, 544),
+                                   (9, 11000, 544), (3, 18433, 96), (7, 22010, 160), (6, 40001, 96), (8, 33000, 544), (1, 70000, 32)])
+def test_linear_few_rows(qb, M, N, K, t):
+    gu.announce(f"mx linear few rows {M}x{N}x{K} type {t}")
+    X, xv, W, wv, xc, wc = product_data(qb, M, N, K, t, M + N + K)
+    ref, size = mx.linear(xv, wv)
+    got = gu.host_bf16_f32(qb.qlora_mx_linear(X, W)).astype(np.float64)
+    check_product(got, ref, size, K, t)
+    check_sharply(got, xc, wc, t, K)
+
+
 # sizes at which each of the larger tiles is chosen, with whole and ragged rows of Y, one step and several pieces
 @pytest.mark.parametrize("t", TYPES)
 @pytest.mark.parametrize("M,N,K", [(4000, 4090, 160), (4096, 4096, 544), (3900, 4096, 1056), (2040, 4090, 1056), (2048, 4096, 96),
