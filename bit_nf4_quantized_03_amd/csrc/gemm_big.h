@@ -90,10 +90,7 @@ struct DirectRowsT {
       uint32_t o = min(off + static_cast<uint32_t>(i) * bstride, clamp);
       if constexpr (!kOneChunk) o += 16u * static_cast<uint32_t>(prb ^ ((w + kWaves * i) & 3));
       const uint32_t dst = dst0 + static_cast<uint32_t>(i) * (1024u * kWaves);   // block w + W i
-      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
-                   :
-                   : "s"(dst), "v"(o), "s"(p)
-                   : "memory", "m0");
+      lds_copy16(dst, o, p);
     }
   }
   // Wait until the copies issued before the last N vector-memory

@@ -52,6 +52,17 @@ __device__ __forceinline__ uint32_t hi16x2(uint32_t a, uint32_t b) {
   return __builtin_amdgcn_perm(b, a, 0x07060302u);
 }
 
+// 16 (4) bytes per lane from src + off into LDS at dst + 16 (4) lane; dst and
+// src are the same in all lanes. Nothing returns into registers and waits are
+// the caller's. The wait state between the write of M0 and the load that reads
+// it is required and, inside inline assembly, not inserted by the compiler.
+__device__ __forceinline__ void lds_copy16(uint32_t dst, uint32_t off, const void *src) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(dst), "v"(off), "s"(src) : "memory", "m0");
+}
+__device__ __forceinline__ void lds_copy4(uint32_t dst, uint32_t off, const void *src) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" : : "s"(dst), "v"(off), "s"(src) : "memory", "m0");
+}
+
 template <int BM_, int BN_, int WAVES_M_, int WAVES_N_>
 struct TileCfg {
   static constexpr int BM = BM_, BN = BN_;

@@ -220,13 +220,6 @@ __device__ __forceinline__ uint32_t lds_addr(const void *p) {
 // This wave's index, known to the compiler as wave-uniform (scalar).
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)); }
 
-__device__ __forceinline__ void copy16(uint32_t dst, uint32_t off, const void *src) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(dst), "v"(off), "s"(src) : "memory", "m0");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, uint32_t off, const void *src) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" : : "s"(dst), "v"(off), "s"(src) : "memory", "m0");
-}
-
 // A Q tile of 64 fp32 rows of 64 floats, row q of the tile at `row_ptr(q)`
 // plus column offset `col` (floats): 16 blocks of 1 KB (4 rows each); wave w
 // copies blocks w + 4 i, lane L of a block fetching row 4 b + L / 16,
@@ -258,7 +251,7 @@ struct QRowsA {
   __device__ __forceinline__ void issue(int64_t k0, float *stage) const {
     const uint32_t dst0 = lds_addr(stage) + static_cast<uint32_t>(wave_id()) * 1024u;
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i) copy16(dst0 + i * 4096u, off[i], A + static_cast<int64_t>(brow[i]) * K + k0);
+    for (int i = 0; i < kCopies; ++i) lds_copy16(dst0 + i * 4096u, off[i], A + static_cast<int64_t>(brow[i]) * K + k0);
   }
   // Stage [64 j][64 k] fp32 -> operand rows j: units (j, chunk c) of 8 floats.
   __device__ __forceinline__ static void convert(const float *st, __bf16 *qb, int r, int j0) {
@@ -295,13 +288,13 @@ struct QColsB {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int b = w + 4 * i;   // rows 4 b .. 4 b + 3
-        copy16(dst0 + b * 1024u, off, B + (n0 + 4 * b) * r);
+        lds_copy16(dst0 + b * 1024u, off, B + (n0 + 4 * b) * r);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int n = w + 4 * i;
-        copy4(dst0 + n * 256u, off, B + (n0 + n) * r);
+        lds_copy4(dst0 + n * 256u, off, B + (n0 + n) * r);
       }
     }
   }

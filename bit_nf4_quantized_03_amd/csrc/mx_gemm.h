@@ -100,10 +100,7 @@ __device__ __forceinline__ const uint8_t *mx_uniform(const uint8_t *p) {
 // 16 bytes per lane from base + off into LDS at dst + 16 lane. Returns nothing
 // into registers; waits are explicit (mx_wait).
 __device__ __forceinline__ void mx_copy(uint32_t dst, uint32_t off, const uint8_t *base) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" 
-               :
-               : "s"(__builtin_amdgcn_readfirstlane(dst)), "v"(off), "s"(base)
-               : "memory", "m0");
+  lds_copy16(__builtin_amdgcn_readfirstlane(dst), off, base);
 }
 
 // Until at most N vector-memory operations of the wave are in flight.
