@@ -369,6 +369,15 @@ __device__ __forceinline__ bool mx_tile_product(MxAcc<T> &acc, const MxOperands 
   return true;
 }
 
+// Orders the wave's LDS accesses in front of it before those behind it, for
+// data that passes between lanes. The LDS takes a wave's accesses in order, so
+// this holds for the compiler only and costs no instruction.
+__device__ __forceinline__ void mx_wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
 // Y[m][n] = bf16(acc), m < m_end, n < N. Lane l holds row m = l % 32 of a
 // fragment, columns 8 q + 4 (l / 32) + 0 .. 3. Rows whose length is a multiple
 // of eight go through LDS, 32 at a time in a place of the wave's own, and out
@@ -395,6 +404,7 @@ __device__ __forceinline__ void mx_store(const MxAcc<T> &acc, __bf16 *y, int64_t
           *reinterpret_cast<uint2 *>(place + (lane & 31) * T::kStoreRow + 64 * i + 16 * q + 8 * (lane >> 5)) =
               make_uint2(pack_bf16x2(v[4 * q], v[4 * q + 1]), pack_bf16x2(v[4 * q + 2], v[4 * q + 3]));
         }
+      mx_wave_order();
       const int c = lane % kChunks;
       const int64_t n = n0 + 8 * c;
 #pragma unroll
@@ -404,6 +414,7 @@ __device__ __forceinline__ void mx_store(const MxAcc<T> &acc, __bf16 *y, int64_t
         const uint4 v = *reinterpret_cast<const uint4 *>(place + r * T::kStoreRow + 16 * c);
         if (m < m_end && n < N) *reinterpret_cast<uint4 *>(y + m * N + n) = v;
       }
+      mx_wave_order();   // the next rows take the place
     }
   } else {
 #pragma unroll

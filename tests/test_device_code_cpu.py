@@ -6,7 +6,11 @@ the program ("manually inserted wait states" of the CDNA ISA documents): one
 between a scalar write of M0 and a load into LDS, which takes its address from
 it, and five between a vector instruction that writes a scalar register and a
 memory instruction that reads it. The compiler inserts them for instructions of
-its own but not inside inline assembly, which the copies into LDS are."""
+its own but not inside inline assembly, which the copies into LDS are.
+
+Data between lanes. Where lanes of a wave read from LDS what others of the
+wave wrote, the hardware keeps the order, but the compiler may only be relied
+on to where a barrier, if only the wave's own, stands in between."""
 import concurrent.futures
 import glob
 import importlib.util
@@ -51,6 +55,7 @@ def assembly(tmp_path_factory):
 class Kernel:
     def __init__(self):
         self.code, self.labels = [], {}
+        self.barriers = []   # the instructions behind the wave's own barriers
 
     def op(self, k):
         parts = self.code[k].split(None, 1)
@@ -85,9 +90,11 @@ class Kernel:
 
 
 def parse(text):
-    """The functions of an assembly listing."""
+    """The functions of an assembly listing, with the places of the barriers."""
     kernels, cur = {}, None
     for line in text.splitlines():
+        if cur and line.strip() == "; wave barrier":
+            cur.barriers.append(len(cur.code))
         code = line.split(";")[0].rstrip()
         label = re.match(r"([\w.$]+):", code)
         if label and not label[1].startswith(".L"):
@@ -128,6 +135,42 @@ def missing_wait_states(kernel):
             if q is not None:
                 found.append((kernel.code[q], code))
     return found
+
+
+def unordered_exchanges(kernel):
+    """Changes between writing and reading LDS behind the last matrix instruction without a barrier in between."""
+    names = [kernel.op(k)[0] for k in range(len(kernel.code))]
+    start = max((k for k, n in enumerate(names) if n.startswith("v_mfma")), default=0)
+    found, last = [], None
+    for k in range(start, len(names)):
+        if k in kernel.barriers or names[k] == "s_barrier":
+            last = None
+        kind = names[k].startswith(("ds_read", "ds_write")) and names[k][:7]
+        if kind:
+            if last and last != kind:
+                found.append(kernel.code[k])
+            last = kind
+    return found
+
+
+def test_the_check_finds_unordered_exchanges():
+    def found(*lines):
+        return len(unordered_exchanges(parse("\n".join(("f:", "v_mfma_f32 a0, v0, v1, a0") + lines))["f"]))
+    write, read = "ds_write_b64 v0, v[2:3]", "ds_read_b128 v[4:7], v1"
+    assert found(write, write, read, read) == 1
+    assert found(write, read, write, read) == 3
+    assert found(write, "\t; wave barrier", read, "\t; wave barrier", write) == 0
+    assert found(write, "s_barrier", read) == 0
+
+
+def test_rows_through_lds_are_ordered(assembly):
+    """The large microscaled products bring their rows together in LDS before they store them."""
+    kernels = {n: k for n, k in assembly["mx_linear.hip"].items() if "k_mx_gemm" in n and k.code}
+    assert len(kernels) == 20
+    for name, kernel in kernels.items():
+        assert any(c.startswith("ds_write") for c in kernel.code), name
+        found = unordered_exchanges(kernel)
+        assert not found, f"{name}: {len(found)}, first {found[0]}"
 
 
 def test_the_check_finds_missing_wait_states():
