@@ -138,18 +138,21 @@ def missing_wait_states(kernel):
 
 
 def unordered_exchanges(kernel):
-    """Changes between writing and reading LDS behind the last matrix instruction without a barrier in between."""
+    """Changes between writing and reading LDS without a barrier in between, from the first write on behind the last
+    matrix instruction and the workgroup's last barrier. (What is read in front of it, the sums of other groups of
+    waves, lies elsewhere.)"""
     names = [kernel.op(k)[0] for k in range(len(kernel.code))]
-    start = max((k for k, n in enumerate(names) if n.startswith("v_mfma")), default=0)
-    found, last = [], None
+    start = max((k for k, n in enumerate(names) if n.startswith("v_mfma") or n == "s_barrier"), default=0)
+    found, last, wrote = [], None, False
     for k in range(start, len(names)):
-        if k in kernel.barriers or names[k] == "s_barrier":
+        if k in kernel.barriers:
             last = None
         kind = names[k].startswith(("ds_read", "ds_write")) and names[k][:7]
         if kind:
             if last and last != kind:
                 found.append(kernel.code[k])
-            last = kind
+            last = kind if wrote or kind == "ds_writ" else None
+            wrote = wrote or kind == "ds_writ"
     return found
 
 
@@ -160,7 +163,8 @@ def test_the_check_finds_unordered_exchanges():
     assert found(write, write, read, read) == 1
     assert found(write, read, write, read) == 3
     assert found(write, "\t; wave barrier", read, "\t; wave barrier", write) == 0
-    assert found(write, "s_barrier", read) == 0
+    assert found(read, "s_barrier", read, write, read) == 1
+    assert found(write, "s_barrier", read, write, "\t; wave barrier", read) == 0
 
 
 def test_rows_through_lds_are_ordered(assembly):
