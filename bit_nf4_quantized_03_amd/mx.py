@@ -18,8 +18,8 @@ from . import QLORA_BF16, QLORA_F32, QloraError, lib, qlora_last_error
 
 try:
     from . import _fastcall as _fast   # whole calls with new outputs; None where the call is not that simple
-except ImportError as e:
-    raise ImportError("_fastcall.so is missing: build it with `python bit_nf4_quantized_03_amd/build.py`") from e
+except ImportError:
+    _fast = None   # not built, or for another torch: every call has its whole path here too, at 3 to 8 us more host time
 
 __all__ = [
     "MXMatrix", "QLORA_MX_FP4", "QLORA_MX_FP8", "MX_EXPORTED_SYMBOLS", "qlora_mx_scale_pitch",
@@ -79,7 +79,7 @@ _stream, _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 def _fast_on(t):
     """(device index, stream) for a whole call on the current device when ``t``
     lies there, else None."""
-    if isinstance(t, torch.Tensor) and t.is_cuda:
+    if _fast is not None and isinstance(t, torch.Tensor) and t.is_cuda:
         index = t.get_device()
         if index == _current():
             return index, _stream(index)
