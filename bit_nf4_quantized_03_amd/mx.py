@@ -19,7 +19,7 @@ from . import QLORA_BF16, QLORA_F32, QloraError, lib, qlora_last_error
 try:
     from . import _fastcall as _fast   # whole calls with new outputs; None where the call is not that simple
 except ImportError:
-    _fast = None   # not built, or for another torch: every call has its whole path here too, at 3 to 8 us more host time
+    _fast = None   # not built, or for another torch: every call has its whole path here too, at 5 to 8 us more host time
 
 __all__ = [
     "MXMatrix", "QLORA_MX_FP4", "QLORA_MX_FP8", "MX_EXPORTED_SYMBOLS", "qlora_mx_scale_pitch",
@@ -73,7 +73,8 @@ _DTYPES = {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}
 _DTYPES_OR_NONE = (None, torch.float32, torch.bfloat16)
 
 
-_stream, _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# a torch without GPU support lacks them; no call gets as far there
+_stream, _current = (getattr(torch._C, name, None) for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
 
 
 def _fast_on(t):

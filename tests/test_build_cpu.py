@@ -41,6 +41,23 @@ print("fine")
     assert r.returncode == 0 and "fine" in r.stdout, r.stdout + r.stderr
 
 
+def test_import_with_a_torch_for_the_cpu():
+    """Sizes, levels and refusals need no GPU support in torch."""
+    r = _python("""
+import torch
+for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import bit_nf4_quantized_03_amd as qb
+assert qb.qlora_nf4_storage_bytes(64, 64) > 0 and qb.qlora_mx_storage_bytes(3, 64, qb.QLORA_MX_FP8) == 240
+try:
+    qb.qlora_mx_quantize(torch.zeros(4, 64))
+except TypeError as e:
+    print("fine", e)
+""")
+    assert r.returncode == 0 and "fine" in r.stdout, r.stdout + r.stderr
+
+
 def _build_in(tmp_path):
     spec = importlib.util.spec_from_file_location("_build_in", BUILD)
     mod = importlib.util.module_from_spec(spec)
