@@ -540,6 +540,10 @@ def qlora_linear_fwd_noalloc(X, W: NF4Weight, A=None, B=None, scale: float = 0.0
 
 # the microscaled formats, RMSNorm and the microscaled products; the module
 # imports the names above, so it comes last
+from . import mx as _mx  # noqa: E402
+if _mx.lib is not lib:   # this module is being loaded again: so must be the one that took its names
+    import importlib
+    importlib.reload(_mx)
 from .mx import *  # noqa: E402,F401,F403
 from .mx import __all__ as _mx_all  # noqa: E402
 

@@ -58,6 +58,23 @@ except TypeError as e:
     assert r.returncode == 0 and "fine" in r.stdout, r.stdout + r.stderr
 
 
+def test_package_loaded_again():
+    """After a reload, which a build does, the microscaled calls are declared and raise the package's error."""
+    r = _python("""
+import ctypes, importlib
+import bit_nf4_quantized_03_amd as qb
+qb = importlib.reload(qb)
+assert qb.mx.lib is qb.lib and qb.mx.QloraError is qb.QloraError
+assert qb.lib.qlora_mx_storage_bytes.restype is ctypes.c_size_t
+qb.mx._stream, qb.mx._current = lambda index: None, lambda: 0   # no device here
+try:
+    qb.mx._entry("qlora_mx_dequantize")(qb.mx._current(), None, None, 0)
+except qb.QloraError as e:
+    print("fine", e)
+""")
+    assert r.returncode == 0 and "fine" in r.stdout, r.stdout + r.stderr
+
+
 def _build_in(tmp_path):
     spec = importlib.util.spec_from_file_location("_build_in", BUILD)
     mod = importlib.util.module_from_spec(spec)
