@@ -54,7 +54,8 @@ struct MxLinear {
   void *Y;
 };
 constexpr int64_t kMxMaxK = int64_t(1) << 22;
-// What keeps a product's launch below 2^32 threads with every tile.
+// What keeps a product's launch below 2^32 threads, with the weight stream and
+// with the tile that the rule of mx_tiles.h chooses.
 constexpr int64_t kMxMaxRows = int64_t(1) << 24, kMxMaxExpertRows = int64_t(1) << 28, kMxMaxOut = int64_t(1) << 37;
 hipError_t launch_mx_linear(const MxLinear &a, hipStream_t s);
 

@@ -13,6 +13,7 @@
 #include <type_traits>
 
 #include "mx_gemm.h"
+#include "mx_tiles.h"
 
 namespace qnf4 {
 namespace {
@@ -257,81 +258,25 @@ hipError_t run_gemv(const GemvParams &p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <class T>
+template <int TILE, class T>
 hipError_t run_gemm(const GemmParams &p, hipStream_t s) {
-  const int64_t tiles_n = ceil_div(p.N, T::BN);
-  if (p.experts) {
-    // an expert's rows end in at most one partial tile
-    const int64_t most = (p.M / T::BM + p.experts) * tiles_n;
-    k_mx_gemm_grouped<T><<<static_cast<unsigned>(most), T::kThreads, 0, s>>>(p);
-    return hipGetLastError();
-  }
-  k_mx_gemm<T><<<static_cast<unsigned>(ceil_div(p.M, T::BM) * tiles_n), T::kThreads, 0, s>>>(p);
+  static_assert(T::BN == kMxTile[TILE].bn && T::BM == kMxTile[TILE].bm && T::kThreads == kMxTile[TILE].threads, "the rule's tile");
+  const unsigned groups = static_cast<unsigned>(mx_tile_groups(T::BM, T::BN, p.M, p.N, p.experts));
+  if (p.experts) k_mx_gemm_grouped<T><<<groups, T::kThreads, 0, s>>>(p);
+  else k_mx_gemm<T><<<groups, T::kThreads, 0, s>>>(p);
   return hipGetLastError();
-}
-
-// The tiles, and what a step of 128 elements costs with them in us: `light` for
-// a workgroup while few compute units work, `full` on every compute unit (there
-// per workgroup). `shared`: a compute unit holds two workgroups or more. All
-// measured at K = 4096, N = 4096 (first an 8-bit X, then 4 bits).
-//
-// Large tiles re-read their operands less, small ones leave fewer compute units
-// without work, so the tile is chosen by the time that these figures give.
-// Times behind the rule (us, 8-bit X, N = K = 4096; its choice first): 4096
-// rows 256 x 256 54, 256 x 128 61, 128 x 128 66; 2048 rows 256 x 128 32, 128 x
-// 128 35, 256 x 256 43; 1000 rows 128 x 128 19, 128 x 64 23, 256 x 128 24; 301
-// rows 128 x 64 12.3, 128 x 128 15.7, 64 x 64 17.3; 128 rows 64 x 64 9.6, 128 x
-// 64 11.8. The 64 x 64 tile has two groups of waves with half the steps each
-// and four stages: one workgroup fills a compute unit, but it is chosen where
-// there is no second (with three stages, two to a unit, 128 rows 10.3; one
-// group 11.6; 128 x 64 in two groups 12.2).
-constexpr int kTiles = 5;
-constexpr struct {
-  int bn, bm;
-  bool shared;
-  struct {
-    double light, full;
-  } cost[2];
-} kTile[kTiles] = {{256, 256, false, {{1.03, 1.53}, {0.61, 1.05}}},
-                   {256, 128, false, {{0.54, 0.88}, {0.41, 0.64}}},
-                   {128, 128, true, {{0.33, 0.47}, {0.29, 0.36}}},
-                   {128, 64, true, {{0.205, 0.305}, {0.19, 0.25}}},
-                   {64, 64, false, {{0.14, 0.185}, {0.12, 0.165}}}};
-constexpr double kCus = 256;
-
-int choose_tile(int64_t M, int64_t N, int experts, bool fp4) {
-  int best = 0;
-  double least = 0;
-  for (int i = 0; i < kTiles; ++i) {
-    const double tiles_n = static_cast<double>(ceil_div(N, kTile[i].bn));
-    double tiles_m = static_cast<double>(ceil_div(M, kTile[i].bm)), spare = 0;
-    if (experts) {
-      // an expert's rows end in a partial tile, on average half of one; the
-      // counts are on the GPU, and `spare` allows for a few more
-      tiles_m = std::max(static_cast<double>(M) / kTile[i].bm + 0.5 * experts,
-                         static_cast<double>(std::min<int64_t>(M, experts)));
-      spare = 0.1;
-    }
-    const double load = tiles_m * tiles_n / kCus + spare;   // workgroups per compute unit
-    const double light = kTile[i].cost[fp4].light, full = kTile[i].cost[fp4].full;
-    double t;
-    if (load <= 1) t = light + (full - light) * load;
-    else t = full * (kTile[i].shared ? (load + std::ceil(load)) / 2 : std::ceil(load));
-    if (i == 0 || t < least) least = t, best = i;
-  }
-  return best;
 }
 
 template <int XT>
 hipError_t run_tiles(const GemmParams &p, hipStream_t s) {
   constexpr bool kPair = XT == QLORA_MX_FP4;
   constexpr int kDeep = kPair ? 4 : 3;   // stages
-  switch (choose_tile(p.M, p.N, p.experts, XT == QLORA_MX_FP4)) {
-    case 0: return run_gemm<MxTile<XT, 4, 2, 2, 4, kDeep, kPair ? 2 : 1, 1, kPair>>(p, s);
-    case 1: return run_gemm<MxTile<XT, 2, 2, 4, 2, kDeep, kPair ? 2 : 4, 1, kPair>>(p, s);
-    case 2: return run_gemm<MxTile<XT, 2, 2, 2, 2, kDeep, kPair ? 2 : 1, 1, kPair>>(p, s);
-    case 3: return run_gemm<MxTile<XT, 2, 1, 2, 2, 4, 2>>(p, s);
-    default: return run_gemm<MxTile<XT, 1, 1, 2, 2, 4, 4, 2>>(p, s);
+  switch (mx_choose_tile(p.M, p.N, p.experts, XT == QLORA_MX_FP4)) {
+    case 0: return run_gemm<0, MxTile<XT, 4, 2, 2, 4, kDeep, kPair ? 2 : 1, 1, kPair>>(p, s);
+    case 1: return run_gemm<1, MxTile<XT, 2, 2, 4, 2, kDeep, kPair ? 2 : 4, 1, kPair>>(p, s);
+    case 2: return run_gemm<2, MxTile<XT, 2, 2, 2, 2, kDeep, kPair ? 2 : 1, 1, kPair>>(p, s);
+    case 3: return run_gemm<3, MxTile<XT, 2, 1, 2, 2, 4, 2>>(p, s);
+    default: return run_gemm<4, MxTile<XT, 1, 1, 2, 2, 4, 4, 2>>(p, s);
   }
 }
 
@@ -364,12 +309,12 @@ bool run_few_rows(const GemvParams &p, hipStream_t s, hipError_t *e) {
     return true;
   }
   const auto uneven = [&](int rows) {
-    const double load = static_cast<double>(ceil_div(p.N, rows)) / kCus;
+    const double load = static_cast<double>(ceil_div(p.N, rows)) / kMxCus;
     return std::ceil(load) / load;
   };
-  if (p.M > (p.N <= 16 * kCus ? 24 : p.N <= 32 * kCus ? 16 : 8)) return false;
+  if (p.M > (p.N <= 16 * kMxCus ? 24 : p.N <= 32 * kMxCus ? 16 : 8)) return false;
   const int rows = p.M > 16 ? 16 : uneven(64) <= 1.15 * uneven(32) ? 64 : uneven(32) <= 1.25 * uneven(16) ? 32 : 16;
-  if (rows == 64) *e = p.N <= 64 * kCus ? run_gemv<XT, 1, 4, 8>(p, s) : run_gemv<XT, 1, 4, 4>(p, s);
+  if (rows == 64) *e = p.N <= 64 * kMxCus ? run_gemv<XT, 1, 4, 8>(p, s) : run_gemv<XT, 1, 4, 4>(p, s);
   else if (rows == 32) *e = run_gemv<XT, 1, 2, 8>(p, s);
   else *e = p.M > 16 ? run_gemv<XT, 2, 1, 8>(p, s) : run_gemv<XT, 1, 1, 8>(p, s);
   return true;
