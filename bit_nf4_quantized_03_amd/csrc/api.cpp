@@ -141,8 +141,6 @@ int api_fail(int status, const char *fmt, ...) {
   return status;
 }
 
-int api_ok() { return ok(); }
-
 int api_hip_status(hipError_t e, const char *where) { return hip_status(e, where); }
 
 }  // namespace qnf4

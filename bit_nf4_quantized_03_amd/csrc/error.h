@@ -8,8 +8,6 @@ namespace qnf4 {
 
 // Records the formatted message for the calling thread and returns `status`.
 int api_fail(int status, const char *fmt, ...);
-// Clears the thread's message and returns QLORA_OK.
-int api_ok();
 // QLORA_OK, or QLORA_ERR_HIP with the HIP error's name behind `where`.
 int api_hip_status(hipError_t e, const char *where);
 
