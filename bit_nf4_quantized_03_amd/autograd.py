@@ -58,7 +58,12 @@ class RMSNormFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, weight, residual, eps: float):
         flat = X.reshape(-1, X.shape[-1]).contiguous()
-        res = None if residual is None else residual.reshape(flat.shape).contiguous()
+        res = None
+        if residual is not None:
+            if residual.shape[-1:] != X.shape[-1:] or residual.numel() != X.numel():
+                raise ValueError(f"residual must hold the rows of X {tuple(X.shape)}, got {tuple(residual.shape)}")
+            res = residual.reshape(flat.shape).contiguous()
+            ctx.residual_shape = residual.shape
         Y, H, rstd = qlora_rmsnorm_fwd(flat, weight, eps, residual=res)
         ctx.save_for_backward(H, weight, rstd)
         ctx.set_materialize_grads(False)
@@ -72,18 +77,18 @@ class RMSNormFn(torch.autograd.Function):
         H, weight, rstd = ctx.saved_tensors
         with_residual = ctx.needs_input_grad[2]
         if dY is None:   # only H went on, X and the residual take its gradient
-            return dH, None, dH if with_residual else None, None
+            return dH, None, dH.reshape(ctx.residual_shape) if with_residual else None, None
         shape = dY.shape
         dY = dY.reshape(H.shape).contiguous()
         if dH is not None:
             dH = dH.reshape(H.shape).contiguous()
         dX, dW = qlora_rmsnorm_bwd(dY, H, weight, rstd, dH=dH)
         dX = dX.reshape(shape)
-        return dX, dW.to(weight.dtype), dX if with_residual else None, None
+        return dX, dW.to(weight.dtype), dX.reshape(ctx.residual_shape) if with_residual else None, None
 
 
 def rmsnorm(X, weight, residual=None, eps: float = 1e-6):
     """RMSNorm of bf16 X [..., D] with autograd to X, weight [D] (fp32 or bf16)
-    and residual. Without a residual the result is Y; with one it is (Y, H), H =
+    and residual (as many rows of D, in any leading shape). Without a residual the result is Y; with one it is (Y, H), H =
     bf16(X + residual) being the residual stream that goes on."""
     return RMSNormFn.apply(X, weight, residual, float(eps))

@@ -1,0 +1,58 @@
+"""What autograd.rmsnorm does around its two library calls: shapes, strides and
+refusals, with plain torch in the calls' place. Needs no GPU."""
+import pytest
+
+qb = pytest.importorskip("bit_nf4_quantized_03_amd")
+import torch  # noqa: E402
+from bit_nf4_quantized_03_amd import autograd  # noqa: E402
+
+
+def _check(t, shape, dtype=torch.bfloat16):
+    """What the library asks of a tensor."""
+    assert t.shape == shape and t.dtype == dtype and t.is_contiguous()
+
+
+@pytest.fixture(autouse=True)
+def plain_calls(monkeypatch):
+    def fwd(X, weight, eps, residual=None):
+        _check(X, X.shape)
+        if residual is not None:
+            _check(residual, X.shape)
+        h = X if residual is None else (X.float() + residual.float()).bfloat16()
+        rstd = 1 / torch.sqrt(h.float().square().mean(-1) + eps)
+        return (h.float() * rstd[:, None] * weight.float()).bfloat16(), h, rstd
+
+    def bwd(dY, H, weight, rstd, dH=None):
+        _check(dY, H.shape)
+        if dH is not None:
+            _check(dH, H.shape)
+        u, g = H.float() * rstd[:, None], dY.float() * weight.float()
+        dx = rstd[:, None] * (g - u * (g * u).mean(-1, keepdim=True))
+        return (dx if dH is None else dx + dH.float()).bfloat16(), (dY.float() * u).sum(0)
+    monkeypatch.setattr(autograd, "qlora_rmsnorm_fwd", fwd)
+    monkeypatch.setattr(autograd, "qlora_rmsnorm_bwd", bwd)
+
+
+def _leaves(*shapes):
+    torch.manual_seed(1)
+    return [torch.randn(s).bfloat16().requires_grad_(True) for s in shapes]
+
+
+@pytest.mark.parametrize("shape", [(6, 64), (1, 6, 64), (3, 2, 64)])
+@pytest.mark.parametrize("use", ["both", "y", "h"])
+def test_residual_in_another_leading_shape(shape, use):
+    x, r = _leaves((2, 3, 64), shape)
+    w = torch.ones(64)
+    y, h = autograd.rmsnorm(x, w, r)
+    assert y.shape == h.shape == x.shape
+    loss = {"both": lambda: y.float().square().sum() + h.float().sum(), "y": lambda: y.float().square().sum(),
+            "h": lambda: h.float().square().sum()}[use]()
+    loss.backward()
+    assert r.grad.shape == r.shape and torch.equal(r.grad.reshape(x.shape), x.grad)
+
+
+@pytest.mark.parametrize("shape", [(64, 6), (2, 3, 32), (2, 4, 64), (64,), (384,)])
+def test_residual_of_other_rows_is_refused(shape):
+    x, r = _leaves((6, 64), shape)
+    with pytest.raises(ValueError, match="residual"):
+        autograd.rmsnorm(x, torch.ones(64), r)
