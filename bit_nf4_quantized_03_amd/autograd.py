@@ -54,15 +54,23 @@ def qlora_linear(X, W: NF4Weight, A=None, B=None, scale: float = 0.0):
     return QLoRALinearFn.apply(X, A, B, W, float(scale))
 
 
+def _rows(t, cols):
+    """``t`` as contiguous rows of ``cols``, 16-byte aligned as the library
+    takes them: a gradient may be a view that begins anywhere."""
+    t = t.reshape(-1, cols).contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class RMSNormFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, weight, residual, eps: float):
-        flat = X.reshape(-1, X.shape[-1]).contiguous()
+        cols = X.shape[-1]
+        flat = _rows(X, cols)
         res = None
         if residual is not None:
             if residual.shape[-1:] != X.shape[-1:] or residual.numel() != X.numel():
                 raise ValueError(f"residual must hold the rows of X {tuple(X.shape)}, got {tuple(residual.shape)}")
-            res = residual.reshape(flat.shape).contiguous()
+            res = _rows(residual, cols)
             ctx.residual_shape = residual.shape
         Y, H, rstd = qlora_rmsnorm_fwd(flat, weight, eps, residual=res)
         ctx.save_for_backward(H, weight, rstd)
@@ -79,9 +87,9 @@ class RMSNormFn(torch.autograd.Function):
         if dY is None:   # only H went on, X and the residual take its gradient
             return dH, None, dH.reshape(ctx.residual_shape) if with_residual else None, None
         shape = dY.shape
-        dY = dY.reshape(H.shape).contiguous()
+        dY = _rows(dY, H.shape[1])
         if dH is not None:
-            dH = dH.reshape(H.shape).contiguous()
+            dH = _rows(dH, H.shape[1])
         dX, dW = qlora_rmsnorm_bwd(dY, H, weight, rstd, dH=dH)
         dX = dX.reshape(shape)
         return dX, dW.to(weight.dtype), dX.reshape(ctx.residual_shape) if with_residual else None, None

@@ -9,7 +9,7 @@ from bit_nf4_quantized_03_amd import autograd  # noqa: E402
 
 def _check(t, shape, dtype=torch.bfloat16):
     """What the library asks of a tensor."""
-    assert t.shape == shape and t.dtype == dtype and t.is_contiguous()
+    assert t.shape == shape and t.dtype == dtype and t.is_contiguous() and t.data_ptr() % 16 == 0
 
 
 @pytest.fixture(autouse=True)
@@ -56,3 +56,24 @@ def test_residual_of_other_rows_is_refused(shape):
     x, r = _leaves((6, 64), shape)
     with pytest.raises(ValueError, match="residual"):
         autograd.rmsnorm(x, torch.ones(64), r)
+
+
+def _shifted(t):
+    """The same values where they are not 16-byte aligned."""
+    return torch.cat([t.new_zeros(1), t.detach().reshape(-1)])[1:].view(t.shape)
+
+
+def test_views_that_begin_anywhere():
+    """Inputs and gradients that are views into larger tensors, as a split or a concatenation leaves them."""
+    x, r = _leaves((4, 64), (4, 64))
+    dy, dh = (torch.randn(4, 64).bfloat16() for _ in range(2))
+    w = torch.rand(64) + 0.5
+    torch.autograd.backward(autograd.rmsnorm(x, w, r), [dy, dh])
+    x2, r2 = (_shifted(t).requires_grad_(True) for t in (x, r))
+    assert x2.data_ptr() % 16 and x2.is_contiguous()
+    torch.autograd.backward(autograd.rmsnorm(x2, w, r2), [_shifted(dy), _shifted(dh)])
+    assert torch.equal(x2.grad, x.grad) and torch.equal(r2.grad, r.grad)
+    x3 = x.detach().clone().requires_grad_(True)
+    y = autograd.rmsnorm(x3, w, r.detach())[0]
+    torch.cat([torch.zeros(1).bfloat16(), y.reshape(-1)]).float().square().sum().backward()   # its gradient begins 2 bytes on
+    assert x3.grad.shape == x3.shape
