@@ -9,6 +9,8 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <optional>
+
 #include <ATen/ATen.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -99,9 +101,11 @@ struct Norm {
     if (a[3] != Py_None) {
       res = tensor(a[3], at::kBFloat16, dev);
       if (!res || !is(*res, rows, cols)) return false;
-      h = fresh(*x, {rows, cols}, at::kBFloat16);
     }
     return true;
+  }
+  void new_h() {
+    if (res) h = fresh(*x, {rows, cols}, at::kBFloat16);
   }
   const void *residual() const { return res ? res->data_ptr() : nullptr; }
   void *h_ptr() const { return res ? h.data_ptr() : nullptr; }
@@ -112,6 +116,18 @@ struct Norm {
     return x_object;
   }
 };
+
+// f() without the interpreter's lock, which other threads get while an
+// allocation or a launch waits for the GPU. (The caller keeps the tensors.)
+struct Unlocked {
+  PyThreadState *state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <class F>
+int unlocked(F f) {
+  Unlocked u;
+  return f();
+}
 
 // Each function: (device, stream, ...) -> result or None.
 template <class F>
@@ -136,9 +152,14 @@ PyObject *quantize(PyObject *, PyObject *const *a, Py_ssize_t n) {   // X, mx
       return none();
     }
     if (!x || x->dim() != 2 || !valid(x->size(0), x->size(1), mx)) return none();
-    NewMatrix q(*x, x->size(0), x->size(1), mx);
-    if (qlora_mx_quantize(x->data_ptr(), dt, q.m.rows, q.m.cols, &q.m, stream_of(a[1])) != QLORA_OK) return none();
-    return pack({wrap(std::move(q.codes)), wrap(std::move(q.scales))});
+    void *stream = stream_of(a[1]);
+    std::optional<NewMatrix> q;
+    const int status = unlocked([&] {
+      q.emplace(*x, x->size(0), x->size(1), mx);
+      return qlora_mx_quantize(x->data_ptr(), dt, q->m.rows, q->m.cols, &q->m, stream);
+    });
+    if (status != QLORA_OK) return none();
+    return pack({wrap(std::move(q->codes)), wrap(std::move(q->scales))});
   });
 }
 
@@ -149,8 +170,13 @@ PyObject *dequantize(PyObject *, PyObject *const *a, Py_ssize_t n) {   // codes,
     const Tensor *codes;
     if (!matrix(a + 2, static_cast<int>(PyLong_AsLong(a[0])), &m, &codes)) return none();
     const bool bf16 = a[7] == Py_True;
-    Tensor out = fresh(*codes, {m.rows, m.cols}, bf16 ? at::kBFloat16 : at::kFloat);
-    if (qlora_mx_dequantize(&m, out.data_ptr(), bf16 ? QLORA_BF16 : QLORA_F32, stream_of(a[1])) != QLORA_OK) return none();
+    void *stream = stream_of(a[1]);
+    Tensor out;
+    const int status = unlocked([&] {
+      out = fresh(*codes, {m.rows, m.cols}, bf16 ? at::kBFloat16 : at::kFloat);
+      return qlora_mx_dequantize(&m, out.data_ptr(), bf16 ? QLORA_BF16 : QLORA_F32, stream);
+    });
+    if (status != QLORA_OK) return none();
     return wrap(std::move(out));
   });
 }
@@ -165,11 +191,15 @@ PyObject *norm_mx(PyObject *, PyObject *const *a, Py_ssize_t n) {   // X, weight
       return none();
     }
     if (!valid(p.rows, p.cols, mx)) return none();
-    NewMatrix q(*p.x, p.rows, p.cols, mx);
-    if (qlora_rmsnorm_mx(p.x->data_ptr(), p.residual(), p.w->data_ptr(), p.w_dtype, p.rows, p.cols, p.eps, &q.m, p.h_ptr(),
-                         stream_of(a[1])) != QLORA_OK)
-      return none();
-    return pack({wrap(std::move(q.codes)), wrap(std::move(q.scales)), p.h_object(a[2])});
+    void *stream = stream_of(a[1]);
+    std::optional<NewMatrix> q;
+    const int status = unlocked([&] {
+      q.emplace(*p.x, p.rows, p.cols, mx);
+      p.new_h();
+      return qlora_rmsnorm_mx(p.x->data_ptr(), p.residual(), p.w->data_ptr(), p.w_dtype, p.rows, p.cols, p.eps, &q->m, p.h_ptr(), stream);
+    });
+    if (status != QLORA_OK) return none();
+    return pack({wrap(std::move(q->codes)), wrap(std::move(q->scales)), p.h_object(a[2])});
   });
 }
 
@@ -177,10 +207,15 @@ PyObject *norm_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {   // X, weigh
   return guarded([&]() -> PyObject * {
     Norm p;
     if (n != 6 || !p.read(a + 2, static_cast<int>(PyLong_AsLong(a[0])))) return none();
-    Tensor y = fresh(*p.x, {p.rows, p.cols}, at::kBFloat16), rstd = fresh(*p.x, {p.rows}, at::kFloat);
-    if (qlora_rmsnorm_fwd(p.x->data_ptr(), p.residual(), p.w->data_ptr(), p.w_dtype, p.rows, p.cols, p.eps, y.data_ptr(), p.h_ptr(),
-                          static_cast<float *>(rstd.data_ptr()), stream_of(a[1])) != QLORA_OK)
-      return none();
+    void *stream = stream_of(a[1]);
+    Tensor y, rstd;
+    const int status = unlocked([&] {
+      y = fresh(*p.x, {p.rows, p.cols}, at::kBFloat16), rstd = fresh(*p.x, {p.rows}, at::kFloat);
+      p.new_h();
+      return qlora_rmsnorm_fwd(p.x->data_ptr(), p.residual(), p.w->data_ptr(), p.w_dtype, p.rows, p.cols, p.eps, y.data_ptr(), p.h_ptr(),
+                               static_cast<float *>(rstd.data_ptr()), stream);
+    });
+    if (status != QLORA_OK) return none();
     return pack({wrap(std::move(y)), p.h_object(a[2]), wrap(std::move(rstd))});
   });
 }
@@ -197,13 +232,18 @@ PyObject *norm_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {   // dY, H, w
     const int64_t rows = h->size(0), cols = h->size(1);
     if (!is(*dy, rows, cols) || w->dim() != 1 || w->size(0) != cols || rstd->dim() != 1 || rstd->size(0) != rows || (dh && !is(*dh, rows, cols)))
       return none();
-    Tensor dx = fresh(*h, {rows, cols}, at::kBFloat16), dw = fresh(*h, {cols}, at::kFloat), ws;
-    const size_t size = qlora_rmsnorm_bwd_workspace_bytes(rows, cols);
-    if (size) ws = fresh(*h, {static_cast<int64_t>(size)}, at::kByte);
-    if (qlora_rmsnorm_bwd(dy->data_ptr(), h->data_ptr(), w->data_ptr(), dt, static_cast<const float *>(rstd->data_ptr()),
-                          dh ? dh->data_ptr() : nullptr, rows, cols, dx.data_ptr(), static_cast<float *>(dw.data_ptr()),
-                          size ? ws.data_ptr() : nullptr, size, stream_of(a[1])) != QLORA_OK)
-      return none();
+    void *stream = stream_of(a[1]);
+    Tensor dx, dw;
+    const int status = unlocked([&] {
+      dx = fresh(*h, {rows, cols}, at::kBFloat16), dw = fresh(*h, {cols}, at::kFloat);
+      Tensor ws;
+      const size_t size = qlora_rmsnorm_bwd_workspace_bytes(rows, cols);
+      if (size) ws = fresh(*h, {static_cast<int64_t>(size)}, at::kByte);
+      return qlora_rmsnorm_bwd(dy->data_ptr(), h->data_ptr(), w->data_ptr(), dt, static_cast<const float *>(rstd->data_ptr()),
+                               dh ? dh->data_ptr() : nullptr, rows, cols, dx.data_ptr(), static_cast<float *>(dw.data_ptr()),
+                               size ? ws.data_ptr() : nullptr, size, stream);
+    });
+    if (status != QLORA_OK) return none();
     return pack({wrap(std::move(dx)), wrap(std::move(dw))});
   });
 }
@@ -215,8 +255,13 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n) {   // X's five, 
     qlora_mx_matrix x, w;
     const Tensor *xc, *wc;
     if (!matrix(a + 2, dev, &x, &xc) || !matrix(a + 7, dev, &w, &wc) || x.cols != w.cols) return none();
-    Tensor y = fresh(*xc, {x.rows, w.rows}, at::kBFloat16);
-    if (qlora_mx_linear(&x, &w, y.data_ptr(), stream_of(a[1])) != QLORA_OK) return none();
+    void *stream = stream_of(a[1]);
+    Tensor y;
+    const int status = unlocked([&] {
+      y = fresh(*xc, {x.rows, w.rows}, at::kBFloat16);
+      return qlora_mx_linear(&x, &w, y.data_ptr(), stream);
+    });
+    if (status != QLORA_OK) return none();
     return wrap(std::move(y));
   });
 }

@@ -150,3 +150,61 @@ def test_autograd_norm_of_views(qb):  # noqa: F811
     turned = run(lambda t: t.t().contiguous().t())
     for got in (shifted, turned):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+_WAITING = """
+import sys, threading, time, torch
+import bit_nf4_quantized_03_amd as qb
+import bit_nf4_quantized_03_amd.mx as binding
+assert binding._fast is not None
+x, res, dy = (torch.randn(64, 512, device="cuda").bfloat16() for _ in range(3))
+g = torch.ones(512, device="cuda")
+q = qb.qlora_mx_quantize(x)
+y, h, rstd = qb.qlora_rmsnorm_fwd(x, g, residual=res)
+calls = {
+    "quantize": lambda: qb.qlora_mx_quantize(x), "dequantize": lambda: qb.qlora_mx_dequantize(q), "linear": lambda: qb.qlora_mx_linear(q, q),
+    "norm": lambda: qb.qlora_rmsnorm_fwd(x, g, residual=res), "norm mx": lambda: qb.qlora_rmsnorm_mx(x, g, residual=res),
+    "backward": lambda: qb.qlora_rmsnorm_bwd(dy, h, g, rstd)}
+for f in calls.values():
+    f()
+torch.cuda.synchronize()
+a = time.perf_counter()
+torch.cuda._sleep(1 << 22)
+torch.cuda.synchronize()
+cycles = int((1 << 22) * 0.2 / (time.perf_counter() - a))   # of a fifth of a second at the most
+print(f"{cycles} cycles", flush=True)
+ticks = []
+def count():
+    while True:
+        ticks.append(time.perf_counter())
+        time.sleep(0.0005)
+threading.Thread(target=count, daemon=True).start()
+for name, f in calls.items():
+    busy = threading.Thread(target=torch.cuda._sleep, args=(cycles,), daemon=True)   # on this thread's stream, the default one
+    busy.start()
+    time.sleep(0.02)
+    a = time.perf_counter()
+    f()
+    b = time.perf_counter()
+    busy.join()
+    torch.cuda.synchronize()
+    inside = [a] + [v for v in ticks if a < v < b] + [b]
+    gap = max(q - p for p, q in zip(inside, inside[1:]))
+    print(f"{name}: waited {(b - a) * 1e3:.1f} ms, the other thread at most {gap * 1e3:.1f}", flush=True)
+    assert b - a > 0.02, "the call does not wait"
+    assert gap < 0.5 * (b - a), name
+print("all fine", flush=True)
+"""
+
+
+def test_other_threads_run_while_a_call_waits(qb):  # noqa: F811
+    """Where launches wait for their kernel (a process with AMD_SERIALIZE_KERNEL=3) and a thread keeps the stream busy,
+    a third thread of the program goes on while a call waits."""
+    import os
+    import subprocess
+    import sys
+    gu.announce("calls that wait, in a process of their own")
+    r = subprocess.run([sys.executable, "-u", "-c", _WAITING], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       env=dict(os.environ, AMD_SERIALIZE_KERNEL="3"), capture_output=True, text=True, timeout=40)
+    print(r.stdout)
+    assert r.returncode == 0 and "all fine" in r.stdout, r.stdout + r.stderr
