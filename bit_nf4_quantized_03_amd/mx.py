@@ -268,7 +268,8 @@ def _norm_inputs(X, weight, residual, h):
 def qlora_rmsnorm_fwd(X, weight, eps: float = 1e-6, residual=None, out=None, h=None, rstd=None):
     """(Y, H, rstd): Y = H * rstd * weight in bf16 with H = bf16(X + residual),
     rstd = 1 / sqrt(mean(H^2) + eps) fp32 [rows]. Without a residual H is X
-    itself. ``h`` may be X or ``residual`` (in place)."""
+    itself, or None where ``out`` is X and has taken its place. ``h`` may be X or
+    ``residual`` (in place)."""
     if out is None and h is None and rstd is None and (at := _fast_on(X)):
         new = _fast.norm_fwd(*at, X, weight, eps, residual)
         if new is not None:
@@ -283,7 +284,9 @@ def qlora_rmsnorm_fwd(X, weight, eps: float = 1e-6, residual=None, out=None, h=N
     else:
         _tensor("rstd", rstd, torch.float32, (rows,), index)
     _rmsnorm_fwd(index, *args, float(eps), out.data_ptr(), _at(h), rstd.data_ptr())
-    return out, X if h is None else h, rstd
+    if h is None and out.data_ptr() != X.data_ptr():
+        h = X
+    return out, h, rstd
 
 
 def qlora_rmsnorm_mx(X, weight, eps: float = 1e-6, residual=None, mx: Optional[int] = None,

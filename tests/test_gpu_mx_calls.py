@@ -152,6 +152,22 @@ def test_autograd_norm_of_views(qb):  # noqa: F811
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_norm_over_its_input_has_no_h(qb):  # noqa: F811
+    """Without a residual H is X; where the output takes X's place there is none, and the backward refuses that."""
+    import torch
+    gu.announce("rmsnorm over its input")
+    x, g = torch.randn(5, 96, device="cuda").bfloat16(), torch.rand(96, device="cuda") + 0.5
+    y, h, rstd = qb.qlora_rmsnorm_fwd(x, g)
+    assert h is x
+    z = x.clone()
+    y2, h2, rstd2 = qb.qlora_rmsnorm_fwd(z, g, out=z)
+    assert y2 is z and torch.equal(y2, y) and torch.equal(rstd2, rstd) and h2 is None
+    with pytest.raises(TypeError):
+        qb.qlora_rmsnorm_bwd(y, h2, g, rstd2)
+    y3, h3, _ = qb.qlora_rmsnorm_fwd(x, g, out=torch.empty_like(x))
+    assert h3 is x and torch.equal(y3, y)
+
+
 _WAITING = """
 import sys, threading, time, torch
 import bit_nf4_quantized_03_amd as qb
