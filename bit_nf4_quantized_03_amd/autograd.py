@@ -15,6 +15,10 @@ Tensors: X bf16 [M, K] (any leading shape, flattened to M rows), A fp32
 
 ``rmsnorm`` is the norm in front of the projections, with the residual's
 addition: one ``qlora_rmsnorm_fwd`` call and one ``qlora_rmsnorm_bwd`` call.
+
+A backward pass may be captured into a HIP graph. As with any of torch's, no
+eager graph of the same leaves may be alive then: its gradient accumulation
+belongs to another stream, and torch ends the process.
 """
 from __future__ import annotations
 

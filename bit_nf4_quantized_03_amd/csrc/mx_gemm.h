@@ -21,16 +21,19 @@
 // a 4-bit X 25.5 -> 23.6). The matrix instructions of a step's second half run
 // after the next step's barrier: they cover its first LDS reads.
 //
-// Bound by the copies and the matrix cores together: 4096^3 with an 8-bit X 55
-// us (2.5 PFLOP/s, the cores 70 % busy; the copies alone 34), 2048 x 22016 x 8192
-// with a 4-bit one 197 us (3.8 PFLOP/s; the copies alone 162).
+// Bound by the copies and the matrix cores together: 4096^3 with an 8-bit X 52
+// to 55 us (2.5 PFLOP/s, the cores 69 % busy), 2048 x 22016 x 8192 with a 4-bit
+// one 183 to 193 (3.8 to 4.0 PFLOP/s, 56 %). The copies alone, with the matrix
+// instructions left out of builds that took 57 and 204 us: 34 and 162.
 //
 // LDS rows are 128 bytes (8-bit codes) or 64 (4-bit), unpadded. Sixteen lanes
 // of a 16-byte read go through the 64 banks at a time, so a row's chunks are
 // swapped by an exclusive or with row / 2 (128 bytes) or row / 4 (64 bytes):
 // sixteen consecutive rows read at one chunk then lie on all banks. (With the
-// row itself in the exclusive or, half of the LDS's cycles were conflicts.) A
-// copy fetches the chunk that belongs at its lane's place.
+// row itself in the exclusive or, half of the LDS's cycles were conflicts. The
+// counters still call 31 to 39 % of them that, about 42 cycles of a wave's step
+// with either type of X; which reads they belong to is not known.) A copy
+// fetches the chunk that belongs at its lane's place.
 //
 // Behind the end of K the last step re-reads chunks of the same rows; their
 // scale bytes are the pad bytes 0 of both operands, 2^-254 together, which

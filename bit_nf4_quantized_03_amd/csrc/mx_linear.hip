@@ -85,9 +85,10 @@ __device__ __forceinline__ bool find_piece(const int32_t *offsets, int experts, 
 // workgroups (512 rows of one expert among 64: 57 us; by the workgroups of its
 // first 16 rows in turn 160).
 //
-// Bound by the weight's bytes: 1 x 11008 x 4096 8.0 us (3.0 TB/s: one load's
+// Bound by the weight's bytes: 1 x 11008 x 4096 8.2 us (2.9 TB/s: one load's
 // round trip for each wave, then the sums), 33 rows over eight 11008 x 4096
-// 39 us (4.6 TB/s), 64 over 64 4096 x 4096 98 us (5.8 TB/s).
+// 32 us (5.5 TB/s of the weights that have a row), 64 over 64 4096 x 4096 98 us
+// (5.8 TB/s).
 template <int XT, int MT, int RT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_mx_gemv(const GemvParams p) {
   __shared__ float part[WAVES][MT][RT][16][17];

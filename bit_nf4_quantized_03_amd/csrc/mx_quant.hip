@@ -6,8 +6,8 @@
 // away; blocks never cross a row, so the matrix is walked as one run of
 // rows * cols / 32 blocks and only the address of the scale byte asks for the
 // row. Four loads a lane are in flight. Bound by memory: 22016 x 8192 between
-// bf16 and 4 bits 74.8 us there and 70.7 back, 6.1 and 6.5 TB/s; 37 x 11008 and 8
-// bits 3.5 and 2.7 us, a launch and one round trip.
+// bf16 and 4 bits 74.2 us there and 71.8 back, 6.2 and 6.4 TB/s; 37 x 11008 and 8
+// bits 3.5 and 2.8 us, a launch and one round trip.
 #include "mx_device.h"
 
 namespace qnf4 {

@@ -111,8 +111,9 @@ __device__ __forceinline__ F row_sum(F v, F *part) {
 
 // A workgroup of THREADS takes R = THREADS / T rows, T threads to a row with up
 // to NV runs of eight elements each. Bound by memory for many rows (4096 x 4096
-// with residual 25.8 us into bf16, 5.2 TB/s, 27.8 into 8 bits, 4.2), by the
-// round trip of its loads and the sum for a few (1 x 4096 2.8 us).
+// with residual 25.3 us into bf16, 5.3 TB/s, 26.7 into 8 bits, 4.4), by the
+// round trip of its loads and the sum for a few (1 x 4096 2.8 us). These are
+// times of the kernel alone; those of two forms below are of calls in a row.
 template <int T, int THREADS, int NV, int OUT>
 __global__ __launch_bounds__(THREADS) void k_rms_fwd(const FwdParams p) {
   __shared__ double part[THREADS / 64];
@@ -206,11 +207,11 @@ struct BwdParams {
 // further on for a grid of G. A thread keeps the sums of dy u of its columns
 // over its rows; the R sums of a column are added in order through LDS, so that
 // a workgroup writes one row of partial sums. Bound by memory: 4096 x 4096 with
-// dh 28 us with the sums of k_rms_dw, 6.0 TB/s of the 168 MB that the rows
-// are. Where the registers are there, the next rows' loads are under way while
-// the current ones are worked on, and the weights stay in registers (loaded
-// again twice a row they were more bytes than the row: 4096 x 4096 32 us, 4096
-// x 8192 58 against 49).
+// dh 25.0 us, 5.4 TB/s of the 134 MB that the rows are, and 4.5 for k_rms_dw.
+// Where the registers are there, the next rows' loads are under way while the
+// current ones are worked on, and the weights stay in registers (loaded again
+// twice a row they were more bytes than the row; calls in a row, both kernels:
+// 4096 x 4096 32 us against 28, 4096 x 8192 58 against 49). 300 x 24576: 29.0 us.
 template <int T, int THREADS, int NV>
 __global__ __launch_bounds__(THREADS) void k_rms_bwd(const BwdParams p) {
   constexpr int R = THREADS / T;
@@ -270,7 +271,8 @@ __global__ __launch_bounds__(THREADS) void k_rms_bwd(const BwdParams p) {
     if (!live) continue;
     if (!kKeep) {
       // the row stays packed: without this the compiler keeps it as fp32 for
-      // the second use and spills (300 x 24576 65 us)
+      // the second use and spills most of it (300 x 24576, both kernels, 65 us
+      // against 35; six registers of 1024 threads' 128 are still spilled)
 #pragma unroll
       for (int i = 0; i < NV; ++i) asm volatile("" : "+v"(dy[i]), "+v"(h[i]));
     }
@@ -399,8 +401,8 @@ hipError_t launch_rms_fwd(const RmsFwd &a, hipStream_t s) {
   p.eps = a.eps;
   p.inv_cols = 1.0 / static_cast<double>(a.cols);
   const int out = a.codes ? a.type : kOutBf16;
-  // Few rows: the most threads to a row (1 x 4096 3.3 us against 3.8 with 256).
-  // Many: 256 threads of two or four runs keep more loads in flight (777 x 8192
+  // Few rows: the most threads to a row (1 x 4096, calls in a row, 3.3 us
+  // against 3.8 with 256). Many: 256 threads of two or four runs keep more loads in flight (777 x 8192
   // into 8 bits without a residual 10.1 us against 10.8).
   const bool few = a.rows < 512;
   if (a.cols <= 512) return fwd_run<64, 256, 1>(p, out, s);
