@@ -65,6 +65,13 @@ def _rows(t, cols):
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
+def _second_grad(t, shape):
+    """``t``, already the gradient of X, as that of a residual of this shape. The
+    same tensor, which torch copies for one of the two, or a copy: a view of it
+    would leave both leaves with one gradient's memory."""
+    return t if t.shape == shape else t.reshape(shape).clone()
+
+
 class RMSNormFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, weight, residual, eps: float):
@@ -89,18 +96,19 @@ class RMSNormFn(torch.autograd.Function):
         H, weight, rstd = ctx.saved_tensors
         with_residual = ctx.needs_input_grad[2]
         if dY is None:   # only H went on, X and the residual take its gradient
-            return dH, None, dH.reshape(ctx.residual_shape) if with_residual else None, None
+            return dH, None, _second_grad(dH, ctx.residual_shape) if with_residual else None, None
         shape = dY.shape
         dY = _rows(dY, H.shape[1])
         if dH is not None:
             dH = _rows(dH, H.shape[1])
         dX, dW = qlora_rmsnorm_bwd(dY, H, weight, rstd, dH=dH)
         dX = dX.reshape(shape)
-        return dX, dW.to(weight.dtype), dX.reshape(ctx.residual_shape) if with_residual else None, None
+        return dX, dW.to(weight.dtype), _second_grad(dX, ctx.residual_shape) if with_residual else None, None
 
 
 def rmsnorm(X, weight, residual=None, eps: float = 1e-6):
     """RMSNorm of bf16 X [..., D] with autograd to X, weight [D] (fp32 or bf16)
-    and residual (as many rows of D, in any leading shape). Without a residual the result is Y; with one it is (Y, H), H =
-    bf16(X + residual) being the residual stream that goes on."""
+    and residual (as many rows of D, in any leading shape). Without a residual
+    the result is Y; with one it is (Y, H), H = bf16(X + residual) being the
+    residual stream that goes on."""
     return RMSNormFn.apply(X, weight, residual, float(eps))

@@ -77,3 +77,24 @@ def test_views_that_begin_anywhere():
     y = autograd.rmsnorm(x3, w, r.detach())[0]
     torch.cat([torch.zeros(1).bfloat16(), y.reshape(-1)]).float().square().sum().backward()   # its gradient begins 2 bytes on
     assert x3.grad.shape == x3.shape
+
+
+@pytest.mark.parametrize("shape", [(2, 3, 64), (6, 64), (1, 6, 64)])
+@pytest.mark.parametrize("use", ["both", "y", "h"])
+def test_gradients_have_memory_of_their_own(shape, use):
+    """What is added to one leaf's gradient later does not reach the other's."""
+    x, r = _leaves((2, 3, 64), shape)
+    for turn in (1, 2):
+        y, h = autograd.rmsnorm(x, torch.ones(64), r)
+        dy = torch.ones_like(y) if use != "h" else None
+        dh = torch.ones_like(h) if use != "y" else None
+        torch.autograd.backward([t for t, d in ((y, dy), (h, dh)) if d is not None], [d for d in (dy, dh) if d is not None])
+        if turn == 1:
+            first = x.grad.clone()
+            assert x.grad.untyped_storage().data_ptr() != r.grad.untyped_storage().data_ptr()
+    assert torch.equal(x.grad, 2 * first) and torch.equal(r.grad.reshape(x.shape), 2 * first)
+    # gradients that nobody else holds
+    x.grad = r.grad = None
+    y, h = autograd.rmsnorm(x, torch.ones(64), r)
+    ((y.float().square().sum() if use != "h" else 0) + (h.float().square().sum() if use != "y" else 0)).backward()
+    assert x.grad.untyped_storage().data_ptr() != r.grad.untyped_storage().data_ptr()

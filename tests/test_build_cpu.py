@@ -10,12 +10,15 @@ import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 BUILD = os.path.join(ROOT, "bit_nf4_quantized_03_amd", "build.py")
+built = pytest.mark.skipif(not os.path.exists(os.path.join(ROOT, "bit_nf4_quantized_03_amd", "libqlora_nf4.so")),
+                           reason="the library is not built")
 
 
 def _python(code):
     return subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
 
 
+@built
 def test_import_without_fastcall():
     r = _python("""
 import sys
@@ -41,6 +44,7 @@ print("fine")
     assert r.returncode == 0 and "fine" in r.stdout, r.stdout + r.stderr
 
 
+@built
 def test_import_with_a_torch_for_the_cpu():
     """Sizes, levels and refusals need no GPU support in torch."""
     r = _python("""
@@ -58,6 +62,7 @@ except TypeError as e:
     assert r.returncode == 0 and "fine" in r.stdout, r.stdout + r.stderr
 
 
+@built
 def test_package_loaded_again():
     """After a reload, which a build does, the microscaled calls are declared and raise the package's error."""
     r = _python("""
@@ -112,6 +117,7 @@ def test_library_that_does_not_compile_is_an_error(tmp_path, monkeypatch):
         mod.build()
 
 
+@built
 @pytest.mark.skipif(shutil.which("g++") is None, reason="no host compiler")
 def test_fastcall_is_built_where_it_can_be():
     assert os.path.exists(os.path.join(ROOT, "bit_nf4_quantized_03_amd", "_fastcall.so"))
