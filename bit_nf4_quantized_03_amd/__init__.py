@@ -547,4 +547,12 @@ if _mx.lib is not lib:   # this module is being loaded again: so must be the one
 from .mx import *  # noqa: E402,F401,F403
 from .mx import __all__ as _mx_all  # noqa: E402
 
-__all__ += _mx_all
+# what stands between the projections; it imports the names above
+from . import block as _block  # noqa: E402
+if _block.lib is not lib:
+    import importlib
+    importlib.reload(_block)
+from .block import *  # noqa: E402,F401,F403
+from .block import __all__ as _block_all  # noqa: E402
+
+__all__ += _mx_all + _block_all

@@ -1,0 +1,204 @@
+"""Python binding of what stands between a decoder layer's projections
+(include/qlora_block.h): the gated feed-forward product and rotary positions.
+
+As in the package itself, the functions carry the names of the C entry points
+and only marshal arguments: torch supplies device memory and the current
+stream of the tensors' device. They are re-exported by the package.
+"""
+from __future__ import annotations
+
+import ctypes
+from ctypes import byref
+from typing import Optional, Tuple
+
+import torch
+
+from . import QLORA_BF16, QLORA_F32, QloraError, lib, qlora_last_error
+from .mx import (_DTYPES, _MX, MXMatrix, QLORA_MX_FP4, QLORA_MX_FP8, _empty, _entry, _tensor)
+
+__all__ = [
+    "BLOCK_EXPORTED_SYMBOLS", "QLORA_ROPE_PLAIN", "QLORA_ROPE_LINEAR", "QLORA_ROPE_NTK", "QLORA_ROPE_PARTS",
+    "qlora_mx_pair", "qlora_mx_gated", "qlora_mx_gated_grouped", "qlora_rope_freqs", "qlora_rope_fwd",
+    "qlora_rope_bwd",
+]
+
+BLOCK_EXPORTED_SYMBOLS = (
+    "qlora_mx_pair", "qlora_mx_gated", "qlora_mx_gated_grouped", "qlora_rope_freqs", "qlora_rope_fwd",
+    "qlora_rope_bwd",
+)
+
+QLORA_ROPE_PLAIN = 0    # the frequencies as they are
+QLORA_ROPE_LINEAR = 1   # positions pressed together
+QLORA_ROPE_NTK = 2      # a larger base
+QLORA_ROPE_PARTS = 3    # by parts: fast pairs as they are, slow ones pressed together
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("inp", ctypes.c_void_p), ("out", ctypes.c_void_p)] + \
+        [(name, ctypes.c_int64) for name in ("heads", "in_row", "in_head", "out_row", "out_head")]
+
+
+def _declare():
+    i64, vp, i32, f64, ci = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32, ctypes.c_double, ctypes.c_int
+    mp, hp, dp = ctypes.POINTER(_MX), ctypes.POINTER(_Heads), ctypes.POINTER(ctypes.c_double)
+    rope = [hp, hp, ci, i64, i32, i32, vp, i32, vp, f64, i32, vp]
+    sigs = {
+        "qlora_mx_pair": (ci, [mp, mp, mp, vp]),
+        "qlora_mx_gated": (ci, [mp, mp, vp, mp, vp]),
+        "qlora_mx_gated_grouped": (ci, [mp, mp, vp, i32, vp, mp, vp]),
+        "qlora_rope_freqs": (ci, [i32, f64, i32, f64, i64, f64, f64, dp, dp]),
+        "qlora_rope_fwd": (ci, rope),
+        "qlora_rope_bwd": (ci, rope),
+    }
+    for name, (res, args) in sigs.items():
+        fn = getattr(lib, name)
+        fn.restype = res
+        fn.argtypes = args
+
+
+_declare()
+
+_pair, _gated, _gated_grouped = _entry("qlora_mx_pair"), _entry("qlora_mx_gated"), _entry("qlora_mx_gated_grouped")
+_rope_fwd, _rope_bwd = _entry("qlora_rope_fwd"), _entry("qlora_rope_bwd")
+
+
+def qlora_mx_pair(gate: MXMatrix, up: MXMatrix, out: Optional[MXMatrix] = None) -> MXMatrix:
+    """The pair [2 N, K] of two 4-bit weights [N, K], N a multiple of 8, that
+    qlora_mx_gated reads: eight rows of each in turn."""
+    sg = gate.c_struct("gate")
+    index = gate.codes.get_device()
+    su = up.c_struct("up", index)
+    if out is None:
+        out = MXMatrix.empty(2 * gate.rows, gate.cols, gate.codes.device, gate.mx)
+    _pair(index, byref(sg), byref(su), byref(out.c_struct("out", index)))
+    return out
+
+
+def _gated_out(X, index, N, mx, out, fresh):
+    """H and how the entry point takes it: (result, address of a bf16 H, struct of a microscaled one)"""
+    if N % 32:
+        raise ValueError(f"H would have {N} columns: a pair has a multiple of 64 rows")
+    if out is None:
+        if mx is None:
+            out = (torch.zeros if fresh else torch.empty)((X.rows, N), dtype=torch.bfloat16, device=X.codes.device)
+        else:
+            out = MXMatrix.empty(X.rows, N, X.codes.device, mx)
+            if fresh:
+                out.codes.zero_()
+                out.scales.zero_()
+    if isinstance(out, MXMatrix):
+        if mx is not None and mx != out.mx:
+            raise ValueError(f"mx {mx} differs from out.mx {out.mx}")
+        return out, None, byref(out.c_struct("out", index))
+    return out, _tensor("out", out, torch.bfloat16, (X.rows, N), index), None
+
+
+def qlora_mx_gated(X: MXMatrix, W: MXMatrix, mx: Optional[int] = QLORA_MX_FP8, out=None):
+    """H = silu(X Wg^T) * (X Wu^T), W the pair [2 N, K] of both weights (N a
+    multiple of 32): a new matrix in microscaled floats of type ``mx`` (what the
+    down projection takes), a new bf16 tensor [M, N] with ``mx`` None, or
+    ``out``, which is one or the other and decides."""
+    sx = X.c_struct("X")
+    index = X.codes.get_device()
+    sw = W.c_struct("W", index)
+    if out is not None:
+        mx = None
+    out, h, hq = _gated_out(X, index, W.rows // 2, mx, out, False)
+    _gated(index, byref(sx), byref(sw), h, hq)
+    return out
+
+
+def qlora_mx_gated_grouped(X: MXMatrix, W: MXMatrix, offsets, mx: Optional[int] = QLORA_MX_FP8, out=None):
+    """qlora_mx_gated by expert: X [M, K] with its rows sorted by expert, W
+    [experts * 2 N, K] the experts' pairs one below the other, offsets int32
+    [experts + 1] on the device. Rows that no expert has are left as they were
+    (zero in a new H)."""
+    sx = X.c_struct("X")
+    index = X.codes.get_device()
+    sw = W.c_struct("W", index)
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("offsets must be a tensor [experts + 1]")
+    off = _tensor("offsets", offsets, torch.int32, offsets.shape, index)
+    experts = offsets.shape[0] - 1
+    if W.rows % (2 * experts):
+        raise ValueError(f"W has {W.rows} rows, not a multiple of two for each of {experts} experts")
+    if out is not None:
+        mx = None
+    out, h, hq = _gated_out(X, index, W.rows // experts // 2, mx, out, True)
+    _gated_grouped(index, byref(sx), byref(sw), off, experts, h, hq)
+    return out
+
+
+def qlora_rope_freqs(rot: int, base: float = 10000.0, scaling: int = QLORA_ROPE_PLAIN, factor: float = 1.0,
+                     trained: int = 4096, low: float = 1.0, high: float = 32.0, device=None):
+    """(freqs, amplitude): fp64 [rot / 2], radians a position of each pair, and
+    the factor of the rotated values, for a context ``factor`` times as long as
+    the ``trained`` positions. Formed once and kept with the model."""
+    if rot < 2 or rot % 2:
+        raise ValueError(f"rot must be even and at least 2, got {rot}")
+    freqs, amplitude = (ctypes.c_double * (rot // 2))(), ctypes.c_double()
+    status = lib.qlora_rope_freqs(rot, float(base), scaling, float(factor), int(trained), float(low), float(high), freqs, byref(amplitude))
+    if status != 0:
+        raise QloraError("qlora_rope_freqs", status, qlora_last_error())
+    return torch.tensor(list(freqs), dtype=torch.float64, device=device), amplitude.value
+
+
+def _heads(name, t, out, dtype, shape, index):
+    """The C struct of heads [rows, heads, dim] and of their output, the elements of a head next to each other."""
+    for what, x in ((name, t), (f"out {name}", out)):
+        if not isinstance(x, torch.Tensor) or not x.is_cuda:
+            raise TypeError(f"{what} must be a CUDA (HIP) tensor")
+        if x.dtype is not dtype:
+            raise TypeError(f"{what} must be {dtype}, got {x.dtype}")
+        if x.dim() != 3 or x.numel() == 0 or (x.shape[0], x.shape[2]) != shape or x.shape[1] != t.shape[1]:
+            raise ValueError(f"{what} must be [{shape[0]}, heads, {shape[1]}], got {tuple(x.shape)}")
+        if x.stride(2) != 1:
+            raise ValueError(f"the elements of a head of {what} must lie next to each other")
+        if x.get_device() != index:
+            raise ValueError(f"{what} is on {x.device}, expected cuda:{index}")
+    return _Heads(t.data_ptr(), out.data_ptr(), t.shape[1], t.stride(0), t.stride(1), out.stride(0), out.stride(1))
+
+
+def _rope(entry, Q, K, positions, freqs, amplitude, interleaved, outs):
+    if not isinstance(Q, torch.Tensor) or not Q.is_cuda:
+        raise TypeError("the heads must be CUDA (HIP) tensors")
+    if Q.dim() != 3:
+        raise ValueError(f"the heads must be [rows, heads, dim], got {tuple(Q.shape)}")
+    if Q.dtype not in _DTYPES:
+        raise TypeError(f"the heads must be float32 or bfloat16, got {Q.dtype}")
+    index, rows, dim = Q.get_device(), Q.shape[0], Q.shape[2]
+    if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64):
+        raise TypeError("positions must be an int32 or int64 tensor")
+    pos = _tensor("positions", positions, None, (rows,), index)
+    if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
+        raise ValueError("freqs must be a tensor [rot / 2]")
+    f = _tensor("freqs", freqs, torch.float64, freqs.shape, index)
+    if outs is None:
+        q, k = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device), None
+        if K is not None:
+            k = torch.empty(K.shape, dtype=Q.dtype, device=Q.device) if isinstance(K, torch.Tensor) else K
+    else:
+        q, k = outs
+        if (K is None) != (k is None):
+            raise ValueError("outs must have what there are heads for")
+    sq = _heads("Q", Q, q, Q.dtype, (rows, dim), index)
+    sk = None if K is None else _heads("K", K, k, Q.dtype, (rows, dim), index)
+    entry(index, byref(sq), None if sk is None else byref(sk), _DTYPES[Q.dtype], rows, dim, 2 * freqs.shape[0], pos,
+          positions.dtype is torch.int64, f, float(amplitude), bool(interleaved))
+    return q, k
+
+
+def qlora_rope_fwd(Q, K, positions, freqs, amplitude: float = 1.0, interleaved: bool = False,
+                   outs: Optional[Tuple] = None):
+    """(Q', K'): the heads [rows, heads, dim] (fp32 or bf16, any strides of rows
+    and heads) rotated by their positions [rows] (int32 or int64). The first 2
+    len(freqs) elements of a head are rotated, element i with i + len(freqs) or,
+    ``interleaved``, 2 i with 2 i + 1; the others pass through. K may be None.
+    ``outs`` may be (Q, K) themselves."""
+    return _rope(_rope_fwd, Q, K, positions, freqs, amplitude, interleaved, outs)
+
+
+def qlora_rope_bwd(dQ, dK, positions, freqs, amplitude: float = 1.0, interleaved: bool = False,
+                   outs: Optional[Tuple] = None):
+    """(gradients of Q and K) of qlora_rope_fwd from those of its outputs; with the same arguments as it."""
+    return _rope(_rope_bwd, dQ, dK, positions, freqs, amplitude, interleaved, outs)

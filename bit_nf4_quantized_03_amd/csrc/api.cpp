@@ -143,6 +143,8 @@ int api_fail(int status, const char *fmt, ...) {
 
 int api_hip_status(hipError_t e, const char *where) { return hip_status(e, where); }
 
+int api_check_weight(const qlora_nf4_weight *w, const char *fn) { return check_weight(w, fn); }
+
 }  // namespace qnf4
 
 extern "C" {

@@ -113,6 +113,12 @@ qnf4::MxLinear product_args(const qlora_mx_matrix *X, const qlora_mx_matrix *W, 
 
 }  // namespace
 
+namespace qnf4 {
+
+int api_check_matrix(const char *fn, const char *name, const qlora_mx_matrix *q) { return check_matrix(fn, name, q); }
+
+}  // namespace qnf4
+
 extern "C" {
 
 int64_t qlora_mx_scale_pitch(int64_t cols) { return valid_shape(1, cols) ? qnf4::mx_pitch(cols) : 0; }

@@ -1,0 +1,165 @@
+// The gated feed-forward product on microscaled operands, dense or by expert,
+// and the pair of weights that it reads.
+#include <algorithm>
+#include <cmath>
+
+#include "block.h"
+#include "mx_gated.h"
+
+namespace qnf4 {
+namespace {
+
+// Rows of a pair: 16-byte pieces of a row's codes and scales, one wave a row.
+struct PairParams {
+  const uint8_t *codes[2], *scales[2];   // gate, up
+  uint8_t *to_codes, *to_scales;
+  int64_t first, rows;                   // rows of the pair that the launch begins with / that there are
+  int64_t ld, pitch;
+};
+
+__global__ __launch_bounds__(256) void k_mx_pair(const PairParams p) {
+  const int64_t row = p.first + 4 * static_cast<int64_t>(blockIdx.x) + (threadIdx.x >> 6);
+  if (row >= p.rows) return;
+  const int up = static_cast<int>(row >> 3) & 1;
+  const int64_t from = (row >> 4) * 8 + (row & 7);
+  const uint8_t *c = p.codes[up] + from * p.ld, *s = p.scales[up] + from * p.pitch;
+  uint8_t *to = p.to_codes + row * p.ld, *ts = p.to_scales + row * p.pitch;
+  for (int64_t i = 16 * (threadIdx.x & 63); i < p.ld; i += 1024) *reinterpret_cast<uint4 *>(to + i) = *reinterpret_cast<const uint4 *>(c + i);
+  for (int64_t i = 16 * (threadIdx.x & 63); i < p.pitch; i += 1024) *reinterpret_cast<uint4 *>(ts + i) = *reinterpret_cast<const uint4 *>(s + i);
+}
+
+// Few rows: 16 RT rows of the pair, 8 RT columns of H a workgroup. The waves'
+// sums are added in wave order, then a lane takes eight columns of a row.
+template <int XT, int MT, int RT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_mx_gated_gemv(const MxGemvParams p, const MxGatedOut o) {
+  __shared__ float part[WAVES][MT][RT][16][17];
+  int64_t m0, m_end;
+  if (!mx_stream<XT, MT, RT, WAVES>(p, part, m0, m_end)) return;
+  const int rows = static_cast<int>(min(m_end - m0, int64_t(16 * MT)));
+  __syncthreads();
+  for (int i = threadIdx.x; i < 16 * RT * rows; i += 64 * WAVES) {
+    const int c = i & 15, k = (i >> 4) % RT, m = (i >> 4) / RT;
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) sum += part[w][m >> 4][k][m & 15][c];
+    part[0][m >> 4][k][m & 15][c] = sum;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < RT * rows; i += 64 * WAVES) {
+    const int k = i % RT, m = i / RT;
+    const float *both = part[0][m >> 4][k][m & 15];
+    float v[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] = gate_value(both[c], both[8 + c]);
+    const int64_t n = static_cast<int64_t>(blockIdx.x) * (8 * RT) + 8 * k;
+    mx_gated_put(o, v, m0 + m, n, n < o.N);
+  }
+}
+
+template <class T>
+__global__ __launch_bounds__(T::kThreads, 1) void k_mx_gated(const MxGemmParams p, const MxGatedOut o) {
+  __shared__ __attribute__((aligned(16))) char smem[T::kLds];
+  const int tiles_m = static_cast<int>((p.M + T::BM - 1) / T::BM), tiles_n = static_cast<int>((p.N + T::BN - 1) / T::BN);
+  int tm, tn, wave;
+  tile_of(static_cast<int>(blockIdx.x), tiles_m, tiles_n, tm, tn);
+  const int64_t n0 = static_cast<int64_t>(tn) * T::BN, m0 = static_cast<int64_t>(tm) * T::BM;
+  MxAcc<T> acc;
+  const bool mine = mx_tile_product<T>(acc, p.op, n0, m0, p.steps, smem, wave);
+  mx_gated_store<T>(acc, o, n0, m0, p.M, wave, mine, smem);
+}
+
+template <class T>
+__global__ __launch_bounds__(T::kThreads, 1) void k_mx_gated_grouped(const MxGemmParams p, const MxGatedOut o) {
+  __shared__ __attribute__((aligned(16))) char smem[T::kLds];
+  MxGroupTile t;
+  if (!mx_group_tile<T>(p, static_cast<int>(blockIdx.x), t)) return;
+  const int64_t n0 = static_cast<int64_t>(t.tn) * T::BN;
+  const int64_t m0 = t.m_begin + static_cast<int64_t>(t.tm) * T::BM;
+  MxOperands op = p.op;
+  op.w += static_cast<int64_t>(t.expert) * p.N * op.w_ld;
+  op.ws += static_cast<int64_t>(t.expert) * p.N * op.pitch;
+  op.x_rows = t.m_end;
+  MxAcc<T> acc;
+  int wave;
+  const bool mine = mx_tile_product<T>(acc, op, n0, m0, p.steps, smem, wave);
+  mx_gated_store<T>(acc, o, n0, m0, t.m_end, wave, mine, smem);
+}
+
+template <int XT, int MT, int RT, int WAVES>
+hipError_t run_gemv(const MxGemvParams &p, const MxGatedOut &o, hipStream_t s) {
+  // by expert: every run of 16 rows but an expert's first is a whole one or follows one
+  const dim3 g(static_cast<unsigned>(ceil_div(p.N, 16 * RT)), p.experts ? p.experts + static_cast<unsigned>(p.M / 16) : 1);
+  k_mx_gated_gemv<XT, MT, RT, WAVES><<<g, 64 * WAVES, 0, s>>>(p, o);
+  return hipGetLastError();
+}
+
+template <int TILE, class T>
+hipError_t run_tile(const MxGemmParams &p, const MxGatedOut &o, hipStream_t s) {
+  static_assert(T::BN == kMxTile[TILE].bn && T::BM == kMxTile[TILE].bm && T::kThreads == kMxTile[TILE].threads, "the rule's tile");
+  const unsigned groups = static_cast<unsigned>(mx_tile_groups(T::BM, T::BN, p.M, p.N, p.experts));
+  if (p.experts) k_mx_gated_grouped<T><<<groups, T::kThreads, 0, s>>>(p, o);
+  else k_mx_gated<T><<<groups, T::kThreads, 0, s>>>(p, o);
+  return hipGetLastError();
+}
+
+template <int XT>
+hipError_t run_tiles(const MxGemmParams &p, const MxGatedOut &o, hipStream_t s) {
+  constexpr bool kPair = XT == QLORA_MX_FP4;
+  constexpr int kDeep = kPair ? 4 : 3;   // stages
+  switch (mx_choose_tile(p.M, p.N, p.experts, XT == QLORA_MX_FP4)) {
+    case 0: return run_tile<0, MxTile<XT, 4, 2, 2, 4, kDeep, kPair ? 2 : 1, 1, kPair>>(p, o, s);
+    case 1: return run_tile<1, MxTile<XT, 2, 2, 4, 2, kDeep, kPair ? 2 : 4, 1, kPair>>(p, o, s);
+    case 2: return run_tile<2, MxTile<XT, 2, 2, 2, 2, kDeep, kPair ? 2 : 1, 1, kPair>>(p, o, s);
+    case 3: return run_tile<3, MxTile<XT, 2, 1, 2, 2, 4, 2>>(p, o, s);
+    default: return run_tile<4, MxTile<XT, 1, 1, 2, 2, 4, 4, 2>>(p, o, s);
+  }
+}
+
+// Few rows, the weight's stream: false where the tiles are faster. A workgroup
+// has whole blocks of 32 columns of H, 64 rows of the pair.
+template <int XT>
+bool run_few_rows(const MxGemvParams &p, const MxGatedOut &o, hipStream_t s, hipError_t *e) {
+  if (p.experts) {
+    if (p.M > 8 * static_cast<int64_t>(p.experts)) return false;
+    *e = p.nblk <= 32 ? run_gemv<XT, 1, 4, 2>(p, o, s) : run_gemv<XT, 1, 4, 4>(p, o, s);
+    return true;
+  }
+  if (p.M > (p.N <= 32 * kMxCus ? 16 : 8)) return false;
+  *e = p.N <= 64 * kMxCus ? run_gemv<XT, 1, 4, 8>(p, o, s) : run_gemv<XT, 1, 4, 4>(p, o, s);
+  return true;
+}
+
+template <int XT>
+hipError_t run_gated(const MxLinear &a, const MxGatedOut &o, hipStream_t s) {
+  MxGemvParams p;
+  MxGemmParams q;
+  mx_product_params(a, p, q);
+  hipError_t e;
+  return run_few_rows<XT>(p, o, s, &e) ? e : run_tiles<XT>(q, o, s);
+}
+
+}  // namespace
+
+hipError_t launch_mx_pair(const MxPair &a, hipStream_t s) {
+  PairParams p{{a.gate, a.up}, {a.gate_scales, a.up_scales}, a.out, a.out_scales, 0, a.rows, a.K / 2, mx_pitch(a.K)};
+  for (; p.first < a.rows; p.first += 4 * kMaxGroups) {
+    const int64_t groups = std::min(ceil_div(a.rows - p.first, 4), kMaxGroups);
+    k_mx_pair<<<static_cast<unsigned>(groups), 256, 0, s>>>(p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_mx_gated(const MxLinear &a, uint8_t *codes, uint8_t *scales, int type, hipStream_t s) {
+  MxGatedOut o;
+  o.h = static_cast<__bf16 *>(a.Y);
+  o.codes = codes;
+  o.scales = scales;
+  o.N = a.N / 2;
+  o.pitch = static_cast<uint32_t>(mx_pitch(o.N));
+  o.type = a.Y ? -1 : type;
+  return a.x_type == QLORA_MX_FP4 ? run_gated<QLORA_MX_FP4>(a, o, s) : run_gated<QLORA_MX_FP8>(a, o, s);
+}
+
+}  // namespace qnf4

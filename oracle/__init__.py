@@ -20,6 +20,8 @@ Modules
   adamw   one AdamW step of the adapter parameters in fp32, op by op.
   mx      microscaled formats (OCP Microscaling Formats specification 1.0),
           RMSNorm forward and backward, and the products, in fp64.
+  block   the gated feed-forward product, forward and backward, and rotary
+          positions, in fp64.
 
 Sources (the pages the method is taken from):
   * Guanaco topic page (chipfoundryservices.com), "Technical Innovations":
@@ -40,4 +42,4 @@ Sources (the pages the method is taken from):
 Every function whose result is pinned only by its own self-consistency says
 "parity unpinned" in its docstring; at present none does.
 """
-from . import nf4, linear, merge, adamw, mx  # noqa: F401
+from . import nf4, linear, merge, adamw, mx, block  # noqa: F401
