@@ -1,4 +1,5 @@
-"""torch.autograd wrappers of the QLoRA linear layer and of RMSNorm.
+"""torch.autograd wrappers of the QLoRA linear layer, of the gated feed-forward
+block, of RMSNorm and of rotary positions.
 
 Marshalling only: the forward is one ``qlora_linear_fwd_save`` call, which
 also keeps the adapter activations bf16(scale X A^T) [M, r], and the backward
@@ -15,6 +16,8 @@ Tensors: X bf16 [M, K] (any leading shape, flattened to M rows), A fp32
 
 ``rmsnorm`` is the norm in front of the projections, with the residual's
 addition: one ``qlora_rmsnorm_fwd`` call and one ``qlora_rmsnorm_bwd`` call.
+``qlora_gated`` is the feed-forward block up to its down projection, ``rope``
+the rotary positions of queries and keys, each one call a pass.
 
 A backward pass may be captured into a HIP graph. As with any of torch's, no
 eager graph of the same leaves may be alive then: its gradient accumulation
@@ -25,8 +28,8 @@ from __future__ import annotations
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (NF4Weight, qlora_linear_bwd, qlora_linear_bwd_saved, qlora_linear_fwd, qlora_linear_fwd_save,
-               qlora_rmsnorm_bwd, qlora_rmsnorm_fwd)
+from . import (NF4Weight, qlora_gated_bwd, qlora_gated_fwd, qlora_gated_fwd_save, qlora_linear_bwd, qlora_linear_bwd_saved,
+               qlora_linear_fwd, qlora_linear_fwd_save, qlora_rmsnorm_bwd, qlora_rmsnorm_fwd, qlora_rope_bwd, qlora_rope_fwd)
 
 
 class QLoRALinearFn(torch.autograd.Function):
@@ -112,3 +115,64 @@ def rmsnorm(X, weight, residual=None, eps: float = 1e-6):
     the result is Y; with one it is (Y, H), H = bf16(X + residual) being the
     residual stream that goes on."""
     return RMSNormFn.apply(X, weight, residual, float(eps))
+
+
+class GatedFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, Ag, Bg, Au, Bu, gate: NF4Weight, up: NF4Weight, scale: float):
+        X2 = _rows(X, X.shape[-1])
+        args = (gate, up, Ag, Bg, Au, Bu, scale)
+        shape = (*X.shape[:-1], gate.rows)
+        if not any(ctx.needs_input_grad):   # nothing to keep
+            return qlora_gated_fwd(X2, *args).reshape(shape)
+        H, G, U, Hs = qlora_gated_fwd_save(X2, *args)
+        ctx.save_for_backward(X2, G, U, Hs, Ag, Bg, Au, Bu)
+        ctx.weights, ctx.scale, ctx.shape = (gate, up), scale, X.shape
+        return H.reshape(shape)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dH):
+        X2, G, U, Hs, *factors = ctx.saved_tensors
+        dH = _rows(dH.to(torch.bfloat16), G.shape[1])
+        dX, *grads = qlora_gated_bwd(dH, X2, G, U, Hs, *ctx.weights, *factors, ctx.scale)
+        return (dX.reshape(ctx.shape), *grads, None, None, None)
+
+
+def qlora_gated(X, gate: NF4Weight, up: NF4Weight, Ag=None, Bg=None, Au=None, Bu=None, scale: float = 0.0):
+    """H = silu(G) * U, G = X Wg-hat^T + scale (X Ag^T) Bg^T and U likewise, with
+    autograd to X (bf16, any leading shape) and the adapters (fp32 or bf16, all
+    four or none): the feed-forward block up to its down projection in one
+    ``qlora_gated_fwd_save`` and one ``qlora_gated_bwd`` call."""
+    return GatedFn.apply(X, Ag, Bg, Au, Bu, gate, up, float(scale))
+
+
+class RopeFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, Q, K, positions, freqs, amplitude: float, interleaved: bool):
+        ctx.save_for_backward(positions, freqs)
+        ctx.how = (amplitude, interleaved)
+        ctx.set_materialize_grads(False)
+        return qlora_rope_fwd(Q, K, positions, freqs, amplitude, interleaved)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dQ, dK):
+        given = [None if t is None else t if t.stride(-1) == 1 else t.contiguous() for t in (dQ, dK)]
+        first = given[0] if given[0] is not None else given[1]
+        if first is None:
+            return (None,) * 6
+        second = given[1] if given[0] is not None else None
+        a, b = qlora_rope_bwd(first, second, *ctx.saved_tensors, *ctx.how)
+        return (a, b, None, None, None, None) if given[0] is not None else (None, a, None, None, None, None)
+
+
+def rope(Q, K, positions, freqs, amplitude: float = 1.0, interleaved: bool = False):
+    """(Q, K) with rotary positions, with autograd to both: heads [..., heads,
+    dim] in fp32 or bf16, positions [...] of the same leading shape (int32 or
+    int64), freqs and amplitude of ``qlora_rope_freqs``. K may be None."""
+    def flat(t):
+        t = t.reshape(-1, *t.shape[-2:])
+        return t if t.stride(2) == 1 else t.contiguous()
+    q, k = RopeFn.apply(flat(Q), None if K is None else flat(K), positions.reshape(-1).contiguous(), freqs, float(amplitude), bool(interleaved))
+    return q.reshape(Q.shape), None if k is None else k.reshape(K.shape)

@@ -13,17 +13,19 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import QLORA_BF16, QLORA_F32, QloraError, lib, qlora_last_error
-from .mx import (_DTYPES, _MX, MXMatrix, QLORA_MX_FP4, QLORA_MX_FP8, _empty, _entry, _tensor)
+from . import NF4Weight, QloraError, _Weight, format_has_dq, lib, qlora_last_error
+from .mx import _DTYPES, _MX, MXMatrix, QLORA_MX_FP8, _empty, _empty_1d, _entry, _tensor
 
 __all__ = [
     "BLOCK_EXPORTED_SYMBOLS", "QLORA_ROPE_PLAIN", "QLORA_ROPE_LINEAR", "QLORA_ROPE_NTK", "QLORA_ROPE_PARTS",
-    "qlora_mx_pair", "qlora_mx_gated", "qlora_mx_gated_grouped", "qlora_rope_freqs", "qlora_rope_fwd",
-    "qlora_rope_bwd",
+    "qlora_mx_pair", "qlora_mx_gated", "qlora_mx_gated_grouped", "qlora_gated_saved_cols",
+    "qlora_gated_workspace_bytes", "qlora_gated_fwd", "qlora_gated_fwd_save", "qlora_gated_bwd", "qlora_rope_freqs",
+    "qlora_rope_fwd", "qlora_rope_bwd",
 ]
 
 BLOCK_EXPORTED_SYMBOLS = (
-    "qlora_mx_pair", "qlora_mx_gated", "qlora_mx_gated_grouped", "qlora_rope_freqs", "qlora_rope_fwd",
+    "qlora_mx_pair", "qlora_mx_gated", "qlora_mx_gated_grouped", "qlora_gated_saved_cols",
+    "qlora_gated_workspace_bytes", "qlora_gated_fwd", "qlora_gated_bwd", "qlora_rope_freqs", "qlora_rope_fwd",
     "qlora_rope_bwd",
 )
 
@@ -31,6 +33,15 @@ QLORA_ROPE_PLAIN = 0    # the frequencies as they are
 QLORA_ROPE_LINEAR = 1   # positions pressed together
 QLORA_ROPE_NTK = 2      # a larger base
 QLORA_ROPE_PARTS = 3    # by parts: fast pairs as they are, slow ones pressed together
+
+
+class _Adapters(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("gate_A", "gate_B", "up_A", "up_B")] + \
+        [("r", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class _Grads(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("gate_A", "gate_B", "up_A", "up_B")]
 
 
 class _Heads(ctypes.Structure):
@@ -41,11 +52,16 @@ class _Heads(ctypes.Structure):
 def _declare():
     i64, vp, i32, f64, ci = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32, ctypes.c_double, ctypes.c_int
     mp, hp, dp = ctypes.POINTER(_MX), ctypes.POINTER(_Heads), ctypes.POINTER(ctypes.c_double)
+    wp, ap, gp, sz = ctypes.POINTER(_Weight), ctypes.POINTER(_Adapters), ctypes.POINTER(_Grads), ctypes.c_size_t
     rope = [hp, hp, ci, i64, i32, i32, vp, i32, vp, f64, i32, vp]
     sigs = {
         "qlora_mx_pair": (ci, [mp, mp, mp, vp]),
         "qlora_mx_gated": (ci, [mp, mp, vp, mp, vp]),
         "qlora_mx_gated_grouped": (ci, [mp, mp, vp, i32, vp, mp, vp]),
+        "qlora_gated_saved_cols": (i64, [i32]),
+        "qlora_gated_workspace_bytes": (sz, [i64, i64, i64, i32, i32]),
+        "qlora_gated_fwd": (ci, [vp, i64, wp, wp, ap, vp, vp, vp, vp, vp, sz, vp]),
+        "qlora_gated_bwd": (ci, [vp, vp, vp, vp, vp, i64, wp, wp, ap, vp, gp, vp, sz, vp]),
         "qlora_rope_freqs": (ci, [i32, f64, i32, f64, i64, f64, f64, dp, dp]),
         "qlora_rope_fwd": (ci, rope),
         "qlora_rope_bwd": (ci, rope),
@@ -59,6 +75,7 @@ def _declare():
 _declare()
 
 _pair, _gated, _gated_grouped = _entry("qlora_mx_pair"), _entry("qlora_mx_gated"), _entry("qlora_mx_gated_grouped")
+_block_fwd, _block_bwd = _entry("qlora_gated_fwd"), _entry("qlora_gated_bwd")
 _rope_fwd, _rope_bwd = _entry("qlora_rope_fwd"), _entry("qlora_rope_bwd")
 
 
@@ -127,6 +144,122 @@ def qlora_mx_gated_grouped(X: MXMatrix, W: MXMatrix, offsets, mx: Optional[int] 
     out, h, hq = _gated_out(X, index, W.rows // experts // 2, mx, out, True)
     _gated_grouped(index, byref(sx), byref(sw), off, experts, h, hq)
     return out
+
+
+def qlora_gated_saved_cols(r: int) -> int:
+    """Columns of the kept adapter activations of adapters of rank ``r``."""
+    return int(lib.qlora_gated_saved_cols(r))
+
+
+def qlora_gated_workspace_bytes(M: int, N: int, K: int, r: int, backward: bool) -> int:
+    return int(lib.qlora_gated_workspace_bytes(M, N, K, r, bool(backward)))
+
+
+def _weight(name, W: NF4Weight, index):
+    """The C struct of a weight, after checking its buffers against its shape and format."""
+    n = W.rows * W.cols
+    blocks = -(-n // 64)
+    if format_has_dq(W.fmt):
+        parts = (("absmax_q", torch.int8, blocks), ("dq_scale", torch.float32, -(-blocks // 256)), ("dq_mean", torch.float32, 1))
+    else:
+        parts = (("absmax", torch.float32, blocks),)
+    for part, dtype, count in (("codes", torch.uint8, (n + 1) // 2),) + parts:
+        _tensor(f"{name}.{part}", getattr(W, part), dtype, (count,), index)
+    return W.c_struct()
+
+
+def _block_args(X, gate, up, Ag, Bg, Au, Bu, scale):
+    """(M, N, K, r, device index, the two weights' structs, the adapters' struct or None, their type)"""
+    if not isinstance(X, torch.Tensor) or not X.is_cuda:
+        raise TypeError("X must be a CUDA (HIP) tensor")
+    index, N, K = X.get_device(), gate.rows, gate.cols
+    if X.dim() != 2 or X.shape[0] < 1:
+        raise ValueError(f"X must be [M, {K}] with M >= 1, got {tuple(X.shape)}")
+    M = X.shape[0]
+    _tensor("X", X, torch.bfloat16, (M, K), index)
+    sg, su = _weight("gate", gate, index), _weight("up", up, index)
+    factors = (Ag, Bg, Au, Bu)
+    if all(t is None for t in factors):
+        return M, N, K, 0, index, sg, su, None, None
+    if any(t is None for t in factors):
+        raise ValueError("Ag, Bg, Au and Bu must all be given or all be None")
+    if not isinstance(Ag, torch.Tensor) or Ag.dim() != 2 or Ag.shape[0] < 1:
+        raise ValueError(f"Ag must be a tensor [r, {K}] with r >= 1")
+    r, dtype = Ag.shape[0], Ag.dtype
+    if dtype not in _DTYPES:
+        raise TypeError(f"the adapters must be float32 or bfloat16, got {dtype}")
+    at = [_tensor(name, t, dtype, shape, index)
+          for name, t, shape in zip(("Ag", "Bg", "Au", "Bu"), factors, ((r, K), (N, r), (r, K), (N, r)))]
+    return M, N, K, r, index, sg, su, _Adapters(*at, r, _DTYPES[dtype], float(scale)), dtype
+
+
+def _block_ws(ws, M, N, K, r, backward, index, device):
+    """(address, bytes, tensor) of the workspace; nothing of it is expected or kept."""
+    if ws is None:
+        ws = _empty_1d(lib.qlora_gated_workspace_bytes(M, N, K, r, backward), torch.uint8, device)
+    else:
+        _tensor("ws", ws, None, ws.shape, index)
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+
+
+def _given(t, name, shape, dtype, index, device):
+    """``t`` after its checks, or a new tensor."""
+    if t is None:
+        return _empty(*shape, dtype, device)
+    _tensor(name, t, dtype, shape, index)
+    return t
+
+
+def qlora_gated_fwd(X, gate: NF4Weight, up: NF4Weight, Ag=None, Bg=None, Au=None, Bu=None, scale: float = 0.0, ws=None, out=None):
+    """H = silu(G) * U, G = X Wg^T + scale (X Ag^T) Bg^T and U likewise: X bf16
+    [M, K], two frozen 4-bit weights [N, K] of one format, adapters A [r, K] and
+    B [N, r] in fp32 or bf16 (all four or none). H bf16 [M, N]."""
+    M, N, K, r, index, sg, su, ad, _ = _block_args(X, gate, up, Ag, Bg, Au, Bu, scale)
+    out = _given(out, "out", (M, N), torch.bfloat16, index, X.device)
+    at, size, ws = _block_ws(ws, M, N, K, r, False, index, X.device)
+    _block_fwd(index, X.data_ptr(), M, byref(sg), byref(su), ad and byref(ad), out.data_ptr(), None, None, None, at, size)
+    return out
+
+
+def qlora_gated_fwd_save(X, gate: NF4Weight, up: NF4Weight, Ag=None, Bg=None, Au=None, Bu=None, scale: float = 0.0, ws=None,
+                         outs: Optional[Tuple] = None):
+    """(H, G, U, Hs): qlora_gated_fwd's H and what qlora_gated_bwd takes: G and U
+    in bf16 and the adapter activations Hs bf16 [M, qlora_gated_saved_cols(r)]
+    (None without adapters)."""
+    M, N, K, r, index, sg, su, ad, _ = _block_args(X, gate, up, Ag, Bg, Au, Bu, scale)
+    H, G, U, Hs = (None,) * 4 if outs is None else outs
+    H, G, U = (_given(t, name, (M, N), torch.bfloat16, index, X.device) for name, t in (("H", H), ("G", G), ("U", U)))
+    if r:
+        Hs = _given(Hs, "Hs", (M, lib.qlora_gated_saved_cols(r)), torch.bfloat16, index, X.device)
+    elif Hs is not None:
+        raise ValueError("without adapters Hs must be None")
+    at, size, ws = _block_ws(ws, M, N, K, r, False, index, X.device)
+    _block_fwd(index, X.data_ptr(), M, byref(sg), byref(su), ad and byref(ad), H.data_ptr(), G.data_ptr(), U.data_ptr(),
+               Hs.data_ptr() if r else None, at, size)
+    return H, G, U, Hs
+
+
+def qlora_gated_bwd(dH, X, G, U, Hs, gate: NF4Weight, up: NF4Weight, Ag=None, Bg=None, Au=None, Bu=None, scale: float = 0.0,
+                    ws=None, outs: Optional[Tuple] = None):
+    """(dX, dAg, dBg, dAu, dBu) from the gradient of H and what
+    qlora_gated_fwd_save kept, with its arguments: dX bf16, the others in the
+    adapters' type (None without adapters). The weights get no gradient."""
+    M, N, K, r, index, sg, su, ad, dtype = _block_args(X, gate, up, Ag, Bg, Au, Bu, scale)
+    ins = [_tensor(name, t, torch.bfloat16, (M, N), index) for name, t in (("dH", dH), ("G", G), ("U", U))]
+    dX, *grads = (None,) * 5 if outs is None else outs
+    dX = _given(dX, "dX", (M, K), torch.bfloat16, index, X.device)
+    hs = sgr = None
+    if r:
+        hs = _tensor("Hs", Hs, torch.bfloat16, (M, lib.qlora_gated_saved_cols(r)), index)
+        grads = [_given(t, name, shape, dtype, index, X.device)
+                 for t, name, shape in zip(grads, ("dAg", "dBg", "dAu", "dBu"), ((r, K), (N, r), (r, K), (N, r)))]
+        sgr = _Grads(*(t.data_ptr() for t in grads))
+    elif Hs is not None or any(t is not None for t in grads):
+        raise ValueError("without adapters Hs and their gradients must be None")
+    at, size, ws = _block_ws(ws, M, N, K, r, True, index, X.device)
+    _block_bwd(index, ins[0], X.data_ptr(), ins[1], ins[2], hs, M, byref(sg), byref(su), ad and byref(ad), dX.data_ptr(),
+               sgr and byref(sgr), at, size)
+    return (dX, *grads)
 
 
 def qlora_rope_freqs(rot: int, base: float = 10000.0, scaling: int = QLORA_ROPE_PLAIN, factor: float = 1.0,

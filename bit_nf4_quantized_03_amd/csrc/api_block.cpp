@@ -54,6 +54,57 @@ int gated(const char *fn, const qnf4::MxLinear &a, const qlora_mx_matrix *Hq, vo
                                                     Hq ? Hq->type : 0, static_cast<hipStream_t>(stream)), fn);
 }
 
+bool valid_gated(int64_t M, int64_t N, int64_t K, int32_t r) {
+  return M >= 1 && M <= qnf4::kGatedMaxRows && N >= 1 && K >= 1 && N <= qnf4::kGatedMaxDim && K <= qnf4::kGatedMaxDim &&
+         N % QLORA_NF4_BLOCK == 0 && K % QLORA_NF4_BLOCK == 0 && M <= qnf4::kGatedMaxOut / N && M <= qnf4::kGatedMaxOut / K &&
+         N <= qnf4::kGatedMaxOut / K && r >= 0 && r <= 256;
+}
+
+// The checks that both passes of the block with adapters share, and their arguments.
+int block_args(const char *fn, int64_t M, const qlora_nf4_weight *gate, const qlora_nf4_weight *up,
+               const qlora_gated_adapters *ad, bool backward, const void *ws, size_t ws_bytes, qnf4::GatedArgs *a) {
+  int st = qnf4::api_check_weight(gate, fn);
+  if (st == QLORA_OK) st = qnf4::api_check_weight(up, fn);
+  if (st != QLORA_OK) return st;
+  if (gate->rows != up->rows || gate->cols != up->cols)
+    return api_fail(QLORA_ERR_SHAPE, "%s: the weights are %lld x %lld and %lld x %lld", fn, ll(gate->rows), ll(gate->cols),
+                    ll(up->rows), ll(up->cols));
+  if (gate->format != up->format)
+    return api_fail(QLORA_ERR_FORMAT, "%s: the weights' formats %d and %d differ", fn, gate->format, up->format);
+  const int32_t r = ad ? ad->r : 0;
+  if (ad && (r < 1 || r > 256)) return api_fail(QLORA_ERR_SHAPE, "%s: r = %d out of [1, 256]", fn, r);
+  if (!valid_gated(M, gate->rows, gate->cols, r))
+    return api_fail(QLORA_ERR_SHAPE, "%s: M = %lld, N = %lld, K = %lld: needs M >= 1, N and K multiples of %d, and sizes within the limits",
+                    fn, ll(M), ll(gate->rows), ll(gate->cols), QLORA_NF4_BLOCK);
+  *a = qnf4::GatedArgs{};
+  if (ad) {
+    if (ad->dtype != QLORA_F32 && ad->dtype != QLORA_BF16)
+      return api_fail(QLORA_ERR_DTYPE, "%s: the adapters' dtype %d is not QLORA_F32 or QLORA_BF16", fn, ad->dtype);
+    const void *const all[4] = {ad->gate_A, ad->gate_B, ad->up_A, ad->up_B};
+    for (const void *p : all) {
+      if (!p) return api_fail(QLORA_ERR_NULL, "%s: a factor of the adapters is NULL", fn);
+      if (!aligned(p, 16)) return api_fail(QLORA_ERR_ALIGN, "%s: the adapters' factors must be 16-byte aligned", fn);
+    }
+    if (!std::isfinite(ad->scale)) return api_fail(QLORA_ERR_SHAPE, "%s: scale must be finite", fn);
+    a->A[0] = ad->gate_A, a->B[0] = ad->gate_B, a->A[1] = ad->up_A, a->B[1] = ad->up_B;
+    a->adapter_bf16 = ad->dtype == QLORA_BF16;
+    a->scale = ad->scale;
+  }
+  a->M = M;
+  a->N = gate->rows;
+  a->K = gate->cols;
+  a->format = gate->format;
+  a->r = r;
+  const qlora_nf4_weight *const both[2] = {gate, up};
+  for (int i = 0; i < 2; ++i)
+    a->w[i] = {both[i]->codes, both[i]->absmax_q, both[i]->dq_scale, both[i]->dq_mean, both[i]->absmax};
+  const size_t need = qnf4::gated_ws_bytes(M, a->N, a->K, r, backward);
+  if (!ws || ws_bytes < need)
+    return api_fail(QLORA_ERR_WORKSPACE, "%s: workspace needs %zu bytes, got %zu", fn, need, ws ? ws_bytes : size_t(0));
+  if (!aligned(ws, 16)) return api_fail(QLORA_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
+  return QLORA_OK;
+}
+
 int check_heads(const char *fn, const char *name, const qlora_rope_heads *x, int64_t rows, int32_t dim, int size) {
   if (!x->in || !x->out) return api_fail(QLORA_ERR_NULL, "%s: a buffer of %s is NULL", fn, name);
   if (!aligned(x->in, size) || !aligned(x->out, size))
@@ -166,6 +217,48 @@ int qlora_mx_gated_grouped(const qlora_mx_matrix *X, const qlora_mx_matrix *W, c
   a.offsets = offsets;
   a.experts = experts;
   return gated(fn, a, Hq, stream);
+}
+
+int64_t qlora_gated_saved_cols(int32_t r) { return r < 0 || r > 256 ? 0 : 2 * qnf4::gated_padded_rank(r); }
+
+size_t qlora_gated_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r, int32_t backward) {
+  return valid_gated(M, N, K, r) ? qnf4::gated_ws_bytes(M, N, K, r, backward != 0) : 0;
+}
+
+int qlora_gated_fwd(const void *X, int64_t M, const qlora_nf4_weight *gate, const qlora_nf4_weight *up,
+                    const qlora_gated_adapters *adapters, void *H, void *G, void *U, void *Hs, void *ws, size_t ws_bytes,
+                    void *stream) {
+  const char *fn = "qlora_gated_fwd";
+  if (!X || !H) return api_fail(QLORA_ERR_NULL, "%s: X and H must not be NULL", fn);
+  qnf4::GatedArgs a;
+  const int st = block_args(fn, M, gate, up, adapters, false, ws, ws_bytes, &a);
+  if (st != QLORA_OK) return st;
+  if (!G != !U) return api_fail(QLORA_ERR_NULL, "%s: G and U are given together", fn);
+  if (!Hs != !(G && adapters)) return api_fail(QLORA_ERR_NULL, "%s: Hs is given with G, U and adapters, and only then", fn);
+  if (!aligned(X, 16) || !aligned(H, 16) || !aligned(G, 16) || !aligned(U, 16) || !aligned(Hs, 16))
+    return api_fail(QLORA_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
+  return qnf4::api_hip_status(qnf4::launch_gated_fwd(a, X, H, G, U, Hs, ws, static_cast<hipStream_t>(stream)), fn);
+}
+
+int qlora_gated_bwd(const void *dH, const void *X, const void *G, const void *U, const void *Hs, int64_t M,
+                    const qlora_nf4_weight *gate, const qlora_nf4_weight *up, const qlora_gated_adapters *adapters, void *dX,
+                    const qlora_gated_grads *grads, void *ws, size_t ws_bytes, void *stream) {
+  const char *fn = "qlora_gated_bwd";
+  if (!dH || !X || !G || !U || !dX) return api_fail(QLORA_ERR_NULL, "%s: dH, X, G, U and dX must not be NULL", fn);
+  qnf4::GatedArgs a;
+  const int st = block_args(fn, M, gate, up, adapters, true, ws, ws_bytes, &a);
+  if (st != QLORA_OK) return st;
+  if (!Hs != !adapters || !grads != !adapters)
+    return api_fail(QLORA_ERR_NULL, "%s: Hs and grads are given with adapters, and only then", fn);
+  void *dA[2] = {}, *dB[2] = {};
+  if (grads) {
+    dA[0] = grads->gate_A, dB[0] = grads->gate_B, dA[1] = grads->up_A, dB[1] = grads->up_B;
+    if (!dA[0] || !dB[0] || !dA[1] || !dB[1]) return api_fail(QLORA_ERR_NULL, "%s: a gradient is NULL", fn);
+  }
+  for (const void *p : {dH, X, G, U, Hs, static_cast<const void *>(dX), static_cast<const void *>(dA[0]), static_cast<const void *>(dB[0]),
+                        static_cast<const void *>(dA[1]), static_cast<const void *>(dB[1])})
+    if (!aligned(p, 16)) return api_fail(QLORA_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
+  return qnf4::api_hip_status(qnf4::launch_gated_bwd(a, dH, X, G, U, Hs, dX, dA, dB, ws, static_cast<hipStream_t>(stream)), fn);
 }
 
 int qlora_rope_freqs(int32_t rot, double base, int32_t scaling, double factor, int64_t trained, double low,

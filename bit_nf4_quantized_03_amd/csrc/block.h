@@ -40,4 +40,29 @@ constexpr int kRopeMaxDim = 1024;
 constexpr int64_t kRopeMaxHeads = 1 << 15;   // of q and k together
 hipError_t launch_rope(const Rope &a, hipStream_t s);
 
+// The gated block around two 4-bit weights [N, K] of one format, gate first;
+// adapters A [r, K], B [N, r] of each, or r = 0.
+struct GatedWeight {
+  const uint8_t *codes;
+  const int8_t *absmax_q;   // with DQ
+  const float *dq_scale, *dq_mean;
+  const float *absmax;      // without
+};
+struct GatedArgs {
+  int64_t M, N, K;
+  int format, r;
+  float scale;
+  bool adapter_bf16;
+  GatedWeight w[2];
+  const void *A[2], *B[2];
+};
+// Adapter columns in Hs and in the kernels' operands.
+inline int gated_padded_rank(int r) { return static_cast<int>(ceil_div(r, 64) * 64); }
+constexpr int64_t kGatedMaxRows = int64_t(1) << 24, kGatedMaxDim = int64_t(1) << 23, kGatedMaxOut = int64_t(1) << 36;
+size_t gated_ws_bytes(int64_t M, int64_t N, int64_t K, int r, bool backward);
+// G, U, Hs: kept for the backward, or null.
+hipError_t launch_gated_fwd(const GatedArgs &a, const void *X, void *H, void *G, void *U, void *Hs, void *ws, hipStream_t s);
+hipError_t launch_gated_bwd(const GatedArgs &a, const void *dH, const void *X, const void *G, const void *U, const void *Hs,
+                            void *dX, void *const (&dA)[2], void *const (&dB)[2], void *ws, hipStream_t s);
+
 }  // namespace qnf4

@@ -1,0 +1,701 @@
+// The gated feed-forward block around two frozen 4-bit weights with adapters,
+// forward and backward:
+//
+//   G = X Wg^T + s (X Ag^T) Bg^T,  U = X Wu^T + s (X Au^T) Bu^T,  H = silu(G) U
+//   dG = dH U sigma (1 + G (1 - sigma)),  dU = dH G sigma,  sigma = 1 / (1 + e^-G)
+//   dX = dG Wg + dU Wu + lg Ag + lu Au,  lg = s dG Bg,  lu = s dU Bu
+//   dAg = lg^T X,  dBg = dG^T (s X Ag^T),  and likewise of the other weight
+//
+// Forward, on the caller's stream:
+//   k_gated_prep   block scales of both weights, and the adapters as bf16
+//                  operands: [Ag; Au] as 2 rp rows of K, Bg and Bu as rows of the
+//                  interleaved tiles below (rp: r rounded up to 64, zero padded)
+//   k_gated_down   split partials of X [Ag; Au]^T: X is read once for both
+//   k_gated_sum    Hs = bf16(s sums) [M][2 rp]
+//   k_gated_fwd    256 rows by 128 columns of H a workgroup: the large-tile loop of
+//                  gemm_big.h on 128 rows of each weight, 32 of one and 32 of
+//                  the other in turn, so that both products of an element of H
+//                  end in one lane and the gate needs no exchange
+//   k_gated_out    few tiles: the reduction is split into fp32 partials, and
+//                  this sums them and gates
+// Backward:
+//   k_gated_prep   block scales, [Ag; Au]^T [K][2 rp] and Bg^T, Bu^T [2][rp][N]
+//   k_gated_act    dG, dU from dH, G, U
+//   k_gated_down, k_gated_sum   l = bf16(s [dG Bg, dU Bu]) [M][2 rp]
+//   k_gated_dx     dX = [dG, dU, l] [Wg; Wu; [Ag; Au]]: one reduction over both
+//                  weights, so dX is rounded and written once
+//   k_gated_grad, k_gated_grad_sum   split-M partials of the adapters' gradients and their sums
+//
+// Roundings to bf16, the operand type of the matrix instructions: the decoded
+// weights, A and B, Hs and l (as in linear.hip), and the kept G and U, dG and
+// dU. H comes from the unrounded G and U.
+#include "block.h"
+#include "gate.h"
+#include "nf4_linear.h"
+
+namespace qnf4 {
+namespace {
+
+using Cfg = CfgBig8;
+constexpr int kT = Cfg::kThreads;
+
+// --------------------------------------------------------- operands and scales
+
+__device__ __forceinline__ float adapter_at(const void *p, bool bf16, int64_t i) {
+  return bf16 ? static_cast<float>(static_cast<const __bf16 *>(p)[i]) : static_cast<const float *>(p)[i];
+}
+
+struct PrepParams {
+  const void *A[2], *B[2];
+  bool bf16;
+  int64_t N, K, nb;
+  int r, rp;
+  const int8_t *absmax_q[2];
+  const float *dq_scale[2], *dq_mean[2];
+  float *cs[2];
+  // forward: Acat [2 rp][K], Bi [2 N][rp]; backward: At [K][2 rp], Bt [2][rp][N]
+  __bf16 *Acat, *Bi, *At, *Bt;
+  int64_t g_cs, g_a, g_b;   // workgroups of a segment
+};
+
+__device__ __forceinline__ void put8(__bf16 *dst, const float (&v)[8]) {
+  *reinterpret_cast<uint4 *>(dst) =
+      make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+__global__ __launch_bounds__(256) void k_gated_prep(const PrepParams p) {
+  int64_t g = blockIdx.x;
+  if (g < p.g_cs) {   // block scales, as k_adapter_finish forms them
+    const int64_t b0 = (g * 256 + threadIdx.x) * 4;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t e = b0 + u;
+      const int w = e >= p.nb;
+      const int64_t b = e - (w ? p.nb : 0);
+      if (e < 2 * p.nb) {
+        const float kd = __fdiv_rn(p.dq_scale[w][b / kDqBlock], 127.0f);
+        p.cs[w][b] = __fadd_rn(__fmul_rn(static_cast<float>(p.absmax_q[w][b]), kd), p.dq_mean[w][0]);
+      }
+    }
+    return;
+  }
+  g -= p.g_cs;
+  float v[8];
+  if (g < p.g_a) {
+    const int64_t i = g * 256 + threadIdx.x;
+    if (p.Acat) {   // row j of both, eight columns
+      const int64_t k8 = p.K / 8;
+      if (i >= 2 * p.rp * k8) return;
+      const int row = static_cast<int>(i / k8), w = row >= p.rp, j = row - w * p.rp;
+      const int64_t k = (i - row * k8) * 8;
+#pragma unroll
+      for (int t = 0; t < 8; ++t) v[t] = j < p.r ? adapter_at(p.A[w], p.bf16, j * p.K + k + t) : 0.0f;
+      put8(p.Acat + row * p.K + k, v);
+    } else {        // column k, eight rows; consecutive lanes take consecutive k
+      const int q8 = 2 * p.rp / 8;
+      if (i >= p.K * q8) return;
+      const int q = static_cast<int>(i / p.K), w = 8 * q >= p.rp, j = 8 * q - w * p.rp;
+      const int64_t k = i - q * p.K;
+#pragma unroll
+      for (int t = 0; t < 8; ++t) v[t] = j + t < p.r ? adapter_at(p.A[w], p.bf16, (j + t) * p.K + k) : 0.0f;
+      put8(p.At + k * 2 * p.rp + 8 * q, v);
+    }
+    return;
+  }
+  g -= p.g_a;
+  const int64_t i = g * 256 + threadIdx.x;
+  if (p.Bi) {       // eight columns of row n, in the tiles' order of rows
+    const int q8 = p.rp / 8;
+    if (i >= 2 * p.N * q8) return;
+    const int64_t row = i / q8, n = 32 * (row >> 6) + (row & 31);
+    const int w = static_cast<int>(row >> 5) & 1, j = static_cast<int>(i - row * q8) * 8;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) v[t] = j + t < p.r ? adapter_at(p.B[w], p.bf16, n * p.r + j + t) : 0.0f;
+    put8(p.Bi + row * p.rp + j, v);
+  } else {          // eight rows n of column j; consecutive lanes take consecutive j
+    if (i >= 2 * p.rp * (p.N / 8)) return;
+    const int64_t part = i / p.rp;
+    const int j = static_cast<int>(i - part * p.rp), w = part >= p.N / 8;
+    const int64_t n = (part - (w ? p.N / 8 : 0)) * 8;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) v[t] = j < p.r ? adapter_at(p.B[w], p.bf16, (n + t) * p.r + j) : 0.0f;
+    put8(p.Bt + (static_cast<int64_t>(w) * p.rp + j) * p.N + n, v);
+  }
+}
+
+// ------------------------------------------------------- adapter down products
+
+// Split partials of P Q^T, both bf16, for one or two such products beside each
+// other: a workgroup has 128 rows of P by BN rows of Q over some 64-deep steps,
+// copied into a ring of four stages three steps ahead. Behind the last step it
+// is copied again, into a stage that nobody reads any more, so that every wait
+// is for the same number of copies.
+struct DownParams {
+  const void *P[2], *Q[2];
+  float *part;        // [splits][M][ld]
+  int64_t M, L;       // L: the reduction, row length of P and Q
+  int rows;           // rows of each Q
+  int ld;
+  int tiles_n, tiles_m, tiles;   // of one product; of all
+  int steps, per;     // 64-deep steps, and those of a split
+};
+
+template <int BN>
+__global__ __launch_bounds__(256, 1) void k_gated_down(const DownParams p) {
+  using C = TileCfg<128, BN, 2, 2>;
+  using RowsP = DirectRowsT<256, 128>;
+  using RowsQ = DirectRowsT<256, BN>;
+  constexpr int kCopies = RowsP::kPerWave + RowsQ::kPerWave;
+  __shared__ __attribute__((aligned(16))) __bf16 ring[4][C::kLdsA + C::kLdsB];
+  const int z = static_cast<int>(blockIdx.x) / p.tiles, t = static_cast<int>(blockIdx.x) - z * p.tiles;
+  const int one = p.tiles_m * p.tiles_n, w = t >= one, in = t - w * one;
+  const int64_t m0 = static_cast<int64_t>(in / p.tiles_n) * 128;
+  const int j0 = in % p.tiles_n * BN;
+  const int s0 = z * p.per, n = min(p.per, p.steps - s0);
+  const int64_t k0 = static_cast<int64_t>(s0) * kBK;
+  const RowsP rp(static_cast<const __bf16 *>(w ? p.P[1] : p.P[0]) + k0, p.L, p.M, m0);
+  const RowsQ rq(static_cast<const __bf16 *>(w ? p.Q[1] : p.Q[0]) + k0, p.L, p.rows, j0);
+  auto issue = [&](int s, int stage) {
+    const int64_t red = static_cast<int64_t>(min(s, n - 1)) * kBK;
+    rp.issue(red, ring[stage]);
+    rq.issue(red, ring[stage] + C::kLdsA);
+  };
+#pragma unroll
+  for (int s = 0; s < 3; ++s) issue(s, s);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const FragAddr<C::WTM> fa(wave / C::WAVES_N * C::WTM, lane);
+  const FragAddr<C::WTN> fb(wave % C::WAVES_N * C::WTN, lane);
+  Acc<C> acc;
+  acc.zero();
+  for (int s = 0; s < n; ++s) {
+    RowsP::template wait_copies<2 * kCopies>();
+    __syncthreads();   // the step has landed, and everybody is done with the one before
+    issue(s + 3, (s + 3) & 3);
+    const __bf16 *stage = ring[s & 3];
+    mma_step<C>(acc, stage, stage + C::kLdsA, fa, fb);
+  }
+  RowsP::template wait_copies<0>();
+  store_f32<C>(acc, p.part + static_cast<int64_t>(z) * p.M * p.ld + w * p.rows, p.ld, p.M, p.rows, m0, j0);
+}
+
+// out = bf16(scale * the sum of the partials, in split order).
+__global__ __launch_bounds__(256) void k_gated_sum(const float *part, int splits, int64_t n, float scale, __bf16 *out) {
+  const int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (e >= n) return;
+  const float4 v = split_sum4(part, n, e, splits);
+  *reinterpret_cast<uint2 *>(out + e) = make_uint2(pack_bf16x2(scale * v.x, scale * v.y), pack_bf16x2(scale * v.z, scale * v.w));
+}
+
+// ------------------------------------------------------------------ forward
+
+struct FwdParams {
+  const void *X;            // bf16 [M, K]
+  const uint8_t *codes[2];  // [N, K] each
+  const float *cs[2];
+  const void *Hs;           // bf16 [M, 2 rp]
+  const void *Bi;           // bf16 [2 N, rp], rows as the tiles'
+  __bf16 *H, *G, *U;        // bf16 [M, N]; G and U or null
+  int64_t M, N, K;
+  int rp;
+  float *part;              // fp32 [S][M][2 N], columns as the tiles' rows (S > 1)
+  int S, per;
+};
+
+// The rows of a tile: row R of the interleaved weight is row 32 (R / 64) + R %
+// 32 of the gate (R / 32 even) or of the other one. A wave decodes 32 rows, all
+// of one weight.
+struct PairRows {
+  using One = Nf4RowBigT<kT>;
+  static_assert(One::CH == 1, "a row half a thread");
+  static constexpr int kLoads = One::kLoads, kWrites = One::kWrites;
+  using Pairs = One::Pairs;
+  One one;
+  __device__ PairRows(const FwdParams &p, int64_t n0) : one(p.codes[0], p.cs[0], p.N, p.K, 0) {
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+    const int up = wave & 1;
+    const int64_t first = n0 + 32 * (wave >> 1);
+    one.cbase = (up ? p.codes[1] : p.codes[0]) + min(first, p.N - 1) * p.K / 2;
+    one.sbase = (up ? p.cs[1] : p.cs[0]) + min(first, p.N - 1) * p.K / kBlock;
+    // N is a multiple of 64: a wave's rows are all there or none of them
+    const int64_t row = first < p.N ? (threadIdx.x >> 1) & 31 : 0;
+    one.coff[0] = static_cast<uint32_t>(row * p.K / 2 + (threadIdx.x & 1) * 16);
+    one.soff[0] = static_cast<uint32_t>(row * p.K / kBlock);
+  }
+  __device__ __forceinline__ void load(int64_t red0) { one.load(red0); }
+  __device__ __forceinline__ void lookup(Pairs &q, const float2 *lv2, int i) const { one.lookup(q, lv2, i); }
+  __device__ __forceinline__ void finish(__bf16 *lds, const Pairs &q, int i) const { one.finish(lds, q, i); }
+  __device__ __forceinline__ void store_part(__bf16 *lds, const float2 *lv2, int i) const { one.store_part(lds, lv2, i); }
+};
+
+// 256 rows by 128 columns of H: a wave ends with 128 rows of 32 columns, the
+// gate's sums in its first fragment column and the other weight's in its second.
+__global__ __launch_bounds__(kT, 1) void k_gated_fwd(const FwdParams p, const Nf4Tables tab) {
+  static_assert(Cfg::TN == 2, "a fragment column of each weight");
+  __shared__ __attribute__((aligned(16))) __bf16 sa0[Cfg::kLdsA], sa1[Cfg::kLdsA];
+  __shared__ __attribute__((aligned(16))) __bf16 sb0[Cfg::kLdsB], sb1[Cfg::kLdsB];
+  const BigSmem smem{sa0, sa1, sb0, sb1};
+  __shared__ float2 lv_tab[256 * kLvCopies];
+  const float2 *lv = load_level_pairs(lv_tab, tab);
+  const int tiles_m = static_cast<int>((p.M + 255) / 256), tiles_n = static_cast<int>((p.N + 127) / 128);
+  const int tiles = tiles_m * tiles_n;
+  const int z = static_cast<int>(blockIdx.x) / tiles;
+  int tm, tn;
+  tile_of(static_cast<int>(blockIdx.x) - z * tiles, tiles_m, tiles_n, tm, tn);
+  const int64_t n0 = static_cast<int64_t>(tn) * 128, m0 = static_cast<int64_t>(tm) * 256;
+  const int s0 = z * p.per, s1 = min(static_cast<int>(p.K / kBK), s0 + p.per);
+  __syncthreads();
+  Acc<Cfg> acc;
+  acc.zero();
+  {
+    DirectRowsT<kT> da(static_cast<const __bf16 *>(p.X) + static_cast<int64_t>(s0) * kBK, p.K, p.M, m0);
+    PairRows l0(p, n0), l1 = l0;
+    auto load = [s0](PairRows &l, int s) { l.load(static_cast<int64_t>(s0 + s) * kBK); };
+    big_mainloop_nf4<Cfg>(acc, da, l0, l1, load, s1 - s0, smem, lv);
+  }
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int wm = w / Cfg::WAVES_N, wn = w % Cfg::WAVES_N;
+  if (p.rp > 0 && z == 0) {
+    // each weight's columns take its own half of Hs
+    const DirectRowsT<kT> ag(p.Hs, 2 * p.rp, p.M, m0), au(static_cast<const __bf16 *>(p.Hs) + p.rp, 2 * p.rp, p.M, m0);
+    const DirectRowsT<kT> db(p.Bi, p.rp, 2 * p.N, 2 * n0);
+    const FragAddr<Cfg::WTM> fa(wm * Cfg::WTM, lane);
+    const FragAddr<Cfg::WTN> fb(wn * Cfg::WTN, lane);
+    for (int s = 0; s < p.rp / kBK; ++s) {
+      const int64_t red = static_cast<int64_t>(s) * kBK;
+      ag.issue(red, sa0);
+      au.issue(red, sa1);
+      db.issue(red, sb0);
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const __bf16 *sa = j ? sa1 : sa0;
+          const bf16x8 b = *reinterpret_cast<const bf16x8 *>(sb0 + fb.off[kk] + j * 32 * kLDK);
+#pragma unroll
+          for (int i = 0; i < Cfg::TM; ++i) {
+            const bf16x8 a = *reinterpret_cast<const bf16x8 *>(sa + fa.off[kk] + i * 32 * kLDK);
+            acc.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc.v[i][j], 0, 0, 0);
+          }
+        }
+      __syncthreads();
+    }
+  }
+  if (p.S > 1) {
+    store_f32<Cfg>(acc, p.part + static_cast<int64_t>(z) * p.M * 2 * p.N, 2 * p.N, p.M, 2 * p.N, m0, 2 * n0);
+    return;
+  }
+  const int64_t n = n0 + 32 * wn + (lane & 31);
+  if (n >= p.N) return;
+#pragma unroll
+  for (int i = 0; i < Cfg::TM; ++i)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const int64_t m = m0 + wm * Cfg::WTM + i * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
+      if (m >= p.M) continue;
+      const float g = acc.v[i][0][v], u = acc.v[i][1][v];
+      p.H[m * p.N + n] = static_cast<__bf16>(gate_value(g, u));
+      if (p.G) {
+        p.G[m * p.N + n] = static_cast<__bf16>(g);
+        p.U[m * p.N + n] = static_cast<__bf16>(u);
+      }
+    }
+}
+
+// H (and G, U) of the summed partials, four columns a lane.
+__global__ __launch_bounds__(256) void k_gated_out(const float *part, int S, int64_t M, int64_t N, __bf16 *H, __bf16 *G, __bf16 *U) {
+  const int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (e >= M * N) return;
+  const int64_t m = e / N, n = e - m * N;
+  const int64_t at = m * 2 * N + 64 * (n >> 5) + (n & 31);
+  const float4 g = split_sum4(part, M * 2 * N, at, S), u = split_sum4(part, M * 2 * N, at + 32, S);
+  *reinterpret_cast<uint2 *>(H + e) = make_uint2(pack_bf16x2(gate_value(g.x, u.x), gate_value(g.y, u.y)),
+                                                 pack_bf16x2(gate_value(g.z, u.z), gate_value(g.w, u.w)));
+  if (G) {
+    *reinterpret_cast<uint2 *>(G + e) = make_uint2(pack_bf16x2(g.x, g.y), pack_bf16x2(g.z, g.w));
+    *reinterpret_cast<uint2 *>(U + e) = make_uint2(pack_bf16x2(u.x, u.y), pack_bf16x2(u.z, u.w));
+  }
+}
+
+// ----------------------------------------------------------------- backward
+
+constexpr int64_t kActGroups = 8192;
+
+// dG, dU, eight elements a lane and turn.
+__global__ __launch_bounds__(256) void k_gated_act(const void *dH, const void *G, const void *U, __bf16 *dG, __bf16 *dU, int64_t n) {
+  for (int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8; e < n; e += static_cast<int64_t>(gridDim.x) * 2048) {
+    const auto in = [e](const void *p) { return *reinterpret_cast<const uint4 *>(static_cast<const __bf16 *>(p) + e); };
+    const uint4 a = in(dH), b = in(G), c = in(U);
+    const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w}, wc[4] = {c.x, c.y, c.z, c.w};
+    float dg[8], du[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const auto part = [i](const uint32_t (&w)[4]) {
+        return __builtin_bit_cast(float, (i & 1) ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+      };
+      gate_backward(part(wa), part(wb), part(wc), dg[i], du[i]);
+    }
+    put8(dG + e, dg);
+    put8(dU + e, du);
+  }
+}
+
+struct DxParams {
+  const void *dG, *dU;      // bf16 [M, N]
+  const uint8_t *codes[2];
+  const float *cs[2];
+  const void *low;          // bf16 [M, 2 rp]
+  const void *At;           // bf16 [K, 2 rp]
+  void *dX;                 // bf16 [M, K]
+  int64_t M, N, K;
+  int rp;
+  float *part;              // fp32 [S][M][K] (S > 1)
+  int S, per;               // of the 2 N / 64 steps, the gate's in front
+};
+
+// Rows of dG for steps below N, of dU behind them.
+struct DualRows {
+  static constexpr int kPerWave = DirectRowsT<kT>::kPerWave;
+  DirectRowsT<kT> rows;
+  const char *base[2];
+  int64_t red0, N;
+  __device__ DualRows(const DxParams &p, int64_t m0, int64_t red0_)
+      : rows(p.dG, p.N, p.M, m0), base{rows.base, static_cast<const char *>(p.dU) + m0 * p.N * 2}, red0(red0_), N(p.N) {}
+  __device__ __forceinline__ void issue(int64_t red, __bf16 *lds) const { issue_range(red, lds, 0, kPerWave); }
+  __device__ __forceinline__ void issue_range(int64_t red, __bf16 *lds, int i0, int n) const {
+    red += red0;
+    const bool up = red >= N;
+    DirectRowsT<kT> r = rows;
+    r.base = up ? base[1] : base[0];
+    r.issue_range(up ? red - N : red, lds, i0, n);
+  }
+  template <int L>
+  __device__ __forceinline__ static void wait_copies() { DirectRowsT<kT>::wait_copies<L>(); }
+};
+
+__global__ __launch_bounds__(kT, 1) void k_gated_dx(const DxParams p, const Nf4Tables tab) {
+  __shared__ __attribute__((aligned(16))) __bf16 sa0[Cfg::kLdsA], sa1[Cfg::kLdsA];
+  __shared__ __attribute__((aligned(16))) __bf16 sb0[Cfg::kLdsB], sb1[Cfg::kLdsB];
+  const BigSmem smem{sa0, sa1, sb0, sb1};
+  __shared__ float2 lv_tab[256 * kLvCopies];
+  const float2 *lv = load_level_pairs(lv_tab, tab);
+  const int tiles_m = static_cast<int>((p.M + 255) / 256), tiles_k = static_cast<int>((p.K + 255) / 256);
+  const int tiles = tiles_m * tiles_k;
+  const int z = static_cast<int>(blockIdx.x) / tiles;
+  int tm, tn;
+  tile_of(static_cast<int>(blockIdx.x) - z * tiles, tiles_m, tiles_k, tm, tn);
+  const int64_t k0 = static_cast<int64_t>(tn) * 256, m0 = static_cast<int64_t>(tm) * 256;
+  const int s0 = z * p.per, s1 = min(static_cast<int>(2 * p.N / kBK), s0 + p.per);
+  __syncthreads();
+  Acc<Cfg> acc;
+  acc.zero();
+  {
+    const DualRows da(p, m0, static_cast<int64_t>(s0) * kBK);
+    Nf4TransBigT<kT> l0(p.codes[0], p.cs[0], p.K, k0), l1 = l0;
+    const uint8_t *const codes[2] = {p.codes[0] + k0 / 2, p.codes[1] + k0 / 2};
+    const float *const cs[2] = {p.cs[0] + k0 / kBlock, p.cs[1] + k0 / kBlock};
+    const int64_t K = p.K, N = p.N;
+    auto load = [&](Nf4TransBigT<kT> &l, int s) {
+      const int64_t red = static_cast<int64_t>(s0 + s) * kBK;
+      const bool up = red >= N;
+      l.cbase = up ? codes[1] : codes[0];
+      l.sbase = up ? cs[1] : cs[0];
+      l.load(up ? red - N : red, K);
+    };
+    big_mainloop_nf4<Cfg>(acc, da, l0, l1, load, s1 - s0, smem, lv);
+  }
+  if (p.rp > 0 && z == 0) {
+    const DirectRowsT<kT> da(p.low, 2 * p.rp, p.M, m0), db(p.At, 2 * p.rp, p.K, k0);
+    big_mainloop_dense<Cfg>(acc, da, db, 2 * p.rp / kBK, smem);
+  }
+  if (p.S > 1)
+    store_f32<Cfg>(acc, p.part + static_cast<int64_t>(z) * p.M * p.K, p.K, p.M, p.K, m0, k0);
+  else if (m0 + 256 <= p.M && k0 + 256 <= p.K)
+    store_bf16<Cfg, false>(acc, static_cast<__bf16 *>(p.dX), p.K, p.M, p.K, m0, k0, 1.0f);
+  else
+    store_bf16<Cfg, true>(acc, static_cast<__bf16 *>(p.dX), p.K, p.M, p.K, m0, k0, 1.0f);
+}
+
+// Split-M partials of the adapters' gradients: 64 x 256 tiles of [lg, lu]^T X
+// first, then 256 x 64 tiles of dG^T Hs_g and dU^T Hs_u.
+struct GradParams {
+  const void *X, *d[2], *Hs, *low;
+  float *a_part, *b_part;   // [splits][2 rp][K], [splits][2][N][rp]
+  int64_t M, N, K;
+  int rp;
+  int a_tiles_c, a_tiles, a_splits, a_steps;
+  int b_tiles_c, b_tiles, b_splits, b_steps;   // tiles: of one weight
+};
+
+using CfgGradA = TileCfg<64, 256, 1, 4>;
+using CfgGradB = TileCfg<256, 64, 4, 1>;
+
+__global__ __launch_bounds__(256) void k_gated_grad(const GradParams p) {
+  __shared__ __attribute__((aligned(16))) __bf16 smem[2 * (CfgGradA::kLdsA + CfgGradA::kLdsB)];
+  int g = blockIdx.x;
+  const bool is_a = g < p.a_tiles * p.a_splits;
+  if (!is_a) g -= p.a_tiles * p.a_splits;
+  const int tiles = is_a ? p.a_tiles : 2 * p.b_tiles;
+  const int per = is_a ? p.a_steps : p.b_steps;
+  const int z = g / tiles;
+  int t = g % tiles;
+  const int total = static_cast<int>((p.M + kBK - 1) / kBK);
+  const int s0 = z * per, steps = min(per, total - s0);
+  // rows of this split's range only: the two-stage loop reads past its end
+  const int64_t red_end = min(p.M, static_cast<int64_t>(s0 + steps) * kBK);
+  if (is_a) {
+    const int64_t c0 = static_cast<int64_t>(t % p.a_tiles_c) * 256, r0 = static_cast<int64_t>(t / p.a_tiles_c) * 64;
+    Acc<CfgGradA> acc;
+    acc.zero();
+    TransBf16Narrow<64, 256> la(p.low, 2 * p.rp, red_end, r0), la1 = la;
+    TransBf16<256, 256> lb(p.X, p.K, red_end, p.K, c0), lb1 = lb;
+    mainloop2<CfgGradA>(acc, la, la1, lb, lb1, static_cast<int64_t>(s0) * kBK, steps, smem);
+    store_f32<CfgGradA>(acc, p.a_part + static_cast<int64_t>(z) * 2 * p.rp * p.K, p.K, 2 * p.rp, p.K, r0, c0);
+  } else {
+    const int w = t >= p.b_tiles;
+    t -= w * p.b_tiles;
+    const int64_t c0 = static_cast<int64_t>(t % p.b_tiles_c) * 64, r0 = static_cast<int64_t>(t / p.b_tiles_c) * 256;
+    Acc<CfgGradB> acc;
+    acc.zero();
+    TransBf16<256, 256> la(w ? p.d[1] : p.d[0], p.N, red_end, p.N, r0), la1 = la;
+    TransBf16Narrow<64, 256> lb(p.Hs, 2 * p.rp, red_end, w * p.rp + c0), lb1 = lb;
+    mainloop2<CfgGradB>(acc, la, la1, lb, lb1, static_cast<int64_t>(s0) * kBK, steps, smem);
+    store_f32<CfgGradB>(acc, p.b_part + (2 * static_cast<int64_t>(z) + w) * p.N * p.rp, p.rp, p.N, p.rp, r0, c0);
+  }
+}
+
+struct GradSumParams {
+  const float *a_part, *b_part;
+  void *dA[2], *dB[2];
+  bool bf16;
+  int64_t N, K;
+  int r, rp, a_splits, b_splits;
+};
+
+__global__ __launch_bounds__(256) void k_gated_grad_sum(const GradSumParams p) {
+  const int64_t na = p.r * p.K, nb = p.N * p.r, n = 2 * (na + nb);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
+    float v;
+    void *to;
+    int64_t e;
+    if (i < 2 * na) {
+      const int w = i >= na;
+      e = i - w * na;
+      v = split_sum(p.a_part, 2 * p.rp * p.K, w * p.rp * p.K + e, p.a_splits);
+      to = p.dA[w];
+    } else {
+      const int64_t b = i - 2 * na;
+      const int w = b >= nb;
+      e = b - w * nb;
+      const int64_t row = e / p.r;
+      v = split_sum(p.b_part, 2 * p.N * p.rp, (w * p.N + row) * p.rp + (e - row * p.r), p.b_splits);
+      to = p.dB[w];
+    }
+    if (p.bf16) static_cast<__bf16 *>(to)[e] = static_cast<__bf16>(v);
+    else static_cast<float *>(to)[e] = v;
+  }
+}
+
+// dX = bf16(sum of the partials, in split order).
+__global__ __launch_bounds__(256) void k_gated_dx_sum(const float *part, int S, int64_t plane, __bf16 *out) {
+  const int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (e >= plane) return;
+  const float4 v = split_sum4(part, plane, e, S);
+  *reinterpret_cast<uint2 *>(out + e) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
+// -------------------------------------------------------------------- plan
+
+struct Plan {
+  int rp;
+  Split down, gemm, ga, gb;
+};
+
+Plan make_plan(int64_t M, int64_t N, int64_t K, int r, bool backward) {
+  Plan pl{};
+  pl.rp = gated_padded_rank(r);
+  const int64_t tiles_m = grid_blocks(M, 256);
+  if (!backward) {
+    pl.gemm = gemm_split(tiles_m * grid_blocks(N, 128), static_cast<int>(K / kBK), M, 2 * N, true);
+    if (r) pl.down = choose_split(grid_blocks(M, 128) * (2 * pl.rp / 128), static_cast<int>(K / kBK), 64, kCus);
+    return pl;
+  }
+  pl.gemm = gemm_split(tiles_m * grid_blocks(K, 256), static_cast<int>(2 * N / kBK), M, K, true);
+  if (r) {
+    pl.down = choose_split(grid_blocks(M, 128) * 2 * (pl.rp / 64), static_cast<int>(N / kBK), 64, kCus);
+    const int msteps = static_cast<int>(ceil_div(M, kBK));
+    pl.ga = choose_split(grid_blocks(K, 256) * (2 * pl.rp / 64), msteps, 8);
+    pl.gb = choose_split(2 * grid_blocks(N, 256) * (pl.rp / 64), msteps, 8);
+  }
+  return pl;
+}
+
+struct Buffers {
+  float *cs[2], *part, *down, *ga, *gb;
+  __bf16 *Acat, *Bi, *At, *Bt, *low, *dG, *dU, *Hs;
+};
+
+size_t carve(void *ws, const Plan &pl, int64_t M, int64_t N, int64_t K, bool backward, Buffers *b) {
+  Carve c{static_cast<char *>(ws)};
+  const int64_t nb = N * K / kBlock;
+  b->cs[0] = c.take<float>(nb);
+  b->cs[1] = c.take<float>(nb);
+  if (pl.gemm.splits > 1) b->part = c.take<float>(static_cast<size_t>(pl.gemm.splits) * M * (backward ? K : 2 * N));
+  const size_t cols = 2 * static_cast<size_t>(pl.rp);
+  if (pl.rp) b->down = c.take<float>(pl.down.splits * M * cols);
+  if (!backward) {
+    if (pl.rp) {
+      b->Acat = c.take<__bf16>(cols * K);
+      b->Bi = c.take<__bf16>(cols * N);
+      b->Hs = c.take<__bf16>(cols * M);
+    }
+    return c.off;
+  }
+  b->dG = c.take<__bf16>(static_cast<size_t>(M) * N);
+  b->dU = c.take<__bf16>(static_cast<size_t>(M) * N);
+  if (pl.rp) {
+    b->At = c.take<__bf16>(cols * K);
+    b->Bt = c.take<__bf16>(cols * N);
+    b->low = c.take<__bf16>(cols * M);
+    b->ga = c.take<float>(pl.ga.splits * cols * K);
+    b->gb = c.take<float>(pl.gb.splits * cols * N);
+  }
+  return c.off;
+}
+
+unsigned blocks(int64_t n, int64_t per) { return static_cast<unsigned>(ceil_div(n, per)); }
+
+// Block scales and bf16 operands.
+void run_prep(const GatedArgs &a, const Plan &pl, const Buffers &b, bool backward, hipStream_t s) {
+  PrepParams p{};
+  for (int w = 0; w < 2; ++w) {
+    p.A[w] = a.A[w];
+    p.B[w] = a.B[w];
+    p.absmax_q[w] = a.w[w].absmax_q;
+    p.dq_scale[w] = a.w[w].dq_scale;
+    p.dq_mean[w] = a.w[w].dq_mean;
+    p.cs[w] = b.cs[w];
+  }
+  p.bf16 = a.adapter_bf16;
+  p.N = a.N;
+  p.K = a.K;
+  p.nb = a.N * a.K / kBlock;
+  p.r = a.r;
+  p.rp = pl.rp;
+  if (backward) p.At = b.At, p.Bt = b.Bt;
+  else p.Acat = b.Acat, p.Bi = b.Bi;
+  p.g_cs = fmt_dq(a.format) ? ceil_div(2 * p.nb, 1024) : 0;
+  if (pl.rp) {
+    p.g_a = ceil_div(2 * pl.rp * a.K / 8, 256);
+    p.g_b = ceil_div(2 * pl.rp * a.N / 8, 256);
+  }
+  const int64_t groups = p.g_cs + p.g_a + p.g_b;
+  if (groups > 0) k_gated_prep<<<static_cast<unsigned>(groups), 256, 0, s>>>(p);
+}
+
+const float *scales(const GatedArgs &a, const Buffers &b, int w) { return fmt_dq(a.format) ? b.cs[w] : a.w[w].absmax; }
+
+}  // namespace
+
+size_t gated_ws_bytes(int64_t M, int64_t N, int64_t K, int r, bool backward) {
+  Buffers b{};
+  return carve(nullptr, make_plan(M, N, K, r, backward), M, N, K, backward, &b);
+}
+
+hipError_t launch_gated_fwd(const GatedArgs &a, const void *X, void *H, void *G, void *U, void *Hs, void *ws, hipStream_t s) {
+  const Plan pl = make_plan(a.M, a.N, a.K, a.r, false);
+  Buffers b{};
+  carve(ws, pl, a.M, a.N, a.K, false, &b);
+  if (Hs) b.Hs = static_cast<__bf16 *>(Hs);
+  run_prep(a, pl, b, false, s);
+  if (pl.rp) {
+    DownParams d{};
+    d.P[0] = X;
+    d.Q[0] = b.Acat;
+    d.part = b.down;
+    d.M = a.M;
+    d.L = a.K;
+    d.rows = d.ld = 2 * pl.rp;
+    d.tiles_n = 2 * pl.rp / 128;
+    d.tiles_m = static_cast<int>(ceil_div(a.M, 128));
+    d.tiles = d.tiles_m * d.tiles_n;
+    d.steps = static_cast<int>(a.K / kBK);
+    d.per = pl.down.steps_per_split;
+    k_gated_down<128><<<static_cast<unsigned>(d.tiles * pl.down.splits), 256, 0, s>>>(d);
+    const int64_t n = a.M * 2 * pl.rp;
+    k_gated_sum<<<blocks(n, 1024), 256, 0, s>>>(b.down, pl.down.splits, n, a.scale, b.Hs);
+  }
+  FwdParams p{X, {a.w[0].codes, a.w[1].codes}, {scales(a, b, 0), scales(a, b, 1)}, b.Hs, b.Bi, static_cast<__bf16 *>(H),
+              static_cast<__bf16 *>(G), static_cast<__bf16 *>(U), a.M, a.N, a.K, pl.rp, b.part, pl.gemm.splits,
+              pl.gemm.steps_per_split};
+  const int64_t tiles = grid_blocks(a.M, 256) * grid_blocks(a.N, 128);
+  k_gated_fwd<<<static_cast<unsigned>(tiles * pl.gemm.splits), kT, 0, s>>>(p, format_tables(a.format));
+  if (pl.gemm.splits > 1) k_gated_out<<<blocks(a.M * a.N, 1024), 256, 0, s>>>(b.part, pl.gemm.splits, a.M, a.N, p.H, p.G, p.U);
+  return hipGetLastError();
+}
+
+hipError_t launch_gated_bwd(const GatedArgs &a, const void *dH, const void *X, const void *G, const void *U, const void *Hs,
+                            void *dX, void *const (&dA)[2], void *const (&dB)[2], void *ws, hipStream_t s) {
+  const Plan pl = make_plan(a.M, a.N, a.K, a.r, true);
+  Buffers b{};
+  carve(ws, pl, a.M, a.N, a.K, true, &b);
+  run_prep(a, pl, b, true, s);
+  const int64_t n = a.M * a.N;
+  k_gated_act<<<static_cast<unsigned>(std::min(ceil_div(n, 2048), kActGroups)), 256, 0, s>>>(dH, G, U, b.dG, b.dU, n);
+  if (pl.rp) {
+    DownParams d{};
+    d.P[0] = b.dG;
+    d.P[1] = b.dU;
+    d.Q[0] = b.Bt;
+    d.Q[1] = b.Bt + pl.rp * a.N;
+    d.part = b.down;
+    d.M = a.M;
+    d.L = a.N;
+    d.rows = pl.rp;
+    d.ld = 2 * pl.rp;
+    d.tiles_n = pl.rp / 64;
+    d.tiles_m = static_cast<int>(ceil_div(a.M, 128));
+    d.tiles = 2 * d.tiles_m * d.tiles_n;
+    d.steps = static_cast<int>(a.N / kBK);
+    d.per = pl.down.steps_per_split;
+    k_gated_down<64><<<static_cast<unsigned>(d.tiles * pl.down.splits), 256, 0, s>>>(d);
+    const int64_t count = a.M * 2 * pl.rp;
+    k_gated_sum<<<blocks(count, 1024), 256, 0, s>>>(b.down, pl.down.splits, count, a.scale, b.low);
+  }
+  DxParams p{b.dG, b.dU, {a.w[0].codes, a.w[1].codes}, {scales(a, b, 0), scales(a, b, 1)}, b.low, b.At, dX, a.M, a.N, a.K,
+             pl.rp, b.part, pl.gemm.splits, pl.gemm.steps_per_split};
+  const int64_t tiles = grid_blocks(a.M, 256) * grid_blocks(a.K, 256);
+  k_gated_dx<<<static_cast<unsigned>(tiles * pl.gemm.splits), kT, 0, s>>>(p, format_tables(a.format));
+  if (pl.gemm.splits > 1)
+    k_gated_dx_sum<<<blocks(a.M * a.K, 1024), 256, 0, s>>>(b.part, pl.gemm.splits, a.M * a.K, static_cast<__bf16 *>(dX));
+  if (pl.rp) {
+    GradParams g{};
+    g.X = X;
+    g.d[0] = b.dG;
+    g.d[1] = b.dU;
+    g.Hs = Hs;
+    g.low = b.low;
+    g.a_part = b.ga;
+    g.b_part = b.gb;
+    g.M = a.M;
+    g.N = a.N;
+    g.K = a.K;
+    g.rp = pl.rp;
+    g.a_tiles_c = static_cast<int>(grid_blocks(a.K, 256));
+    g.a_tiles = g.a_tiles_c * (2 * pl.rp / 64);
+    g.a_splits = pl.ga.splits;
+    g.a_steps = pl.ga.steps_per_split;
+    g.b_tiles_c = pl.rp / 64;
+    g.b_tiles = g.b_tiles_c * static_cast<int>(grid_blocks(a.N, 256));
+    g.b_splits = pl.gb.splits;
+    g.b_steps = pl.gb.steps_per_split;
+    k_gated_grad<<<static_cast<unsigned>(g.a_tiles * g.a_splits + 2 * g.b_tiles * g.b_splits), 256, 0, s>>>(g);
+    const GradSumParams q{b.ga, b.gb, {dA[0], dA[1]}, {dB[0], dB[1]}, a.adapter_bf16, a.N, a.K, a.r, pl.rp, pl.ga.splits, pl.gb.splits};
+    const int64_t count = 2 * a.r * (a.N + a.K);
+    k_gated_grad_sum<<<static_cast<unsigned>(std::min<int64_t>(ceil_div(count, 256), 4096)), 256, 0, s>>>(q);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace qnf4

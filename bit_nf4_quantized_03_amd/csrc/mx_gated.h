@@ -12,6 +12,7 @@
 // rows.
 #pragma once
 
+#include "gate.h"
 #include "mx_product.h"
 
 namespace qnf4 {
@@ -23,12 +24,6 @@ struct MxGatedOut {
   uint32_t pitch;
   int type;
 };
-
-// In fp32; e^-g past the largest fp32 makes the product the zero that it is
-// next to. The exponential and the reciprocal are the hardware's, within 1 ulp.
-__device__ __forceinline__ float gate_value(float g, float u) {
-  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g)) * u;
-}
 
 // Columns n .. n + 7 of row m. Microscaled: the four lanes of a quad hold one
 // block of 32 and all of them are here; `on` says whether to store.

@@ -57,6 +57,63 @@ int qlora_mx_gated(const qlora_mx_matrix *X, const qlora_mx_matrix *W, void *H, 
 int qlora_mx_gated_grouped(const qlora_mx_matrix *X, const qlora_mx_matrix *W, const int32_t *offsets,
                            int32_t experts, void *H, const qlora_mx_matrix *Hq, void *stream);
 
+/* ------------------------------------------------ the gated block, with adapters
+ *
+ *     G = X Wg^T + s (X Ag^T) Bg^T,  U = X Wu^T + s (X Au^T) Bu^T,  H = silu(G) * U
+ *
+ * around two frozen 4-bit weights [N, K] of the same shape and format (N and K
+ * multiples of 64), each with an adapter of the same rank or both without.
+ */
+
+/* A [r, K] and B [N, r] of each weight, fp32 or bf16 (dtype), 1 <= r <= 256. */
+typedef struct {
+  const void *gate_A, *gate_B, *up_A, *up_B;
+  int32_t r;
+  int32_t dtype;
+  float scale;
+} qlora_gated_adapters;
+
+/* Columns of the kept adapter activations, 2 * 64 ceil(r / 64) (0 for an invalid r and for 0). Host-only. */
+int64_t qlora_gated_saved_cols(int32_t r);
+
+/* Workspace bytes of qlora_gated_fwd (backward = 0) and qlora_gated_bwd (1); 0
+ * for invalid sizes. No contents are expected or kept. Host-only. */
+size_t qlora_gated_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r, int32_t backward);
+
+/*
+ * Forward. X bf16 [M, K]; adapters NULL: none. H bf16 [M, N], rounded once.
+ * What the backward takes is written where it is asked for:
+ *   G, U  bf16 [M, N], both or neither (NULL)
+ *   Hs    bf16 [M, qlora_gated_saved_cols(r)], s X Ag^T and s X Au^T, each padded
+ *         to a multiple of 64 columns with zeros; with G and U and adapters,
+ *         NULL otherwise
+ * M up to 2^24, N and K up to 2^23, M N, M K and N K up to 2^36. The decoded
+ * weights, A, B and Hs enter the sums as bf16; sums and silu are fp32, in a
+ * fixed order (deterministic).
+ */
+int qlora_gated_fwd(const void *X, int64_t M, const qlora_nf4_weight *gate, const qlora_nf4_weight *up,
+                    const qlora_gated_adapters *adapters, void *H, void *G, void *U, void *Hs, void *ws,
+                    size_t ws_bytes, void *stream);
+
+/* Gradients of the adapters, in their type. */
+typedef struct {
+  void *gate_A, *gate_B, *up_A, *up_B;
+} qlora_gated_grads;
+
+/*
+ * Backward, from the forward's X, G, U and Hs (of the same adapters):
+ *     dG = dH U t (1 + G (1 - t)),  dU = dH G t,  t = 1 / (1 + e^-G)
+ *     lg = s dG Bg,  lu = s dU Bu
+ *     dX = dG Wg + dU Wu + lg Ag + lu Au
+ *     dAg = lg^T X,  dBg = dG^T Hs_g,  dAu = lu^T X,  dBu = dU^T Hs_u
+ * dH, dX bf16; dX overlaps no input. grads NULL without adapters.
+ * dG, dU, lg and lu are rounded to bf16, each sum is fp32 in a fixed order and
+ * rounded once.
+ */
+int qlora_gated_bwd(const void *dH, const void *X, const void *G, const void *U, const void *Hs, int64_t M,
+                    const qlora_nf4_weight *gate, const qlora_nf4_weight *up, const qlora_gated_adapters *adapters,
+                    void *dX, const qlora_gated_grads *grads, void *ws, size_t ws_bytes, void *stream);
+
 /* ------------------------------------------------------------ rotary positions
  *
  * Pair i of a head, (a, b), of the token at position t becomes

@@ -1,0 +1,504 @@
+"""GPU parity of the gated feed-forward block with adapters, forward and
+backward, against the fp64 oracle (oracle/block.py).
+
+Bars. A bf16 rounding is off by at most 2^-8 of the value, uniformly within its
+step: 2^-8 / sqrt(3) = 2.26e-3 (r, below) of a tensor in the root mean square, and
+as much of a sum of products one of whose factors is rounded, since the errors
+are independent. Counting the roundings of each result, squared and added:
+  G, U   decoded weights, the store                      sqrt(2) r          3.2e-3
+  H      weights of G and of U, and its own; the gate passes 1.1 of G's     sqrt(1.21 + 1 + 1) r  4.1e-3
+  dX     G and U (2 each, 1.21 of G's twice over in dG and dU), dG and dU,
+         weights, its own                                sqrt(2.42 + 2 + 1 + 1 + 1) r   6.2e-3
+  dA     dX's in dG and dU, B, l, and its own in bf16    sqrt(5.42 + 1 + 1 + 1) r    6.6e-3
+  dB     dX's in dG and dU, A, Hs, and its own in bf16   the same
+asserted at 7e-3 for the gradients and 4.5e-3 for H and the kept G, U (their sums
+with an adapter add its three roundings, of a term that is smaller than the
+base's here). Every 256 x 256 tile is held to 2e-2. The exact pins below leave no
+such room: they compare bit for bit.
+
+These speak of many roundings beside each other. In Hs and in the gradients of
+A and B everything passes through the M r sums of Hs or of l, and one such sum
+may be far smaller than its terms and so its error as large as it (M = r = 1: all
+of dA is one l times X). They are asserted from 512 such sums on. Of any number
+each element has its bound by cases, every rounding at its largest:
+  l    s sum (2^-8 |dG| |B| + |dG| |B - bf16(B)|) + 2^-8 |l|
+  dA   sum over rows of l's |X|,   dB  sum over rows 2^-8 |dG| |Hs|
+  dX   sum 2^-8 * 2 |dG| |Wg|, likewise of the other, and of l's |A| + 2^-8 |l| |A|
+from the kept G, U and Hs, each with half a step of its own, 2^-8, and fp32 sums'
+2^-23 for each term.
+"""
+import numpy as np
+import pytest
+
+from oracle import block
+from tests import gpu_util as gu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def qb():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import bit_nf4_quantized_03_amd as m
+    return m
+
+
+def f64(t):
+    return None if t is None else t.detach().cpu().double().numpy()
+
+
+class Data:
+    def __init__(self, qb, M, N, K, r, fmt=0, bf16=True, seed=0, weight=True):
+        import torch
+        gen = torch.Generator(device="cuda")
+        gen.manual_seed(seed + M + N + K + r)
+        rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+        self.X, self.dH = rnd(M, K).bfloat16(), (0.1 * rnd(M, N)).bfloat16()
+        self.gate, self.up = (qb.qlora_nf4_quantize((rnd(N, K) * (weight / K ** 0.5)).bfloat16(), fmt=fmt) for _ in range(2))
+        self.factors, self.scale = (None,) * 4, 0.0
+        if r:
+            dt = torch.bfloat16 if bf16 else torch.float32
+            a, b = 0.7 / K ** 0.5, 0.7 / r ** 0.5
+            self.factors = tuple((rnd(*s) * std).to(dt) for s, std in (((r, K), a), ((N, r), b), ((r, K), a), ((N, r), b)))
+            self.scale = 0.75
+        self.args = (self.gate, self.up, *self.factors, self.scale)
+        self.qb = qb
+
+    def oracle(self):
+        """(h, g, u, gradients)"""
+        w = [f64(self.qb.qlora_nf4_dequantize(x)) for x in (self.gate, self.up)]
+        ad = None if self.factors[0] is None else [f64(t) for t in self.factors]
+        x = f64(self.X)
+        return (*block.feed_forward(x, *w, ad, self.scale), block.feed_forward_backward(f64(self.dH), x, *w, ad, self.scale))
+
+
+def near(got, ref, bar, label):
+    assert tuple(got.shape) == ref.shape, label
+    g = f64(got)
+    e = gu.rel_fro(g, ref)
+    assert e <= bar, f"{label}: {e:.2e} > {bar}"
+    e = gu.max_tile_rel(g, ref)
+    assert e <= 2e-2, f"{label}: a tile is {e:.2e} off"
+
+
+GRADS = ("dX", "dAg", "dBg", "dAu", "dBu")
+MANY = 512
+STEP = 2.0 ** -8
+
+
+def within(got, ref, bound, label):
+    err = np.abs(f64(got) - ref)
+    assert (err <= bound + 1e-30).all(), f"{label}: worst {np.nanmax(err / (bound + 1e-30))} of the bound by cases"
+
+
+def rounded(t):
+    import torch
+    return f64(t.to(torch.bfloat16))
+
+
+def check_backward_by_cases(d, out, G, U, Hs):
+    """Every gradient against the formula at the kept G, U and Hs, element by element."""
+    qb, x, dh = d.qb, np.abs(f64(d.X)), f64(d.dH)
+    big = 1 + 2.0 ** -7                                     # a rounded value's own step, and the gate's fp32 arithmetic
+    sides, dx, dxb = [], 0.0, 0.0
+    for w, dd in zip((d.gate, d.up), block.gate_backward(dh, f64(G), f64(U))):
+        wv = f64(qb.qlora_nf4_dequantize(w))
+        dx = dx + dd @ wv
+        dxb = dxb + big * (2 * STEP + 2.0 ** -23 * wv.shape[0]) * (np.abs(dd) @ np.abs(wv))
+        sides.append(dd)
+    if Hs is not None:
+        r, cols, s, hs = d.factors[0].shape[0], Hs.shape[1], d.scale, f64(Hs)
+        for i, dd in enumerate(sides):
+            a, b = f64(d.factors[2 * i]), f64(d.factors[2 * i + 1])
+            sums = 2.0 ** -23 * b.shape[0]
+            low = s * dd @ b
+            lowb = big * s * ((STEP + sums) * np.abs(dd) @ np.abs(b) + np.abs(dd) @ np.abs(b - rounded(d.factors[2 * i + 1]))) + STEP * np.abs(low)
+            own = STEP if str(d.factors[0].dtype) == "torch.bfloat16" else 0.0
+            rows = 2.0 ** -23 * len(x)
+            da, db = low.T @ f64(d.X), dd.T @ hs[:, i * cols // 2:i * cols // 2 + r]
+            within(out[1 + 2 * i], da, big * (lowb.T @ x + rows * np.abs(low).T @ x) + own * np.abs(da), GRADS[1 + 2 * i])
+            h = np.abs(hs[:, i * cols // 2:i * cols // 2 + r])
+            within(out[2 + 2 * i], db, big * (STEP + rows) * np.abs(dd).T @ h + own * np.abs(db), GRADS[2 + 2 * i])
+            dx = dx + low @ a
+            dxb = dxb + big * (lowb @ np.abs(a) + (STEP + 2.0 ** -23 * r) * np.abs(low) @ np.abs(a))
+    within(out[0], dx, dxb + STEP * (np.abs(dx) + dxb), "dX")
+
+# tiles that fill less than half the GPU split their reduction, the last two do not
+SHAPES = [(1, 64, 64, 0), (1, 64, 64, 1), (1, 1088, 512, 64), (5, 192, 128, 8), (17, 320, 576, 33), (32, 256, 1024, 64), (33, 128, 192, 65),
+          (130, 704, 512, 16), (257, 384, 640, 128), (300, 1024, 256, 200), (513, 576, 1152, 256), (4096, 1152, 256, 64), (4100, 1088, 2176, 24)]
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("M,N,K,r", SHAPES)
+def test_block(qb, M, N, K, r, bf16):
+    import torch
+    gu.announce(f"gated block {M}x{N}x{K} r={r} bf16={bf16}")
+    d = Data(qb, M, N, K, r, bf16=bf16)
+    h, g, u, grads = d.oracle()
+    H, G, U, Hs = qb.qlora_gated_fwd_save(d.X, *d.args)
+    for got, ref, label in ((H, h, "H"), (G, g, "G"), (U, u, "U")):
+        near(got, ref, 4.5e-3, label)
+    assert torch.equal(qb.qlora_gated_fwd(d.X, *d.args), H)
+    assert (Hs is None) == (r == 0)
+    if r:
+        cols = qb.qlora_gated_saved_cols(r)
+        assert Hs.shape == (M, cols) and not Hs[:, r:cols // 2].any() and not Hs[:, cols // 2 + r:].any()
+        for a, at in ((d.factors[0], 0), (d.factors[2], cols // 2)):
+            x, ref = np.abs(f64(d.X)), d.scale * (f64(d.X) @ f64(a).T)
+            off = d.scale * (x @ (np.abs(f64(a) - rounded(a)) + 2.0 ** -23 * K * np.abs(f64(a))).T)
+            within(Hs[:, at:at + r], ref, off + STEP * (np.abs(ref) + off), "Hs")
+            if M * r >= MANY:
+                near(Hs[:, at:at + r], ref, 4.5e-3, "Hs")
+    out = qb.qlora_gated_bwd(d.dH, d.X, G, U, Hs, *d.args)
+    for got, ref, label in zip(out, grads, GRADS):
+        if ref is None:
+            assert got is None
+            continue
+        assert got.dtype is (torch.bfloat16 if label == "dX" or bf16 else torch.float32)
+        if label == "dX" or M * r >= MANY:
+            near(got, ref, 7e-3, label)
+    check_backward_by_cases(d, out, G, U, Hs)
+    for a, b in zip(out, qb.qlora_gated_bwd(d.dH, d.X, G, U, Hs, *d.args)):
+        assert a is None and b is None or torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", [0, 1, 2, 3])
+@pytest.mark.parametrize("M", [3, 200])
+def test_formats_and_given_buffers(qb, M, fmt):
+    import torch
+    gu.announce(f"gated formats {fmt} {M}")
+    N, K, r = 448, 320, 12
+    d = Data(qb, M, N, K, r, fmt=fmt)
+    h, _, _, grads = d.oracle()
+    outs = tuple(torch.full((M, n), 7.0, dtype=torch.bfloat16, device="cuda") for n in (N, N, N, 128))
+    ws = torch.full((qb.qlora_gated_workspace_bytes(M, N, K, r, False),), 255, dtype=torch.uint8, device="cuda")
+    got = qb.qlora_gated_fwd_save(d.X, *d.args, ws=ws, outs=outs)
+    assert all(a is b for a, b in zip(got, outs))
+    near(outs[0], h, 4.5e-3, "H")
+    out = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    assert qb.qlora_gated_fwd(d.X, *d.args, ws=ws, out=out) is out and torch.equal(out, outs[0])
+    like = lambda t: torch.full_like(t, 7.0)  # noqa: E731
+    bouts = (like(d.X), *(like(t) for t in d.factors))
+    ws = torch.full((qb.qlora_gated_workspace_bytes(M, N, K, r, True),), 255, dtype=torch.uint8, device="cuda")
+    got = qb.qlora_gated_bwd(d.dH, d.X, *outs[1:], *d.args, ws=ws, outs=bouts)
+    for a, b, ref, label in zip(got, bouts, grads, GRADS):
+        assert a is b
+        if label == "dX" or M * r >= MANY:
+            near(a, ref, 7e-3, label)
+    check_backward_by_cases(d, bouts, *outs[1:])
+
+
+@pytest.mark.parametrize("M,N,K", [(64, 192, 64), (256, 1088, 256), (320, 64, 320), (4096, 1152, 4096)])
+def test_exact_forward_with_unit_rows(qb, M, N, K):
+    """X a unit matrix: G and U are the decoded weights, bit for bit."""
+    import torch
+    gu.announce(f"gated unit X {M}x{N}x{K}")
+    d = Data(qb, M, N, K, 0)
+    X = torch.eye(M, K, device="cuda").bfloat16()
+    H, G, U, _ = qb.qlora_gated_fwd_save(X, *d.args)
+    wg, wu = (qb.qlora_nf4_dequantize(w, torch.bfloat16)[:, :M].t() for w in (d.gate, d.up))
+    assert torch.equal(G, wg) and torch.equal(U, wu)
+    want = block.gate(f64(G), f64(U))
+    # the gate's own fp32 arithmetic, 2^-20 of it at these values, and half a step
+    assert (np.abs(f64(H) - want) <= np.abs(want) * (2.0 ** -8 + 2.0 ** -19)).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(64, 64, 192), (320, 320, 128), (192, 192, 1088), (4096, 4096, 2304)])
+def test_exact_backward_with_unit_rows(qb, M, N, K):
+    """G = 0, U = 2 and dH a unit matrix: dG = dH, dU = 0, so dX is the decoded gate; G = 32, U = 0 and dH a 32nd of
+    it: dG = 0, dU = dH 32, so dX is the other weight. Bit for bit."""
+    import torch
+    gu.announce(f"gated unit dH {M}x{N}x{K}")
+    d = Data(qb, M, N, K, 0)
+    eye = torch.eye(M, N, device="cuda").bfloat16()
+    full = lambda v: torch.full((M, N), v, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    dX = qb.qlora_gated_bwd(eye, d.X, full(0.0), full(2.0), None, *d.args)[0]
+    assert torch.equal(dX, qb.qlora_nf4_dequantize(d.gate, torch.bfloat16)[:M])
+    dX = qb.qlora_gated_bwd(eye / 32, d.X, full(32.0), full(0.0), None, *d.args)[0]
+    assert torch.equal(dX, qb.qlora_nf4_dequantize(d.up, torch.bfloat16)[:M])
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("M,r", [(7, 3), (150, 64), (300, 130)])
+def test_adapters_alone(qb, M, r, bf16):
+    """Weights of zeros: only the adapters' terms are left."""
+    gu.announce(f"gated adapters alone {M} r={r}")
+    d = Data(qb, M, 320, 448, r, bf16=bf16, weight=False)
+    h, g, u, grads = d.oracle()
+    H, G, U, Hs = qb.qlora_gated_fwd_save(d.X, *d.args)
+    # A, Hs and B are rounded for each of G and U: sqrt(3 (1.21 + 1) + 1) r = 6.2e-3; kept G, U: 2 r
+    near(G, g, 5e-3, "G")
+    near(U, u, 5e-3, "U")
+    near(H, h, 7e-3, "H")
+    # G and U are off by 2 r each, 1.21 of G's twice over: 4 (2.42 + 1) + dG, dU, B, l, A, its own = 18.7: 9.8e-3
+    for got, ref, label in zip(qb.qlora_gated_bwd(d.dH, d.X, G, U, Hs, *d.args), grads, GRADS):
+        near(got, ref, 1e-2, label)
+
+
+def test_each_adapter_reaches_its_own_side(qb):
+    """Factors of zero for one of the weights: its sums are those without an adapter, the other's are not."""
+    import torch
+    gu.announce("gated adapters' sides")
+    d = Data(qb, 70, 256, 192, 16)
+    _, G0, U0, _ = qb.qlora_gated_fwd_save(d.X, d.gate, d.up)
+    ag, bg, au, bu = d.factors
+    z = torch.zeros_like
+    _, G, U, _ = qb.qlora_gated_fwd_save(d.X, d.gate, d.up, ag, bg, z(au), z(bu), d.scale)
+    assert torch.equal(U, U0) and not torch.equal(G, G0)
+    _, G, U, _ = qb.qlora_gated_fwd_save(d.X, d.gate, d.up, z(ag), z(bg), au, bu, d.scale)
+    assert torch.equal(G, G0) and not torch.equal(U, U0)
+
+
+def test_gradients_by_differences(qb):
+    """Directional differences of the pass in the adapters and in X. The differences are taken over steps that move H by
+    far more than its rounding, in fp64 from bf16 outputs of many elements, which average their roundings: each H is
+    off by 4.1e-3 in the root mean square, the difference of two by sqrt(2) times that over sqrt(elements) of what is summed."""
+    import torch
+    gu.announce("gated differences")
+    M, N, K, r = 200, 512, 256, 16
+    d = Data(qb, M, N, K, r, bf16=False)
+    H, G, U, Hs = qb.qlora_gated_fwd_save(d.X, *d.args)
+    grads = qb.qlora_gated_bwd(d.dH, d.X, G, U, Hs, *d.args)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    for i, (t, grad) in enumerate(zip((d.X, *d.factors), grads)):
+        step = (torch.randn(t.shape, generator=gen, device="cuda") * t.float().std() * 0.1).to(t.dtype)
+        # along the gradient, so that the change is much larger than the noise
+        step = (step.float() + 0.3 * t.float().std() * grad.float() / grad.float().std()).to(t.dtype)
+        args = [d.X, *d.factors]
+        sums = []
+        for sign in (1, -1):
+            moved = list(args)
+            moved[i] = (t + sign * step) if t.dtype is torch.float32 else (t.float() + sign * step.float()).bfloat16()
+            h = qb.qlora_gated_fwd(moved[0], d.gate, d.up, *moved[1:], d.scale)
+            sums.append(((h.double() * d.dH.double()).sum().item(), moved[i].double()))
+        diff = sums[0][0] - sums[1][0]
+        want = ((sums[0][1] - sums[1][1]) * grad.double()).sum().item()
+        noise = 4.1e-3 * 2 ** 0.5 * (H.double().pow(2).mean() * d.dH.double().pow(2).sum()).sqrt().item()
+        # third derivatives of the gate over steps of up to half a unit, and the gradient's own 7e-3: 5 %
+        assert abs(diff - want) <= 4 * noise + 0.05 * abs(want), (i, diff, want, noise)
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_captured_with_shared_workspace(qb, M):
+    """Forward and backward captured, replayed with new inputs and eager calls between, two graphs that share a workspace one after the other."""
+    import torch
+    gu.announce(f"gated captured {M}")
+    N, K, r = 320, 256, 16
+    d = Data(qb, M, N, K, r)
+    ws = torch.empty(max(qb.qlora_gated_workspace_bytes(M, N, K, r, b) for b in (False, True)), dtype=torch.uint8, device="cuda")
+
+    def step(ws):
+        H, G, U, Hs = qb.qlora_gated_fwd_save(d.X, *d.args, ws=ws)
+        return (H, *qb.qlora_gated_bwd(d.dH, d.X, G, U, Hs, *d.args, ws=ws))
+    stream = torch.cuda.Stream()
+    graphs = []
+    with torch.cuda.stream(stream):
+        step(ws)
+        torch.cuda.synchronize()
+        for _ in range(2):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=stream):
+                graphs.append((g, step(ws)))
+            graphs[-1] = (g, graphs[-1][1])
+    for i in range(3):
+        d.X.copy_(torch.randn_like(d.X))
+        d.factors[1].mul_(1.5)
+        ws.fill_(255)
+        torch.cuda.synchronize()
+        for g, _ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        kept = [[t.clone() for t in outs] for _, outs in graphs]
+        want = step(None)
+        for outs in kept:
+            assert all(torch.equal(a, b) for a, b in zip(outs, want)), f"replay {i}"
+
+
+def test_two_streams(qb):
+    import torch
+    gu.announce("gated two streams")
+    d = Data(qb, 130, 320, 256, 16)
+
+    def step():
+        H, G, U, Hs = qb.qlora_gated_fwd_save(d.X, *d.args)
+        return (H, *qb.qlora_gated_bwd(d.dH, d.X, G, U, Hs, *d.args))
+    want = step()
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for _ in range(6):
+        for st in streams:
+            with torch.cuda.stream(st):
+                got.append(step())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for outs in got for a, b in zip(outs, want))
+
+
+def test_rows_with_nan_stay_alone(qb):
+    """A NaN or Inf in one row of X, or of dH, spoils that row only (and the sums over rows)."""
+    import torch
+    gu.announce("gated nan rows")
+    d = Data(qb, 300, 256, 192, 8)
+    H, G, U, Hs = qb.qlora_gated_fwd_save(d.X, *d.args)
+    dX = qb.qlora_gated_bwd(d.dH, d.X, G, U, Hs, *d.args)[0]
+    X, dH = d.X.clone(), d.dH.clone()
+    X[5, 7], dH[9, 3] = float("nan"), float("inf")
+    H2, G2, U2, Hs2 = qb.qlora_gated_fwd_save(X, *d.args)
+    keep = torch.ones(300, dtype=torch.bool, device="cuda")
+    keep[5] = False
+    assert torch.isnan(H2[5]).all() and torch.equal(H2[keep], H[keep])
+    keep[9] = False
+    out = qb.qlora_gated_bwd(dH, X, G2, U2, Hs2, *d.args)[0]
+    assert torch.equal(out[keep], dX[keep]) and not torch.isfinite(out[5]).any()
+
+
+def test_decoder_layer_with_autograd(qb):
+    """A layer's pieces in a row with autograd: norm, queries and keys with rotary positions, norm, gated block, down
+    projection. The gradients against the same layer with the gate and the rotation in torch, on the same kernels
+    otherwise: what differs is G's and U's rounding and the gate's, so the bars of this file hold."""
+    import torch
+    from bit_nf4_quantized_03_amd import autograd as ag
+    gu.announce("gated and rope in a layer")
+    torch.manual_seed(3)
+    b, T, heads, dh, f, r = 2, 40, 4, 64, 448, 8
+    D = heads * dh
+    rnd = lambda *s, std=1.0: torch.randn(*s, device="cuda") * std  # noqa: E731
+    shapes = {"q": (D, D), "k": (D, D), "gate": (f, D), "up": (f, D), "down": (D, f)}
+    W = {n: qb.qlora_nf4_quantize(rnd(*s, std=s[1] ** -0.5).bfloat16()) for n, s in shapes.items()}
+    A = {n: rnd(r, s[1], std=s[1] ** -0.5).requires_grad_(True) for n, s in shapes.items()}
+    B = {n: rnd(s[0], r, std=0.3).requires_grad_(True) for n, s in shapes.items()}
+    gain = torch.ones(D, device="cuda", requires_grad=True)
+    x = rnd(b, T, D).bfloat16().requires_grad_(True)
+    freqs, amp = qb.qlora_rope_freqs(dh, device="cuda")
+    pos = torch.arange(T, device="cuda").expand(b, T)
+    leaves = [x, gain, *A.values(), *B.values()]
+
+    def lin(n, t):
+        return ag.qlora_linear(t, W[n], A[n], B[n], 0.5)
+
+    def layer(own):
+        h = ag.rmsnorm(x, gain)
+        q, k = (lin(n, h).view(b, T, heads, dh) for n in ("q", "k"))
+        if own:
+            q, k = ag.rope(q, k, pos, freqs, amp)
+        else:
+            w = pos[..., None].double() * freqs
+            c, s = w.cos().float()[:, :, None], w.sin().float()[:, :, None]
+            half = dh // 2
+            turn = lambda t: torch.cat([t[..., :half].float() * c - t[..., half:].float() * s, t[..., half:].float() * c + t[..., :half].float() * s], -1).bfloat16()  # noqa: E731
+            q, k = turn(q), turn(k)
+        mix = (q.float() * k.float()).sum(-1, keepdim=True) * dh ** -0.5
+        y, res = ag.rmsnorm((mix * q.float()).reshape(b, T, D).bfloat16(), gain, residual=x)
+        if own:
+            m = ag.qlora_gated(y, W["gate"], W["up"], A["gate"], B["gate"], A["up"], B["up"], 0.5)
+        else:
+            m = (torch.nn.functional.silu(lin("gate", y).float()) * lin("up", y).float()).bfloat16()
+        return res.float() + lin("down", m).float()
+    up = rnd(b, T, D)
+    results = []
+    for own in (True, False):
+        for t in leaves:
+            t.grad = None
+        out = layer(own)
+        out.backward(up)
+        results.append((out.detach(), [t.grad.clone() for t in leaves]))
+    assert gu.rel_fro(f64(results[0][0]), f64(results[1][0])) <= 7e-3
+    for a, c in zip(results[0][1], results[1][1]):
+        assert gu.rel_fro(f64(a), f64(c)) <= 1.5e-2   # two paths, each within its 7e-3 of the exact one
+
+
+def test_autograd_checkpointed_and_without_gradients(qb):
+    import torch
+    from torch.utils.checkpoint import checkpoint
+    from bit_nf4_quantized_03_amd import autograd as ag
+    gu.announce("gated checkpointed")
+    d = Data(qb, 60, 192, 128, 8, bf16=False)
+    leaves = [d.X.view(3, 20, 128).clone().requires_grad_(True), *(t.clone().requires_grad_(True) for t in d.factors)]
+    fn = lambda x, *f: ag.qlora_gated(x, d.gate, d.up, *f, d.scale)  # noqa: E731
+    grads = []
+    for call in (fn, lambda *a: checkpoint(fn, *a, use_reentrant=False)):
+        for t in leaves:
+            t.grad = None
+        h = call(*leaves)
+        assert h.shape == (3, 20, 192)
+        h.backward(d.dH.view(3, 20, 192))
+        grads.append([t.grad.clone() for t in leaves])
+    assert all(torch.equal(a, b) for a, b in zip(*grads))
+    with torch.no_grad():
+        assert torch.equal(fn(*leaves), h)
+    # only some of the inputs want a gradient, and a gradient that begins anywhere
+    x = leaves[0].detach().clone().requires_grad_(True)
+    odd = torch.zeros(60 * 192 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(3, 20, 192)
+    odd.copy_(d.dH.view(3, 20, 192))
+    fn(x, *(t.detach() for t in leaves[1:])).backward(odd)
+    assert torch.equal(x.grad, grads[0][0])
+    plain = ag.qlora_gated(x, d.gate, d.up)
+    x.grad = None
+    plain.sum().backward()
+    assert torch.isfinite(x.grad).all()
+
+
+def test_backward_captured(qb):
+    """A training step of the block and of rope captured into a graph and replayed with other inputs."""
+    import torch
+    from bit_nf4_quantized_03_amd import autograd as ag
+    gu.announce("gated backward captured")
+    d = Data(qb, 24, 128, 128, 8, bf16=False)
+    freqs, amp = qb.qlora_rope_freqs(64, device="cuda")
+    pos = torch.arange(24, device="cuda")
+    leaves = [d.X.clone().requires_grad_(True), *(t.clone().requires_grad_(True) for t in d.factors)]
+
+    def grads():
+        q, k = ag.rope(leaves[0].view(24, 2, 64), 0.5 * leaves[0].view(24, 2, 64), pos, freqs, amp)
+        x = (q.reshape(24, 128) + k.reshape(24, 128))
+        h = ag.qlora_gated(x, d.gate, d.up, *leaves[1:], d.scale)
+        return torch.autograd.grad(h, leaves, d.dH)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        for _ in range(2):
+            grads()
+    torch.cuda.current_stream().wait_stream(stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = grads()
+    for i in range(3):
+        with torch.no_grad():
+            leaves[0].copy_(torch.randn_like(leaves[0]))
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = [t.clone() for t in outs]
+        assert all(torch.equal(a, b) for a, b in zip(kept, grads())), f"replay {i}"
+
+
+def test_refusals_with_tensors(qb):
+    import torch
+    gu.announce("gated refusals")
+    d = Data(qb, 10, 128, 64, 4)
+    X, g, u = d.X, d.gate, d.up
+    ag, bg, au, bu = d.factors
+    other = qb.qlora_nf4_quantize(torch.randn(192, 64, device="cuda"))
+    plain = qb.qlora_nf4_quantize(torch.randn(128, 64, device="cuda"), fmt=1)
+    for args, error in (((X.float(), g, u), TypeError), ((X[:, :32].contiguous(), g, u), ValueError), ((X.cpu(), g, u), TypeError),
+                        ((X[0], g, u), ValueError), ((X, g, other), qb.QloraError), ((X, g, plain), qb.QloraError),
+                        ((X, g, u, ag, bg), ValueError), ((X, g, u, ag, bg, au.float(), bu, 1.0), TypeError),
+                        ((X, g, u, ag, bg, au[:2], bu, 1.0), ValueError), ((X, g, u, ag.half(), bg, au, bu, 1.0), TypeError),
+                        ((X, g, u, ag, bg.t().contiguous(), au, bu, 1.0), ValueError), ((X, g, u, ag, bg, au, bu, float("nan")), qb.QloraError)):
+        with pytest.raises(error):
+            qb.qlora_gated_fwd(*args)
+    short = qb.NF4Weight(128, 64, g.codes[:-1], g.absmax_q, g.dq_scale, g.dq_mean)
+    with pytest.raises(ValueError):
+        qb.qlora_gated_fwd(X, short, u)
+    with pytest.raises(qb.QloraError, match="workspace"):
+        qb.qlora_gated_fwd(X, g, u, ws=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    H, G, U, Hs = qb.qlora_gated_fwd_save(X, *d.args)
+    for args, error in (((d.dH[:5], X, G, U, Hs), ValueError), ((d.dH, X, G, U, None), TypeError), ((d.dH, X, G.float(), U, Hs), TypeError),
+                        ((d.dH, X, G, U, Hs[:, :64].contiguous()), ValueError)):
+        with pytest.raises(error):
+            qb.qlora_gated_bwd(*args, *d.args)
+    with pytest.raises(ValueError):
+        qb.qlora_gated_bwd(d.dH, X, G, U, Hs, g, u)
+    with pytest.raises(qb.QloraError):
+        qb.qlora_gated_fwd(X, *(qb.qlora_nf4_quantize(torch.randn(100, 64, device="cuda")) for _ in range(2)))
