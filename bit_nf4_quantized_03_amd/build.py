@@ -33,7 +33,8 @@ FASTCALL_PATH = os.path.join(PKG_DIR, "_fastcall.so")
 
 SOURCES = ["api.cpp", "codebook.cpp", "profile.cpp", "nf4_quant.hip", "linear.hip", "gemv.hip", "merge.hip", "adamw.hip",
            "noalloc.hip", "api_mx.cpp", "mx_quant.hip", "rmsnorm.hip", "mx_linear.hip",
-           "api_block.cpp", "mx_gated.hip", "rope.hip", "gated.hip"]
+           "api_block.cpp", "mx_gated.hip", "rope.hip", "gated.hip",
+           "gated_stream.hip"]
 ARCH = os.environ.get("QLORA_OFFLOAD_ARCH", "gfx950")
 
 

@@ -99,7 +99,7 @@ int block_args(const char *fn, int64_t M, const qlora_nf4_weight *gate, const ql
   for (int i = 0; i < 2; ++i)
     a->w[i] = {both[i]->codes, both[i]->absmax_q, both[i]->dq_scale, both[i]->dq_mean, both[i]->absmax};
   const size_t need = qnf4::gated_ws_bytes(M, a->N, a->K, r, backward);
-  if (!ws || ws_bytes < need)
+  if (need > 0 && (!ws || ws_bytes < need))
     return api_fail(QLORA_ERR_WORKSPACE, "%s: workspace needs %zu bytes, got %zu", fn, need, ws ? ws_bytes : size_t(0));
   if (!aligned(ws, 16)) return api_fail(QLORA_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
   return QLORA_OK;

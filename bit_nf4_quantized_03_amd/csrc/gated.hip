@@ -538,6 +538,10 @@ struct Buffers {
 
 size_t carve(void *ws, const Plan &pl, int64_t M, int64_t N, int64_t K, bool backward, Buffers *b) {
   Carve c{static_cast<char *>(ws)};
+  if (!backward && M <= kGatedStreamRows) {
+    if (pl.rp) b->Hs = c.take<__bf16>(2 * static_cast<size_t>(pl.rp) * M);
+    return c.off;
+  }
   const int64_t nb = N * K / kBlock;
   b->cs[0] = c.take<float>(nb);
   b->cs[1] = c.take<float>(nb);
@@ -608,6 +612,7 @@ hipError_t launch_gated_fwd(const GatedArgs &a, const void *X, void *H, void *G,
   Buffers b{};
   carve(ws, pl, a.M, a.N, a.K, false, &b);
   if (Hs) b.Hs = static_cast<__bf16 *>(Hs);
+  if (a.M <= kGatedStreamRows) return launch_gated_stream(a, X, H, G, U, b.Hs, s);
   run_prep(a, pl, b, false, s);
   if (pl.rp) {
     DownParams d{};

@@ -76,8 +76,9 @@ typedef struct {
 /* Columns of the kept adapter activations, 2 * 64 ceil(r / 64) (0 for an invalid r and for 0). Host-only. */
 int64_t qlora_gated_saved_cols(int32_t r);
 
-/* Workspace bytes of qlora_gated_fwd (backward = 0) and qlora_gated_bwd (1); 0
- * for invalid sizes. No contents are expected or kept. Host-only. */
+/* Workspace bytes of qlora_gated_fwd (backward = 0) and qlora_gated_bwd (1): 0
+ * for a few rows without adapters (ws may then be NULL) and for invalid sizes.
+ * No contents are expected or kept. Host-only. */
 size_t qlora_gated_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r, int32_t backward);
 
 /*

@@ -125,8 +125,8 @@ def check_backward_by_cases(d, out, G, U, Hs):
             dxb = dxb + big * (lowb @ np.abs(a) + (STEP + 2.0 ** -23 * r) * np.abs(low) @ np.abs(a))
     within(out[0], dx, dxb + STEP * (np.abs(dx) + dxb), "dX")
 
-# tiles that fill less than half the GPU split their reduction, the last two do not
-SHAPES = [(1, 64, 64, 0), (1, 64, 64, 1), (1, 1088, 512, 64), (5, 192, 128, 8), (17, 320, 576, 33), (32, 256, 1024, 64), (33, 128, 192, 65),
+# up to 32 rows the weights stream; tiles that fill less than half the GPU split their reduction, the last two do not
+SHAPES = [(1, 64, 64, 0), (1, 64, 64, 1), (1, 1088, 512, 64), (2, 6400, 192, 40), (4, 192, 4160, 8), (16, 128, 8256, 256), (3, 128, 5120, 0), (1, 64, 20352, 8), (4, 64, 8192, 16), (2, 16448, 64, 0), (31, 320, 11008, 64), (9, 64, 4096, 33), (5, 192, 128, 8), (17, 320, 576, 33), (32, 256, 1024, 64), (33, 128, 192, 65),
           (130, 704, 512, 16), (257, 384, 640, 128), (300, 1024, 256, 200), (513, 576, 1152, 256), (4096, 1152, 256, 64), (4100, 1088, 2176, 24)]
 
 
@@ -492,7 +492,7 @@ def test_refusals_with_tensors(qb):
     with pytest.raises(ValueError):
         qb.qlora_gated_fwd(X, short, u)
     with pytest.raises(qb.QloraError, match="workspace"):
-        qb.qlora_gated_fwd(X, g, u, ws=torch.empty(64, dtype=torch.uint8, device="cuda"))
+        qb.qlora_gated_fwd(X, *d.args, ws=torch.empty(64, dtype=torch.uint8, device="cuda"))
     H, G, U, Hs = qb.qlora_gated_fwd_save(X, *d.args)
     for args, error in (((d.dH[:5], X, G, U, Hs), ValueError), ((d.dH, X, G, U, None), TypeError), ((d.dH, X, G.float(), U, Hs), TypeError),
                         ((d.dH, X, G, U, Hs[:, :64].contiguous()), ValueError)):
