@@ -21,8 +21,14 @@
 // constants of the next 4096 elements (or the next unit: a workgroup takes
 // several) are requested before this one's are used.
 //
-// Bound by the weights' bytes; the table's reads (one for two weights) and the
-// address of each (two operations) are next.
+// Two weights of 11008 x 4096 (46 MB), double quantisation: 1 row 17.9 us
+// without adapters (2.6 TB/s), 14.5 with the table's reads left out; with r = 64
+// 23.6, 4 rows 27.1, 16 rows 39.1, 32 rows 51.6 (k_gated_low and its launch are
+// 4 of these). Each turn of a workgroup waits for its loads, which the next
+// turn's, under way, do not hide whole; the table's reads (one for two weights)
+// come next. 32 copies of the table measured the same (19.4 against 19.6 us), 64
+// leave one workgroup on a compute unit (29); waves that go through a reduction
+// alone (no barrier) measured 20 to 23 us for one row.
 #include <algorithm>
 
 #include "block.h"
@@ -57,21 +63,22 @@ __device__ __forceinline__ bf16x8 adapter8(const void *p, bool bf16, int64_t i) 
                 static_cast<__bf16>(b.x), static_cast<__bf16>(b.y), static_cast<__bf16>(b.z), static_cast<__bf16>(b.w)};
 }
 
-// A workgroup has one adapter row and up to eight rows of X; its four waves
+// A workgroup has one adapter row and one row or up to eight of X; its four waves
 // share the reduction. Sums in a fixed order.
+template <int ROWS>
 __global__ __launch_bounds__(256) void k_gated_low(const LowParams p) {
-  __shared__ float part[4][8];
+  __shared__ float part[4][ROWS];
   const int row = blockIdx.x, w = row >= p.rp, j = row - w * p.rp;
-  const int m0 = 8 * static_cast<int>(blockIdx.y), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float acc[8];
+  const int m0 = ROWS * static_cast<int>(blockIdx.y), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float acc[ROWS];
 #pragma unroll
-  for (int m = 0; m < 8; ++m) acc[m] = 0.0f;
+  for (int m = 0; m < ROWS; ++m) acc[m] = 0.0f;
   if (j < p.r) {
     for (int64_t k = 8 * threadIdx.x; k < p.K; k += 2048) {
       const bf16x8 a = adapter8(w ? p.A[1] : p.A[0], p.bf16, j * p.K + k);
 #pragma unroll
-      for (int m = 0; m < 8; ++m) {
-        if (m0 + m >= p.M) break;   // uniform
+      for (int m = 0; m < ROWS; ++m) {
+        if (ROWS > 1 && m0 + m >= p.M) break;   // uniform
         const bf16x8 x = *reinterpret_cast<const bf16x8 *>(p.X + (m0 + m) * p.K + k);
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[m] = fmaf(static_cast<float>(a[e]), static_cast<float>(x[e]), acc[m]);
@@ -79,13 +86,13 @@ __global__ __launch_bounds__(256) void k_gated_low(const LowParams p) {
     }
   }
 #pragma unroll
-  for (int m = 0; m < 8; ++m) {
+  for (int m = 0; m < ROWS; ++m) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) acc[m] += __shfl_xor(acc[m], o);
     if (lane == 0) part[wave][m] = acc[m];
   }
   __syncthreads();
-  if (threadIdx.x < 8 && m0 + static_cast<int>(threadIdx.x) < p.M) {
+  if (threadIdx.x < ROWS && m0 + static_cast<int>(threadIdx.x) < p.M) {
     const int m = threadIdx.x;
     const float v = (part[0][m] + part[1][m]) + (part[2][m] + part[3][m]);
     p.Hs[static_cast<int64_t>(m0 + m) * 2 * p.rp + row] = static_cast<__bf16>(p.scale * v);
@@ -152,38 +159,45 @@ __device__ __forceinline__ void decode_step(f32x4 (&acc)[MT], u32x4 v, const u32
   }
 }
 
-// A block's constant from what is stored.
+// A block's constant from what is stored: the bits as loaded, and converted
+// where they are used. A conversion beside the load would wait for it, and for
+// every load in front of it (1 x 11008 x 4096 19.6 us so, without adapters).
 template <bool DQ>
-__device__ __forceinline__ float constant_of(float raw, float factor, float mean) {
-  if constexpr (DQ) return __fadd_rn(__fmul_rn(raw, __fdiv_rn(factor, 127.0f)), mean);
-  return raw;
-}
-template <bool DQ>
-__device__ __forceinline__ void request_constant(const StreamParams &p, int w, int64_t e, float &raw, float &factor) {
+__device__ __forceinline__ void request_constant(const StreamParams &p, int w, int64_t e, uint32_t &raw, float &factor) {
   if constexpr (DQ) {
-    raw = static_cast<float>((w ? p.absmax_q[1] : p.absmax_q[0])[e]);
+    raw = static_cast<uint32_t>(static_cast<int32_t>((w ? p.absmax_q[1] : p.absmax_q[0])[e]));
     factor = (w ? p.dq_scale[1] : p.dq_scale[0])[e / kDqBlock];
   } else {
-    raw = (w ? p.absmax[1] : p.absmax[0])[e];
+    raw = __builtin_bit_cast(uint32_t, (w ? p.absmax[1] : p.absmax[0])[e]);
   }
 }
+template <bool DQ>
+__device__ __forceinline__ float constant_of(uint32_t raw, float factor, float mean) {
+  if constexpr (DQ) return __fadd_rn(__fmul_rn(static_cast<float>(static_cast<int32_t>(raw)), __fdiv_rn(factor, 127.0f)), mean);
+  return __builtin_bit_cast(float, raw);
+}
 
-// Eight values of B's row n, adapter columns j0 .. j0 + 7, zero from r on.
-__device__ __forceinline__ void request_b(const StreamParams &p, int up, int64_t n, int j0, float (&b)[8]) {
+// Eight values of B's row n, adapter columns j0 .. j0 + 7: bits too.
+__device__ __forceinline__ void request_b(const StreamParams &p, int up, int64_t n, int j0, uint32_t (&b)[8]) {
   const void *from = up ? p.B[1] : p.B[0];
+  const int64_t at = n * p.r;
+  // a column that is not there reads the last one, and its bits are dropped
+  if (p.bf16) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    b[e] = 0.0f;
-    if (j0 + e < p.r) b[e] = p.bf16 ? static_cast<float>(static_cast<const __bf16 *>(from)[n * p.r + j0 + e]) : static_cast<const float *>(from)[n * p.r + j0 + e];
+    for (int e = 0; e < 8; ++e) b[e] = static_cast<const uint16_t *>(from)[at + min(j0 + e, p.r - 1)];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) b[e] = static_cast<const uint32_t *>(from)[at + min(j0 + e, p.r - 1)];
   }
 }
 
 // acc += the adapters' terms of 32 of their columns: each weight's rows with its own half of Hs.
 template <int MT>
-__device__ __forceinline__ void adapt(f32x4 (&acc)[MT], const float (&b)[8], const u32x4 (&hs)[MT][2], int up) {
-  bf16x8 v;
+__device__ __forceinline__ void adapt(f32x4 (&acc)[MT], const uint32_t (&b)[8], const u32x4 (&hs)[MT][2], int up, const StreamParams &p, int j0) {
+  float f[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = static_cast<__bf16>(b[e]);
+  for (int e = 0; e < 8; ++e) f[e] = j0 + e < p.r ? __builtin_bit_cast(float, p.bf16 ? b[e] << 16 : b[e]) : 0.0f;
+  const bf16x8 v = __builtin_bit_cast(bf16x8, u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])});
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     const bf16x8 mine = up == w ? v : bf16x8{};
@@ -239,7 +253,8 @@ __global__ __launch_bounds__(kThreads, 4) void k_gated_few(const StreamParams p,
 
   // codes and raw constants of a unit's chunk; a wave has constants of one row of each weight
   u32x4 cur[kSteps], nxt[kSteps];
-  float raw[2], factor[2] = {0.0f, 0.0f}, mean[2] = {0.0f, 0.0f};
+  uint32_t raw[2];
+  float factor[2] = {0.0f, 0.0f}, mean[2] = {0.0f, 0.0f};
   const uint8_t *const codes = (up ? p.codes[1] : p.codes[0]) + (r & 7) * row_bytes + 64 * wave + 16 * g;
   auto request = [&](int unit, int chunk, u32x4 (&v)[kSteps]) {
     const int64_t first = static_cast<int64_t>(chunk) * (kChunk / 2);
@@ -253,7 +268,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_gated_few(const StreamParams p,
     const int64_t b = static_cast<int64_t>(chunk) * kChunkBlocks + lane, e = (8 * static_cast<int64_t>(unit) + wave) * blocks + b;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      raw[i] = 0.0f;
+      raw[i] = 0;
       if (b < blocks) request_constant<DQ>(p, i, e, raw[i], factor[i]);
     }
   };
@@ -262,7 +277,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_gated_few(const StreamParams p,
   if constexpr (DQ) mean[0] = p.dq_mean[0][0], mean[1] = p.dq_mean[1][0];
   // the adapters: a wave has 32 of their columns
   const bool adapts = 32 * wave < p.r;
-  float bc[8], bn[8];
+  uint32_t bc[8], bn[8];
   u32x4 hs[1][2];
   if (adapts) {
     request_b(p, up, 8 * static_cast<int64_t>(unit) + (r & 7), 32 * wave + 8 * g, bc);
@@ -302,7 +317,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_gated_few(const StreamParams p,
     }
     if (last) {
       if (adapts) {
-        adapt<1>(acc, bc, hs, up);
+        adapt<1>(acc, bc, hs, up, p, 32 * wave + 8 * g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) bc[e] = bn[e];
       }
@@ -367,7 +382,8 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void k_gated_stream(cons
   for (int t = 0; t < MT; ++t) xo[t] = 16 * t + r < p.M ? static_cast<uint32_t>((16 * t + r) * p.K * 2 + 16 * g) : kNowhere;
   u32x4 cur[kTiles], nxt[kTiles], x[MT][4], xn[MT][4];
   constexpr int kRaw = 16 * kTiles * kTurnBlocks / kThreads;   // constants a thread forms
-  float raw[kRaw], factor[kRaw], mean[2] = {0.0f, 0.0f};
+  uint32_t raw[kRaw];
+  float factor[kRaw], mean[2] = {0.0f, 0.0f};
   const uint8_t *const codes = (up ? p.codes[1] : p.codes[0]) + (unit_row + (r & 7)) * row_bytes + 64 * wave + 16 * g;
   auto request = [&](int turn, u32x4 (&v)[kTiles], u32x4 (&xv)[MT][4]) {
     const int64_t first = static_cast<int64_t>(turn) * (kTurn / 2), k0 = 2 * first + 128 * wave;
@@ -389,7 +405,7 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void k_gated_stream(cons
     for (int i = 0; i < kRaw; ++i) {
       const int e = threadIdx.x + kThreads * i, row = e / kTurnBlocks;
       const int64_t b = static_cast<int64_t>(turn) * kTurnBlocks + e % kTurnBlocks;
-      raw[i] = factor[i] = 0.0f;
+      raw[i] = 0, factor[i] = 0.0f;
       if (b < blocks) request_constant<DQ>(p, (row >> 3) & 1, (unit_row + 8 * (row >> 4) + (row & 7)) * blocks + b, raw[i], factor[i]);
     }
   };
@@ -422,12 +438,12 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void k_gated_stream(cons
   }
   if (32 * wave < p.r) {
     u32x4 hs[MT][2];
-    float b[kTiles][8];
+    uint32_t b[kTiles][8];
     load_hs<MT>(p, r, 32 * wave + 8 * g, hs);
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) request_b(p, up, unit_row + 8 * i + (r & 7), 32 * wave + 8 * g, b[i]);
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) adapt<MT>(acc[i], b[i], hs, up);
+    for (int i = 0; i < kTiles; ++i) adapt<MT>(acc[i], b[i], hs, up, p, 32 * wave + 8 * g);
   }
 #pragma unroll
   for (int i = 0; i < kTiles; ++i) {
@@ -479,7 +495,8 @@ hipError_t launch_gated_stream(const GatedArgs &a, const void *X, void *H, void 
   const int rp = gated_padded_rank(a.r);
   if (a.r) {
     const LowParams p{static_cast<const __bf16 *>(X), {a.A[0], a.A[1]}, a.adapter_bf16, a.K, static_cast<int>(a.M), a.r, rp, a.scale, Hs};
-    k_gated_low<<<dim3(2 * rp, static_cast<unsigned>(ceil_div(a.M, 8))), 256, 0, s>>>(p);
+    if (a.M == 1) k_gated_low<1><<<2 * rp, 256, 0, s>>>(p);
+    else k_gated_low<8><<<dim3(2 * rp, static_cast<unsigned>(ceil_div(a.M, 8))), 256, 0, s>>>(p);
   }
   StreamParams p{};
   p.X = static_cast<const __bf16 *>(X);
