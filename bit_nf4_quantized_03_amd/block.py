@@ -14,7 +14,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import NF4Weight, QloraError, _Weight, format_has_dq, lib, qlora_last_error
-from .mx import _DTYPES, _MX, MXMatrix, QLORA_MX_FP8, _empty, _empty_1d, _entry, _tensor
+from .mx import _DTYPES, _MX, MXMatrix, QLORA_MX_FP8, _empty, _empty_1d, _entry, _fast, _fast_on, _tensor
 
 __all__ = [
     "BLOCK_EXPORTED_SYMBOLS", "QLORA_ROPE_PLAIN", "QLORA_ROPE_LINEAR", "QLORA_ROPE_NTK", "QLORA_ROPE_PARTS",
@@ -115,6 +115,10 @@ def qlora_mx_gated(X: MXMatrix, W: MXMatrix, mx: Optional[int] = QLORA_MX_FP8, o
     multiple of 32): a new matrix in microscaled floats of type ``mx`` (what the
     down projection takes), a new bf16 tensor [M, N] with ``mx`` None, or
     ``out``, which is one or the other and decides."""
+    if out is None and (at := _fast_on(X.codes)):
+        new = _fast.gated(*at, X.codes, X.scales, X.rows, X.cols, X.mx, W.codes, W.scales, W.rows, W.cols, W.mx, mx)
+        if new is not None:
+            return new if mx is None else MXMatrix(X.rows, W.rows // 2, *new, mx)
     sx = X.c_struct("X")
     index = X.codes.get_device()
     sw = W.c_struct("W", index)
@@ -292,7 +296,11 @@ def _heads(name, t, out, dtype, shape, index):
     return _Heads(t.data_ptr(), out.data_ptr(), t.shape[1], t.stride(0), t.stride(1), out.stride(0), out.stride(1))
 
 
-def _rope(entry, Q, K, positions, freqs, amplitude, interleaved, outs):
+def _rope(backward, Q, K, positions, freqs, amplitude, interleaved, outs):
+    if outs is None and (at := _fast_on(Q)):
+        new = _fast.rope(*at, Q, K, positions, freqs, amplitude, bool(interleaved), backward)
+        if new is not None:
+            return new
     if not isinstance(Q, torch.Tensor) or not Q.is_cuda:
         raise TypeError("the heads must be CUDA (HIP) tensors")
     if Q.dim() != 3:
@@ -316,6 +324,7 @@ def _rope(entry, Q, K, positions, freqs, amplitude, interleaved, outs):
             raise ValueError("outs must have what there are heads for")
     sq = _heads("Q", Q, q, Q.dtype, (rows, dim), index)
     sk = None if K is None else _heads("K", K, k, Q.dtype, (rows, dim), index)
+    entry = _rope_bwd if backward else _rope_fwd
     entry(index, byref(sq), None if sk is None else byref(sk), _DTYPES[Q.dtype], rows, dim, 2 * freqs.shape[0], pos,
           positions.dtype is torch.int64, f, float(amplitude), bool(interleaved))
     return q, k
@@ -328,10 +337,10 @@ def qlora_rope_fwd(Q, K, positions, freqs, amplitude: float = 1.0, interleaved: 
     len(freqs) elements of a head are rotated, element i with i + len(freqs) or,
     ``interleaved``, 2 i with 2 i + 1; the others pass through. K may be None.
     ``outs`` may be (Q, K) themselves."""
-    return _rope(_rope_fwd, Q, K, positions, freqs, amplitude, interleaved, outs)
+    return _rope(False, Q, K, positions, freqs, amplitude, interleaved, outs)
 
 
 def qlora_rope_bwd(dQ, dK, positions, freqs, amplitude: float = 1.0, interleaved: bool = False,
                    outs: Optional[Tuple] = None):
     """(gradients of Q and K) of qlora_rope_fwd from those of its outputs; with the same arguments as it."""
-    return _rope(_rope_bwd, dQ, dK, positions, freqs, amplitude, interleaved, outs)
+    return _rope(True, dQ, dK, positions, freqs, amplitude, interleaved, outs)

@@ -1,7 +1,7 @@
-// The calls of mx.py whose arguments are all as they should be and whose
-// outputs are new, in one step: checks, allocation through torch and the C
-// entry point. Everything else (given outputs, a refusal and its message) is
-// mx.py's own; a function here then returns None and has done nothing.
+// The calls of mx.py and block.py whose arguments are all as they should be and
+// whose outputs are new, in one step: checks, allocation through torch and the
+// C entry point. Everything else (given outputs, a refusal and its message) is
+// those modules' own; a function here then returns None and has done nothing.
 //
 // A call costs 5 us of host time in mx.py besides the launch (attribute checks,
 // two to three allocations at 1.3 us, the argument conversion); for one token's
@@ -14,7 +14,7 @@
 #include <ATen/ATen.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include "../../include/qlora_mx.h"
+#include "../../include/qlora_block.h"
 
 namespace {
 
@@ -266,6 +266,83 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n) {   // X's five, 
   });
 }
 
+PyObject *gated(PyObject *, PyObject *const *a, Py_ssize_t n) {   // X's five, W's five, type of H or None
+  return guarded([&]() -> PyObject * {
+    if (n != 13) return none();
+    const int dev = static_cast<int>(PyLong_AsLong(a[0]));
+    qlora_mx_matrix x, w;
+    const Tensor *xc, *wc;
+    if (!matrix(a + 2, dev, &x, &xc) || !matrix(a + 7, dev, &w, &wc) || x.cols != w.cols || w.rows % (2 * QLORA_MX_BLOCK) != 0) return none();
+    const bool plain = a[12] == Py_None;
+    const long mx = plain ? 0 : PyLong_AsLong(a[12]);
+    if (PyErr_Occurred()) {
+      PyErr_Clear();
+      return none();
+    }
+    if (!valid(x.rows, w.rows / 2, mx)) return none();
+    void *stream = stream_of(a[1]);
+    Tensor h;
+    std::optional<NewMatrix> q;
+    const int status = unlocked([&] {
+      if (plain) h = fresh(*xc, {x.rows, w.rows / 2}, at::kBFloat16);
+      else q.emplace(*xc, x.rows, w.rows / 2, mx);
+      return qlora_mx_gated(&x, &w, plain ? h.data_ptr() : nullptr, plain ? nullptr : &q->m, stream);
+    });
+    if (status != QLORA_OK) return none();
+    return plain ? wrap(std::move(h)) : pack({wrap(std::move(q->codes)), wrap(std::move(q->scales))});
+  });
+}
+
+// Heads [rows, heads, dim] of `type` on GPU `dev`, the elements of a head next
+// to each other; null otherwise.
+const Tensor *heads_of(PyObject *o, at::ScalarType type, int dev) {
+  if (!THPVariable_Check(o)) return nullptr;
+  const Tensor &t = THPVariable_Unpack(o);
+  if (!t.is_cuda() || t.scalar_type() != type || t.dim() != 3 || t.numel() == 0 || t.stride(2) != 1 || t.get_device() != dev) return nullptr;
+  return &t;
+}
+
+PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {   // Q, K or None, positions, freqs, amplitude, interleaved, backward
+  return guarded([&]() -> PyObject * {
+    if (n != 9) return none();
+    const int dev = static_cast<int>(PyLong_AsLong(a[0]));
+    int dt = QLORA_BF16;
+    at::ScalarType type = at::kBFloat16;
+    const Tensor *q = heads_of(a[2], type, dev);
+    if (!q) dt = QLORA_F32, type = at::kFloat, q = heads_of(a[2], type, dev);
+    const Tensor *k = a[3] == Py_None ? nullptr : heads_of(a[3], type, dev);
+    if (!q || (a[3] != Py_None && !k)) return none();
+    const int64_t rows = q->size(0), dim = q->size(2);
+    if (dim > 1024 || (k && (k->size(0) != rows || k->size(2) != dim))) return none();
+    const Tensor *pos = tensor(a[4], at::kLong, dev);
+    const bool wide = pos != nullptr;
+    if (!pos) pos = tensor(a[4], at::kInt, dev);
+    const Tensor *freqs = tensor(a[5], at::kDouble, dev);
+    if (!pos || pos->dim() != 1 || pos->size(0) != rows || !freqs || freqs->dim() != 1 || freqs->size(0) > 512) return none();
+    const double amplitude = PyFloat_AsDouble(a[6]);
+    if (PyErr_Occurred()) {
+      PyErr_Clear();
+      return none();
+    }
+    const bool interleaved = a[7] == Py_True, backward = a[8] == Py_True;
+    void *stream = stream_of(a[1]);
+    Tensor qo, ko;
+    const int status = unlocked([&] {
+      const auto heads = [&](const Tensor &t, Tensor &out) {
+        out = fresh(t, {rows, t.size(1), dim}, type);
+        return qlora_rope_heads{t.data_ptr(), out.data_ptr(), t.size(1), t.stride(0), t.stride(1), t.size(1) * dim, dim};
+      };
+      const qlora_rope_heads hq = heads(*q, qo), hk = k ? heads(*k, ko) : qlora_rope_heads{};
+      return (backward ? qlora_rope_bwd : qlora_rope_fwd)(&hq, k ? &hk : nullptr, dt, rows, static_cast<int32_t>(dim),
+                                                          static_cast<int32_t>(2 * freqs->size(0)), pos->data_ptr(), wide,
+                                                          static_cast<const double *>(freqs->data_ptr()), amplitude, interleaved, stream);
+    });
+    if (status != QLORA_OK) return none();
+    PyObject *second = k ? wrap(std::move(ko)) : none();
+    return pack({wrap(std::move(qo)), second});
+  });
+}
+
 PyMethodDef methods[] = {
     {"quantize", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(quantize)), METH_FASTCALL, nullptr},
     {"dequantize", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(dequantize)), METH_FASTCALL, nullptr},
@@ -273,6 +350,8 @@ PyMethodDef methods[] = {
     {"norm_fwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(norm_fwd)), METH_FASTCALL, nullptr},
     {"norm_bwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(norm_bwd)), METH_FASTCALL, nullptr},
     {"linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(linear)), METH_FASTCALL, nullptr},
+    {"gated", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(gated)), METH_FASTCALL, nullptr},
+    {"rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(rope)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
