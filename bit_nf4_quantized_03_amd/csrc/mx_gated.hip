@@ -116,7 +116,12 @@ hipError_t run_tiles(const MxGemmParams &p, const MxGatedOut &o, hipStream_t s) 
 }
 
 // Few rows, the weight's stream: false where the tiles are faster. A workgroup
-// has whole blocks of 32 columns of H, 64 rows of the pair.
+// has 64 rows of the pair, the 32 columns of one block of a microscaled H. A
+// bf16 H has no such blocks: half as many rows, eight waves, where that loads
+// the compute units more evenly (1 row, 4096 elements: 4096 columns 8.2 us with
+// 64 rows, 6.3 with 32, 6.6 with 16; 11008 15.7, 13.1, 15.4; 8 rows of 11008
+// 17.2, 14.8, 19.1; but 5504 8.3, 9.0, 8.9 and 8192 columns of 8192 elements
+// 19.0, 19.5, 18.9). Sixteen waves are slower with 32 rows (11008 16.6 us).
 template <int XT>
 bool run_few_rows(const MxGemvParams &p, const MxGatedOut &o, hipStream_t s, hipError_t *e) {
   if (p.experts) {
@@ -125,7 +130,12 @@ bool run_few_rows(const MxGemvParams &p, const MxGatedOut &o, hipStream_t s, hip
     return true;
   }
   if (p.M > (p.N <= 32 * kMxCus ? 16 : 8)) return false;
-  *e = p.N <= 64 * kMxCus ? run_gemv<XT, 1, 4, 8>(p, o, s) : run_gemv<XT, 1, 4, 4>(p, o, s);
+  const auto uneven = [&](int rows) {
+    const double load = static_cast<double>(ceil_div(p.N, rows)) / kMxCus;
+    return std::ceil(load) / load;
+  };
+  if (o.type < 0 && uneven(64) > 1.15 * uneven(32)) *e = run_gemv<XT, 1, 2, 8>(p, o, s);
+  else *e = p.N <= 64 * kMxCus ? run_gemv<XT, 1, 4, 8>(p, o, s) : run_gemv<XT, 1, 4, 4>(p, o, s);
   return true;
 }
 
