@@ -16,14 +16,14 @@
 //                  gemm_big.h on 128 rows of each weight, 32 of one and 32 of
 //                  the other in turn, so that both products of an element of H
 //                  end in one lane and the gate needs no exchange
-//   k_gated_out    few tiles: the reduction is split into fp32 partials, and
-//                  this sums them and gates
+//   k_gated_out    sums and gates the tiles whose reduction was split (below)
 // Backward:
 //   k_gated_prep   block scales, [Ag; Au]^T [K][2 rp] and Bg^T, Bu^T [2][rp][N]
 //   k_gated_act    dG, dU from dH, G, U
 //   k_gated_down, k_gated_sum   l = bf16(s [dG Bg, dU Bu]) [M][2 rp]
 //   k_gated_dx     dX = [dG, dU, l] [Wg; Wu; [Ag; Au]]: one reduction over both
 //                  weights, so dX is rounded and written once
+//   k_gated_dx_sum sums the tiles whose reduction was split
 //   k_gated_grad, k_gated_grad_sum   split-M partials of the adapters' gradients and their sums
 //
 // Roundings to bf16, the operand type of the matrix instructions: the decoded
@@ -38,6 +38,8 @@ namespace {
 
 using Cfg = CfgBig8;
 constexpr int kT = Cfg::kThreads;
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // --------------------------------------------------------- operands and scales
 
@@ -186,6 +188,34 @@ __global__ __launch_bounds__(256) void k_gated_sum(const float *part, int splits
   *reinterpret_cast<uint2 *>(out + e) = make_uint2(pack_bf16x2(scale * v.x, scale * v.y), pack_bf16x2(scale * v.z, scale * v.w));
 }
 
+// -------------------------------------------------------------- split tiles
+
+// A tile occupies a compute unit, so tiles run in rounds of one for each, and
+// the last `rest` tiles, where they would fill no more than half of a round,
+// are split along the reduction into S parts, fp32 sums [S][rest][256][256]
+// that a kernel behind adds in order (4096 x 11008 x 4096, 96 tiles behind five
+// rounds: 738 -> 721 us; 1536 rows, both directions: 757 -> 707). Fewer tiles
+// than that in all are all split.
+struct Tail {
+  int64_t whole, rest;   // tiles
+  int S, per;            // steps of a part
+  float *part;
+};
+struct Piece {
+  int tile, s0, s1;
+  float *part;   // null: the whole reduction
+  int z;
+};
+__device__ __forceinline__ Piece piece_of(const Tail &t, int b, int steps) {
+  if (b < t.whole) return {b, 0, steps, nullptr, 0};
+  const int q = b - static_cast<int>(t.whole), rest = static_cast<int>(t.rest), z = q / rest;
+  return {static_cast<int>(t.whole) + q - z * rest, z * t.per, min(steps, (z + 1) * t.per), t.part + static_cast<int64_t>(q) * 65536, z};
+}
+// The sums of four columns from `col` on of row `row` of split tile `i`.
+__device__ __forceinline__ float4 sums_of(const Tail &t, int i, int row, int col) {
+  return split_sum4(t.part, t.rest * 65536, static_cast<int64_t>(i) * 65536 + row * 256 + col, t.S);
+}
+
 // ------------------------------------------------------------------ forward
 
 struct FwdParams {
@@ -197,8 +227,7 @@ struct FwdParams {
   __bf16 *H, *G, *U;        // bf16 [M, N]; G and U or null
   int64_t M, N, K;
   int rp;
-  float *part;              // fp32 [S][M][2 N], columns as the tiles' rows (S > 1)
-  int S, per;
+  Tail tail;                // a part's columns as the tiles' rows
 };
 
 // The rows of a tile: row R of the interleaved weight is row 32 (R / 64) + R %
@@ -227,6 +256,46 @@ struct PairRows {
   __device__ __forceinline__ void store_part(__bf16 *lds, const float2 *lv2, int i) const { one.store_part(lds, lv2, i); }
 };
 
+// A wave's 128 rows of 32 columns to its rows of 128 columns in LDS, as bf16.
+// Neighbouring lanes have neighbouring columns: of two rows, the even one takes
+// the first and the odd one the second, so that a store is of two columns. The
+// four rows that one store reaches lie on different banks. (Without the detour,
+// from lanes with one column each, the forward took 735 us instead of 718.)
+template <class F>
+__device__ __forceinline__ void stage_rows(__bf16 *place, F value) {
+  static_assert(Cfg::WTM == 128 && Cfg::WAVES_N == 4 && Cfg::kLdsA >= 128 * 128 && Cfg::kLdsB >= 128 * 128, "the places");
+  const int lane = threadIdx.x & 63, wn = (threadIdx.x >> 6) % Cfg::WAVES_N, odd = lane & 1, upper = lane >> 5;
+  uint32_t *const to = reinterpret_cast<uint32_t *>(place) + (4 * upper + odd) * 64 + ((16 * wn + ((lane & 31) >> 1)) ^ (16 * (odd + 2 * upper)));
+#pragma unroll
+  for (int i = 0; i < Cfg::TM; ++i)
+#pragma unroll
+    for (int v = 0; v < 16; v += 2) {
+      const float a = value(i, v), b = value(i, v + 1);
+      const int other = __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, odd ? a : b), 0xb1, 0xf, 0xf, true);   // the neighbour's
+      const float o = __builtin_bit_cast(float, other);
+      to[(32 * i + 8 * (v >> 2) + (v & 3)) * 64] = odd ? pack_bf16x2(o, b) : pack_bf16x2(a, o);
+    }
+}
+
+// The tile's 256 rows of 128 columns to C [M, N], 256 bytes of a row by 16
+// lanes. KEPT: nobody reads it soon, so it does not displace what the tiles read
+// from the caches (4096 x 11008 x 4096, both directions: 4 to 18 us of 1570 less;
+// with H written so too the forward alone takes 726 us instead of 718).
+template <bool KEPT>
+__device__ __forceinline__ void store_rows(const __bf16 *lo, const __bf16 *hi, __bf16 *C, int64_t M, int64_t N, int64_t m0, int64_t n0) {
+  const int q = threadIdx.x & 15;
+  const bool there = n0 + 8 * q < N;
+#pragma unroll
+  for (int k = 0; k < 256 * 16 / kT; ++k) {
+    const int row = static_cast<int>(threadIdx.x >> 4) + kT / 16 * k, in = row & 127, bank = (row & 1) + (row >> 1 & 2);
+    const u32x4 v = *reinterpret_cast<const u32x4 *>((row < 128 ? lo : hi) + in * 128 + 8 * (q ^ (4 * bank)));
+    if (!there || m0 + row >= M) continue;
+    u32x4 *const to = reinterpret_cast<u32x4 *>(C + (m0 + row) * N + n0 + 8 * q);
+    if (KEPT) __builtin_nontemporal_store(v, to);
+    else *to = v;
+  }
+}
+
 // 256 rows by 128 columns of H: a wave ends with 128 rows of 32 columns, the
 // gate's sums in its first fragment column and the other weight's in its second.
 __global__ __launch_bounds__(kT, 1) void k_gated_fwd(const FwdParams p, const Nf4Tables tab) {
@@ -237,12 +306,11 @@ __global__ __launch_bounds__(kT, 1) void k_gated_fwd(const FwdParams p, const Nf
   __shared__ float2 lv_tab[256 * kLvCopies];
   const float2 *lv = load_level_pairs(lv_tab, tab);
   const int tiles_m = static_cast<int>((p.M + 255) / 256), tiles_n = static_cast<int>((p.N + 127) / 128);
-  const int tiles = tiles_m * tiles_n;
-  const int z = static_cast<int>(blockIdx.x) / tiles;
+  const Piece piece = piece_of(p.tail, static_cast<int>(blockIdx.x), static_cast<int>(p.K / kBK));
   int tm, tn;
-  tile_of(static_cast<int>(blockIdx.x) - z * tiles, tiles_m, tiles_n, tm, tn);
+  tile_of(piece.tile, tiles_m, tiles_n, tm, tn);
   const int64_t n0 = static_cast<int64_t>(tn) * 128, m0 = static_cast<int64_t>(tm) * 256;
-  const int s0 = z * p.per, s1 = min(static_cast<int>(p.K / kBK), s0 + p.per);
+  const int s0 = piece.s0, s1 = piece.s1;
   __syncthreads();
   Acc<Cfg> acc;
   acc.zero();
@@ -254,7 +322,7 @@ __global__ __launch_bounds__(kT, 1) void k_gated_fwd(const FwdParams p, const Nf
   }
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int wm = w / Cfg::WAVES_N, wn = w % Cfg::WAVES_N;
-  if (p.rp > 0 && z == 0) {
+  if (p.rp > 0 && piece.z == 0) {
     // each weight's columns take its own half of Hs
     const DirectRowsT<kT> ag(p.Hs, 2 * p.rp, p.M, m0), au(static_cast<const __bf16 *>(p.Hs) + p.rp, 2 * p.rp, p.M, m0);
     const DirectRowsT<kT> db(p.Bi, p.rp, 2 * p.N, 2 * n0);
@@ -282,39 +350,40 @@ __global__ __launch_bounds__(kT, 1) void k_gated_fwd(const FwdParams p, const Nf
       __syncthreads();
     }
   }
-  if (p.S > 1) {
-    store_f32<Cfg>(acc, p.part + static_cast<int64_t>(z) * p.M * 2 * p.N, 2 * p.N, p.M, 2 * p.N, m0, 2 * n0);
+  if (piece.part) {
+    store_f32<Cfg>(acc, piece.part, 256, min(p.M - m0, int64_t(256)), 256, 0, 0);
     return;
   }
-  const int64_t n = n0 + 32 * wn + (lane & 31);
-  if (n >= p.N) return;
-#pragma unroll
-  for (int i = 0; i < Cfg::TM; ++i)
-#pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const int64_t m = m0 + wm * Cfg::WTM + i * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-      if (m >= p.M) continue;
-      const float g = acc.v[i][0][v], u = acc.v[i][1][v];
-      p.H[m * p.N + n] = static_cast<__bf16>(gate_value(g, u));
-      if (p.G) {
-        p.G[m * p.N + n] = static_cast<__bf16>(g);
-        p.U[m * p.N + n] = static_cast<__bf16>(u);
-      }
-    }
+  // through LDS, where each array is 128 rows of the tile
+  const auto put = [&](__bf16 *lo, __bf16 *hi, auto value) { stage_rows(wm ? hi : lo, value); };
+  if (p.G) {
+    put(sa0, sa1, [&](int i, int v) { return acc.v[i][0][v]; });
+    put(sb0, sb1, [&](int i, int v) { return acc.v[i][1][v]; });
+    __syncthreads();
+    store_rows<true>(sa0, sa1, p.G, p.M, p.N, m0, n0);
+    store_rows<true>(sb0, sb1, p.U, p.M, p.N, m0, n0);
+    __syncthreads();
+  }
+  put(sa0, sa1, [&](int i, int v) { return gate_value(acc.v[i][0][v], acc.v[i][1][v]); });
+  __syncthreads();
+  store_rows<false>(sa0, sa1, p.H, p.M, p.N, m0, n0);
 }
 
-// H (and G, U) of the summed partials, four columns a lane.
-__global__ __launch_bounds__(256) void k_gated_out(const float *part, int S, int64_t M, int64_t N, __bf16 *H, __bf16 *G, __bf16 *U) {
-  const int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-  if (e >= M * N) return;
-  const int64_t m = e / N, n = e - m * N;
-  const int64_t at = m * 2 * N + 64 * (n >> 5) + (n & 31);
-  const float4 g = split_sum4(part, M * 2 * N, at, S), u = split_sum4(part, M * 2 * N, at + 32, S);
-  *reinterpret_cast<uint2 *>(H + e) = make_uint2(pack_bf16x2(gate_value(g.x, u.x), gate_value(g.y, u.y)),
-                                                 pack_bf16x2(gate_value(g.z, u.z), gate_value(g.w, u.w)));
-  if (G) {
-    *reinterpret_cast<uint2 *>(G + e) = make_uint2(pack_bf16x2(g.x, g.y), pack_bf16x2(g.z, g.w));
-    *reinterpret_cast<uint2 *>(U + e) = make_uint2(pack_bf16x2(u.x, u.y), pack_bf16x2(u.z, u.w));
+// H (and G, U) of the split tiles, four columns a lane, 32 workgroups a tile.
+__global__ __launch_bounds__(256) void k_gated_out(const FwdParams p) {
+  const int i = static_cast<int>(blockIdx.x) >> 5, at = (static_cast<int>(blockIdx.x) & 31) * 256 + static_cast<int>(threadIdx.x);
+  const int row = at >> 5, c = 4 * (at & 31);
+  int tm, tn;
+  tile_of(static_cast<int>(p.tail.whole) + i, static_cast<int>((p.M + 255) / 256), static_cast<int>((p.N + 127) / 128), tm, tn);
+  const int64_t m = static_cast<int64_t>(tm) * 256 + row, n = static_cast<int64_t>(tn) * 128 + c, e = m * p.N + n;
+  if (m >= p.M || n >= p.N) return;
+  const int col = 64 * (c >> 5) + (c & 31);
+  const float4 g = sums_of(p.tail, i, row, col), u = sums_of(p.tail, i, row, col + 32);
+  *reinterpret_cast<uint2 *>(p.H + e) = make_uint2(pack_bf16x2(gate_value(g.x, u.x), gate_value(g.y, u.y)),
+                                                   pack_bf16x2(gate_value(g.z, u.z), gate_value(g.w, u.w)));
+  if (p.G) {
+    *reinterpret_cast<uint2 *>(p.G + e) = make_uint2(pack_bf16x2(g.x, g.y), pack_bf16x2(g.z, g.w));
+    *reinterpret_cast<uint2 *>(p.U + e) = make_uint2(pack_bf16x2(u.x, u.y), pack_bf16x2(u.z, u.w));
   }
 }
 
@@ -350,8 +419,7 @@ struct DxParams {
   void *dX;                 // bf16 [M, K]
   int64_t M, N, K;
   int rp;
-  float *part;              // fp32 [S][M][K] (S > 1)
-  int S, per;               // of the 2 N / 64 steps, the gate's in front
+  Tail tail;                // of the 2 N / 64 steps, the gate's in front
 };
 
 // Rows of dG for steps below N, of dU behind them.
@@ -381,12 +449,11 @@ __global__ __launch_bounds__(kT, 1) void k_gated_dx(const DxParams p, const Nf4T
   __shared__ float2 lv_tab[256 * kLvCopies];
   const float2 *lv = load_level_pairs(lv_tab, tab);
   const int tiles_m = static_cast<int>((p.M + 255) / 256), tiles_k = static_cast<int>((p.K + 255) / 256);
-  const int tiles = tiles_m * tiles_k;
-  const int z = static_cast<int>(blockIdx.x) / tiles;
+  const Piece piece = piece_of(p.tail, static_cast<int>(blockIdx.x), static_cast<int>(2 * p.N / kBK));
   int tm, tn;
-  tile_of(static_cast<int>(blockIdx.x) - z * tiles, tiles_m, tiles_k, tm, tn);
+  tile_of(piece.tile, tiles_m, tiles_k, tm, tn);
   const int64_t k0 = static_cast<int64_t>(tn) * 256, m0 = static_cast<int64_t>(tm) * 256;
-  const int s0 = z * p.per, s1 = min(static_cast<int>(2 * p.N / kBK), s0 + p.per);
+  const int s0 = piece.s0, s1 = piece.s1;
   __syncthreads();
   Acc<Cfg> acc;
   acc.zero();
@@ -405,12 +472,12 @@ __global__ __launch_bounds__(kT, 1) void k_gated_dx(const DxParams p, const Nf4T
     };
     big_mainloop_nf4<Cfg>(acc, da, l0, l1, load, s1 - s0, smem, lv);
   }
-  if (p.rp > 0 && z == 0) {
+  if (p.rp > 0 && piece.z == 0) {
     const DirectRowsT<kT> da(p.low, 2 * p.rp, p.M, m0), db(p.At, 2 * p.rp, p.K, k0);
     big_mainloop_dense<Cfg>(acc, da, db, 2 * p.rp / kBK, smem);
   }
-  if (p.S > 1)
-    store_f32<Cfg>(acc, p.part + static_cast<int64_t>(z) * p.M * p.K, p.K, p.M, p.K, m0, k0);
+  if (piece.part)
+    store_f32<Cfg>(acc, piece.part, 256, min(p.M - m0, int64_t(256)), 256, 0, 0);
   else if (m0 + 256 <= p.M && k0 + 256 <= p.K)
     store_bf16<Cfg, false>(acc, static_cast<__bf16 *>(p.dX), p.K, p.M, p.K, m0, k0, 1.0f);
   else
@@ -497,31 +564,50 @@ __global__ __launch_bounds__(256) void k_gated_grad_sum(const GradSumParams p) {
   }
 }
 
-// dX = bf16(sum of the partials, in split order).
-__global__ __launch_bounds__(256) void k_gated_dx_sum(const float *part, int S, int64_t plane, __bf16 *out) {
-  const int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-  if (e >= plane) return;
-  const float4 v = split_sum4(part, plane, e, S);
-  *reinterpret_cast<uint2 *>(out + e) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+// dX of the split tiles, four columns a lane, 64 workgroups a tile.
+__global__ __launch_bounds__(256) void k_gated_dx_sum(const DxParams p) {
+  const int i = static_cast<int>(blockIdx.x) >> 6, at = (static_cast<int>(blockIdx.x) & 63) * 256 + static_cast<int>(threadIdx.x);
+  const int row = at >> 6, c = 4 * (at & 63);
+  int tm, tn;
+  tile_of(static_cast<int>(p.tail.whole) + i, static_cast<int>((p.M + 255) / 256), static_cast<int>((p.K + 255) / 256), tm, tn);
+  const int64_t m = static_cast<int64_t>(tm) * 256 + row, k = static_cast<int64_t>(tn) * 256 + c;
+  if (m >= p.M || k >= p.K) return;
+  const float4 v = sums_of(p.tail, i, row, c);
+  *reinterpret_cast<uint2 *>(static_cast<__bf16 *>(p.dX) + m * p.K + k) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
 // -------------------------------------------------------------------- plan
 
 struct Plan {
   int rp;
-  Split down, gemm, ga, gb;
+  Tail tail;
+  Split down, ga, gb;
 };
+
+// Parts of sixteen steps at least where there are whole rounds in front.
+Tail make_tail(int64_t tiles, int steps) {
+  Tail t{tiles, 0, 1, steps, nullptr};
+  const int64_t rest = tiles % kCus;
+  if (rest == 0 || 2 * rest > kCus) return t;
+  const int S = static_cast<int>(std::min<int64_t>(kCus / rest, steps / (tiles > rest ? 16 : kMinSplitSteps)));
+  if (S < 2) return t;
+  t.per = static_cast<int>(ceil_div(steps, S));
+  t.S = static_cast<int>(ceil_div(steps, t.per));
+  t.whole = tiles - rest;
+  t.rest = rest;
+  return t;
+}
 
 Plan make_plan(int64_t M, int64_t N, int64_t K, int r, bool backward) {
   Plan pl{};
   pl.rp = gated_padded_rank(r);
   const int64_t tiles_m = grid_blocks(M, 256);
   if (!backward) {
-    pl.gemm = gemm_split(tiles_m * grid_blocks(N, 128), static_cast<int>(K / kBK), M, 2 * N, true);
+    pl.tail = make_tail(tiles_m * grid_blocks(N, 128), static_cast<int>(K / kBK));
     if (r) pl.down = choose_split(grid_blocks(M, 128) * (2 * pl.rp / 128), static_cast<int>(K / kBK), 64, kCus);
     return pl;
   }
-  pl.gemm = gemm_split(tiles_m * grid_blocks(K, 256), static_cast<int>(2 * N / kBK), M, K, true);
+  pl.tail = make_tail(tiles_m * grid_blocks(K, 256), static_cast<int>(2 * N / kBK));
   if (r) {
     pl.down = choose_split(grid_blocks(M, 128) * 2 * (pl.rp / 64), static_cast<int>(N / kBK), 64, kCus);
     const int msteps = static_cast<int>(ceil_div(M, kBK));
@@ -532,11 +618,11 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int r, bool backward) {
 }
 
 struct Buffers {
-  float *cs[2], *part, *down, *ga, *gb;
+  float *cs[2], *down, *ga, *gb;
   __bf16 *Acat, *Bi, *At, *Bt, *low, *dG, *dU, *Hs;
 };
 
-size_t carve(void *ws, const Plan &pl, int64_t M, int64_t N, int64_t K, bool backward, Buffers *b) {
+size_t carve(void *ws, Plan &pl, int64_t M, int64_t N, int64_t K, bool backward, Buffers *b) {
   Carve c{static_cast<char *>(ws)};
   if (!backward && M <= kGatedStreamRows) {
     if (pl.rp) b->Hs = c.take<__bf16>(2 * static_cast<size_t>(pl.rp) * M);
@@ -545,7 +631,7 @@ size_t carve(void *ws, const Plan &pl, int64_t M, int64_t N, int64_t K, bool bac
   const int64_t nb = N * K / kBlock;
   b->cs[0] = c.take<float>(nb);
   b->cs[1] = c.take<float>(nb);
-  if (pl.gemm.splits > 1) b->part = c.take<float>(static_cast<size_t>(pl.gemm.splits) * M * (backward ? K : 2 * N));
+  if (pl.tail.rest) pl.tail.part = c.take<float>(static_cast<size_t>(pl.tail.S) * pl.tail.rest * 65536);
   const size_t cols = 2 * static_cast<size_t>(pl.rp);
   if (pl.rp) b->down = c.take<float>(pl.down.splits * M * cols);
   if (!backward) {
@@ -603,12 +689,13 @@ const float *scales(const GatedArgs &a, const Buffers &b, int w) { return fmt_dq
 }  // namespace
 
 size_t gated_ws_bytes(int64_t M, int64_t N, int64_t K, int r, bool backward) {
+  Plan pl = make_plan(M, N, K, r, backward);
   Buffers b{};
-  return carve(nullptr, make_plan(M, N, K, r, backward), M, N, K, backward, &b);
+  return carve(nullptr, pl, M, N, K, backward, &b);
 }
 
 hipError_t launch_gated_fwd(const GatedArgs &a, const void *X, void *H, void *G, void *U, void *Hs, void *ws, hipStream_t s) {
-  const Plan pl = make_plan(a.M, a.N, a.K, a.r, false);
+  Plan pl = make_plan(a.M, a.N, a.K, a.r, false);
   Buffers b{};
   carve(ws, pl, a.M, a.N, a.K, false, &b);
   if (Hs) b.Hs = static_cast<__bf16 *>(Hs);
@@ -632,17 +719,15 @@ hipError_t launch_gated_fwd(const GatedArgs &a, const void *X, void *H, void *G,
     k_gated_sum<<<blocks(n, 1024), 256, 0, s>>>(b.down, pl.down.splits, n, a.scale, b.Hs);
   }
   FwdParams p{X, {a.w[0].codes, a.w[1].codes}, {scales(a, b, 0), scales(a, b, 1)}, b.Hs, b.Bi, static_cast<__bf16 *>(H),
-              static_cast<__bf16 *>(G), static_cast<__bf16 *>(U), a.M, a.N, a.K, pl.rp, b.part, pl.gemm.splits,
-              pl.gemm.steps_per_split};
-  const int64_t tiles = grid_blocks(a.M, 256) * grid_blocks(a.N, 128);
-  k_gated_fwd<<<static_cast<unsigned>(tiles * pl.gemm.splits), kT, 0, s>>>(p, format_tables(a.format));
-  if (pl.gemm.splits > 1) k_gated_out<<<blocks(a.M * a.N, 1024), 256, 0, s>>>(b.part, pl.gemm.splits, a.M, a.N, p.H, p.G, p.U);
+              static_cast<__bf16 *>(G), static_cast<__bf16 *>(U), a.M, a.N, a.K, pl.rp, pl.tail};
+  k_gated_fwd<<<static_cast<unsigned>(pl.tail.whole + pl.tail.rest * pl.tail.S), kT, 0, s>>>(p, format_tables(a.format));
+  if (pl.tail.rest) k_gated_out<<<static_cast<unsigned>(32 * pl.tail.rest), 256, 0, s>>>(p);
   return hipGetLastError();
 }
 
 hipError_t launch_gated_bwd(const GatedArgs &a, const void *dH, const void *X, const void *G, const void *U, const void *Hs,
                             void *dX, void *const (&dA)[2], void *const (&dB)[2], void *ws, hipStream_t s) {
-  const Plan pl = make_plan(a.M, a.N, a.K, a.r, true);
+  Plan pl = make_plan(a.M, a.N, a.K, a.r, true);
   Buffers b{};
   carve(ws, pl, a.M, a.N, a.K, true, &b);
   run_prep(a, pl, b, true, s);
@@ -669,11 +754,9 @@ hipError_t launch_gated_bwd(const GatedArgs &a, const void *dH, const void *X, c
     k_gated_sum<<<blocks(count, 1024), 256, 0, s>>>(b.down, pl.down.splits, count, a.scale, b.low);
   }
   DxParams p{b.dG, b.dU, {a.w[0].codes, a.w[1].codes}, {scales(a, b, 0), scales(a, b, 1)}, b.low, b.At, dX, a.M, a.N, a.K,
-             pl.rp, b.part, pl.gemm.splits, pl.gemm.steps_per_split};
-  const int64_t tiles = grid_blocks(a.M, 256) * grid_blocks(a.K, 256);
-  k_gated_dx<<<static_cast<unsigned>(tiles * pl.gemm.splits), kT, 0, s>>>(p, format_tables(a.format));
-  if (pl.gemm.splits > 1)
-    k_gated_dx_sum<<<blocks(a.M * a.K, 1024), 256, 0, s>>>(b.part, pl.gemm.splits, a.M * a.K, static_cast<__bf16 *>(dX));
+             pl.rp, pl.tail};
+  k_gated_dx<<<static_cast<unsigned>(pl.tail.whole + pl.tail.rest * pl.tail.S), kT, 0, s>>>(p, format_tables(a.format));
+  if (pl.tail.rest) k_gated_dx_sum<<<static_cast<unsigned>(64 * pl.tail.rest), 256, 0, s>>>(p);
   if (pl.rp) {
     GradParams g{};
     g.X = X;
