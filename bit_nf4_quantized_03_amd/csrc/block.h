@@ -63,7 +63,7 @@ size_t gated_ws_bytes(int64_t M, int64_t N, int64_t K, int r, bool backward);
 // The forward of at most kGatedStreamRows rows; Hs [M][2 padded rank] as above (r > 0).
 constexpr int64_t kGatedStreamRows = 32;
 constexpr int kGatedFewGroups = 512;
-hipError_t launch_gated_stream(const GatedArgs &a, const void *X, void *H, void *G, void *U, __bf16 *Hs, hipStream_t s);
+hipError_t launch_gated_stream(const GatedArgs &a, const void *X, void *H, void *G, void *U, void *Hs, hipStream_t s);
 // G, U, Hs: kept for the backward, or null.
 hipError_t launch_gated_fwd(const GatedArgs &a, const void *X, void *H, void *G, void *U, void *Hs, void *ws, hipStream_t s);
 hipError_t launch_gated_bwd(const GatedArgs &a, const void *dH, const void *X, const void *G, const void *U, const void *Hs,

@@ -491,10 +491,10 @@ void run_rows(StreamParams p, const Nf4Tables &tab, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_gated_stream(const GatedArgs &a, const void *X, void *H, void *G, void *U, __bf16 *Hs, hipStream_t s) {
+hipError_t launch_gated_stream(const GatedArgs &a, const void *X, void *H, void *G, void *U, void *Hs, hipStream_t s) {
   const int rp = gated_padded_rank(a.r);
   if (a.r) {
-    const LowParams p{static_cast<const __bf16 *>(X), {a.A[0], a.A[1]}, a.adapter_bf16, a.K, static_cast<int>(a.M), a.r, rp, a.scale, Hs};
+    const LowParams p{static_cast<const __bf16 *>(X), {a.A[0], a.A[1]}, a.adapter_bf16, a.K, static_cast<int>(a.M), a.r, rp, a.scale, static_cast<__bf16 *>(Hs)};
     if (a.M == 1) k_gated_low<1><<<2 * rp, 256, 0, s>>>(p);
     else k_gated_low<8><<<dim3(2 * rp, static_cast<unsigned>(ceil_div(a.M, 8))), 256, 0, s>>>(p);
   }
@@ -508,7 +508,7 @@ hipError_t launch_gated_stream(const GatedArgs &a, const void *X, void *H, void 
     p.absmax[w] = a.w[w].absmax;
     p.B[w] = a.B[w];
   }
-  p.Hs = Hs;
+  p.Hs = static_cast<const __bf16 *>(Hs);
   p.bf16 = a.adapter_bf16;
   p.r = a.r;
   p.rp = rp;

@@ -85,6 +85,71 @@ def test_gated_grouped_rejects():
     assert g(X, W, off, 2, None, None, None) == -1
 
 
+def weight(rows=128, cols=192, fmt=qb.QLORA_FMT_NF4_DQ, **kw):
+    parts = {**dict.fromkeys(("codes", "absmax_q", "dq_scale", "dq_mean", "absmax"), FAKE), **kw}
+    return ref(qb._Weight(rows, cols, parts["codes"], parts["absmax_q"], parts["dq_scale"], parts["dq_mean"], parts["absmax"], fmt))
+
+
+def adapters(r=8, dtype=BF16, scale=2.0, **kw):
+    parts = {**dict.fromkeys(("gate_A", "gate_B", "up_A", "up_B"), FAKE), **kw}
+    return ref(binding._Adapters(parts["gate_A"], parts["gate_B"], parts["up_A"], parts["up_B"], r, dtype, scale))
+
+
+def test_block_sizes():
+    cols, ws = lib.qlora_gated_saved_cols, lib.qlora_gated_workspace_bytes
+    assert [cols(r) for r in (-1, 0, 1, 64, 65, 256, 257)] == [0, 0, 128, 128, 256, 512, 0]
+    for M, N, K, r in ((0, 128, 192, 8), (-1, 128, 192, 8), (1 << 25, 128, 192, 8), (5, 100, 192, 8), (5, 128, 96, 8), (5, 128, 192, -1),
+                       (5, 128, 192, 257), (5, 1 << 23, 1 << 23, 8), (1 << 24, 1 << 23, 64, 8), (5, 1 << 24, 64, 8)):
+        for backward in (0, 1):
+            assert ws(M, N, K, r, backward) == 0
+    assert ws(5, 128, 192, 0, 0) == 0   # a few rows without adapters
+    for M, N, K, r in ((5, 128, 192, 8), (33, 128, 192, 0), (4096, 11008, 4096, 64), (1 << 24, 64, 64, 1), (1, 1 << 23, 1 << 13, 256)):
+        forward, back = ws(M, N, K, r, 0), ws(M, N, K, r, 1)
+        assert back >= 4 * M * N                       # dG and dU
+        assert not r or M > 32 or forward >= 256 * M   # Hs
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_block_rejects(backward):
+    need = lib.qlora_gated_workspace_bytes(40, 128, 192, 8, backward)
+    grads = ref(binding._Grads(FAKE, FAKE, FAKE, FAKE))
+
+    def call(M=40, gate=weight(), up=weight(), ad=adapters(), ws=FAKE, size=need, first=FAKE, X=FAKE, G=FAKE, U=FAKE, Hs=FAKE, out=FAKE, grads=grads):
+        if backward:
+            return lib.qlora_gated_bwd(first, X, G, U, Hs, M, gate, up, ad, out, grads, ws, size, None)
+        return lib.qlora_gated_fwd(X, M, gate, up, ad, out, G, U, Hs, ws, size, None)
+    assert call(gate=None) == -1 and call(up=None) == -1 and call(X=0) == -1 and call(out=0) == -1
+    assert call(G=0) == -1 and call(U=0) == -1 and call(Hs=0) == -1
+    assert call(ad=None, size=1 << 30) == -1            # Hs without adapters
+    for M in (0, -1, (1 << 24) + 1):
+        assert call(M=M) == -2 and "M =" in qb.qlora_last_error()
+    for bad in (weight(64), weight(cols=128), weight(rows=100), weight(cols=96)):
+        assert call(up=bad) == -2
+    for bad in (weight(100), weight(cols=96), weight(1 << 23, 1 << 23)):
+        assert call(gate=bad, up=bad) == -2
+    assert call(up=weight(fmt=qb.QLORA_FMT_NF4)) == -7 and "differ" in qb.qlora_last_error()
+    for part in ("codes", "absmax_q", "dq_scale", "dq_mean"):
+        assert call(up=weight(**{part: 0})) == -1
+    for r in (0, -1, 257):
+        assert call(ad=adapters(r)) == -2
+    assert call(ad=adapters(dtype=2)) == -3
+    for part in ("gate_A", "gate_B", "up_A", "up_B"):
+        assert call(ad=adapters(**{part: 0})) == -1
+        assert call(ad=adapters(**{part: FAKE + 8})) == -6
+    for scale in (float("nan"), float("inf")):
+        assert call(ad=adapters(scale=scale)) == -2
+    assert call(ws=0) == -4 and call(size=need - 1) == -4 and "workspace" in qb.qlora_last_error()
+    assert call(ws=FAKE + 8) == -6
+    for name in ("X", "G", "U", "Hs", "out") + (("first",) if backward else ()):
+        assert call(**{name: FAKE + 2}) == -6, name
+    if backward:
+        assert call(first=0) == -1 and call(grads=None) == -1
+        for i in range(4):
+            at = [FAKE] * 4
+            assert call(grads=ref(binding._Grads(*at[:i], 0, *at[i + 1:]))) == -1
+            assert call(grads=ref(binding._Grads(*at[:i], FAKE + 4, *at[i + 1:]))) == -6
+
+
 @pytest.mark.parametrize("rot", [2, 4, 64, 128, 1024])
 @pytest.mark.parametrize("scaling,kind", [("plain", 0), ("linear", 1), ("ntk", 2), ("parts", 3)])
 def test_rope_freqs(rot, scaling, kind):
