@@ -56,16 +56,33 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_gated_gemv(const MxGemvParams
   }
 }
 
+// Tile number b of those of rows n_first on of the pair, tiles_n of them beside each other.
 template <class T>
-__global__ __launch_bounds__(T::kThreads, 1) void k_mx_gated(const MxGemmParams p, const MxGatedOut o) {
-  __shared__ __attribute__((aligned(16))) char smem[T::kLds];
-  const int tiles_m = static_cast<int>((p.M + T::BM - 1) / T::BM), tiles_n = static_cast<int>((p.N + T::BN - 1) / T::BN);
+__device__ __forceinline__ void gated_tile(const MxGemmParams &p, const MxGatedOut &o, int b, int64_t n_first, int tiles_n, char *smem) {
   int tm, tn, wave;
-  tile_of(static_cast<int>(blockIdx.x), tiles_m, tiles_n, tm, tn);
-  const int64_t n0 = static_cast<int64_t>(tn) * T::BN, m0 = static_cast<int64_t>(tm) * T::BM;
+  tile_of(b, static_cast<int>((p.M + T::BM - 1) / T::BM), tiles_n, tm, tn);
+  const int64_t n0 = n_first + static_cast<int64_t>(tn) * T::BN, m0 = static_cast<int64_t>(tm) * T::BM;
   MxAcc<T> acc;
   const bool mine = mx_tile_product<T>(acc, p.op, n0, m0, p.steps, smem, wave);
   mx_gated_store<T>(acc, o, n0, m0, p.M, wave, mine, smem);
+}
+
+template <class T>
+__global__ __launch_bounds__(T::kThreads, 1) void k_mx_gated(const MxGemmParams p, const MxGatedOut o) {
+  __shared__ __attribute__((aligned(16))) char smem[T::kLds];
+  gated_tile<T>(p, o, static_cast<int>(blockIdx.x), 0, static_cast<int>((p.N + T::BN - 1) / T::BN), smem);
+}
+
+// Large tiles, n_tiles beside each other, and smaller ones for the rows of the
+// pair behind them.
+template <class T, class S>
+__global__ __launch_bounds__(T::kThreads, 1) void k_mx_gated_two(const MxGemmParams p, const MxGatedOut o, int n_tiles) {
+  static_assert(T::kThreads == S::kThreads, "one launch");
+  __shared__ __attribute__((aligned(16))) char smem[T::kLds > S::kLds ? T::kLds : S::kLds];
+  const int large = n_tiles * static_cast<int>((p.M + T::BM - 1) / T::BM), b = static_cast<int>(blockIdx.x);
+  const int64_t first = static_cast<int64_t>(n_tiles) * T::BN;
+  if (b < large) gated_tile<T>(p, o, b, 0, n_tiles, smem);
+  else gated_tile<S>(p, o, b - large, first, static_cast<int>((p.N - first + S::BN - 1) / S::BN), smem);
 }
 
 template <class T>
@@ -102,13 +119,41 @@ hipError_t run_tile(const MxGemmParams &p, const MxGatedOut &o, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The N tiles of kMxTile[0] in front of smaller ones, kMxTile[1], or 0: all are
+// of one kind. Large tiles come in rounds of one for each compute unit, and a
+// last round that is not full costs as much as any; the smaller tiles halve it
+// where that is less by the figures that choose the tile (4096 x 11008 x 4096,
+// 1376 large tiles in six rounds: 293 us, 279 with 96 of them as 192 smaller
+// ones; 2500 rows 188 and 180; 2048 x 22016 x 8192, 4 bits, 375 and 368).
+int large_tiles(int64_t M, int64_t N, bool fp4) {
+  const double tiles_m = static_cast<double>(mx_ceil(M, kMxTile[0].bm)), tiles_n = static_cast<double>(mx_ceil(N, kMxTile[0].bn));
+  const double rounds = std::floor(tiles_m * tiles_n / kMxCus), n = std::floor(rounds * kMxCus / tiles_m);
+  if (n < 1 || n >= tiles_n) return 0;
+  const auto &c = kMxTile[1].cost[fp4];
+  const double load = static_cast<double>(mx_ceil(M, kMxTile[1].bm)) * (tiles_n - n) * kMxTile[0].bn / kMxTile[1].bn / kMxCus;
+  const double rest = load <= 1 ? c.light + (c.full - c.light) * load : c.full * std::ceil(load);
+  return rest < kMxTile[0].cost[fp4].full ? static_cast<int>(n) : 0;
+}
+
+template <class T, class S>
+hipError_t run_two(const MxGemmParams &p, const MxGatedOut &o, int n_tiles, hipStream_t s) {
+  const int64_t rest = mx_tile_groups(S::BM, S::BN, p.M, p.N - static_cast<int64_t>(n_tiles) * T::BN, 0);
+  k_mx_gated_two<T, S><<<static_cast<unsigned>(n_tiles * mx_ceil(p.M, T::BM) + rest), T::kThreads, 0, s>>>(p, o, n_tiles);
+  return hipGetLastError();
+}
+
 template <int XT>
 hipError_t run_tiles(const MxGemmParams &p, const MxGatedOut &o, hipStream_t s) {
   constexpr bool kPair = XT == QLORA_MX_FP4;
   constexpr int kDeep = kPair ? 4 : 3;   // stages
-  switch (mx_choose_tile(p.M, p.N, p.experts, XT == QLORA_MX_FP4)) {
-    case 0: return run_tile<0, MxTile<XT, 4, 2, 2, 4, kDeep, kPair ? 2 : 1, 1, kPair>>(p, o, s);
-    case 1: return run_tile<1, MxTile<XT, 2, 2, 4, 2, kDeep, kPair ? 2 : 4, 1, kPair>>(p, o, s);
+  using Large = MxTile<XT, 4, 2, 2, 4, kDeep, kPair ? 2 : 1, 1, kPair>;
+  using Half = MxTile<XT, 2, 2, 4, 2, kDeep, kPair ? 2 : 4, 1, kPair>;
+  switch (mx_choose_tile(p.M, p.N, p.experts, kPair)) {
+    case 0: {
+      const int n = p.experts ? 0 : large_tiles(p.M, p.N, kPair);
+      return n ? run_two<Large, Half>(p, o, n, s) : run_tile<0, Large>(p, o, s);
+    }
+    case 1: return run_tile<1, Half>(p, o, s);
     case 2: return run_tile<2, MxTile<XT, 2, 2, 2, 2, kDeep, kPair ? 2 : 1, 1, kPair>>(p, o, s);
     case 3: return run_tile<3, MxTile<XT, 2, 1, 2, 2, 4, 2>>(p, o, s);
     default: return run_tile<4, MxTile<XT, 1, 1, 2, 2, 4, 4, 2>>(p, o, s);

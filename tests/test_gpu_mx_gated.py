@@ -171,6 +171,29 @@ def test_gated_on_exact_sums(qb, M, N, K, t):
         check_microscaled(qb.qlora_mx_gated(X, W, mx=o), h, d)
 
 
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("M,N", [(3900, 7136), (3841, 7008)])
+def test_rounds_of_tiles_and_a_rest(qb, M, N, t):
+    """Sizes whose last columns have smaller tiles than the rest, exact sums: bit for bit what row blocks give by themselves."""
+    import torch
+    K = 96
+    gu.announce(f"mx gated rounds and a rest {M}x{N} type {t}")
+    rng = np.random.default_rng(N)
+    x = np.zeros((M, K))
+    x[np.arange(M), rng.integers(0, K, M)] = np.exp2(rng.integers(-4, 4, M))
+    X, _ = dev_mx(qb, x, t)
+    W, *_ = pair(qb, rng.normal(size=(N, K)), rng.normal(size=(N, K)))
+    for o in (None, *TYPES):
+        H = qb.qlora_mx_gated(X, W, mx=o)
+        for a in range(0, M, 300):
+            b = min(a + 300, M)
+            part = qb.qlora_mx_gated(qb.MXMatrix(b - a, K, X.codes[a:b], X.scales[a:b], t), W, mx=o)
+            if o is None:
+                assert torch.equal(H[a:b], part)
+            else:
+                assert torch.equal(H.codes[a:b], part.codes) and torch.equal(H.scales[a:b], part.scales)
+
+
 @pytest.mark.parametrize("M", [3, 90, 400])
 def test_large_and_nan_values(qb, M):
     """Gates far past the exponential's range, and NaN blocks, which stay in their row, column or block."""
