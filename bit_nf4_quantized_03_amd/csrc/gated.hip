@@ -12,7 +12,7 @@
 //                  interleaved tiles below (rp: r rounded up to 64, zero padded)
 //   k_gated_down   split partials of X [Ag; Au]^T: X is read once for both
 //   k_gated_sum    Hs = bf16(s sums) [M][2 rp]
-//   k_gated_fwd    256 rows by 128 columns of H a workgroup: the large-tile loop of
+//   k_gated_fwd    up to 256 rows by 128 columns of H a workgroup: the large-tile loop of
 //                  gemm_big.h on 128 rows of each weight, 32 of one and 32 of
 //                  the other in turn, so that both products of an element of H
 //                  end in one lane and the gate needs no exchange
@@ -36,8 +36,10 @@
 namespace qnf4 {
 namespace {
 
-using Cfg = CfgBig8;
-constexpr int kT = Cfg::kThreads;
+// Tiles of BM rows: eight waves of BM / 2 rows by 64.
+template <int BM>
+using TileOf = TileCfg<BM, 256, 2, 4>;
+constexpr int kT = TileOf<256>::kThreads;
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -192,11 +194,12 @@ __global__ __launch_bounds__(256) void k_gated_sum(const float *part, int splits
 
 // A tile occupies a compute unit, so tiles run in rounds of one for each, and
 // the last `rest` tiles, where they would fill no more than half of a round,
-// are split along the reduction into S parts, fp32 sums [S][rest][256][256]
+// are split along the reduction into S parts, fp32 sums [S][rest][BM][256]
 // that a kernel behind adds in order (4096 x 11008 x 4096, 96 tiles behind five
 // rounds: 738 -> 721 us; 1536 rows, both directions: 757 -> 707). Fewer tiles
 // than that in all are all split.
 struct Tail {
+  int bm;                // rows of a tile
   int64_t whole, rest;   // tiles
   int S, per;            // steps of a part
   float *part;
@@ -209,11 +212,12 @@ struct Piece {
 __device__ __forceinline__ Piece piece_of(const Tail &t, int b, int steps) {
   if (b < t.whole) return {b, 0, steps, nullptr, 0};
   const int q = b - static_cast<int>(t.whole), rest = static_cast<int>(t.rest), z = q / rest;
-  return {static_cast<int>(t.whole) + q - z * rest, z * t.per, min(steps, (z + 1) * t.per), t.part + static_cast<int64_t>(q) * 65536, z};
+  return {static_cast<int>(t.whole) + q - z * rest, z * t.per, min(steps, (z + 1) * t.per), t.part + static_cast<int64_t>(q) * 256 * t.bm, z};
 }
 // The sums of four columns from `col` on of row `row` of split tile `i`.
 __device__ __forceinline__ float4 sums_of(const Tail &t, int i, int row, int col) {
-  return split_sum4(t.part, t.rest * 65536, static_cast<int64_t>(i) * 65536 + row * 256 + col, t.S);
+  const int64_t size = 256 * t.bm;
+  return split_sum4(t.part, t.rest * size, i * size + row * 256 + col, t.S);
 }
 
 // ------------------------------------------------------------------ forward
@@ -256,14 +260,14 @@ struct PairRows {
   __device__ __forceinline__ void store_part(__bf16 *lds, const float2 *lv2, int i) const { one.store_part(lds, lv2, i); }
 };
 
-// A wave's 128 rows of 32 columns to its rows of 128 columns in LDS, as bf16.
+// A wave's BM / 2 rows of 32 columns to its rows of 128 columns in LDS, as bf16.
 // Neighbouring lanes have neighbouring columns: of two rows, the even one takes
 // the first and the odd one the second, so that a store is of two columns. The
 // four rows that one store reaches lie on different banks. (Without the detour,
 // from lanes with one column each, the forward took 735 us instead of 718.)
-template <class F>
+template <class Cfg, class F>
 __device__ __forceinline__ void stage_rows(__bf16 *place, F value) {
-  static_assert(Cfg::WTM == 128 && Cfg::WAVES_N == 4 && Cfg::kLdsA >= 128 * 128 && Cfg::kLdsB >= 128 * 128, "the places");
+  static_assert(Cfg::WAVES_N == 4 && Cfg::kLdsA >= Cfg::WTM * 128 && Cfg::kLdsB >= Cfg::WTM * 128, "the places");
   const int lane = threadIdx.x & 63, wn = (threadIdx.x >> 6) % Cfg::WAVES_N, odd = lane & 1, upper = lane >> 5;
   uint32_t *const to = reinterpret_cast<uint32_t *>(place) + (4 * upper + odd) * 64 + ((16 * wn + ((lane & 31) >> 1)) ^ (16 * (odd + 2 * upper)));
 #pragma unroll
@@ -277,18 +281,18 @@ __device__ __forceinline__ void stage_rows(__bf16 *place, F value) {
     }
 }
 
-// The tile's 256 rows of 128 columns to C [M, N], 256 bytes of a row by 16
+// The tile's BM rows of 128 columns to C [M, N], 256 bytes of a row by 16
 // lanes. KEPT: nobody reads it soon, so it does not displace what the tiles read
 // from the caches (4096 x 11008 x 4096, both directions: 4 to 18 us of 1570 less;
 // with H written so too the forward alone takes 726 us instead of 718).
-template <bool KEPT>
+template <class Cfg, bool KEPT>
 __device__ __forceinline__ void store_rows(const __bf16 *lo, const __bf16 *hi, __bf16 *C, int64_t M, int64_t N, int64_t m0, int64_t n0) {
   const int q = threadIdx.x & 15;
   const bool there = n0 + 8 * q < N;
 #pragma unroll
-  for (int k = 0; k < 256 * 16 / kT; ++k) {
-    const int row = static_cast<int>(threadIdx.x >> 4) + kT / 16 * k, in = row & 127, bank = (row & 1) + (row >> 1 & 2);
-    const u32x4 v = *reinterpret_cast<const u32x4 *>((row < 128 ? lo : hi) + in * 128 + 8 * (q ^ (4 * bank)));
+  for (int k = 0; k < Cfg::BM * 16 / kT; ++k) {
+    const int row = static_cast<int>(threadIdx.x >> 4) + kT / 16 * k, in = row < Cfg::WTM ? row : row - Cfg::WTM, bank = (in & 1) + (in >> 1 & 2);
+    const u32x4 v = *reinterpret_cast<const u32x4 *>((row < Cfg::WTM ? lo : hi) + in * 128 + 8 * (q ^ (4 * bank)));
     if (!there || m0 + row >= M) continue;
     u32x4 *const to = reinterpret_cast<u32x4 *>(C + (m0 + row) * N + n0 + 8 * q);
     if (KEPT) __builtin_nontemporal_store(v, to);
@@ -296,26 +300,29 @@ __device__ __forceinline__ void store_rows(const __bf16 *lo, const __bf16 *hi, _
   }
 }
 
-// 256 rows by 128 columns of H: a wave ends with 128 rows of 32 columns, the
+// BM rows by 128 columns of H: a wave ends with BM / 2 rows of 32 columns, the
 // gate's sums in its first fragment column and the other weight's in its second.
+template <int BM>
 __global__ __launch_bounds__(kT, 1) void k_gated_fwd(const FwdParams p, const Nf4Tables tab) {
+  using Cfg = TileOf<BM>;
+  using Rows = DirectRowsT<kT, BM>;
   static_assert(Cfg::TN == 2, "a fragment column of each weight");
   __shared__ __attribute__((aligned(16))) __bf16 sa0[Cfg::kLdsA], sa1[Cfg::kLdsA];
   __shared__ __attribute__((aligned(16))) __bf16 sb0[Cfg::kLdsB], sb1[Cfg::kLdsB];
   const BigSmem smem{sa0, sa1, sb0, sb1};
   __shared__ float2 lv_tab[256 * kLvCopies];
   const float2 *lv = load_level_pairs(lv_tab, tab);
-  const int tiles_m = static_cast<int>((p.M + 255) / 256), tiles_n = static_cast<int>((p.N + 127) / 128);
+  const int tiles_m = static_cast<int>((p.M + BM - 1) / BM), tiles_n = static_cast<int>((p.N + 127) / 128);
   const Piece piece = piece_of(p.tail, static_cast<int>(blockIdx.x), static_cast<int>(p.K / kBK));
   int tm, tn;
   tile_of(piece.tile, tiles_m, tiles_n, tm, tn);
-  const int64_t n0 = static_cast<int64_t>(tn) * 128, m0 = static_cast<int64_t>(tm) * 256;
+  const int64_t n0 = static_cast<int64_t>(tn) * 128, m0 = static_cast<int64_t>(tm) * BM;
   const int s0 = piece.s0, s1 = piece.s1;
   __syncthreads();
   Acc<Cfg> acc;
   acc.zero();
   {
-    DirectRowsT<kT> da(static_cast<const __bf16 *>(p.X) + static_cast<int64_t>(s0) * kBK, p.K, p.M, m0);
+    Rows da(static_cast<const __bf16 *>(p.X) + static_cast<int64_t>(s0) * kBK, p.K, p.M, m0);
     PairRows l0(p, n0), l1 = l0;
     auto load = [s0](PairRows &l, int s) { l.load(static_cast<int64_t>(s0 + s) * kBK); };
     big_mainloop_nf4<Cfg>(acc, da, l0, l1, load, s1 - s0, smem, lv);
@@ -324,7 +331,7 @@ __global__ __launch_bounds__(kT, 1) void k_gated_fwd(const FwdParams p, const Nf
   const int wm = w / Cfg::WAVES_N, wn = w % Cfg::WAVES_N;
   if (p.rp > 0 && piece.z == 0) {
     // each weight's columns take its own half of Hs
-    const DirectRowsT<kT> ag(p.Hs, 2 * p.rp, p.M, m0), au(static_cast<const __bf16 *>(p.Hs) + p.rp, 2 * p.rp, p.M, m0);
+    const Rows ag(p.Hs, 2 * p.rp, p.M, m0), au(static_cast<const __bf16 *>(p.Hs) + p.rp, 2 * p.rp, p.M, m0);
     const DirectRowsT<kT> db(p.Bi, p.rp, 2 * p.N, 2 * n0);
     const FragAddr<Cfg::WTM> fa(wm * Cfg::WTM, lane);
     const FragAddr<Cfg::WTN> fb(wn * Cfg::WTN, lane);
@@ -351,31 +358,31 @@ __global__ __launch_bounds__(kT, 1) void k_gated_fwd(const FwdParams p, const Nf
     }
   }
   if (piece.part) {
-    store_f32<Cfg>(acc, piece.part, 256, min(p.M - m0, int64_t(256)), 256, 0, 0);
+    store_f32<Cfg>(acc, piece.part, 256, min(p.M - m0, int64_t(BM)), 256, 0, 0);
     return;
   }
-  // through LDS, where each array is 128 rows of the tile
-  const auto put = [&](__bf16 *lo, __bf16 *hi, auto value) { stage_rows(wm ? hi : lo, value); };
+  // through LDS, where each array is half of the tile's rows
+  const auto put = [&](__bf16 *lo, __bf16 *hi, auto value) { stage_rows<Cfg>(wm ? hi : lo, value); };
   if (p.G) {
     put(sa0, sa1, [&](int i, int v) { return acc.v[i][0][v]; });
     put(sb0, sb1, [&](int i, int v) { return acc.v[i][1][v]; });
     __syncthreads();
-    store_rows<true>(sa0, sa1, p.G, p.M, p.N, m0, n0);
-    store_rows<true>(sb0, sb1, p.U, p.M, p.N, m0, n0);
+    store_rows<Cfg, true>(sa0, sa1, p.G, p.M, p.N, m0, n0);
+    store_rows<Cfg, true>(sb0, sb1, p.U, p.M, p.N, m0, n0);
     __syncthreads();
   }
   put(sa0, sa1, [&](int i, int v) { return gate_value(acc.v[i][0][v], acc.v[i][1][v]); });
   __syncthreads();
-  store_rows<false>(sa0, sa1, p.H, p.M, p.N, m0, n0);
+  store_rows<Cfg, false>(sa0, sa1, p.H, p.M, p.N, m0, n0);
 }
 
-// H (and G, U) of the split tiles, four columns a lane, 32 workgroups a tile.
+// H (and G, U) of the split tiles, four columns a lane, BM / 8 workgroups a tile.
 __global__ __launch_bounds__(256) void k_gated_out(const FwdParams p) {
-  const int i = static_cast<int>(blockIdx.x) >> 5, at = (static_cast<int>(blockIdx.x) & 31) * 256 + static_cast<int>(threadIdx.x);
+  const int bm = p.tail.bm, i = static_cast<int>(blockIdx.x) / (bm / 8), at = (static_cast<int>(blockIdx.x) - i * (bm / 8)) * 256 + static_cast<int>(threadIdx.x);
   const int row = at >> 5, c = 4 * (at & 31);
   int tm, tn;
-  tile_of(static_cast<int>(p.tail.whole) + i, static_cast<int>((p.M + 255) / 256), static_cast<int>((p.N + 127) / 128), tm, tn);
-  const int64_t m = static_cast<int64_t>(tm) * 256 + row, n = static_cast<int64_t>(tn) * 128 + c, e = m * p.N + n;
+  tile_of(static_cast<int>(p.tail.whole) + i, static_cast<int>((p.M + bm - 1) / bm), static_cast<int>((p.N + 127) / 128), tm, tn);
+  const int64_t m = static_cast<int64_t>(tm) * bm + row, n = static_cast<int64_t>(tn) * 128 + c, e = m * p.N + n;
   if (m >= p.M || n >= p.N) return;
   const int col = 64 * (c >> 5) + (c & 31);
   const float4 g = sums_of(p.tail, i, row, col), u = sums_of(p.tail, i, row, col + 32);
@@ -423,9 +430,11 @@ struct DxParams {
 };
 
 // Rows of dG for steps below N, of dU behind them.
+template <int BM>
 struct DualRows {
-  static constexpr int kPerWave = DirectRowsT<kT>::kPerWave;
-  DirectRowsT<kT> rows;
+  using Rows = DirectRowsT<kT, BM>;
+  static constexpr int kPerWave = Rows::kPerWave;
+  Rows rows;
   const char *base[2];
   int64_t red0, N;
   __device__ DualRows(const DxParams &p, int64_t m0, int64_t red0_)
@@ -434,31 +443,33 @@ struct DualRows {
   __device__ __forceinline__ void issue_range(int64_t red, __bf16 *lds, int i0, int n) const {
     red += red0;
     const bool up = red >= N;
-    DirectRowsT<kT> r = rows;
+    Rows r = rows;
     r.base = up ? base[1] : base[0];
     r.issue_range(up ? red - N : red, lds, i0, n);
   }
   template <int L>
-  __device__ __forceinline__ static void wait_copies() { DirectRowsT<kT>::wait_copies<L>(); }
+  __device__ __forceinline__ static void wait_copies() { Rows::template wait_copies<L>(); }
 };
 
+template <int BM>
 __global__ __launch_bounds__(kT, 1) void k_gated_dx(const DxParams p, const Nf4Tables tab) {
+  using Cfg = TileOf<BM>;
   __shared__ __attribute__((aligned(16))) __bf16 sa0[Cfg::kLdsA], sa1[Cfg::kLdsA];
   __shared__ __attribute__((aligned(16))) __bf16 sb0[Cfg::kLdsB], sb1[Cfg::kLdsB];
   const BigSmem smem{sa0, sa1, sb0, sb1};
   __shared__ float2 lv_tab[256 * kLvCopies];
   const float2 *lv = load_level_pairs(lv_tab, tab);
-  const int tiles_m = static_cast<int>((p.M + 255) / 256), tiles_k = static_cast<int>((p.K + 255) / 256);
+  const int tiles_m = static_cast<int>((p.M + BM - 1) / BM), tiles_k = static_cast<int>((p.K + 255) / 256);
   const Piece piece = piece_of(p.tail, static_cast<int>(blockIdx.x), static_cast<int>(2 * p.N / kBK));
   int tm, tn;
   tile_of(piece.tile, tiles_m, tiles_k, tm, tn);
-  const int64_t k0 = static_cast<int64_t>(tn) * 256, m0 = static_cast<int64_t>(tm) * 256;
+  const int64_t k0 = static_cast<int64_t>(tn) * 256, m0 = static_cast<int64_t>(tm) * BM;
   const int s0 = piece.s0, s1 = piece.s1;
   __syncthreads();
   Acc<Cfg> acc;
   acc.zero();
   {
-    const DualRows da(p, m0, static_cast<int64_t>(s0) * kBK);
+    const DualRows<BM> da(p, m0, static_cast<int64_t>(s0) * kBK);
     Nf4TransBigT<kT> l0(p.codes[0], p.cs[0], p.K, k0), l1 = l0;
     const uint8_t *const codes[2] = {p.codes[0] + k0 / 2, p.codes[1] + k0 / 2};
     const float *const cs[2] = {p.cs[0] + k0 / kBlock, p.cs[1] + k0 / kBlock};
@@ -473,12 +484,13 @@ __global__ __launch_bounds__(kT, 1) void k_gated_dx(const DxParams p, const Nf4T
     big_mainloop_nf4<Cfg>(acc, da, l0, l1, load, s1 - s0, smem, lv);
   }
   if (p.rp > 0 && piece.z == 0) {
-    const DirectRowsT<kT> da(p.low, 2 * p.rp, p.M, m0), db(p.At, 2 * p.rp, p.K, k0);
+    const DirectRowsT<kT, BM> da(p.low, 2 * p.rp, p.M, m0);
+    const DirectRowsT<kT> db(p.At, 2 * p.rp, p.K, k0);
     big_mainloop_dense<Cfg>(acc, da, db, 2 * p.rp / kBK, smem);
   }
   if (piece.part)
-    store_f32<Cfg>(acc, piece.part, 256, min(p.M - m0, int64_t(256)), 256, 0, 0);
-  else if (m0 + 256 <= p.M && k0 + 256 <= p.K)
+    store_f32<Cfg>(acc, piece.part, 256, min(p.M - m0, int64_t(BM)), 256, 0, 0);
+  else if (m0 + BM <= p.M && k0 + 256 <= p.K)
     store_bf16<Cfg, false>(acc, static_cast<__bf16 *>(p.dX), p.K, p.M, p.K, m0, k0, 1.0f);
   else
     store_bf16<Cfg, true>(acc, static_cast<__bf16 *>(p.dX), p.K, p.M, p.K, m0, k0, 1.0f);
@@ -564,13 +576,13 @@ __global__ __launch_bounds__(256) void k_gated_grad_sum(const GradSumParams p) {
   }
 }
 
-// dX of the split tiles, four columns a lane, 64 workgroups a tile.
+// dX of the split tiles, four columns a lane, BM / 4 workgroups a tile.
 __global__ __launch_bounds__(256) void k_gated_dx_sum(const DxParams p) {
-  const int i = static_cast<int>(blockIdx.x) >> 6, at = (static_cast<int>(blockIdx.x) & 63) * 256 + static_cast<int>(threadIdx.x);
+  const int bm = p.tail.bm, i = static_cast<int>(blockIdx.x) / (bm / 4), at = (static_cast<int>(blockIdx.x) - i * (bm / 4)) * 256 + static_cast<int>(threadIdx.x);
   const int row = at >> 6, c = 4 * (at & 63);
   int tm, tn;
-  tile_of(static_cast<int>(p.tail.whole) + i, static_cast<int>((p.M + 255) / 256), static_cast<int>((p.K + 255) / 256), tm, tn);
-  const int64_t m = static_cast<int64_t>(tm) * 256 + row, k = static_cast<int64_t>(tn) * 256 + c;
+  tile_of(static_cast<int>(p.tail.whole) + i, static_cast<int>((p.M + bm - 1) / bm), static_cast<int>((p.K + 255) / 256), tm, tn);
+  const int64_t m = static_cast<int64_t>(tm) * bm + row, k = static_cast<int64_t>(tn) * 256 + c;
   if (m >= p.M || k >= p.K) return;
   const float4 v = sums_of(p.tail, i, row, c);
   *reinterpret_cast<uint2 *>(static_cast<__bf16 *>(p.dX) + m * p.K + k) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
@@ -584,9 +596,10 @@ struct Plan {
   Split down, ga, gb;
 };
 
-// Parts of sixteen steps at least where there are whole rounds in front.
-Tail make_tail(int64_t tiles, int steps) {
-  Tail t{tiles, 0, 1, steps, nullptr};
+// The tiles with BM = bm. Parts of sixteen steps at least where there are whole
+// rounds in front.
+Tail tail_of(int bm, int64_t tiles, int steps) {
+  Tail t{bm, tiles, 0, 1, steps, nullptr};
   const int64_t rest = tiles % kCus;
   if (rest == 0 || 2 * rest > kCus) return t;
   const int S = static_cast<int>(std::min<int64_t>(kCus / rest, steps / (tiles > rest ? 16 : kMinSplitSteps)));
@@ -598,16 +611,39 @@ Tail make_tail(int64_t tiles, int steps) {
   return t;
 }
 
+// Fewer rows to a tile decode the weights more often for the same product but
+// leave fewer rows empty and fewer compute units without a tile. A round of
+// 256, 192, 128 and 64 rows costs as 1, 0.82, 0.635 and 0.485 (4096 x 11008 x
+// 4096: 128, 105, 81 and 62 us), the kernel that adds split tiles about 0.1. Of
+// these the least (11008 x 4096, forward, us with 256, 192, 128 and 64 rows: 64
+// rows 97, 86, 78, 72; 128 rows 98, 86, 79, 93; 192 rows 97, 88, 101, 113; 333
+// rows 130, 114, 132, 171; 512 rows 134, 158, 156, 213; both directions of 333
+// rows 289, 260, 284, 396).
+Tail make_tail(int64_t M, int64_t tiles_n, int steps) {
+  constexpr struct {
+    int bm;
+    double cost;
+  } kTiles[] = {{256, 1.0}, {192, 0.82}, {128, 0.635}, {64, 0.485}};
+  Tail best{};
+  double least = 0;
+  for (const auto &k : kTiles) {
+    const Tail t = tail_of(k.bm, grid_blocks(M, k.bm) * tiles_n, steps);
+    const double rounds = static_cast<double>(ceil_div(t.whole, kCus)) + (t.rest ? 1.0 / t.S : 0.0);
+    const double cost = k.cost * rounds + (t.rest ? 0.1 : 0.0);
+    if (best.bm == 0 || cost < least) best = t, least = cost;
+  }
+  return best;
+}
+
 Plan make_plan(int64_t M, int64_t N, int64_t K, int r, bool backward) {
   Plan pl{};
   pl.rp = gated_padded_rank(r);
-  const int64_t tiles_m = grid_blocks(M, 256);
   if (!backward) {
-    pl.tail = make_tail(tiles_m * grid_blocks(N, 128), static_cast<int>(K / kBK));
+    pl.tail = make_tail(M, grid_blocks(N, 128), static_cast<int>(K / kBK));
     if (r) pl.down = choose_split(grid_blocks(M, 128) * (2 * pl.rp / 128), static_cast<int>(K / kBK), 64, kCus);
     return pl;
   }
-  pl.tail = make_tail(tiles_m * grid_blocks(K, 256), static_cast<int>(2 * N / kBK));
+  pl.tail = make_tail(M, grid_blocks(K, 256), static_cast<int>(2 * N / kBK));
   if (r) {
     pl.down = choose_split(grid_blocks(M, 128) * 2 * (pl.rp / 64), static_cast<int>(N / kBK), 64, kCus);
     const int msteps = static_cast<int>(ceil_div(M, kBK));
@@ -631,7 +667,7 @@ size_t carve(void *ws, Plan &pl, int64_t M, int64_t N, int64_t K, bool backward,
   const int64_t nb = N * K / kBlock;
   b->cs[0] = c.take<float>(nb);
   b->cs[1] = c.take<float>(nb);
-  if (pl.tail.rest) pl.tail.part = c.take<float>(static_cast<size_t>(pl.tail.S) * pl.tail.rest * 65536);
+  if (pl.tail.rest) pl.tail.part = c.take<float>(static_cast<size_t>(pl.tail.S) * pl.tail.rest * 256 * pl.tail.bm);
   const size_t cols = 2 * static_cast<size_t>(pl.rp);
   if (pl.rp) b->down = c.take<float>(pl.down.splits * M * cols);
   if (!backward) {
@@ -720,8 +756,16 @@ hipError_t launch_gated_fwd(const GatedArgs &a, const void *X, void *H, void *G,
   }
   FwdParams p{X, {a.w[0].codes, a.w[1].codes}, {scales(a, b, 0), scales(a, b, 1)}, b.Hs, b.Bi, static_cast<__bf16 *>(H),
               static_cast<__bf16 *>(G), static_cast<__bf16 *>(U), a.M, a.N, a.K, pl.rp, pl.tail};
-  k_gated_fwd<<<static_cast<unsigned>(pl.tail.whole + pl.tail.rest * pl.tail.S), kT, 0, s>>>(p, format_tables(a.format));
-  if (pl.tail.rest) k_gated_out<<<static_cast<unsigned>(32 * pl.tail.rest), 256, 0, s>>>(p);
+  const auto run = [&](auto kernel) {
+    kernel<<<static_cast<unsigned>(pl.tail.whole + pl.tail.rest * pl.tail.S), kT, 0, s>>>(p, format_tables(a.format));
+  };
+  switch (pl.tail.bm) {
+    case 64: run(k_gated_fwd<64>); break;
+    case 128: run(k_gated_fwd<128>); break;
+    case 192: run(k_gated_fwd<192>); break;
+    default: run(k_gated_fwd<256>); break;
+  }
+  if (pl.tail.rest) k_gated_out<<<static_cast<unsigned>(pl.tail.bm / 8 * pl.tail.rest), 256, 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -755,8 +799,16 @@ hipError_t launch_gated_bwd(const GatedArgs &a, const void *dH, const void *X, c
   }
   DxParams p{b.dG, b.dU, {a.w[0].codes, a.w[1].codes}, {scales(a, b, 0), scales(a, b, 1)}, b.low, b.At, dX, a.M, a.N, a.K,
              pl.rp, pl.tail};
-  k_gated_dx<<<static_cast<unsigned>(pl.tail.whole + pl.tail.rest * pl.tail.S), kT, 0, s>>>(p, format_tables(a.format));
-  if (pl.tail.rest) k_gated_dx_sum<<<static_cast<unsigned>(64 * pl.tail.rest), 256, 0, s>>>(p);
+  const auto run = [&](auto kernel) {
+    kernel<<<static_cast<unsigned>(pl.tail.whole + pl.tail.rest * pl.tail.S), kT, 0, s>>>(p, format_tables(a.format));
+  };
+  switch (pl.tail.bm) {
+    case 64: run(k_gated_dx<64>); break;
+    case 128: run(k_gated_dx<128>); break;
+    case 192: run(k_gated_dx<192>); break;
+    default: run(k_gated_dx<256>); break;
+  }
+  if (pl.tail.rest) k_gated_dx_sum<<<static_cast<unsigned>(pl.tail.bm / 4 * pl.tail.rest), 256, 0, s>>>(p);
   if (pl.rp) {
     GradParams g{};
     g.X = X;

@@ -422,8 +422,8 @@ __device__ __forceinline__ void big_mainloop_nf4(Acc<Cfg> &acc, const DA &da, LB
 }
 
 // Both operands dense bf16 (the adapter steps): plain double-buffered loop.
-template <class Cfg, class DA>
-__device__ __forceinline__ void big_mainloop_dense(Acc<Cfg> &acc, const DA &da, const DA &db, int steps,
+template <class Cfg, class DA, class DB>
+__device__ __forceinline__ void big_mainloop_dense(Acc<Cfg> &acc, const DA &da, const DB &db, int steps,
                                                    const BigSmem &sm) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int wm = w / Cfg::WAVES_N, wn = w % Cfg::WAVES_N;

@@ -129,6 +129,9 @@ def check_backward_by_cases(d, out, G, U, Hs):
 # the last one's rest behind whole rounds
 SHAPES = [(1, 64, 64, 0), (1, 64, 64, 1), (1, 1088, 512, 64), (2, 6400, 192, 40), (4, 192, 4160, 8), (16, 128, 8256, 256), (3, 128, 5120, 0), (1, 64, 20352, 8), (4, 64, 8192, 16), (2, 16448, 64, 0), (31, 320, 11008, 64), (9, 64, 4096, 33), (5, 192, 128, 8), (17, 320, 576, 33), (32, 256, 1024, 64), (33, 128, 192, 65),
           (130, 704, 512, 16), (257, 384, 640, 128), (300, 1024, 256, 200), (513, 576, 1152, 256), (4096, 1152, 256, 64), (4100, 1088, 2176, 24), (2250, 3648, 2304, 8)]
+# each number of rows to a tile, whole and split
+SHAPES += [(40, 320, 64, 5), (180, 11008, 64, 8), (250, 11008, 64, 64), (300, 3008, 1088, 16), (250, 10048, 576, 16), (500, 11008, 64, 40), (3000, 64, 2112, 8),
+           (1000, 6400, 64, 16), (2500, 2048, 64, 1)]
 
 
 @pytest.mark.parametrize("bf16", [True, False])
@@ -191,7 +194,7 @@ def test_formats_and_given_buffers(qb, M, fmt):
     check_backward_by_cases(d, bouts, *outs[1:])
 
 
-@pytest.mark.parametrize("M,N,K", [(64, 192, 64), (256, 1088, 256), (320, 64, 320), (4096, 1152, 4096), (2250, 3648, 2304)])
+@pytest.mark.parametrize("M,N,K", [(64, 192, 64), (256, 1088, 256), (320, 64, 320), (4096, 1152, 4096), (2250, 3648, 2304), (1500, 6400, 2112)])
 def test_exact_forward_with_unit_rows(qb, M, N, K):
     """X a unit matrix: G and U are the decoded weights, bit for bit."""
     import torch
@@ -206,7 +209,7 @@ def test_exact_forward_with_unit_rows(qb, M, N, K):
     assert (np.abs(f64(H) - want) <= np.abs(want) * (2.0 ** -8 + 2.0 ** -19)).all()
 
 
-@pytest.mark.parametrize("M,N,K", [(64, 64, 192), (320, 320, 128), (192, 192, 1088), (4096, 4096, 2304), (2250, 2304, 7360)])
+@pytest.mark.parametrize("M,N,K", [(64, 64, 192), (320, 320, 128), (192, 192, 1088), (4096, 4096, 2304), (2250, 2304, 7360), (3800, 5056, 2112)])
 def test_exact_backward_with_unit_rows(qb, M, N, K):
     """G = 0, U = 2 and dH a unit matrix: dG = dH, dU = 0, so dX is the decoded gate; G = 32, U = 0 and dH a 32nd of
     it: dG = 0, dU = dH 32, so dX is the other weight. Bit for bit."""
