@@ -18,8 +18,8 @@
 //                  end in one lane and the gate needs no exchange
 //   k_gated_out    sums and gates the tiles whose reduction was split (below)
 // Backward:
-//   k_gated_prep   block scales, [Ag; Au]^T [K][2 rp] and Bg^T, Bu^T [2][rp][N]
-//   k_gated_act    dG, dU from dH, G, U
+//   k_gated_prep   dG, dU from dH, G, U; block scales, [Ag; Au]^T [K][2 rp] and
+//                  Bg^T, Bu^T [2][rp][N]
 //   k_gated_down, k_gated_sum   l = bf16(s [dG Bg, dU Bu]) [M][2 rp]
 //   k_gated_dx     dX = [dG, dU, l] [Wg; Wu; [Ag; Au]]: one reduction over both
 //                  weights, so dX is rounded and written once
@@ -49,7 +49,15 @@ __device__ __forceinline__ float adapter_at(const void *p, bool bf16, int64_t i)
   return bf16 ? static_cast<float>(static_cast<const __bf16 *>(p)[i]) : static_cast<const float *>(p)[i];
 }
 
+constexpr int64_t kActGroups = 8192;
+
+struct ActParams {
+  const void *dH, *G, *U;
+  __bf16 *dG, *dU;
+  int64_t n, groups;
+};
 struct PrepParams {
+  ActParams act;      // backward: its workgroups in front, the longest work
   const void *A[2], *B[2];
   bool bf16;
   int64_t N, K, nb;
@@ -67,8 +75,29 @@ __device__ __forceinline__ void put8(__bf16 *dst, const float (&v)[8]) {
       make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
+// dG, dU, eight elements a lane and turn, by workgroup g of the `groups`.
+__device__ __forceinline__ void gated_act(const ActParams &p, int64_t g) {
+  for (int64_t e = (g * 256 + threadIdx.x) * 8; e < p.n; e += p.groups * 2048) {
+    const auto in = [e](const void *p) { return *reinterpret_cast<const uint4 *>(static_cast<const __bf16 *>(p) + e); };
+    const uint4 a = in(p.dH), b = in(p.G), c = in(p.U);
+    const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w}, wc[4] = {c.x, c.y, c.z, c.w};
+    float dg[8], du[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const auto part = [i](const uint32_t (&w)[4]) {
+        return __builtin_bit_cast(float, (i & 1) ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+      };
+      gate_backward(part(wa), part(wb), part(wc), dg[i], du[i]);
+    }
+    put8(p.dG + e, dg);
+    put8(p.dU + e, du);
+  }
+}
+
 __global__ __launch_bounds__(256) void k_gated_prep(const PrepParams p) {
   int64_t g = blockIdx.x;
+  if (g < p.act.groups) return gated_act(p.act, g);
+  g -= p.act.groups;
   if (g < p.g_cs) {   // block scales, as k_adapter_finish forms them
     const int64_t b0 = (g * 256 + threadIdx.x) * 4;
 #pragma unroll
@@ -182,11 +211,24 @@ __global__ __launch_bounds__(256, 1) void k_gated_down(const DownParams p) {
   store_f32<C>(acc, p.part + static_cast<int64_t>(z) * p.M * p.ld + w * p.rows, p.ld, p.M, p.rows, m0, j0);
 }
 
-// out = bf16(scale * the sum of the partials, in split order).
+// out = bf16(scale * the sum of the partials), four elements a lane: each of the
+// four waves adds a quarter of the splits in order, then the quarters are added
+// (64 rows of 11008 x 4096 with r = 64: the forward takes 72 us with one wave
+// for all splits, 68 so).
 __global__ __launch_bounds__(256) void k_gated_sum(const float *part, int splits, int64_t n, float scale, __bf16 *out) {
-  const int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-  if (e >= n) return;
-  const float4 v = split_sum4(part, n, e, splits);
+  __shared__ float4 sums[3][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, per = (splits + 3) / 4, z0 = wave * per;
+  const int64_t e = (static_cast<int64_t>(blockIdx.x) * 64 + lane) * 4;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (e < n && z0 < splits) v = split_sum4(part + z0 * n, n, e, min(per, splits - z0));
+  if (wave > 0) sums[wave - 1][lane] = v;
+  __syncthreads();
+  if (wave > 0 || e >= n) return;
+#pragma unroll
+  for (int w = 0; w < 3; ++w) {
+    const float4 s = sums[w][lane];
+    v.x += s.x, v.y += s.y, v.z += s.z, v.w += s.w;
+  }
   *reinterpret_cast<uint2 *>(out + e) = make_uint2(pack_bf16x2(scale * v.x, scale * v.y), pack_bf16x2(scale * v.z, scale * v.w));
 }
 
@@ -396,27 +438,6 @@ __global__ __launch_bounds__(256) void k_gated_out(const FwdParams p) {
 
 // ----------------------------------------------------------------- backward
 
-constexpr int64_t kActGroups = 8192;
-
-// dG, dU, eight elements a lane and turn.
-__global__ __launch_bounds__(256) void k_gated_act(const void *dH, const void *G, const void *U, __bf16 *dG, __bf16 *dU, int64_t n) {
-  for (int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8; e < n; e += static_cast<int64_t>(gridDim.x) * 2048) {
-    const auto in = [e](const void *p) { return *reinterpret_cast<const uint4 *>(static_cast<const __bf16 *>(p) + e); };
-    const uint4 a = in(dH), b = in(G), c = in(U);
-    const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w}, wc[4] = {c.x, c.y, c.z, c.w};
-    float dg[8], du[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const auto part = [i](const uint32_t (&w)[4]) {
-        return __builtin_bit_cast(float, (i & 1) ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-      };
-      gate_backward(part(wa), part(wb), part(wc), dg[i], du[i]);
-    }
-    put8(dG + e, dg);
-    put8(dU + e, du);
-  }
-}
-
 struct DxParams {
   const void *dG, *dU;      // bf16 [M, N]
   const uint8_t *codes[2];
@@ -590,6 +611,10 @@ __global__ __launch_bounds__(256) void k_gated_dx_sum(const DxParams p) {
 
 // -------------------------------------------------------------------- plan
 
+// Splits of the adapters' down products at most (11008 x 4096, both directions,
+// 333 and 64 rows: 253 and 142 us with 64, 249 and 141 with 32, 247 and 143 with 16).
+constexpr int kDownSplits = 32;
+
 struct Plan {
   int rp;
   Tail tail;
@@ -640,12 +665,12 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int r, bool backward) {
   pl.rp = gated_padded_rank(r);
   if (!backward) {
     pl.tail = make_tail(M, grid_blocks(N, 128), static_cast<int>(K / kBK));
-    if (r) pl.down = choose_split(grid_blocks(M, 128) * (2 * pl.rp / 128), static_cast<int>(K / kBK), 64, kCus);
+    if (r) pl.down = choose_split(grid_blocks(M, 128) * (2 * pl.rp / 128), static_cast<int>(K / kBK), kDownSplits, kCus);
     return pl;
   }
   pl.tail = make_tail(M, grid_blocks(K, 256), static_cast<int>(2 * N / kBK));
   if (r) {
-    pl.down = choose_split(grid_blocks(M, 128) * 2 * (pl.rp / 64), static_cast<int>(N / kBK), 64, kCus);
+    pl.down = choose_split(grid_blocks(M, 128) * 2 * (pl.rp / 64), static_cast<int>(N / kBK), kDownSplits, kCus);
     const int msteps = static_cast<int>(ceil_div(M, kBK));
     pl.ga = choose_split(grid_blocks(K, 256) * (2 * pl.rp / 64), msteps, 8);
     pl.gb = choose_split(2 * grid_blocks(N, 256) * (pl.rp / 64), msteps, 8);
@@ -693,8 +718,9 @@ size_t carve(void *ws, Plan &pl, int64_t M, int64_t N, int64_t K, bool backward,
 unsigned blocks(int64_t n, int64_t per) { return static_cast<unsigned>(ceil_div(n, per)); }
 
 // Block scales and bf16 operands.
-void run_prep(const GatedArgs &a, const Plan &pl, const Buffers &b, bool backward, hipStream_t s) {
+void run_prep(const GatedArgs &a, const Plan &pl, const Buffers &b, bool backward, const ActParams &act, hipStream_t s) {
   PrepParams p{};
+  p.act = act;
   for (int w = 0; w < 2; ++w) {
     p.A[w] = a.A[w];
     p.B[w] = a.B[w];
@@ -716,7 +742,7 @@ void run_prep(const GatedArgs &a, const Plan &pl, const Buffers &b, bool backwar
     p.g_a = ceil_div(2 * pl.rp * a.K / 8, 256);
     p.g_b = ceil_div(2 * pl.rp * a.N / 8, 256);
   }
-  const int64_t groups = p.g_cs + p.g_a + p.g_b;
+  const int64_t groups = act.groups + p.g_cs + p.g_a + p.g_b;
   if (groups > 0) k_gated_prep<<<static_cast<unsigned>(groups), 256, 0, s>>>(p);
 }
 
@@ -736,7 +762,7 @@ hipError_t launch_gated_fwd(const GatedArgs &a, const void *X, void *H, void *G,
   carve(ws, pl, a.M, a.N, a.K, false, &b);
   if (Hs) b.Hs = static_cast<__bf16 *>(Hs);
   if (a.M <= kGatedStreamRows) return launch_gated_stream(a, X, H, G, U, b.Hs, s);
-  run_prep(a, pl, b, false, s);
+  run_prep(a, pl, b, false, ActParams{}, s);
   if (pl.rp) {
     DownParams d{};
     d.P[0] = X;
@@ -752,7 +778,7 @@ hipError_t launch_gated_fwd(const GatedArgs &a, const void *X, void *H, void *G,
     d.per = pl.down.steps_per_split;
     k_gated_down<128><<<static_cast<unsigned>(d.tiles * pl.down.splits), 256, 0, s>>>(d);
     const int64_t n = a.M * 2 * pl.rp;
-    k_gated_sum<<<blocks(n, 1024), 256, 0, s>>>(b.down, pl.down.splits, n, a.scale, b.Hs);
+    k_gated_sum<<<blocks(n, 256), 256, 0, s>>>(b.down, pl.down.splits, n, a.scale, b.Hs);
   }
   FwdParams p{X, {a.w[0].codes, a.w[1].codes}, {scales(a, b, 0), scales(a, b, 1)}, b.Hs, b.Bi, static_cast<__bf16 *>(H),
               static_cast<__bf16 *>(G), static_cast<__bf16 *>(U), a.M, a.N, a.K, pl.rp, pl.tail};
@@ -774,9 +800,8 @@ hipError_t launch_gated_bwd(const GatedArgs &a, const void *dH, const void *X, c
   Plan pl = make_plan(a.M, a.N, a.K, a.r, true);
   Buffers b{};
   carve(ws, pl, a.M, a.N, a.K, true, &b);
-  run_prep(a, pl, b, true, s);
   const int64_t n = a.M * a.N;
-  k_gated_act<<<static_cast<unsigned>(std::min(ceil_div(n, 2048), kActGroups)), 256, 0, s>>>(dH, G, U, b.dG, b.dU, n);
+  run_prep(a, pl, b, true, ActParams{dH, G, U, b.dG, b.dU, n, std::min(ceil_div(n, 2048), kActGroups)}, s);
   if (pl.rp) {
     DownParams d{};
     d.P[0] = b.dG;
@@ -795,7 +820,7 @@ hipError_t launch_gated_bwd(const GatedArgs &a, const void *dH, const void *X, c
     d.per = pl.down.steps_per_split;
     k_gated_down<64><<<static_cast<unsigned>(d.tiles * pl.down.splits), 256, 0, s>>>(d);
     const int64_t count = a.M * 2 * pl.rp;
-    k_gated_sum<<<blocks(count, 1024), 256, 0, s>>>(b.down, pl.down.splits, count, a.scale, b.low);
+    k_gated_sum<<<blocks(count, 256), 256, 0, s>>>(b.down, pl.down.splits, count, a.scale, b.low);
   }
   DxParams p{b.dG, b.dU, {a.w[0].codes, a.w[1].codes}, {scales(a, b, 0), scales(a, b, 1)}, b.low, b.At, dX, a.M, a.N, a.K,
              pl.rp, pl.tail};
