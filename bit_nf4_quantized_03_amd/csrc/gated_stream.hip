@@ -40,6 +40,7 @@ namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
 constexpr int kCopies = 16;
@@ -227,6 +228,238 @@ __device__ __forceinline__ void put_gated(const StreamParams &p, float g, float 
   }
 }
 
+// A load at or behind kNowhere lies past the end of every buffer here (X of at
+// most 2^29 bytes, offsets within a row below 2^24) and returns zeros. Offsets
+// go into the register that the bounds check looks at, none into the scalar
+// one.
+constexpr uint32_t kNowhere = 0x80000000u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), static_cast<short>(0), static_cast<int>(bytes), 0x00020000);
+}
+
+// One row of X. A workgroup has N / 256 columns of H, one workgroup to a
+// compute unit. Lane l of wave q of the W = ceil(K / 2048) that share a row of a
+// weight holds X's elements 32 (64 q + l) .. + 31 in registers for the whole
+// call; the 16 code bytes that meet them are one load, and a pass of the
+// workgroup covers C = 8 / W columns, the gate's rows in the first C W waves and the
+// other weight's in the next. A byte's two levels (bf16, out of LDS) and two
+// elements of X are one v_dot2_f32_bf16, and a half block's sum takes the block's
+// constant. Lanes add up sixteen passes' sums at once, halving what each holds
+// by every exchange.
+//
+// The table has a copy for each lane, 256 bytes to an entry: an address is one
+// byte permutation (code and lane), no two lanes meet in a bank, and as it lies
+// at address 0 nothing is added. Constants of sixteen passes lie in memory in
+// the order in which the passes use them, four to a lane and load. All loads
+// are buffer loads that return zeros for what is not there, so that none is
+// under a branch and waits are for no more than what is used; three passes are
+// under way.
+constexpr int kRowThreads = 1024, kRowWaves = 16, kRowPasses = 16, kRowRing = 4, kRowMaxK = 16384;
+struct RowLds {
+  uint32_t table[256 * 64];
+  float constants[2][4096];                 // [weight][column of sixteen passes][K / 64]
+  uint32_t x[kRowMaxK / 2];
+  float part[kRowWaves][kRowPasses + 1];
+  float sums[2][kRowPasses * 8];
+  uint32_t hs[2 * 256 / 2];
+};
+
+template <bool DQ>
+__global__ __launch_bounds__(kRowThreads, 4) void k_gated_row(const StreamParams p, const Nf4Tables tab, int cols) {
+  __shared__ __attribute__((aligned(16))) RowLds lds;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int W = static_cast<int>((p.K + 2047) / 2048), C = 8 / W;
+  const int slot = wave / W, up = slot >= C, column = slot - up * C, chunk = 64 * (wave - slot * W) + lane;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * cols;
+  const int count = static_cast<int>(min(p.N - c0, static_cast<int64_t>(cols)));
+  const int nb = static_cast<int>(p.K / kBlock), passes = (count + C - 1) / C;
+  const uint32_t row_bytes = static_cast<uint32_t>(p.K / 2);
+
+  const auto xb = buffer_of(p.X, p.K * 2);
+  const auto hb = buffer_of(p.Hs, p.r ? 4 * p.rp : 0);
+  const auto cb = buffer_of((up ? p.codes[1] : p.codes[0]) + c0 * row_bytes, static_cast<int64_t>(count) * row_bytes);
+  // codes of the lane's chunk, from the first pass on; past the columns nothing is there
+  const bool mine = slot < 2 * C && chunk < p.K / 32;
+  const uint32_t at = mine ? static_cast<uint32_t>(column) * row_bytes + 16u * static_cast<uint32_t>(chunk) : kNowhere;
+  const uint32_t step = mine ? static_cast<uint32_t>(C) * row_bytes : 0;
+  auto codes_of = [&](int pass) { return __builtin_amdgcn_raw_buffer_load_b128(cb, pass < passes ? at + static_cast<uint32_t>(pass) * step : kNowhere, 0, 0); };
+  // four constants of each weight, of sixteen passes from column `from` on
+  u32x4 raw[2];
+  float factor[2] = {0.0f, 0.0f};
+  auto request_constants = [&](int from) {
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const uint32_t e = static_cast<uint32_t>(from * nb + 4 * tid);
+      const bool there = 4 * tid < kRowPasses * C * nb;
+      if constexpr (DQ) {
+        const auto b = buffer_of(p.absmax_q[w] + c0 * nb, static_cast<int64_t>(count) * nb);
+        raw[w][0] = __builtin_amdgcn_raw_buffer_load_b32(b, there ? e : kNowhere, 0, 0);
+        const int64_t groups = (p.N * nb + kDqBlock - 1) / kDqBlock, g = (c0 * nb + e) / kDqBlock;
+        factor[w] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buffer_of(p.dq_scale[w], 4 * groups),
+                                                                                  there && e < static_cast<uint32_t>(count * nb) ? static_cast<uint32_t>(4 * g) : kNowhere, 0, 0));
+      } else {
+        raw[w] = __builtin_amdgcn_raw_buffer_load_b128(buffer_of(p.absmax[w] + c0 * nb, 4 * static_cast<int64_t>(count) * nb), there ? 4 * e : kNowhere, 0, 0);
+      }
+    }
+  };
+  float mean[2] = {0.0f, 0.0f};
+  if constexpr (DQ) mean[0] = p.dq_mean[0][0], mean[1] = p.dq_mean[1][0];
+  auto put_constants = [&]() {
+    if (4 * tid >= kRowPasses * C * nb) return;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      f32x4 v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t bits = raw[w][DQ ? 0 : i];
+        v[i] = DQ ? __fadd_rn(__fmul_rn(static_cast<float>(static_cast<int8_t>(bits >> (8 * i))), __fdiv_rn(factor[w], 127.0f)), mean[w])
+                  : __builtin_bit_cast(float, bits);
+      }
+      *reinterpret_cast<f32x4 *>(&lds.constants[w][4 * tid]) = v;
+    }
+  };
+  // the adapters' terms: four lanes share a row, of each 64 columns of B sixteen a lane
+  const int side = wave >= C, in = 16 * wave + (lane >> 2) - side * kRowPasses * C, j0 = 16 * (tid & 3);
+  const bool adds = wave < 2 * C;   // a row of this weight
+  const bool wide = p.r % (p.bf16 ? 8 : 4) == 0;   // rows of B begin 16-byte aligned
+  const auto bb = buffer_of(static_cast<const char *>(side ? p.B[1] : p.B[0]) + c0 * p.r * (p.bf16 ? 2 : 4),
+                            p.r ? static_cast<int64_t>(count) * p.r * (p.bf16 ? 2 : 4) : 0);
+  u32x4 b[4];
+  auto request_b = [&](int from) {
+    if (!wide || p.r == 0) return;
+    const int n = from + in;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = j0 + (p.bf16 ? 8 : 4) * i;
+      const bool there = adds && n < count && j < p.r && (!p.bf16 || i < 2);
+      b[i] = __builtin_amdgcn_raw_buffer_load_b128(bb, there ? static_cast<uint32_t>((n * p.r + j) * (p.bf16 ? 2 : 4)) : kNowhere, 0, 0);
+    }
+  };
+
+  const u32x4 x0 = __builtin_amdgcn_raw_buffer_load_b128(xb, 16 * tid, 0, 0);
+  const u32x4 x1 = __builtin_amdgcn_raw_buffer_load_b128(xb, 16 * (tid + kRowThreads), 0, 0);
+  request_constants(0);
+  u32x4 v[kRowRing];
+#pragma unroll
+  for (int i = 0; i < kRowRing - 1; ++i) v[i] = codes_of(i);
+  const u32x4 h0 = __builtin_amdgcn_raw_buffer_load_b128(hb, tid < 64 ? 16 * tid : kNowhere, 0, 0);
+  request_b(0);
+#pragma unroll
+  for (int i = 0; i < 256 / kRowWaves; ++i) {
+    const int e = wave + kRowWaves * i;
+    lds.table[64 * e + lane] = pack_bf16x2(tab.lv[e >> 4], tab.lv[e & 15]);
+  }
+  *reinterpret_cast<u32x4 *>(&lds.x[4 * tid]) = x0;
+  *reinterpret_cast<u32x4 *>(&lds.x[4 * (tid + kRowThreads)]) = x1;
+  put_constants();
+  if (tid < 64) *reinterpret_cast<u32x4 *>(&lds.hs[4 * tid]) = h0;
+  __syncthreads();
+  u32x4 x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const u32x4 *>(&lds.x[(16 * chunk + 4 * i) & (kRowMaxK / 2 - 1)]);
+  const uint32_t copy = 4u * lane;
+  const char *const table = reinterpret_cast<const char *>(lds.table);
+
+  for (int first = 0; first < passes; first += kRowPasses) {
+    float sum[kRowPasses];
+    const float *c = &lds.constants[up][column * nb + (chunk >> 1)];
+#pragma unroll
+    for (int t = 0; t < kRowPasses; ++t) {
+      sum[t] = 0.0f;
+      if (first + t >= passes) continue;   // uniform
+      v[(t + kRowRing - 1) % kRowRing] = codes_of(first + t + kRowRing - 1);
+      const u32x4 &code = v[t % kRowRing];
+      float s = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t w = code[q], xx = x[q][e];
+          const uint32_t pair = *reinterpret_cast<const uint32_t *>(table + __builtin_amdgcn_perm(w, copy, 0x0c0c0400u + 0x100u * e));
+          s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, pair), __builtin_bit_cast(bf16x2_t, xx), s, false);
+        }
+      sum[t] = mine ? s * c[t * C * nb] : 0.0f;
+    }
+    const bool more = first + kRowPasses < passes;
+    if (more) request_constants((first + kRowPasses) * C);
+    // lane l: pass l / 4
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const auto s = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, sum[i]), __builtin_bit_cast(uint32_t, sum[i + 8]), false, false);
+      const uint32_t lo = s[0], hi = s[1];
+      sum[i] = __builtin_bit_cast(float, lo) + __builtin_bit_cast(float, hi);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const auto s = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, sum[i]), __builtin_bit_cast(uint32_t, sum[i + 4]), false, false);
+      const uint32_t lo = s[0], hi = s[1];
+      sum[i] = __builtin_bit_cast(float, lo) + __builtin_bit_cast(float, hi);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float keep = lane & 8 ? sum[i + 2] : sum[i], send = lane & 8 ? sum[i] : sum[i + 2];
+      sum[i] = keep + __shfl_xor(send, 8);
+    }
+    const float keep = lane & 4 ? sum[1] : sum[0], send = lane & 4 ? sum[0] : sum[1];
+    float all = keep + __shfl_xor(send, 4);
+    all += __shfl_xor(all, 2);
+    all += __shfl_xor(all, 1);
+    if ((lane & 3) == 0) lds.part[wave][lane >> 2] = all;
+    __syncthreads();   // the sums; and nobody reads these constants any more
+    if (more) put_constants();
+    // a row's waves in order, then its adapter's terms
+    const int from = first * C, n = from + in;
+    if (adds) {
+      float a = 0.0f;
+      for (int j = j0; j < p.r; j += 64) {
+        float f[16];
+        if (wide) {
+          if (j > j0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int k = j + (p.bf16 ? 8 : 4) * i;
+              const bool there = n < count && k < p.r && (!p.bf16 || i < 2);
+              b[i] = __builtin_amdgcn_raw_buffer_load_b128(bb, there ? static_cast<uint32_t>((n * p.r + k) * (p.bf16 ? 2 : 4)) : kNowhere, 0, 0);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint32_t half = b[e >> 3][(e >> 1) & 3], full = b[e >> 2][e & 3];
+            const uint32_t bits = p.bf16 ? (e & 1 ? half & 0xffff0000u : half << 16) : full;
+            f[e] = __builtin_bit_cast(float, bits);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            f[e] = 0.0f;
+            if (n < count && j + e < p.r) {
+              const int64_t i = (c0 + n) * p.r + j + e;
+              const void *from_b = side ? p.B[1] : p.B[0];
+              f[e] = p.bf16 ? static_cast<float>(static_cast<const __bf16 *>(from_b)[i]) : static_cast<const float *>(from_b)[i];
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          const uint32_t h = lds.hs[(side * p.rp + j + e) >> 1], w = pack_bf16x2(f[e], f[e + 1]);
+          a = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, w), __builtin_bit_cast(bf16x2_t, h), a, false);
+        }
+      }
+      a += __shfl_xor(a, 1);
+      a += __shfl_xor(a, 2);
+      if ((tid & 3) == 0) {
+        const int t = in / C, s = (side ? C : 0) + in - t * C;
+        float base = 0.0f;
+        for (int q = 0; q < W; ++q) base += lds.part[s * W + q][t];
+        lds.sums[side][in] = base + a;
+      }
+    }
+    if (more) request_b((first + kRowPasses) * C);
+    __syncthreads();
+    if (tid < kRowPasses * C && from + tid < count) put_gated(p, lds.sums[0][tid], lds.sums[1][tid], 0, c0 + from + tid);
+  }
+}
+
 // One to four rows whose X fits in LDS beside the rest. A unit is one tile of
 // 16 weight rows, eight columns of H; 4096 elements of the reduction at a time,
 // a wave every eighth 128 of them. X comes from LDS and not by loads of its
@@ -354,15 +587,6 @@ __global__ __launch_bounds__(kThreads, 4) void k_gated_few(const StreamParams p,
 constexpr int kTiles = 4, kTurn = 128 * kWaves, kTurnBlocks = kTurn / kBlock;
 constexpr int kTurnRow = 16 * kTiles + 4;
 
-// A load at or behind kNowhere lies past the end of every buffer here (X of at
-// most 2^29 bytes, offsets within a row below 2^24) and returns zeros. Offsets
-// go into the register that the bounds check looks at, none into the scalar
-// one.
-constexpr uint32_t kNowhere = 0x80000000u;
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), static_cast<short>(0), static_cast<int>(bytes), 0x00020000);
-}
-
 template <int MT, bool DQ>
 __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void k_gated_stream(const StreamParams p, const Nf4Tables tab) {
   __shared__ uint32_t lut[256 * kCopies];
@@ -478,7 +702,10 @@ void run_stream(StreamParams p, const Nf4Tables &tab, hipStream_t s) {
 
 template <bool DQ>
 void run_rows(StreamParams p, const Nf4Tables &tab, hipStream_t s) {
-  if (p.M <= kFewRows && p.M * few_row_bytes(p.K) <= kFewBytes) {
+  if (p.M == 1 && p.K <= kRowMaxK && p.K % (4 * kBlock) == 0) {
+    const int cols = static_cast<int>(ceil_div(p.N, kCus));
+    k_gated_row<DQ><<<static_cast<unsigned>(ceil_div(p.N, cols)), kRowThreads, 0, s>>>(p, tab, cols);
+  } else if (p.M <= kFewRows && p.M * few_row_bytes(p.K) <= kFewBytes) {
     p.units = static_cast<int>(p.N / 8);
     p.chunks = static_cast<int>(ceil_div(p.K, kChunk));
     k_gated_few<DQ><<<static_cast<unsigned>(std::min(p.units, kGatedFewGroups)), kThreads, 0, s>>>(p, tab);

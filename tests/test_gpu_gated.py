@@ -129,6 +129,8 @@ def check_backward_by_cases(d, out, G, U, Hs):
 # the last one's rest behind whole rounds
 SHAPES = [(1, 64, 64, 0), (1, 64, 64, 1), (1, 1088, 512, 64), (2, 6400, 192, 40), (4, 192, 4160, 8), (16, 128, 8256, 256), (3, 128, 5120, 0), (1, 64, 20352, 8), (4, 64, 8192, 16), (2, 16448, 64, 0), (31, 320, 11008, 64), (9, 64, 4096, 33), (5, 192, 128, 8), (17, 320, 576, 33), (32, 256, 1024, 64), (33, 128, 192, 65),
           (130, 704, 512, 16), (257, 384, 640, 128), (300, 1024, 256, 200), (513, 576, 1152, 256), (4096, 1152, 256, 64), (4100, 1088, 2176, 24), (2250, 3648, 2304, 8)]
+# one row: each number of waves to a row of the weights, one turn of columns and several, ragged last ones
+SHAPES += [(1, 64, 256, 3), (1, 33088, 256, 40), (1, 576, 2304, 256), (1, 9024, 4608, 8), (1, 1088, 7424, 0), (1, 8256, 9216, 64), (1, 64, 16384, 100), (1, 4160, 12544, 16)]
 # each number of rows to a tile, whole and split
 SHAPES += [(40, 320, 64, 5), (180, 11008, 64, 8), (250, 11008, 64, 64), (300, 3008, 1088, 16), (250, 10048, 576, 16), (500, 11008, 64, 40), (3000, 64, 2112, 8),
            (1000, 6400, 64, 16), (2500, 2048, 64, 1)]
@@ -169,11 +171,11 @@ def test_block(qb, M, N, K, r, bf16):
 
 
 @pytest.mark.parametrize("fmt", [0, 1, 2, 3])
-@pytest.mark.parametrize("M", [3, 200])
+@pytest.mark.parametrize("M", [1, 3, 200])
 def test_formats_and_given_buffers(qb, M, fmt):
     import torch
     gu.announce(f"gated formats {fmt} {M}")
-    N, K, r = 448, 320, 12
+    N, K, r = 448, 320 if M > 1 else 1280, 12
     d = Data(qb, M, N, K, r, fmt=fmt)
     h, _, _, grads = d.oracle()
     outs = tuple(torch.full((M, n), 7.0, dtype=torch.bfloat16, device="cuda") for n in (N, N, N, 128))
