@@ -1,34 +1,33 @@
 // The gated block's forward for a few rows (M <= 32): both weights stream past
 // registers once.
 //
-//   k_gated_low     Hs = bf16(s X [Ag; Au]^T), a wave for each adapter row
-//   k_gated_stream  sums of both weights and the adapters' terms, the gate
+//   k_gated_low     Hs = bf16(s X [Ag; Au]^T), a workgroup for each adapter row
+//   k_gated_row     one row of X: sums of both weights and the adapters' terms, the gate
+//   k_gated_few     up to four rows, and longer or unaligned single ones
+//   k_gated_stream  more rows
 //
-// k_gated_stream. A unit is 16 rows, eight of the gate and the same eight of
-// the other weight: the rows of one v_mfma_f32_16x16x32_bf16 whose columns are
-// rows of X. The eight waves of a workgroup share a unit's reduction, 4096
-// elements at a time, a wave every eighth 128 of them. Lane l (r = l % 16 the row, g
-// = l / 16) loads 16 bytes, the 32 codes of a half block; a transposition over
-// the four lanes of a row (permlane swaps) gives lane g the g-th eight codes of
-// each of the four half blocks, so that an instruction's reduction lies in one
-// block of 64 and its sums can take the block's constant afterwards, once for
-// 64 products: acc += c (instruction's sums). A byte of codes is two bf16 levels
-// out of a table in LDS, in sixteen copies (entry e of copy l % 16), and goes
-// into the instruction as it comes.
+// k_gated_few and k_gated_stream. A unit is 16 rows, eight of the gate and the
+// same eight of the other weight: the rows of one v_mfma_f32_16x16x32_bf16 whose
+// columns are rows of X. The eight waves of a workgroup share a unit's reduction. Lane
+// l (r = l % 16 the row, g = l / 16) loads 16 bytes, the 32 codes of a half
+// block; a transposition over the four lanes of a row (permlane swaps) gives lane
+// g the g-th eight codes of each of the four half blocks, so that an
+// instruction's reduction lies in one block of 64 and its sums can take the
+// block's constant afterwards, once for 64 products: acc += c (instruction's
+// sums). A byte of codes is two bf16 levels out of a table in LDS, in sixteen
+// copies (entry e of copy l % 16), and goes into the instruction as it comes.
+// Constants of a unit's rows are formed together and pass through LDS, where a
+// lane reads those of its four rows of the sums at once. Codes and raw constants
+// of the next turn are requested before this one's are used.
 //
-// The constants of a unit's 16 rows are formed together and pass through LDS,
-// where a lane reads those of its four rows of the sums at once. Codes and raw
-// constants of the next 4096 elements (or the next unit: a workgroup takes
-// several) are requested before this one's are used.
-//
-// Two weights of 11008 x 4096 (46 MB), double quantisation: 1 row 17.9 us
-// without adapters (2.6 TB/s), 14.5 with the table's reads left out; with r = 64
-// 23.6, 4 rows 27.1, 16 rows 39.1, 32 rows 51.6 (k_gated_low and its launch are
-// 4 of these). Each turn of a workgroup waits for its loads, which the next
-// turn's, under way, do not hide whole; the table's reads (one for two weights)
-// come next. 32 copies of the table measured the same (19.4 against 19.6 us), 64
-// leave one workgroup on a compute unit (29); waves that go through a reduction
-// alone (no barrier) measured 20 to 23 us for one row.
+// Two weights of 11008 x 4096 (46 MB), double quantization, r = 64: 1 row 19.1 us
+// (14.2, 3.3 TB/s, without adapters: k_gated_low, its launch and the wait for it
+// are 4 of these), 4 rows 27.1, 16 rows 39.1, 32 rows 51.6. k_gated_few took 23.6
+// and 17.9 us for one row, 14.5 with the table's reads left out: a product per
+// instruction has 15 columns to spare there, and each turn's barrier waits for
+// loads that the next turn's do not hide whole. 32 copies of its table measured
+// the same, 64 leave one workgroup on a compute unit (29 us); waves that go
+// through a reduction alone, without barriers, 20 to 23 us for one row.
 #include <algorithm>
 
 #include "block.h"
@@ -44,6 +43,8 @@ typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
 constexpr int kCopies = 16;
+
+constexpr int kLowWaves = 8;   // for one row (1 x 4096 x 11008 in all: 22.8 us with 4, 21.3 with 8, 20.8 with 16)
 
 struct LowParams {
   const __bf16 *X;
@@ -64,18 +65,18 @@ __device__ __forceinline__ bf16x8 adapter8(const void *p, bool bf16, int64_t i) 
                 static_cast<__bf16>(b.x), static_cast<__bf16>(b.y), static_cast<__bf16>(b.z), static_cast<__bf16>(b.w)};
 }
 
-// A workgroup has one adapter row and one row or up to eight of X; its four waves
+// A workgroup has one adapter row and one row or up to eight of X; its waves
 // share the reduction. Sums in a fixed order.
-template <int ROWS>
-__global__ __launch_bounds__(256) void k_gated_low(const LowParams p) {
-  __shared__ float part[4][ROWS];
+template <int ROWS, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_gated_low(const LowParams p) {
+  __shared__ float part[WAVES][ROWS];
   const int row = blockIdx.x, w = row >= p.rp, j = row - w * p.rp;
   const int m0 = ROWS * static_cast<int>(blockIdx.y), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float acc[ROWS];
 #pragma unroll
   for (int m = 0; m < ROWS; ++m) acc[m] = 0.0f;
   if (j < p.r) {
-    for (int64_t k = 8 * threadIdx.x; k < p.K; k += 2048) {
+    for (int64_t k = 8 * threadIdx.x; k < p.K; k += 512 * WAVES) {
       const bf16x8 a = adapter8(w ? p.A[1] : p.A[0], p.bf16, j * p.K + k);
 #pragma unroll
       for (int m = 0; m < ROWS; ++m) {
@@ -95,7 +96,9 @@ __global__ __launch_bounds__(256) void k_gated_low(const LowParams p) {
   __syncthreads();
   if (threadIdx.x < ROWS && m0 + static_cast<int>(threadIdx.x) < p.M) {
     const int m = threadIdx.x;
-    const float v = (part[0][m] + part[1][m]) + (part[2][m] + part[3][m]);
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) v += part[w][m];
     p.Hs[static_cast<int64_t>(m0 + m) * 2 * p.rp + row] = static_cast<__bf16>(p.scale * v);
   }
 }
@@ -253,7 +256,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, in
 // the order in which the passes use them, four to a lane and load. All loads
 // are buffer loads that return zeros for what is not there, so that none is
 // under a branch and waits are for no more than what is used; three passes are
-// under way.
+// under way. 1 x 11008 x 4096: 14.2 us without adapters (k_gated_few 17.9), r =
+// 64: 19.1 (23.6); 1 x 22016 x 8192 52 (60).
 constexpr int kRowThreads = 1024, kRowWaves = 16, kRowPasses = 16, kRowRing = 4, kRowMaxK = 16384;
 struct RowLds {
   uint32_t table[256 * 64];
@@ -460,7 +464,7 @@ __global__ __launch_bounds__(kRowThreads, 4) void k_gated_row(const StreamParams
   }
 }
 
-// One to four rows whose X fits in LDS beside the rest. A unit is one tile of
+// Up to four rows whose X fits in LDS beside the rest. A unit is one tile of
 // 16 weight rows, eight columns of H; 4096 elements of the reduction at a time,
 // a wave every eighth 128 of them. X comes from LDS and not by loads of its
 // own: loads return in order, and those behind the next codes' would wait for
@@ -722,8 +726,8 @@ hipError_t launch_gated_stream(const GatedArgs &a, const void *X, void *H, void 
   const int rp = gated_padded_rank(a.r);
   if (a.r) {
     const LowParams p{static_cast<const __bf16 *>(X), {a.A[0], a.A[1]}, a.adapter_bf16, a.K, static_cast<int>(a.M), a.r, rp, a.scale, static_cast<__bf16 *>(Hs)};
-    if (a.M == 1) k_gated_low<1><<<2 * rp, 256, 0, s>>>(p);
-    else k_gated_low<8><<<dim3(2 * rp, static_cast<unsigned>(ceil_div(a.M, 8))), 256, 0, s>>>(p);
+    if (a.M == 1) k_gated_low<1, kLowWaves><<<2 * rp, 64 * kLowWaves, 0, s>>>(p);
+    else k_gated_low<8, 4><<<dim3(2 * rp, static_cast<unsigned>(ceil_div(a.M, 8))), 256, 0, s>>>(p);
   }
   StreamParams p{};
   p.X = static_cast<const __bf16 *>(X);
