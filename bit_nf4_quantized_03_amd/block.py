@@ -214,10 +214,18 @@ def _given(t, name, shape, dtype, index, device):
     return t
 
 
+def _parts(W: NF4Weight):
+    return W.rows, W.cols, W.codes, W.absmax_q, W.dq_scale, W.dq_mean, W.absmax, W.fmt
+
+
 def qlora_gated_fwd(X, gate: NF4Weight, up: NF4Weight, Ag=None, Bg=None, Au=None, Bu=None, scale: float = 0.0, ws=None, out=None):
     """H = silu(G) * U, G = X Wg^T + scale (X Ag^T) Bg^T and U likewise: X bf16
     [M, K], two frozen 4-bit weights [N, K] of one format, adapters A [r, K] and
     B [N, r] in fp32 or bf16 (all four or none). H bf16 [M, N]."""
+    if ws is None and out is None and (at := _fast_on(X)):
+        new = _fast.block(*at, X, *_parts(gate), *_parts(up), Ag, Bg, Au, Bu, scale, False)
+        if new is not None:
+            return new
     M, N, K, r, index, sg, su, ad, _ = _block_args(X, gate, up, Ag, Bg, Au, Bu, scale)
     out = _given(out, "out", (M, N), torch.bfloat16, index, X.device)
     at, size, ws = _block_ws(ws, M, N, K, r, False, index, X.device)
@@ -230,6 +238,10 @@ def qlora_gated_fwd_save(X, gate: NF4Weight, up: NF4Weight, Ag=None, Bg=None, Au
     """(H, G, U, Hs): qlora_gated_fwd's H and what qlora_gated_bwd takes: G and U
     in bf16 and the adapter activations Hs bf16 [M, qlora_gated_saved_cols(r)]
     (None without adapters)."""
+    if ws is None and outs is None and (at := _fast_on(X)):
+        new = _fast.block(*at, X, *_parts(gate), *_parts(up), Ag, Bg, Au, Bu, scale, True)
+        if new is not None:
+            return new
     M, N, K, r, index, sg, su, ad, _ = _block_args(X, gate, up, Ag, Bg, Au, Bu, scale)
     H, G, U, Hs = (None,) * 4 if outs is None else outs
     H, G, U = (_given(t, name, (M, N), torch.bfloat16, index, X.device) for name, t in (("H", H), ("G", G), ("U", U)))

@@ -293,6 +293,84 @@ PyObject *gated(PyObject *, PyObject *const *a, Py_ssize_t n) {   // X's five, W
   });
 }
 
+// A vector of `count` elements on GPU `dev`; null otherwise.
+void *vector(PyObject *o, at::ScalarType type, int64_t count, int dev) {
+  const Tensor *t = tensor(o, type, dev);
+  return t && t->dim() == 1 && t->size(0) == count ? t->data_ptr() : nullptr;
+}
+
+// (rows, cols, codes, absmax_q, dq_scale, dq_mean, absmax, format) from args on as a 4-bit weight.
+bool weight(PyObject *const *a, int dev, qlora_nf4_weight *w) {
+  const long long rows = PyLong_AsLongLong(a[0]), cols = PyLong_AsLongLong(a[1]), format = PyLong_AsLongLong(a[7]);
+  if (PyErr_Occurred()) {
+    PyErr_Clear();
+    return false;
+  }
+  constexpr long long kMost = 1 << 24;
+  if (rows < 1 || cols < 1 || rows > kMost || cols > kMost || format < QLORA_FMT_NF4_DQ || format > QLORA_FMT_FP4) return false;
+  const int64_t n = rows * cols, blocks = (n + QLORA_NF4_BLOCK - 1) / QLORA_NF4_BLOCK;
+  *w = qlora_nf4_weight{};
+  w->rows = rows, w->cols = cols, w->format = static_cast<int32_t>(format);
+  w->codes = static_cast<uint8_t *>(vector(a[2], at::kByte, (n + 1) / 2, dev));
+  if (!w->codes) return false;
+  if (format == QLORA_FMT_NF4 || format == QLORA_FMT_FP4)
+    return (w->absmax = static_cast<float *>(vector(a[6], at::kFloat, blocks, dev))) != nullptr;
+  w->absmax_q = static_cast<int8_t *>(vector(a[3], at::kChar, blocks, dev));
+  w->dq_scale = static_cast<float *>(vector(a[4], at::kFloat, (blocks + 255) / 256, dev));
+  w->dq_mean = static_cast<float *>(vector(a[5], at::kFloat, 1, dev));
+  return w->absmax_q && w->dq_scale && w->dq_mean;
+}
+
+PyObject *block(PyObject *, PyObject *const *a, Py_ssize_t n) {   // X, gate's eight, up's eight, Ag, Bg, Au, Bu, scale, save
+  return guarded([&]() -> PyObject * {
+    if (n != 25) return none();
+    const int dev = static_cast<int>(PyLong_AsLong(a[0]));
+    const Tensor *x = tensor(a[2], at::kBFloat16, dev);
+    qlora_nf4_weight gate, up;
+    if (!x || x->dim() != 2 || x->numel() == 0 || !weight(a + 3, dev, &gate) || !weight(a + 11, dev, &up) || x->size(1) != gate.cols) return none();
+    const int64_t M = x->size(0), N = gate.rows, K = gate.cols;
+    qlora_gated_adapters ad{};
+    const bool adapts = a[19] != Py_None, save = a[24] == Py_True;
+    if (adapts) {
+      at::ScalarType type = at::kBFloat16;
+      ad.dtype = QLORA_BF16;
+      const Tensor *first = tensor(a[19], type, dev);
+      if (!first) type = at::kFloat, ad.dtype = QLORA_F32, first = tensor(a[19], type, dev);
+      if (!first || first->dim() != 2) return none();
+      const int64_t r = first->size(0);
+      const void **const to[4] = {&ad.gate_A, &ad.gate_B, &ad.up_A, &ad.up_B};
+      for (int i = 0; i < 4; ++i) {
+        const Tensor *t = tensor(a[19 + i], type, dev);
+        if (!t || !is(*t, i & 1 ? N : r, i & 1 ? r : K)) return none();
+        *to[i] = t->data_ptr();
+      }
+      if (r < 1 || r > 256) return none();
+      ad.r = static_cast<int32_t>(r);
+      ad.scale = static_cast<float>(PyFloat_AsDouble(a[23]));
+      if (PyErr_Occurred()) {
+        PyErr_Clear();
+        return none();
+      }
+    } else if (a[20] != Py_None || a[21] != Py_None || a[22] != Py_None) {
+      return none();
+    }
+    void *stream = stream_of(a[1]);
+    Tensor out[4], ws;
+    const int status = unlocked([&] {
+      for (int i = 0; i < (save ? 3 : 1); ++i) out[i] = fresh(*x, {M, N}, at::kBFloat16);
+      if (save && adapts) out[3] = fresh(*x, {M, qlora_gated_saved_cols(ad.r)}, at::kBFloat16);
+      const size_t size = qlora_gated_workspace_bytes(M, N, K, ad.r, 0);
+      if (size) ws = fresh(*x, {static_cast<int64_t>(size)}, at::kByte);
+      const auto at = [](const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; };
+      return qlora_gated_fwd(x->data_ptr(), M, &gate, &up, adapts ? &ad : nullptr, at(out[0]), at(out[1]), at(out[2]), at(out[3]), at(ws), size, stream);
+    });
+    if (status != QLORA_OK) return none();
+    if (!save) return wrap(std::move(out[0]));
+    PyObject *hs = adapts ? wrap(std::move(out[3])) : none();
+    return pack({wrap(std::move(out[0])), wrap(std::move(out[1])), wrap(std::move(out[2])), hs});
+  });
+}
+
 // Heads [rows, heads, dim] of `type` on GPU `dev`, the elements of a head next
 // to each other; null otherwise.
 const Tensor *heads_of(PyObject *o, at::ScalarType type, int dev) {
@@ -351,6 +429,7 @@ PyMethodDef methods[] = {
     {"norm_bwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(norm_bwd)), METH_FASTCALL, nullptr},
     {"linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(linear)), METH_FASTCALL, nullptr},
     {"gated", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(gated)), METH_FASTCALL, nullptr},
+    {"block", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(block)), METH_FASTCALL, nullptr},
     {"rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(rope)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -508,3 +508,34 @@ def test_refusals_with_tensors(qb):
         qb.qlora_gated_bwd(d.dH, X, G, U, Hs, g, u)
     with pytest.raises(qb.QloraError):
         qb.qlora_gated_fwd(X, *(qb.qlora_nf4_quantize(torch.randn(100, 64, device="cuda")) for _ in range(2)))
+
+
+def test_calls_without_fastcall(qb, monkeypatch):
+    """Every call with new outputs gives the same bits without _fastcall.so."""
+    import torch
+    from bit_nf4_quantized_03_amd import block as binding, mx
+    assert binding._fast is not None, "_fastcall.so is not built"
+    blocks = [(d, d.args if r else (d.gate, d.up)) for M, r, fmt, bf16 in ((1, 8, 0, True), (3, 0, 1, True), (50, 16, 2, False), (70, 5, 3, True))
+              for d in (Data(qb, M, 192, 256, r, fmt=fmt, bf16=bf16),)]
+    X, W = qb.qlora_mx_quantize(torch.randn(5, 256, device="cuda"), 1), qb.qlora_mx_quantize(torch.randn(128, 256, device="cuda"))
+    fused = torch.randn(7, 6, 64, device="cuda")
+    pos, freqs = torch.arange(7, device="cuda"), qb.qlora_rope_freqs(32, device="cuda")[0]
+
+    def calls():
+        out = []
+        for d, args in blocks:
+            out += [qb.qlora_gated_fwd(d.X, *args), *qb.qlora_gated_fwd_save(d.X, *args)]
+        for o in (None, 0, 1):
+            h = qb.qlora_mx_gated(X, W, mx=o)
+            out += [h] if o is None else [h.codes, h.scales]
+        for t in (fused, fused.bfloat16()):
+            for p in (pos, pos.int()):
+                out += [*qb.qlora_rope_fwd(t[:, :4], t[:, 4:], p, freqs), *qb.qlora_rope_bwd(t, None, p, freqs, 1.5, True)]
+        return out
+    gu.announce("block calls with _fastcall")
+    fast = calls()
+    gu.announce("block calls without _fastcall")
+    monkeypatch.setattr(binding, "_fast", None)
+    monkeypatch.setattr(mx, "_fast", None)
+    for i, (a, b) in enumerate(zip(fast, calls())):
+        assert (a is None) == (b is None) and (a is None or (a.dtype == b.dtype and torch.equal(a, b))), i
