@@ -20,8 +20,8 @@
 // lane reads those of its four rows of the sums at once. Codes and raw constants
 // of the next turn are requested before this one's are used.
 //
-// Two weights of 11008 x 4096 (46 MB), double quantization, r = 64: 1 row 19.1 us
-// (14.2, 3.3 TB/s, without adapters: k_gated_low, its launch and the wait for it
+// Two weights of 11008 x 4096 (46 MB), double quantization, r = 64: 1 row 18.1 us
+// (13.3, 3.5 TB/s, without adapters: k_gated_low, its launch and the wait for it
 // are 4 of these), 4 rows 27.1, 16 rows 39.1, 32 rows 51.6. k_gated_few took 23.6
 // and 17.9 us for one row, 14.5 with the table's reads left out: a product per
 // instruction has 15 columns to spare there, and each turn's barrier waits for
@@ -256,8 +256,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, in
 // the order in which the passes use them, four to a lane and load. All loads
 // are buffer loads that return zeros for what is not there, so that none is
 // under a branch and waits are for no more than what is used; three passes are
-// under way. 1 x 11008 x 4096: 14.2 us without adapters (k_gated_few 17.9), r =
-// 64: 19.1 (23.6); 1 x 22016 x 8192 52 (60).
+// under way. 1 x 11008 x 4096: 13.3 us without adapters (k_gated_few 17.9), r =
+// 64: 18.1 (23.6); 1 x 22016 x 8192 47 (60). B's rows in bf16 are requested with
+// the first codes; in fp32 they are not, as the registers for them spilled others
+// (19.1 us so in both).
 constexpr int kRowThreads = 1024, kRowWaves = 16, kRowPasses = 16, kRowRing = 4, kRowMaxK = 16384;
 struct RowLds {
   uint32_t table[256 * 64];
@@ -328,16 +330,13 @@ __global__ __launch_bounds__(kRowThreads, 4) void k_gated_row(const StreamParams
   const bool wide = p.r % (p.bf16 ? 8 : 4) == 0;   // rows of B begin 16-byte aligned
   const auto bb = buffer_of(static_cast<const char *>(side ? p.B[1] : p.B[0]) + c0 * p.r * (p.bf16 ? 2 : 4),
                             p.r ? static_cast<int64_t>(count) * p.r * (p.bf16 ? 2 : 4) : 0);
-  u32x4 b[4];
+  auto load_b = [&](int n, int j, int i) {   // 16 bytes of row n from column j on, the i-th of the lane's
+    const int k = j + (p.bf16 ? 8 : 4) * i;
+    return __builtin_amdgcn_raw_buffer_load_b128(bb, adds && n < count && k < p.r ? static_cast<uint32_t>((n * p.r + k) * (p.bf16 ? 2 : 4)) : kNowhere, 0, 0);
+  };
+  u32x4 b0[2];   // of bf16, the first 64 columns, ahead of the passes
   auto request_b = [&](int from) {
-    if (!wide || p.r == 0) return;
-    const int n = from + in;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int j = j0 + (p.bf16 ? 8 : 4) * i;
-      const bool there = adds && n < count && j < p.r && (!p.bf16 || i < 2);
-      b[i] = __builtin_amdgcn_raw_buffer_load_b128(bb, there ? static_cast<uint32_t>((n * p.r + j) * (p.bf16 ? 2 : 4)) : kNowhere, 0, 0);
-    }
+    if (wide && p.bf16 && p.r > 0) b0[0] = load_b(from + in, j0, 0), b0[1] = load_b(from + in, j0, 1);
   };
 
   const u32x4 x0 = __builtin_amdgcn_raw_buffer_load_b128(xb, 16 * tid, 0, 0);
@@ -417,20 +416,22 @@ __global__ __launch_bounds__(kRowThreads, 4) void k_gated_row(const StreamParams
       float a = 0.0f;
       for (int j = j0; j < p.r; j += 64) {
         float f[16];
-        if (wide) {
-          if (j > j0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int k = j + (p.bf16 ? 8 : 4) * i;
-              const bool there = n < count && k < p.r && (!p.bf16 || i < 2);
-              b[i] = __builtin_amdgcn_raw_buffer_load_b128(bb, there ? static_cast<uint32_t>((n * p.r + k) * (p.bf16 ? 2 : 4)) : kNowhere, 0, 0);
-            }
-          }
+        if (wide && p.bf16) {
+          if (j > j0) b0[0] = load_b(n, j, 0), b0[1] = load_b(n, j, 1);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const uint32_t half = b[e >> 3][(e >> 1) & 3], full = b[e >> 2][e & 3];
-            const uint32_t bits = p.bf16 ? (e & 1 ? half & 0xffff0000u : half << 16) : full;
-            f[e] = __builtin_bit_cast(float, bits);
+            const uint32_t w = b0[e >> 3][(e >> 1) & 3];
+            f[e] = __builtin_bit_cast(float, e & 1 ? w & 0xffff0000u : w << 16);
+          }
+        } else if (wide) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const u32x4 w = load_b(n, j, i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t bits = w[e];
+              f[4 * i + e] = __builtin_bit_cast(float, bits);
+            }
           }
         } else {
 #pragma unroll
