@@ -57,7 +57,7 @@ def _declare():
     sigs = {
         "qlora_mx_pair": (ci, [mp, mp, mp, vp]),
         "qlora_mx_gated": (ci, [mp, mp, vp, mp, vp]),
-        "qlora_mx_gated_grouped": (ci, [mp, mp, vp, i32, vp, mp, vp]),
+        "qlora_mx_gated_grouped": (ci, [mp, mp, vp, i32, vp, mp, i32, vp]),
         "qlora_gated_saved_cols": (i64, [i32]),
         "qlora_gated_workspace_bytes": (sz, [i64, i64, i64, i32, i32]),
         "qlora_gated_fwd": (ci, [vp, i64, wp, wp, ap, vp, vp, vp, vp, vp, sz, vp]),
@@ -91,18 +91,15 @@ def qlora_mx_pair(gate: MXMatrix, up: MXMatrix, out: Optional[MXMatrix] = None) 
     return out
 
 
-def _gated_out(X, index, N, mx, out, fresh):
+def _gated_out(X, index, N, mx, out):
     """H and how the entry point takes it: (result, address of a bf16 H, struct of a microscaled one)"""
     if N % 32:
         raise ValueError(f"H would have {N} columns: a pair has a multiple of 64 rows")
     if out is None:
         if mx is None:
-            out = (torch.zeros if fresh else torch.empty)((X.rows, N), dtype=torch.bfloat16, device=X.codes.device)
+            out = _empty(X.rows, N, torch.bfloat16, X.codes.device)
         else:
             out = MXMatrix.empty(X.rows, N, X.codes.device, mx)
-            if fresh:
-                out.codes.zero_()
-                out.scales.zero_()
     if isinstance(out, MXMatrix):
         if mx is not None and mx != out.mx:
             raise ValueError(f"mx {mx} differs from out.mx {out.mx}")
@@ -124,7 +121,7 @@ def qlora_mx_gated(X: MXMatrix, W: MXMatrix, mx: Optional[int] = QLORA_MX_FP8, o
     sw = W.c_struct("W", index)
     if out is not None:
         mx = None
-    out, h, hq = _gated_out(X, index, W.rows // 2, mx, out, False)
+    out, h, hq = _gated_out(X, index, W.rows // 2, mx, out)
     _gated(index, byref(sx), byref(sw), h, hq)
     return out
 
@@ -143,10 +140,11 @@ def qlora_mx_gated_grouped(X: MXMatrix, W: MXMatrix, offsets, mx: Optional[int] 
     experts = offsets.shape[0] - 1
     if W.rows % (2 * experts):
         raise ValueError(f"W has {W.rows} rows, not a multiple of two for each of {experts} experts")
-    if out is not None:
+    clear = out is None
+    if not clear:
         mx = None
-    out, h, hq = _gated_out(X, index, W.rows // experts // 2, mx, out, True)
-    _gated_grouped(index, byref(sx), byref(sw), off, experts, h, hq)
+    out, h, hq = _gated_out(X, index, W.rows // experts // 2, mx, out)
+    _gated_grouped(index, byref(sx), byref(sw), off, experts, h, hq, clear)
     return out
 
 

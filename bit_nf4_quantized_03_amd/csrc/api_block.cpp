@@ -49,9 +49,9 @@ int gated_args(const char *fn, const qlora_mx_matrix *X, const qlora_mx_matrix *
   return QLORA_OK;
 }
 
-int gated(const char *fn, const qnf4::MxLinear &a, const qlora_mx_matrix *Hq, void *stream) {
+int gated(const char *fn, const qnf4::MxLinear &a, const qlora_mx_matrix *Hq, bool clear, void *stream) {
   return qnf4::api_hip_status(qnf4::launch_mx_gated(a, Hq ? Hq->codes : nullptr, Hq ? Hq->scales : nullptr,
-                                                    Hq ? Hq->type : 0, static_cast<hipStream_t>(stream)), fn);
+                                                    Hq ? Hq->type : 0, clear, static_cast<hipStream_t>(stream)), fn);
 }
 
 bool valid_gated(int64_t M, int64_t N, int64_t K, int32_t r) {
@@ -195,11 +195,11 @@ int qlora_mx_gated(const qlora_mx_matrix *X, const qlora_mx_matrix *W, void *H, 
   if (st != QLORA_OK) return st;
   qnf4::MxLinear a;
   st = gated_args(fn, X, W, W->rows, H, Hq, &a);
-  return st != QLORA_OK ? st : gated(fn, a, Hq, stream);
+  return st != QLORA_OK ? st : gated(fn, a, Hq, false, stream);
 }
 
 int qlora_mx_gated_grouped(const qlora_mx_matrix *X, const qlora_mx_matrix *W, const int32_t *offsets, int32_t experts,
-                           void *H, const qlora_mx_matrix *Hq, void *stream) {
+                           void *H, const qlora_mx_matrix *Hq, int32_t clear, void *stream) {
   const char *fn = "qlora_mx_gated_grouped";
   int st = qnf4::api_check_matrix(fn, "X", X);
   if (st == QLORA_OK) st = qnf4::api_check_matrix(fn, "W", W);
@@ -216,7 +216,7 @@ int qlora_mx_gated_grouped(const qlora_mx_matrix *X, const qlora_mx_matrix *W, c
   if (st != QLORA_OK) return st;
   a.offsets = offsets;
   a.experts = experts;
-  return gated(fn, a, Hq, stream);
+  return gated(fn, a, Hq, clear != 0, stream);
 }
 
 int64_t qlora_gated_saved_cols(int32_t r) { return r < 0 || r > 256 ? 0 : 2 * qnf4::gated_padded_rank(r); }

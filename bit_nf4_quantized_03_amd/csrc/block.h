@@ -15,8 +15,8 @@ struct MxPair {
 hipError_t launch_mx_pair(const MxPair &a, hipStream_t s);
 
 // a.N: rows of one pair. H is a.Y in bf16, or codes and scales of `type` where
-// that is null.
-hipError_t launch_mx_gated(const MxLinear &a, uint8_t *codes, uint8_t *scales, int type, hipStream_t s);
+// that is null. clear: by expert, rows that no expert has become zeros.
+hipError_t launch_mx_gated(const MxLinear &a, uint8_t *codes, uint8_t *scales, int type, bool clear, hipStream_t s);
 
 // Heads [rows][heads][dim], the elements of a head next to each other; strides
 // in elements. No heads: not there.

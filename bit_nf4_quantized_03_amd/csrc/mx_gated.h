@@ -23,6 +23,7 @@ struct MxGatedOut {
   int64_t N;               // columns of H, a multiple of 32
   uint32_t pitch;
   int type;
+  bool clear;              // by expert: zeros in the rows that no expert has
 };
 
 // Columns n .. n + 7 of row m. Microscaled: the four lanes of a quad hold one

@@ -30,11 +30,37 @@ __global__ __launch_bounds__(256) void k_mx_pair(const PairParams p) {
 
 // Few rows: 16 RT rows of the pair, 8 RT columns of H a workgroup. The waves'
 // sums are added in wave order, then a lane takes eight columns of a row.
+// Zeros in the rows of H in front of the first expert's and behind the last
+// one's, by workgroup `part` of `parts`. These are workgroups of the product's own
+// launch behind its others (a fill in front of 4096 rows over 8 experts 4096 x
+// 4096 took 8 us).
+__device__ __forceinline__ void clear_rest(const MxGatedOut &o, const int32_t *offsets, int experts, int64_t M, int part, int parts) {
+  const int64_t first = min(max(static_cast<int64_t>(offsets[0]), int64_t(0)), M);
+  const int64_t last = max(min(max(static_cast<int64_t>(offsets[experts]), int64_t(0)), M), first);
+  const int64_t rows = M - (last - first);
+  const auto clear = [&](void *to, int64_t bytes) {   // of a row, a multiple of 16
+    const int64_t runs = bytes / 16;
+    for (int64_t i = static_cast<int64_t>(part) * blockDim.x + threadIdx.x; i < rows * runs; i += static_cast<int64_t>(parts) * blockDim.x) {
+      const int64_t k = i / runs, row = k < first ? k : k + (last - first);
+      *reinterpret_cast<uint4 *>(static_cast<char *>(to) + row * bytes + 16 * (i - k * runs)) = make_uint4(0, 0, 0, 0);
+    }
+  };
+  if (o.type < 0) return clear(o.h, 2 * o.N);
+  clear(o.codes, o.type == QLORA_MX_FP4 ? o.N / 2 : o.N);
+  clear(o.scales, o.pitch);
+}
+constexpr int kClearGroups = 64;
+
+// The sums of a few rows: as mx_linear.hip's, then the gate.
 template <int XT, int MT, int RT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_mx_gated_gemv(const MxGemvParams p, const MxGatedOut o) {
   __shared__ float part[WAVES][MT][RT][16][17];
   int64_t m0, m_end;
-  if (!mx_stream<XT, MT, RT, WAVES>(p, part, m0, m_end)) return;
+  if (!mx_stream<XT, MT, RT, WAVES>(p, part, m0, m_end)) {
+    // the last row of workgroups has no piece
+    if (o.clear && blockIdx.y + 1 == gridDim.y) clear_rest(o, p.offsets, p.experts, p.M, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
+    return;
+  }
   const int rows = static_cast<int>(min(m_end - m0, int64_t(16 * MT)));
   __syncthreads();
   for (int i = threadIdx.x; i < 16 * RT * rows; i += 64 * WAVES) {
@@ -89,7 +115,11 @@ template <class T>
 __global__ __launch_bounds__(T::kThreads, 1) void k_mx_gated_grouped(const MxGemmParams p, const MxGatedOut o) {
   __shared__ __attribute__((aligned(16))) char smem[T::kLds];
   MxGroupTile t;
-  if (!mx_group_tile<T>(p, static_cast<int>(blockIdx.x), t)) return;
+  if (!mx_group_tile<T>(p, static_cast<int>(blockIdx.x), t)) {
+    const int part = static_cast<int>(blockIdx.x + kClearGroups) - static_cast<int>(gridDim.x);
+    if (o.clear && part >= 0) clear_rest(o, p.offsets, p.experts, p.M, part, kClearGroups);
+    return;
+  }
   const int64_t n0 = static_cast<int64_t>(t.tn) * T::BN;
   const int64_t m0 = t.m_begin + static_cast<int64_t>(t.tm) * T::BM;
   MxOperands op = p.op;
@@ -105,7 +135,7 @@ __global__ __launch_bounds__(T::kThreads, 1) void k_mx_gated_grouped(const MxGem
 template <int XT, int MT, int RT, int WAVES>
 hipError_t run_gemv(const MxGemvParams &p, const MxGatedOut &o, hipStream_t s) {
   // by expert: every run of 16 rows but an expert's first is a whole one or follows one
-  const dim3 g(static_cast<unsigned>(ceil_div(p.N, 16 * RT)), p.experts ? p.experts + static_cast<unsigned>(p.M / 16) : 1);
+  const dim3 g(static_cast<unsigned>(ceil_div(p.N, 16 * RT)), p.experts ? p.experts + static_cast<unsigned>(p.M / 16) + o.clear : 1);
   k_mx_gated_gemv<XT, MT, RT, WAVES><<<g, 64 * WAVES, 0, s>>>(p, o);
   return hipGetLastError();
 }
@@ -114,7 +144,7 @@ template <int TILE, class T>
 hipError_t run_tile(const MxGemmParams &p, const MxGatedOut &o, hipStream_t s) {
   static_assert(T::BN == kMxTile[TILE].bn && T::BM == kMxTile[TILE].bm && T::kThreads == kMxTile[TILE].threads, "the rule's tile");
   const unsigned groups = static_cast<unsigned>(mx_tile_groups(T::BM, T::BN, p.M, p.N, p.experts));
-  if (p.experts) k_mx_gated_grouped<T><<<groups, T::kThreads, 0, s>>>(p, o);
+  if (p.experts) k_mx_gated_grouped<T><<<groups + (o.clear ? kClearGroups : 0), T::kThreads, 0, s>>>(p, o);
   else k_mx_gated<T><<<groups, T::kThreads, 0, s>>>(p, o);
   return hipGetLastError();
 }
@@ -206,7 +236,7 @@ hipError_t launch_mx_pair(const MxPair &a, hipStream_t s) {
   return hipSuccess;
 }
 
-hipError_t launch_mx_gated(const MxLinear &a, uint8_t *codes, uint8_t *scales, int type, hipStream_t s) {
+hipError_t launch_mx_gated(const MxLinear &a, uint8_t *codes, uint8_t *scales, int type, bool clear, hipStream_t s) {
   MxGatedOut o;
   o.h = static_cast<__bf16 *>(a.Y);
   o.codes = codes;
@@ -214,6 +244,7 @@ hipError_t launch_mx_gated(const MxLinear &a, uint8_t *codes, uint8_t *scales, i
   o.N = a.N / 2;
   o.pitch = static_cast<uint32_t>(mx_pitch(o.N));
   o.type = a.Y ? -1 : type;
+  o.clear = clear;
   return a.x_type == QLORA_MX_FP4 ? run_gated<QLORA_MX_FP4>(a, o, s) : run_gated<QLORA_MX_FP8>(a, o, s);
 }
 

@@ -52,10 +52,11 @@ int qlora_mx_gated(const qlora_mx_matrix *X, const qlora_mx_matrix *W, void *H, 
 
 /* The same by expert: rows of X sorted by expert, W [experts * 2 N, K] the
  * experts' pairs one below the other; offsets and experts as in
- * qlora_mx_linear_grouped. Rows of H (codes and scales) that no expert has are
- * left as they were. */
+ * qlora_mx_linear_grouped. Rows of H (codes and scales) in front of offsets[0]
+ * and from offsets[experts] on are left as they were, or with `clear` (not 0)
+ * become zeros, as a new H wants them. */
 int qlora_mx_gated_grouped(const qlora_mx_matrix *X, const qlora_mx_matrix *W, const int32_t *offsets,
-                           int32_t experts, void *H, const qlora_mx_matrix *Hq, void *stream);
+                           int32_t experts, void *H, const qlora_mx_matrix *Hq, int32_t clear, void *stream);
 
 /* ------------------------------------------------ the gated block, with adapters
  *

@@ -86,12 +86,12 @@ static void microscaled(void) {
   REACH(qlora_mx_gated(&x, &pair, pool, NULL, NULL));
   REACH(qlora_mx_gated(&x, &pair, NULL, &h, NULL));
   const int32_t *off = (const int32_t *)pool;
-  REJ(qlora_mx_gated_grouped(&x, &pair, off, 0, pool, NULL, NULL));
-  REJ(qlora_mx_gated_grouped(&x, &pair, off, INT32_MIN, pool, NULL, NULL));
-  REJ(qlora_mx_gated_grouped(&x, &pair, off, INT32_MAX, pool, NULL, NULL));
-  REJ(qlora_mx_gated_grouped(&x, &pair, NULL, 2, pool, NULL, NULL));
-  REJ(qlora_mx_gated_grouped(&x, &pair, off, 4, pool, NULL, NULL));
-  REACH(qlora_mx_gated_grouped(&x, &pair, off, 2, pool, NULL, NULL));
+  REJ(qlora_mx_gated_grouped(&x, &pair, off, 0, pool, NULL, 0, NULL));
+  REJ(qlora_mx_gated_grouped(&x, &pair, off, INT32_MIN, pool, NULL, 0, NULL));
+  REJ(qlora_mx_gated_grouped(&x, &pair, off, INT32_MAX, pool, NULL, 0, NULL));
+  REJ(qlora_mx_gated_grouped(&x, &pair, NULL, 2, pool, NULL, 0, NULL));
+  REJ(qlora_mx_gated_grouped(&x, &pair, off, 4, pool, NULL, 0, NULL));
+  REACH(qlora_mx_gated_grouped(&x, &pair, off, 2, pool, NULL, 0, NULL));
 }
 
 static void block(int format) {

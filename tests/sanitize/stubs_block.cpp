@@ -14,7 +14,7 @@ hipError_t reached() {
 
 namespace qnf4 {
 hipError_t launch_mx_pair(const MxPair &, hipStream_t) { return reached(); }
-hipError_t launch_mx_gated(const MxLinear &, uint8_t *, uint8_t *, int, hipStream_t) { return reached(); }
+hipError_t launch_mx_gated(const MxLinear &, uint8_t *, uint8_t *, int, bool, hipStream_t) { return reached(); }
 hipError_t launch_rope(const Rope &, hipStream_t) { return reached(); }
 size_t gated_ws_bytes(int64_t M, int64_t N, int64_t K, int r, bool backward) {
   return static_cast<size_t>((M + N + K) / 64 + r) * (backward ? 32 : 16);

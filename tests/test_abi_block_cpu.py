@@ -76,13 +76,13 @@ def test_gated_grouped_rejects():
     g = lib.qlora_mx_gated_grouped
     X, W, H, off = M(5, 64, type=FP8), M(256, 64), FAKE, FAKE
     for e in (0, -1, 3, 1025):
-        assert g(X, W, off, e, H, None, None) == -2
-    assert g(X, W, None, 2, H, None, None) == -1
-    assert g(X, W, off + 2, 2, H, None, None) == -6
-    assert g(X, W, off, 8, H, None, None) == -2     # pairs of 32 rows
-    assert g(X, M((1 << 28) + 128, 64), off, 2, H, None, None) == -2
-    assert g(X, W, off, 2, None, M(5, 96, type=FP8), None) == -2
-    assert g(X, W, off, 2, None, None, None) == -1
+        assert g(X, W, off, e, H, None, 0, None) == -2
+    assert g(X, W, None, 2, H, None, 0, None) == -1
+    assert g(X, W, off + 2, 2, H, None, 0, None) == -6
+    assert g(X, W, off, 8, H, None, 0, None) == -2     # pairs of 32 rows
+    assert g(X, M((1 << 28) + 128, 64), off, 2, H, None, 0, None) == -2
+    assert g(X, W, off, 2, None, M(5, 96, type=FP8), 0, None) == -2
+    assert g(X, W, off, 2, None, None, 0, None) == -1
 
 
 def weight(rows=128, cols=192, fmt=qb.QLORA_FMT_NF4_DQ, **kw):
