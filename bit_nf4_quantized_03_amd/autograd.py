@@ -123,8 +123,6 @@ class GatedFn(torch.autograd.Function):
         X2 = _rows(X, X.shape[-1])
         args = (gate, up, Ag, Bg, Au, Bu, scale)
         shape = (*X.shape[:-1], gate.rows)
-        if not any(ctx.needs_input_grad):   # nothing to keep
-            return qlora_gated_fwd(X2, *args).reshape(shape)
         H, G, U, Hs = qlora_gated_fwd_save(X2, *args)
         ctx.save_for_backward(X2, G, U, Hs, Ag, Bg, Au, Bu)
         ctx.weights, ctx.scale, ctx.shape = (gate, up), scale, X.shape
@@ -143,7 +141,10 @@ def qlora_gated(X, gate: NF4Weight, up: NF4Weight, Ag=None, Bg=None, Au=None, Bu
     """H = silu(G) * U, G = X Wg-hat^T + scale (X Ag^T) Bg^T and U likewise, with
     autograd to X (bf16, any leading shape) and the adapters (fp32 or bf16, all
     four or none): the feed-forward block up to its down projection in one
-    ``qlora_gated_fwd_save`` and one ``qlora_gated_bwd`` call."""
+    ``qlora_gated_fwd_save`` and one ``qlora_gated_bwd`` call. Where no gradient
+    is asked for nothing is kept: ``qlora_gated_fwd``."""
+    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (X, Ag, Bg, Au, Bu))):
+        return qlora_gated_fwd(_rows(X, X.shape[-1]), gate, up, Ag, Bg, Au, Bu, float(scale)).reshape(*X.shape[:-1], gate.rows)
     return GatedFn.apply(X, Ag, Bg, Au, Bu, gate, up, float(scale))
 
 

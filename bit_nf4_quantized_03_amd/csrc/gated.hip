@@ -215,21 +215,25 @@ __global__ __launch_bounds__(256, 1) void k_gated_down(const DownParams p) {
 // four waves adds a quarter of the splits in order, then the quarters are added
 // (64 rows of 11008 x 4096 with r = 64: the forward takes 72 us with one wave
 // for all splits, 68 so).
+constexpr int64_t kSumGroups = int64_t(1) << 20;
 __global__ __launch_bounds__(256) void k_gated_sum(const float *part, int splits, int64_t n, float scale, __bf16 *out) {
   __shared__ float4 sums[3][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, per = (splits + 3) / 4, z0 = wave * per;
-  const int64_t e = (static_cast<int64_t>(blockIdx.x) * 64 + lane) * 4;
-  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (e < n && z0 < splits) v = split_sum4(part + z0 * n, n, e, min(per, splits - z0));
-  if (wave > 0) sums[wave - 1][lane] = v;
-  __syncthreads();
-  if (wave > 0 || e >= n) return;
+  for (int64_t e0 = static_cast<int64_t>(blockIdx.x) * 256; e0 < n; e0 += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t e = e0 + 4 * lane;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (e < n && z0 < splits) v = split_sum4(part + z0 * n, n, e, min(per, splits - z0));
+    __syncthreads();   // the first wave is done with the turn before
+    if (wave > 0) sums[wave - 1][lane] = v;
+    __syncthreads();
+    if (wave > 0 || e >= n) continue;
 #pragma unroll
-  for (int w = 0; w < 3; ++w) {
-    const float4 s = sums[w][lane];
-    v.x += s.x, v.y += s.y, v.z += s.z, v.w += s.w;
+    for (int w = 0; w < 3; ++w) {
+      const float4 s = sums[w][lane];
+      v.x += s.x, v.y += s.y, v.z += s.z, v.w += s.w;
+    }
+    *reinterpret_cast<uint2 *>(out + e) = make_uint2(pack_bf16x2(scale * v.x, scale * v.y), pack_bf16x2(scale * v.z, scale * v.w));
   }
-  *reinterpret_cast<uint2 *>(out + e) = make_uint2(pack_bf16x2(scale * v.x, scale * v.y), pack_bf16x2(scale * v.z, scale * v.w));
 }
 
 // -------------------------------------------------------------- split tiles
@@ -715,8 +719,6 @@ size_t carve(void *ws, Plan &pl, int64_t M, int64_t N, int64_t K, bool backward,
   return c.off;
 }
 
-unsigned blocks(int64_t n, int64_t per) { return static_cast<unsigned>(ceil_div(n, per)); }
-
 // Block scales and bf16 operands.
 void run_prep(const GatedArgs &a, const Plan &pl, const Buffers &b, bool backward, const ActParams &act, hipStream_t s) {
   PrepParams p{};
@@ -778,7 +780,7 @@ hipError_t launch_gated_fwd(const GatedArgs &a, const void *X, void *H, void *G,
     d.per = pl.down.steps_per_split;
     k_gated_down<128><<<static_cast<unsigned>(d.tiles * pl.down.splits), 256, 0, s>>>(d);
     const int64_t n = a.M * 2 * pl.rp;
-    k_gated_sum<<<blocks(n, 256), 256, 0, s>>>(b.down, pl.down.splits, n, a.scale, b.Hs);
+    k_gated_sum<<<static_cast<unsigned>(std::min(ceil_div(n, 256), kSumGroups)), 256, 0, s>>>(b.down, pl.down.splits, n, a.scale, b.Hs);
   }
   FwdParams p{X, {a.w[0].codes, a.w[1].codes}, {scales(a, b, 0), scales(a, b, 1)}, b.Hs, b.Bi, static_cast<__bf16 *>(H),
               static_cast<__bf16 *>(G), static_cast<__bf16 *>(U), a.M, a.N, a.K, pl.rp, pl.tail};
@@ -820,7 +822,7 @@ hipError_t launch_gated_bwd(const GatedArgs &a, const void *dH, const void *X, c
     d.per = pl.down.steps_per_split;
     k_gated_down<64><<<static_cast<unsigned>(d.tiles * pl.down.splits), 256, 0, s>>>(d);
     const int64_t count = a.M * 2 * pl.rp;
-    k_gated_sum<<<blocks(count, 256), 256, 0, s>>>(b.down, pl.down.splits, count, a.scale, b.low);
+    k_gated_sum<<<static_cast<unsigned>(std::min(ceil_div(count, 256), kSumGroups)), 256, 0, s>>>(b.down, pl.down.splits, count, a.scale, b.low);
   }
   DxParams p{b.dG, b.dU, {a.w[0].codes, a.w[1].codes}, {scales(a, b, 0), scales(a, b, 1)}, b.low, b.At, dX, a.M, a.N, a.K,
              pl.rp, pl.tail};

@@ -46,7 +46,7 @@ int qlora_mx_pair(const qlora_mx_matrix *gate, const qlora_mx_matrix *up, const 
  *        of the unrounded H: the input of the down projection
  * Sums, sizes and NaN blocks as in qlora_mx_linear with the 2 N rows of W (a
  * NaN block of either weight makes H's column NaN, and with Hq the block of 32
- * that the column is in). The sums and silu are fp32.
+ * that the column is in). The sums and silu are fp32. H overlaps no input.
  */
 int qlora_mx_gated(const qlora_mx_matrix *X, const qlora_mx_matrix *W, void *H, const qlora_mx_matrix *Hq, void *stream);
 
@@ -91,7 +91,8 @@ size_t qlora_gated_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r, i
  *         NULL otherwise
  * M up to 2^24, N and K up to 2^23, M N, M K and N K up to 2^36. The decoded
  * weights, A, B and Hs enter the sums as bf16; sums and silu are fp32, in a
- * fixed order (deterministic).
+ * fixed order (deterministic). No output overlaps an input, another output or
+ * the workspace.
  */
 int qlora_gated_fwd(const void *X, int64_t M, const qlora_nf4_weight *gate, const qlora_nf4_weight *up,
                     const qlora_gated_adapters *adapters, void *H, void *G, void *U, void *Hs, void *ws,
@@ -108,7 +109,8 @@ typedef struct {
  *     lg = s dG Bg,  lu = s dU Bu
  *     dX = dG Wg + dU Wu + lg Ag + lu Au
  *     dAg = lg^T X,  dBg = dG^T Hs_g,  dAu = lu^T X,  dBu = dU^T Hs_u
- * dH, dX bf16; dX overlaps no input. grads NULL without adapters.
+ * dH, dX bf16. No output overlaps an input, another output or the workspace.
+ * grads NULL without adapters.
  * dG, dU, lg and lu are rounded to bf16, each sum is fp32 in a fixed order and
  * rounded once.
  */

@@ -539,3 +539,34 @@ def test_calls_without_fastcall(qb, monkeypatch):
     monkeypatch.setattr(mx, "_fast", None)
     for i, (a, b) in enumerate(zip(fast, calls())):
         assert (a is None) == (b is None) and (a is None or (a.dtype == b.dtype and torch.equal(a, b))), i
+
+
+def test_nothing_is_kept_without_gradients(qb, monkeypatch):
+    import torch
+    from bit_nf4_quantized_03_amd import autograd as ag
+    gu.announce("gated without gradients")
+    d = Data(qb, 40, 128, 128, 8)
+    leaves = [t.clone().requires_grad_(True) for t in d.factors]
+    want = ag.qlora_gated(d.X, d.gate, d.up, *leaves, d.scale).detach()
+    monkeypatch.setattr(ag, "qlora_gated_fwd_save", None)
+    with torch.no_grad():
+        assert torch.equal(ag.qlora_gated(d.X.view(2, 20, 128), d.gate, d.up, *leaves, d.scale), want.view(2, 20, 128))
+    assert torch.equal(ag.qlora_gated(d.X, d.gate, d.up, *d.factors, d.scale), want)
+
+
+@pytest.mark.parametrize("M,N,K,r", [(1 << 24, 64, 64, 200), (524544 + 33, 8192, 64, 8)])
+def test_most_rows_and_past_32_bits(qb, M, N, K, r):
+    """The most rows there may be, and more than 2^32 elements of H: the last rows are what they are in a call of their own."""
+    import torch
+    gu.announce(f"gated large {M}x{N}x{K} r={r}")
+    d = Data(qb, 300, N, K, r)
+    X, dH = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda"), torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    X[-300:], dH[-300:] = d.X, d.dH
+    few, many = qb.qlora_gated_fwd_save(d.X, *d.args), qb.qlora_gated_fwd_save(X, *d.args)
+    for a, b in zip(few, many):   # one step of 64 elements: one order of the sums
+        assert torch.equal(b[-300:], a) and not b[:-300].any()
+    few, many = qb.qlora_gated_bwd(d.dH, d.X, *few[1:], *d.args), qb.qlora_gated_bwd(dH, X, *many[1:], *d.args)
+    assert not many[0][:-300].any()
+    # sums over N and over the rows differ in their order: both are the oracle's within its bars, 7e-3 each
+    for a, b, label in zip(few, (many[0][-300:], *many[1:]), GRADS):
+        near(b, f64(a), 1.4e-2, label)
