@@ -676,8 +676,10 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int r, bool backward) {
   if (r) {
     pl.down = choose_split(grid_blocks(M, 128) * 2 * (pl.rp / 64), static_cast<int>(N / kBK), kDownSplits, kCus);
     const int msteps = static_cast<int>(ceil_div(M, kBK));
-    pl.ga = choose_split(grid_blocks(K, 256) * (2 * pl.rp / 64), msteps, 8);
-    pl.gb = choose_split(2 * grid_blocks(N, 256) * (pl.rp / 64), msteps, 8);
+    // more splits cost more to write and add than they spread (11008 x 4096, both directions of 333, 1024 and 4096
+    // rows: 247, 494 and 1540 us with at most eight, 239, 484 and 1524 with four, 238, 482 and 1527 with two)
+    pl.ga = choose_split(grid_blocks(K, 256) * (2 * pl.rp / 64), msteps, 4);
+    pl.gb = choose_split(2 * grid_blocks(N, 256) * (pl.rp / 64), msteps, 4);
   }
   return pl;
 }
