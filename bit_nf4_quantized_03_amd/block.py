@@ -258,6 +258,10 @@ def qlora_gated_bwd(dH, X, G, U, Hs, gate: NF4Weight, up: NF4Weight, Ag=None, Bg
     """(dX, dAg, dBg, dAu, dBu) from the gradient of H and what
     qlora_gated_fwd_save kept, with its arguments: dX bf16, the others in the
     adapters' type (None without adapters). The weights get no gradient."""
+    if ws is None and outs is None and (at := _fast_on(X)):
+        new = _fast.block_bwd(*at, dH, X, G, U, Hs, *_parts(gate), *_parts(up), Ag, Bg, Au, Bu, scale)
+        if new is not None:
+            return new
     M, N, K, r, index, sg, su, ad, dtype = _block_args(X, gate, up, Ag, Bg, Au, Bu, scale)
     ins = [_tensor(name, t, torch.bfloat16, (M, N), index) for name, t in (("dH", dH), ("G", G), ("U", U))]
     dX, *grads = (None,) * 5 if outs is None else outs

@@ -321,53 +321,96 @@ bool weight(PyObject *const *a, int dev, qlora_nf4_weight *w) {
   return w->absmax_q && w->dq_scale && w->dq_mean;
 }
 
-PyObject *block(PyObject *, PyObject *const *a, Py_ssize_t n) {   // X, gate's eight, up's eight, Ag, Bg, Au, Bu, scale, save
-  return guarded([&]() -> PyObject * {
-    if (n != 25) return none();
-    const int dev = static_cast<int>(PyLong_AsLong(a[0]));
-    const Tensor *x = tensor(a[2], at::kBFloat16, dev);
-    qlora_nf4_weight gate, up;
-    if (!x || x->dim() != 2 || x->numel() == 0 || !weight(a + 3, dev, &gate) || !weight(a + 11, dev, &up) || x->size(1) != gate.cols) return none();
-    const int64_t M = x->size(0), N = gate.rows, K = gate.cols;
-    qlora_gated_adapters ad{};
-    const bool adapts = a[19] != Py_None, save = a[24] == Py_True;
-    if (adapts) {
-      at::ScalarType type = at::kBFloat16;
-      ad.dtype = QLORA_BF16;
-      const Tensor *first = tensor(a[19], type, dev);
-      if (!first) type = at::kFloat, ad.dtype = QLORA_F32, first = tensor(a[19], type, dev);
-      if (!first || first->dim() != 2) return none();
-      const int64_t r = first->size(0);
-      const void **const to[4] = {&ad.gate_A, &ad.gate_B, &ad.up_A, &ad.up_B};
-      for (int i = 0; i < 4; ++i) {
-        const Tensor *t = tensor(a[19 + i], type, dev);
-        if (!t || !is(*t, i & 1 ? N : r, i & 1 ? r : K)) return none();
-        *to[i] = t->data_ptr();
-      }
-      if (r < 1 || r > 256) return none();
-      ad.r = static_cast<int32_t>(r);
-      ad.scale = static_cast<float>(PyFloat_AsDouble(a[23]));
-      if (PyErr_Occurred()) {
-        PyErr_Clear();
-        return none();
-      }
-    } else if (a[20] != Py_None || a[21] != Py_None || a[22] != Py_None) {
-      return none();
+// What the gated block's passes share: X, then from `a` on gate's eight, up's eight, Ag, Bg, Au, Bu, scale.
+struct Block {
+  const Tensor *x;
+  qlora_nf4_weight gate, up;
+  qlora_gated_adapters ad{};
+  int64_t M, N, K;
+  at::ScalarType type = at::kBFloat16;   // of the adapters
+  bool adapts;
+  bool read(PyObject *x_object, PyObject *const *a, int dev) {
+    x = tensor(x_object, at::kBFloat16, dev);
+    if (!x || x->dim() != 2 || x->numel() == 0 || !weight(a, dev, &gate) || !weight(a + 8, dev, &up) || x->size(1) != gate.cols) return false;
+    M = x->size(0), N = gate.rows, K = gate.cols;
+    PyObject *const *const factors = a + 16;
+    adapts = factors[0] != Py_None;
+    if (!adapts) return factors[1] == Py_None && factors[2] == Py_None && factors[3] == Py_None;
+    ad.dtype = QLORA_BF16;
+    const Tensor *first = tensor(factors[0], type, dev);
+    if (!first) type = at::kFloat, ad.dtype = QLORA_F32, first = tensor(factors[0], type, dev);
+    if (!first || first->dim() != 2) return false;
+    const int64_t r = first->size(0);
+    const void **const to[4] = {&ad.gate_A, &ad.gate_B, &ad.up_A, &ad.up_B};
+    for (int i = 0; i < 4; ++i) {
+      const Tensor *t = tensor(factors[i], type, dev);
+      if (!t || !is(*t, i & 1 ? N : r, i & 1 ? r : K)) return false;
+      *to[i] = t->data_ptr();
     }
+    if (r < 1 || r > 256) return false;
+    ad.r = static_cast<int32_t>(r);
+    ad.scale = static_cast<float>(PyFloat_AsDouble(factors[4]));
+    if (PyErr_Occurred()) {
+      PyErr_Clear();
+      return false;
+    }
+    return true;
+  }
+  const qlora_gated_adapters *adapters() const { return adapts ? &ad : nullptr; }
+  size_t workspace(bool backward, Tensor &ws) const {
+    const size_t size = qlora_gated_workspace_bytes(M, N, K, ad.r, backward);
+    if (size) ws = fresh(*x, {static_cast<int64_t>(size)}, at::kByte);
+    return size;
+  }
+};
+
+void *data(const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
+
+PyObject *block(PyObject *, PyObject *const *a, Py_ssize_t n) {   // X, gate, up, Ag, Bg, Au, Bu, scale, save
+  return guarded([&]() -> PyObject * {
+    Block p;
+    if (n != 25 || !p.read(a[2], a + 3, static_cast<int>(PyLong_AsLong(a[0])))) return none();
+    const bool save = a[24] == Py_True;
     void *stream = stream_of(a[1]);
     Tensor out[4], ws;
     const int status = unlocked([&] {
-      for (int i = 0; i < (save ? 3 : 1); ++i) out[i] = fresh(*x, {M, N}, at::kBFloat16);
-      if (save && adapts) out[3] = fresh(*x, {M, qlora_gated_saved_cols(ad.r)}, at::kBFloat16);
-      const size_t size = qlora_gated_workspace_bytes(M, N, K, ad.r, 0);
-      if (size) ws = fresh(*x, {static_cast<int64_t>(size)}, at::kByte);
-      const auto at = [](const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; };
-      return qlora_gated_fwd(x->data_ptr(), M, &gate, &up, adapts ? &ad : nullptr, at(out[0]), at(out[1]), at(out[2]), at(out[3]), at(ws), size, stream);
+      for (int i = 0; i < (save ? 3 : 1); ++i) out[i] = fresh(*p.x, {p.M, p.N}, at::kBFloat16);
+      if (save && p.adapts) out[3] = fresh(*p.x, {p.M, qlora_gated_saved_cols(p.ad.r)}, at::kBFloat16);
+      const size_t size = p.workspace(false, ws);
+      return qlora_gated_fwd(p.x->data_ptr(), p.M, &p.gate, &p.up, p.adapters(), data(out[0]), data(out[1]), data(out[2]), data(out[3]),
+                             data(ws), size, stream);
     });
     if (status != QLORA_OK) return none();
     if (!save) return wrap(std::move(out[0]));
-    PyObject *hs = adapts ? wrap(std::move(out[3])) : none();
+    PyObject *hs = p.adapts ? wrap(std::move(out[3])) : none();
     return pack({wrap(std::move(out[0])), wrap(std::move(out[1])), wrap(std::move(out[2])), hs});
+  });
+}
+
+PyObject *block_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {   // dH, X, G, U, Hs, gate, up, Ag, Bg, Au, Bu, scale
+  return guarded([&]() -> PyObject * {
+    Block p;
+    const int dev = n == 28 ? static_cast<int>(PyLong_AsLong(a[0])) : -1;
+    if (n != 28 || !p.read(a[3], a + 7, dev)) return none();
+    const Tensor *dh = tensor(a[2], at::kBFloat16, dev), *g = tensor(a[4], at::kBFloat16, dev), *u = tensor(a[5], at::kBFloat16, dev);
+    const Tensor *hs = p.adapts ? tensor(a[6], at::kBFloat16, dev) : nullptr;
+    if (!dh || !g || !u || !is(*dh, p.M, p.N) || !is(*g, p.M, p.N) || !is(*u, p.M, p.N)) return none();
+    if (p.adapts ? !hs || !is(*hs, p.M, qlora_gated_saved_cols(p.ad.r)) : a[6] != Py_None) return none();
+    void *stream = stream_of(a[1]);
+    Tensor out[5], ws;
+    const int status = unlocked([&] {
+      out[0] = fresh(*p.x, {p.M, p.K}, at::kBFloat16);
+      if (p.adapts)
+        for (int i = 0; i < 4; ++i) out[1 + i] = fresh(*p.x, {i & 1 ? p.N : p.ad.r, i & 1 ? p.ad.r : p.K}, p.type);
+      const size_t size = p.workspace(true, ws);
+      const qlora_gated_grads grads{data(out[1]), data(out[2]), data(out[3]), data(out[4])};
+      return qlora_gated_bwd(dh->data_ptr(), p.x->data_ptr(), g->data_ptr(), u->data_ptr(), hs ? hs->data_ptr() : nullptr, p.M, &p.gate, &p.up,
+                             p.adapters(), data(out[0]), p.adapts ? &grads : nullptr, data(ws), size, stream);
+    });
+    if (status != QLORA_OK) return none();
+    PyObject *grads[4];
+    for (int i = 0; i < 4; ++i) grads[i] = p.adapts ? wrap(std::move(out[1 + i])) : none();
+    return pack({wrap(std::move(out[0])), grads[0], grads[1], grads[2], grads[3]});
   });
 }
 
@@ -430,6 +473,7 @@ PyMethodDef methods[] = {
     {"linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(linear)), METH_FASTCALL, nullptr},
     {"gated", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(gated)), METH_FASTCALL, nullptr},
     {"block", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(block)), METH_FASTCALL, nullptr},
+    {"block_bwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(block_bwd)), METH_FASTCALL, nullptr},
     {"rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(rope)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -165,7 +165,9 @@ __global__ __launch_bounds__(256) void k_gated_prep(const PrepParams p) {
 // is for the same number of copies.
 struct DownParams {
   const void *P[2], *Q[2];
-  float *part;        // [splits][M][ld]
+  float *part;        // [splits][M][ld]; null: one split, out
+  __bf16 *out;        // [M][ld], scale times the sums
+  float scale;
   int64_t M, L;       // L: the reduction, row length of P and Q
   int rows;           // rows of each Q
   int ld;
@@ -208,7 +210,8 @@ __global__ __launch_bounds__(256, 1) void k_gated_down(const DownParams p) {
     mma_step<C>(acc, stage, stage + C::kLdsA, fa, fb);
   }
   RowsP::template wait_copies<0>();
-  store_f32<C>(acc, p.part + static_cast<int64_t>(z) * p.M * p.ld + w * p.rows, p.ld, p.M, p.rows, m0, j0);
+  if (p.part) store_f32<C>(acc, p.part + static_cast<int64_t>(z) * p.M * p.ld + w * p.rows, p.ld, p.M, p.rows, m0, j0);
+  else store_bf16<C, true>(acc, p.out + w * p.rows, p.ld, p.M, p.rows, m0, j0, p.scale);
 }
 
 // out = bf16(scale * the sum of the partials), four elements a lane: each of the
@@ -525,15 +528,23 @@ __global__ __launch_bounds__(kT, 1) void k_gated_dx(const DxParams p, const Nf4T
 // first, then 256 x 64 tiles of dG^T Hs_g and dU^T Hs_u.
 struct GradParams {
   const void *X, *d[2], *Hs, *low;
-  float *a_part, *b_part;   // [splits][2 rp][K], [splits][2][N][rp]
+  float *a_part, *b_part;   // [splits][2 rp][K], [splits][2][N][rp]; null: one split, the gradients
+  void *dA[2], *dB[2];
+  bool bf16;
   int64_t M, N, K;
-  int rp;
+  int r, rp;
   int a_tiles_c, a_tiles, a_splits, a_steps;
   int b_tiles_c, b_tiles, b_splits, b_steps;   // tiles: of one weight
 };
 
 using CfgGradA = TileCfg<64, 256, 1, 4>;
 using CfgGradB = TileCfg<256, 64, 4, 1>;
+
+template <class C>
+__device__ __forceinline__ void store_grad(const Acc<C> &acc, void *to, bool bf16, int64_t ld, int64_t rows, int64_t cols, int64_t m0, int64_t n0) {
+  if (bf16) store_bf16<C, true>(acc, static_cast<__bf16 *>(to), ld, rows, cols, m0, n0, 1.0f);
+  else store_f32<C>(acc, static_cast<float *>(to), ld, rows, cols, m0, n0);
+}
 
 __global__ __launch_bounds__(256) void k_gated_grad(const GradParams p) {
   __shared__ __attribute__((aligned(16))) __bf16 smem[2 * (CfgGradA::kLdsA + CfgGradA::kLdsB)];
@@ -555,7 +566,12 @@ __global__ __launch_bounds__(256) void k_gated_grad(const GradParams p) {
     TransBf16Narrow<64, 256> la(p.low, 2 * p.rp, red_end, r0), la1 = la;
     TransBf16<256, 256> lb(p.X, p.K, red_end, p.K, c0), lb1 = lb;
     mainloop2<CfgGradA>(acc, la, la1, lb, lb1, static_cast<int64_t>(s0) * kBK, steps, smem);
-    store_f32<CfgGradA>(acc, p.a_part + static_cast<int64_t>(z) * 2 * p.rp * p.K, p.K, 2 * p.rp, p.K, r0, c0);
+    if (p.a_part) {
+      store_f32<CfgGradA>(acc, p.a_part + static_cast<int64_t>(z) * 2 * p.rp * p.K, p.K, 2 * p.rp, p.K, r0, c0);
+    } else {
+      const int up = r0 >= p.rp;
+      store_grad<CfgGradA>(acc, up ? p.dA[1] : p.dA[0], p.bf16, p.K, p.r, p.K, r0 - up * p.rp, c0);
+    }
   } else {
     const int w = t >= p.b_tiles;
     t -= w * p.b_tiles;
@@ -565,12 +581,13 @@ __global__ __launch_bounds__(256) void k_gated_grad(const GradParams p) {
     TransBf16<256, 256> la(w ? p.d[1] : p.d[0], p.N, red_end, p.N, r0), la1 = la;
     TransBf16Narrow<64, 256> lb(p.Hs, 2 * p.rp, red_end, w * p.rp + c0), lb1 = lb;
     mainloop2<CfgGradB>(acc, la, la1, lb, lb1, static_cast<int64_t>(s0) * kBK, steps, smem);
-    store_f32<CfgGradB>(acc, p.b_part + (2 * static_cast<int64_t>(z) + w) * p.N * p.rp, p.rp, p.N, p.rp, r0, c0);
+    if (p.b_part) store_f32<CfgGradB>(acc, p.b_part + (2 * static_cast<int64_t>(z) + w) * p.N * p.rp, p.rp, p.N, p.rp, r0, c0);
+    else store_grad<CfgGradB>(acc, w ? p.dB[1] : p.dB[0], p.bf16, p.r, p.N, p.r, r0, c0);
   }
 }
 
 struct GradSumParams {
-  const float *a_part, *b_part;
+  const float *a_part, *b_part;   // null: nothing to add
   void *dA[2], *dB[2];
   bool bf16;
   int64_t N, K;
@@ -578,7 +595,7 @@ struct GradSumParams {
 };
 
 __global__ __launch_bounds__(256) void k_gated_grad_sum(const GradSumParams p) {
-  const int64_t na = p.r * p.K, nb = p.N * p.r, n = 2 * (na + nb);
+  const int64_t na = p.a_part ? p.r * p.K : 0, nb = p.b_part ? p.N * p.r : 0, n = 2 * (na + nb);
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
     float v;
     void *to;
@@ -617,7 +634,13 @@ __global__ __launch_bounds__(256) void k_gated_dx_sum(const DxParams p) {
 
 // Splits of the adapters' down products at most (11008 x 4096, both directions,
 // 333 and 64 rows: 253 and 142 us with 64, 249 and 141 with 32, 247 and 143 with 16).
-constexpr int kDownSplits = 32;
+// Up to kDownSteps steps are one split, which needs no sum behind (200 rows of 1024 x 1024, both directions: 69.4 us
+// split, 74.2 so).
+constexpr int kDownSplits = 32, kDownSteps = 4;
+Split down_split(int64_t tiles, int steps) { return choose_split(tiles, steps, steps <= kDownSteps ? 1 : kDownSplits, kCus); }
+// The same of the adapters' gradients (11008 x 4096, both directions: 64 rows 141 us split, 131 so; 333 rows 239 and
+// 234; but 800 rows of 2048 x 2048 127 and 134).
+constexpr int kGradSteps = 8;
 
 struct Plan {
   int rp;
@@ -669,17 +692,17 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int r, bool backward) {
   pl.rp = gated_padded_rank(r);
   if (!backward) {
     pl.tail = make_tail(M, grid_blocks(N, 128), static_cast<int>(K / kBK));
-    if (r) pl.down = choose_split(grid_blocks(M, 128) * (2 * pl.rp / 128), static_cast<int>(K / kBK), kDownSplits, kCus);
+    if (r) pl.down = down_split(grid_blocks(M, 128) * (2 * pl.rp / 128), static_cast<int>(K / kBK));
     return pl;
   }
   pl.tail = make_tail(M, grid_blocks(K, 256), static_cast<int>(2 * N / kBK));
   if (r) {
-    pl.down = choose_split(grid_blocks(M, 128) * 2 * (pl.rp / 64), static_cast<int>(N / kBK), kDownSplits, kCus);
+    pl.down = down_split(grid_blocks(M, 128) * 2 * (pl.rp / 64), static_cast<int>(N / kBK));
     const int msteps = static_cast<int>(ceil_div(M, kBK));
     // more splits cost more to write and add than they spread (11008 x 4096, both directions of 333, 1024 and 4096
     // rows: 247, 494 and 1540 us with at most eight, 239, 484 and 1524 with four, 238, 482 and 1527 with two)
-    pl.ga = choose_split(grid_blocks(K, 256) * (2 * pl.rp / 64), msteps, 4);
-    pl.gb = choose_split(2 * grid_blocks(N, 256) * (pl.rp / 64), msteps, 4);
+    pl.ga = choose_split(grid_blocks(K, 256) * (2 * pl.rp / 64), msteps, msteps <= kGradSteps ? 1 : 4);
+    pl.gb = choose_split(2 * grid_blocks(N, 256) * (pl.rp / 64), msteps, msteps <= kGradSteps ? 1 : 4);
   }
   return pl;
 }
@@ -700,7 +723,7 @@ size_t carve(void *ws, Plan &pl, int64_t M, int64_t N, int64_t K, bool backward,
   b->cs[1] = c.take<float>(nb);
   if (pl.tail.rest) pl.tail.part = c.take<float>(static_cast<size_t>(pl.tail.S) * pl.tail.rest * 256 * pl.tail.bm);
   const size_t cols = 2 * static_cast<size_t>(pl.rp);
-  if (pl.rp) b->down = c.take<float>(pl.down.splits * M * cols);
+  if (pl.rp && pl.down.splits > 1) b->down = c.take<float>(pl.down.splits * M * cols);
   if (!backward) {
     if (pl.rp) {
       b->Acat = c.take<__bf16>(cols * K);
@@ -715,8 +738,8 @@ size_t carve(void *ws, Plan &pl, int64_t M, int64_t N, int64_t K, bool backward,
     b->At = c.take<__bf16>(cols * K);
     b->Bt = c.take<__bf16>(cols * N);
     b->low = c.take<__bf16>(cols * M);
-    b->ga = c.take<float>(pl.ga.splits * cols * K);
-    b->gb = c.take<float>(pl.gb.splits * cols * N);
+    if (pl.ga.splits > 1) b->ga = c.take<float>(pl.ga.splits * cols * K);
+    if (pl.gb.splits > 1) b->gb = c.take<float>(pl.gb.splits * cols * N);
   }
   return c.off;
 }
@@ -772,6 +795,8 @@ hipError_t launch_gated_fwd(const GatedArgs &a, const void *X, void *H, void *G,
     d.P[0] = X;
     d.Q[0] = b.Acat;
     d.part = b.down;
+    d.out = b.Hs;
+    d.scale = a.scale;
     d.M = a.M;
     d.L = a.K;
     d.rows = d.ld = 2 * pl.rp;
@@ -782,7 +807,7 @@ hipError_t launch_gated_fwd(const GatedArgs &a, const void *X, void *H, void *G,
     d.per = pl.down.steps_per_split;
     k_gated_down<128><<<static_cast<unsigned>(d.tiles * pl.down.splits), 256, 0, s>>>(d);
     const int64_t n = a.M * 2 * pl.rp;
-    k_gated_sum<<<static_cast<unsigned>(std::min(ceil_div(n, 256), kSumGroups)), 256, 0, s>>>(b.down, pl.down.splits, n, a.scale, b.Hs);
+    if (b.down) k_gated_sum<<<static_cast<unsigned>(std::min(ceil_div(n, 256), kSumGroups)), 256, 0, s>>>(b.down, pl.down.splits, n, a.scale, b.Hs);
   }
   FwdParams p{X, {a.w[0].codes, a.w[1].codes}, {scales(a, b, 0), scales(a, b, 1)}, b.Hs, b.Bi, static_cast<__bf16 *>(H),
               static_cast<__bf16 *>(G), static_cast<__bf16 *>(U), a.M, a.N, a.K, pl.rp, pl.tail};
@@ -813,6 +838,8 @@ hipError_t launch_gated_bwd(const GatedArgs &a, const void *dH, const void *X, c
     d.Q[0] = b.Bt;
     d.Q[1] = b.Bt + pl.rp * a.N;
     d.part = b.down;
+    d.out = b.low;
+    d.scale = a.scale;
     d.M = a.M;
     d.L = a.N;
     d.rows = pl.rp;
@@ -824,7 +851,7 @@ hipError_t launch_gated_bwd(const GatedArgs &a, const void *dH, const void *X, c
     d.per = pl.down.steps_per_split;
     k_gated_down<64><<<static_cast<unsigned>(d.tiles * pl.down.splits), 256, 0, s>>>(d);
     const int64_t count = a.M * 2 * pl.rp;
-    k_gated_sum<<<static_cast<unsigned>(std::min(ceil_div(count, 256), kSumGroups)), 256, 0, s>>>(b.down, pl.down.splits, count, a.scale, b.low);
+    if (b.down) k_gated_sum<<<static_cast<unsigned>(std::min(ceil_div(count, 256), kSumGroups)), 256, 0, s>>>(b.down, pl.down.splits, count, a.scale, b.low);
   }
   DxParams p{b.dG, b.dU, {a.w[0].codes, a.w[1].codes}, {scales(a, b, 0), scales(a, b, 1)}, b.low, b.At, dX, a.M, a.N, a.K,
              pl.rp, pl.tail};
@@ -847,6 +874,9 @@ hipError_t launch_gated_bwd(const GatedArgs &a, const void *dH, const void *X, c
     g.low = b.low;
     g.a_part = b.ga;
     g.b_part = b.gb;
+    for (int w = 0; w < 2; ++w) g.dA[w] = dA[w], g.dB[w] = dB[w];
+    g.bf16 = a.adapter_bf16;
+    g.r = a.r;
     g.M = a.M;
     g.N = a.N;
     g.K = a.K;
@@ -860,8 +890,9 @@ hipError_t launch_gated_bwd(const GatedArgs &a, const void *dH, const void *X, c
     g.b_splits = pl.gb.splits;
     g.b_steps = pl.gb.steps_per_split;
     k_gated_grad<<<static_cast<unsigned>(g.a_tiles * g.a_splits + 2 * g.b_tiles * g.b_splits), 256, 0, s>>>(g);
+    if (!b.ga && !b.gb) return hipGetLastError();
     const GradSumParams q{b.ga, b.gb, {dA[0], dA[1]}, {dB[0], dB[1]}, a.adapter_bf16, a.N, a.K, a.r, pl.rp, pl.ga.splits, pl.gb.splits};
-    const int64_t count = 2 * a.r * (a.N + a.K);
+    const int64_t count = 2 * a.r * ((b.gb ? a.N : 0) + (b.ga ? a.K : 0));
     k_gated_grad_sum<<<static_cast<unsigned>(std::min<int64_t>(ceil_div(count, 256), 4096)), 256, 0, s>>>(q);
   }
   return hipGetLastError();

@@ -524,7 +524,8 @@ def test_calls_without_fastcall(qb, monkeypatch):
     def calls():
         out = []
         for d, args in blocks:
-            out += [qb.qlora_gated_fwd(d.X, *args), *qb.qlora_gated_fwd_save(d.X, *args)]
+            kept = qb.qlora_gated_fwd_save(d.X, *args)
+            out += [qb.qlora_gated_fwd(d.X, *args), *kept, *qb.qlora_gated_bwd(d.dH, d.X, *kept[1:], *args)]
         for o in (None, 0, 1):
             h = qb.qlora_mx_gated(X, W, mx=o)
             out += [h] if o is None else [h.codes, h.scales]
