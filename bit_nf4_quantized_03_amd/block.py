@@ -131,6 +131,10 @@ def qlora_mx_gated_grouped(X: MXMatrix, W: MXMatrix, offsets, mx: Optional[int] 
     [experts * 2 N, K] the experts' pairs one below the other, offsets int32
     [experts + 1] on the device. Rows that no expert has are left as they were
     (zero in a new H)."""
+    if out is None and (at := _fast_on(X.codes)):
+        new = _fast.gated(*at, X.codes, X.scales, X.rows, X.cols, X.mx, W.codes, W.scales, W.rows, W.cols, W.mx, mx, offsets)
+        if new is not None:
+            return new if mx is None else MXMatrix(X.rows, W.rows // 2 // (offsets.shape[0] - 1), *new, mx)
     sx = X.c_struct("X")
     index = X.codes.get_device()
     sw = W.c_struct("W", index)

@@ -266,27 +266,38 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n) {   // X's five, 
   });
 }
 
-PyObject *gated(PyObject *, PyObject *const *a, Py_ssize_t n) {   // X's five, W's five, type of H or None
+PyObject *gated(PyObject *, PyObject *const *a, Py_ssize_t n) {   // X's five, W's five, type of H or None[, offsets]
   return guarded([&]() -> PyObject * {
-    if (n != 13) return none();
+    if (n != 13 && n != 14) return none();
     const int dev = static_cast<int>(PyLong_AsLong(a[0]));
     qlora_mx_matrix x, w;
-    const Tensor *xc, *wc;
-    if (!matrix(a + 2, dev, &x, &xc) || !matrix(a + 7, dev, &w, &wc) || x.cols != w.cols || w.rows % (2 * QLORA_MX_BLOCK) != 0) return none();
+    const Tensor *xc, *wc, *offsets = nullptr;
+    if (!matrix(a + 2, dev, &x, &xc) || !matrix(a + 7, dev, &w, &wc) || x.cols != w.cols) return none();
+    int64_t experts = 1;
+    if (n == 14) {
+      offsets = tensor(a[13], at::kInt, dev);
+      if (!offsets || offsets->dim() != 1 || offsets->size(0) < 2 || offsets->size(0) > QLORA_MX_EXPERTS + 1) return none();
+      experts = offsets->size(0) - 1;
+    }
+    if (w.rows % (2 * QLORA_MX_BLOCK * experts) != 0) return none();
+    const int64_t cols = w.rows / experts / 2;
     const bool plain = a[12] == Py_None;
     const long mx = plain ? 0 : PyLong_AsLong(a[12]);
     if (PyErr_Occurred()) {
       PyErr_Clear();
       return none();
     }
-    if (!valid(x.rows, w.rows / 2, mx)) return none();
+    if (!valid(x.rows, cols, mx)) return none();
     void *stream = stream_of(a[1]);
     Tensor h;
     std::optional<NewMatrix> q;
     const int status = unlocked([&] {
-      if (plain) h = fresh(*xc, {x.rows, w.rows / 2}, at::kBFloat16);
-      else q.emplace(*xc, x.rows, w.rows / 2, mx);
-      return qlora_mx_gated(&x, &w, plain ? h.data_ptr() : nullptr, plain ? nullptr : &q->m, stream);
+      if (plain) h = fresh(*xc, {x.rows, cols}, at::kBFloat16);
+      else q.emplace(*xc, x.rows, cols, mx);
+      void *const to = plain ? h.data_ptr() : nullptr;
+      const qlora_mx_matrix *const hq = plain ? nullptr : &q->m;
+      if (!offsets) return qlora_mx_gated(&x, &w, to, hq, stream);
+      return qlora_mx_gated_grouped(&x, &w, static_cast<const int32_t *>(offsets->data_ptr()), static_cast<int32_t>(experts), to, hq, 1, stream);
     });
     if (status != QLORA_OK) return none();
     return plain ? wrap(std::move(h)) : pack({wrap(std::move(q->codes)), wrap(std::move(q->scales))});

@@ -528,7 +528,8 @@ def test_calls_without_fastcall(qb, monkeypatch):
             out += [qb.qlora_gated_fwd(d.X, *args), *kept, *qb.qlora_gated_bwd(d.dH, d.X, *kept[1:], *args)]
         for o in (None, 0, 1):
             h = qb.qlora_mx_gated(X, W, mx=o)
-            out += [h] if o is None else [h.codes, h.scales]
+            e = qb.qlora_mx_gated_grouped(X, W, torch.tensor([1, 3, 4], dtype=torch.int32, device="cuda"), mx=o)
+            out += [h, e] if o is None else [h.codes, h.scales, e.codes, e.scales]
         for t in (fused, fused.bfloat16()):
             for p in (pos, pos.int()):
                 out += [*qb.qlora_rope_fwd(t[:, :4], t[:, 4:], p, freqs), *qb.qlora_rope_bwd(t, None, p, freqs, 1.5, True)]
