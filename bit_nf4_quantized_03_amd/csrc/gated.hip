@@ -24,6 +24,7 @@
 //   k_gated_dx     dX = [dG, dU, l] [Wg; Wu; [Ag; Au]]: one reduction over both
 //                  weights, so dX is rounded and written once
 //   k_gated_dx_sum sums the tiles whose reduction was split
+//   k_gated_few_low, k_gated_few_grad   instead of k_gated_down and the next two, for few sums
 //   k_gated_grad, k_gated_grad_sum   split-M partials of the adapters' gradients and their sums
 //
 // Roundings to bf16, the operand type of the matrix instructions: the decoded
@@ -214,12 +215,12 @@ __global__ __launch_bounds__(256, 1) void k_gated_down(const DownParams p) {
   else store_bf16<C, true>(acc, p.out + w * p.rows, p.ld, p.M, p.rows, m0, j0, p.scale);
 }
 
-// out = bf16(scale * the sum of the partials), four elements a lane: each of the
+// out = bf16(scale * the sum of the partials), and `wide` the unrounded ones where it is not null, four elements a lane: each of the
 // four waves adds a quarter of the splits in order, then the quarters are added
 // (64 rows of 11008 x 4096 with r = 64: the forward takes 72 us with one wave
 // for all splits, 68 so).
 constexpr int64_t kSumGroups = int64_t(1) << 20;
-__global__ __launch_bounds__(256) void k_gated_sum(const float *part, int splits, int64_t n, float scale, __bf16 *out) {
+__global__ __launch_bounds__(256) void k_gated_sum(const float *part, int splits, int64_t n, float scale, __bf16 *out, float *wide) {
   __shared__ float4 sums[3][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, per = (splits + 3) / 4, z0 = wave * per;
   for (int64_t e0 = static_cast<int64_t>(blockIdx.x) * 256; e0 < n; e0 += static_cast<int64_t>(gridDim.x) * 256) {
@@ -235,7 +236,9 @@ __global__ __launch_bounds__(256) void k_gated_sum(const float *part, int splits
       const float4 s = sums[w][lane];
       v.x += s.x, v.y += s.y, v.z += s.z, v.w += s.w;
     }
-    *reinterpret_cast<uint2 *>(out + e) = make_uint2(pack_bf16x2(scale * v.x, scale * v.y), pack_bf16x2(scale * v.z, scale * v.w));
+    v = make_float4(scale * v.x, scale * v.y, scale * v.z, scale * v.w);
+    *reinterpret_cast<uint2 *>(out + e) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    if (wide) *reinterpret_cast<float4 *>(wide + e) = v;
   }
 }
 
@@ -618,6 +621,110 @@ __global__ __launch_bounds__(256) void k_gated_grad_sum(const GradSumParams p) {
   }
 }
 
+// A's gradient passes through the M r sums l. Where these are few their roundings
+// do not even out (1 row, r = 8: dA off by up to 6e-3 with dG and l rounded to
+// bf16 on their way, 4e-3 so), and dG, dU and l stay fp32 in products without
+// matrix instructions. Both directions, so and with matrix instructions: 4 rows of
+// 1024 x 1024, r = 8, 33 and 38 us; 8 rows of 4096 x 4096, r = 8, 64 and 66; 1 row of
+// 11008 x 4096, r = 64, 78 and 78; 16 rows, r = 4, 98 and 95; but 32 rows, r = 64,
+// 233 and 115.
+struct FewParams {
+  const __bf16 *dH, *G, *U, *X, *Hs;
+  const void *B[2];
+  void *dA[2], *dB[2];
+  bool bf16;
+  int64_t N, K, per;   // columns of a split
+  int M, r, rp;
+  float *part;         // [splits][M][2 rp]
+  const float *low;    // [M][2 rp]
+};
+__device__ __forceinline__ void few_gate(const FewParams &p, int64_t at, float &dg, float &du) {
+  gate_backward(static_cast<float>(p.dH[at]), static_cast<float>(p.G[at]), static_cast<float>(p.U[at]), dg, du);
+}
+
+// Split sums of dG Bg and dU Bu: a row of one of them and `per` columns n a
+// workgroup, 256 at a time; a thread has column j of B and every (256 / J)-th n.
+__global__ __launch_bounds__(256) void k_gated_few_low(const FewParams p) {
+  __shared__ float d[256], sums[256];
+  const int m = static_cast<int>(blockIdx.x) >> 1, w = static_cast<int>(blockIdx.x) & 1, tid = threadIdx.x;
+  int J = 4;
+  while (J < p.r) J *= 2;
+  const int j = tid & (J - 1), slice = tid / J, slices = 256 / J;
+  const int64_t n0 = blockIdx.y * p.per, n1 = min(p.N, n0 + p.per);
+  const void *const B = w ? p.B[1] : p.B[0];
+  float acc = 0.0f;
+  for (int64_t base = n0; base < n1; base += 256) {
+    float dg = 0.0f, du = 0.0f;
+    if (base + tid < n1) few_gate(p, m * p.N + base + tid, dg, du);
+    __syncthreads();   // the turn before is done
+    d[tid] = w ? du : dg;
+    __syncthreads();
+    const int count = static_cast<int>(min(n1 - base, int64_t(256)));
+    if (j < p.r)
+#pragma unroll 8
+      for (int i = slice; i < count; i += slices) acc = fmaf(d[i], adapter_at(B, p.bf16, (base + i) * p.r + j), acc);
+  }
+  sums[tid] = acc;
+  __syncthreads();
+  if (tid >= p.rp) return;
+  float v = 0.0f;
+  if (tid < p.r)
+    for (int s = 0; s < slices; ++s) v += sums[s * J + tid];
+  p.part[(static_cast<int64_t>(blockIdx.y) * p.M + m) * 2 * p.rp + w * p.rp + tid] = v;
+}
+
+// dA = l^T X, eight columns a thread, then dB = dG^T Hs, eight columns of both a thread.
+__global__ __launch_bounds__(256) void k_gated_few_grad(const FewParams p) {
+  const int64_t k8 = p.K / 8, na = 2 * p.r * k8;
+  const int octets = (p.r + 7) / 8;
+  int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i < na) {
+    const int w = i >= na / 2;
+    i -= w ? na / 2 : 0;
+    const int j = static_cast<int>(i / k8);
+    const int64_t k = 8 * (i - j * k8);
+    float v[8] = {};
+    for (int m = 0; m < p.M; ++m) {
+      const float l = p.low[static_cast<int64_t>(m) * 2 * p.rp + w * p.rp + j];
+      const bf16x8 x = *reinterpret_cast<const bf16x8 *>(p.X + m * p.K + k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = fmaf(l, static_cast<float>(x[e]), v[e]);
+    }
+    if (p.bf16) {
+      put8(static_cast<__bf16 *>(w ? p.dA[1] : p.dA[0]) + j * p.K + k, v);
+    } else {
+      float *const to = static_cast<float *>(w ? p.dA[1] : p.dA[0]) + j * p.K + k;
+      *reinterpret_cast<float4 *>(to) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4 *>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    return;
+  }
+  i -= na;
+  if (i >= p.N * octets) return;
+  const int64_t n = i / octets;
+  const int j0 = 8 * static_cast<int>(i - n * octets);
+  float v[2][8] = {};
+  for (int m = 0; m < p.M; ++m) {
+    float d[2];
+    few_gate(p, m * p.N + n, d[0], d[1]);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const bf16x8 h = *reinterpret_cast<const bf16x8 *>(p.Hs + static_cast<int64_t>(m) * 2 * p.rp + w * p.rp + j0);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[w][e] = fmaf(d[w], static_cast<float>(h[e]), v[w][e]);
+    }
+  }
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (j0 + e >= p.r) continue;
+      void *const to = w ? p.dB[1] : p.dB[0];
+      if (p.bf16) static_cast<__bf16 *>(to)[n * p.r + j0 + e] = static_cast<__bf16>(v[w][e]);
+      else static_cast<float *>(to)[n * p.r + j0 + e] = v[w][e];
+    }
+}
+
 // dX of the split tiles, four columns a lane, BM / 4 workgroups a tile.
 __global__ __launch_bounds__(256) void k_gated_dx_sum(const DxParams p) {
   const int bm = p.tail.bm, i = static_cast<int>(blockIdx.x) / (bm / 4), at = (static_cast<int>(blockIdx.x) - i * (bm / 4)) * 256 + static_cast<int>(threadIdx.x);
@@ -687,6 +794,10 @@ Tail make_tail(int64_t M, int64_t tiles_n, int steps) {
   return best;
 }
 
+// Whether the adapters' gradients take the kernels for few sums.
+constexpr int64_t kFewRows = 16, kFewSums = 64;
+bool few_sums(int64_t M, int r) { return r > 0 && M <= kFewRows && M * r <= kFewSums; }
+
 Plan make_plan(int64_t M, int64_t N, int64_t K, int r, bool backward) {
   Plan pl{};
   pl.rp = gated_padded_rank(r);
@@ -696,7 +807,11 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int r, bool backward) {
     return pl;
   }
   pl.tail = make_tail(M, grid_blocks(K, 256), static_cast<int>(2 * N / kBK));
-  if (r) {
+  if (few_sums(M, r)) {   // splits and columns of k_gated_few_low
+    const int64_t turns = ceil_div(N, 64), splits = std::min(turns, kCus / M);
+    pl.down.steps_per_split = static_cast<int>(64 * ceil_div(turns, splits));
+    pl.down.splits = static_cast<int>(ceil_div(N, pl.down.steps_per_split));
+  } else if (r) {
     pl.down = down_split(grid_blocks(M, 128) * 2 * (pl.rp / 64), static_cast<int>(N / kBK));
     const int msteps = static_cast<int>(ceil_div(M, kBK));
     // more splits cost more to write and add than they spread (11008 x 4096, both directions of 333, 1024 and 4096
@@ -708,11 +823,11 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int r, bool backward) {
 }
 
 struct Buffers {
-  float *cs[2], *down, *ga, *gb;
+  float *cs[2], *down, *wide, *ga, *gb;
   __bf16 *Acat, *Bi, *At, *Bt, *low, *dG, *dU, *Hs;
 };
 
-size_t carve(void *ws, Plan &pl, int64_t M, int64_t N, int64_t K, bool backward, Buffers *b) {
+size_t carve(void *ws, Plan &pl, int64_t M, int64_t N, int64_t K, int r, bool backward, Buffers *b) {
   Carve c{static_cast<char *>(ws)};
   if (!backward && M <= kGatedStreamRows) {
     if (pl.rp) b->Hs = c.take<__bf16>(2 * static_cast<size_t>(pl.rp) * M);
@@ -723,7 +838,8 @@ size_t carve(void *ws, Plan &pl, int64_t M, int64_t N, int64_t K, bool backward,
   b->cs[1] = c.take<float>(nb);
   if (pl.tail.rest) pl.tail.part = c.take<float>(static_cast<size_t>(pl.tail.S) * pl.tail.rest * 256 * pl.tail.bm);
   const size_t cols = 2 * static_cast<size_t>(pl.rp);
-  if (pl.rp && pl.down.splits > 1) b->down = c.take<float>(pl.down.splits * M * cols);
+  const bool few = backward && few_sums(M, r);
+  if (pl.rp && (few || pl.down.splits > 1)) b->down = c.take<float>(pl.down.splits * M * cols);
   if (!backward) {
     if (pl.rp) {
       b->Acat = c.take<__bf16>(cols * K);
@@ -736,8 +852,12 @@ size_t carve(void *ws, Plan &pl, int64_t M, int64_t N, int64_t K, bool backward,
   b->dU = c.take<__bf16>(static_cast<size_t>(M) * N);
   if (pl.rp) {
     b->At = c.take<__bf16>(cols * K);
-    b->Bt = c.take<__bf16>(cols * N);
     b->low = c.take<__bf16>(cols * M);
+    if (few) {
+      b->wide = c.take<float>(cols * M);
+      return c.off;
+    }
+    b->Bt = c.take<__bf16>(cols * N);
     if (pl.ga.splits > 1) b->ga = c.take<float>(pl.ga.splits * cols * K);
     if (pl.gb.splits > 1) b->gb = c.take<float>(pl.gb.splits * cols * N);
   }
@@ -767,7 +887,7 @@ void run_prep(const GatedArgs &a, const Plan &pl, const Buffers &b, bool backwar
   p.g_cs = fmt_dq(a.format) ? ceil_div(2 * p.nb, 1024) : 0;
   if (pl.rp) {
     p.g_a = ceil_div(2 * pl.rp * a.K / 8, 256);
-    p.g_b = ceil_div(2 * pl.rp * a.N / 8, 256);
+    if (!backward || b.Bt) p.g_b = ceil_div(2 * pl.rp * a.N / 8, 256);
   }
   const int64_t groups = act.groups + p.g_cs + p.g_a + p.g_b;
   if (groups > 0) k_gated_prep<<<static_cast<unsigned>(groups), 256, 0, s>>>(p);
@@ -780,13 +900,13 @@ const float *scales(const GatedArgs &a, const Buffers &b, int w) { return fmt_dq
 size_t gated_ws_bytes(int64_t M, int64_t N, int64_t K, int r, bool backward) {
   Plan pl = make_plan(M, N, K, r, backward);
   Buffers b{};
-  return carve(nullptr, pl, M, N, K, backward, &b);
+  return carve(nullptr, pl, M, N, K, r, backward, &b);
 }
 
 hipError_t launch_gated_fwd(const GatedArgs &a, const void *X, void *H, void *G, void *U, void *Hs, void *ws, hipStream_t s) {
   Plan pl = make_plan(a.M, a.N, a.K, a.r, false);
   Buffers b{};
-  carve(ws, pl, a.M, a.N, a.K, false, &b);
+  carve(ws, pl, a.M, a.N, a.K, a.r, false, &b);
   if (Hs) b.Hs = static_cast<__bf16 *>(Hs);
   if (a.M <= kGatedStreamRows) return launch_gated_stream(a, X, H, G, U, b.Hs, s);
   run_prep(a, pl, b, false, ActParams{}, s);
@@ -807,7 +927,7 @@ hipError_t launch_gated_fwd(const GatedArgs &a, const void *X, void *H, void *G,
     d.per = pl.down.steps_per_split;
     k_gated_down<128><<<static_cast<unsigned>(d.tiles * pl.down.splits), 256, 0, s>>>(d);
     const int64_t n = a.M * 2 * pl.rp;
-    if (b.down) k_gated_sum<<<static_cast<unsigned>(std::min(ceil_div(n, 256), kSumGroups)), 256, 0, s>>>(b.down, pl.down.splits, n, a.scale, b.Hs);
+    if (b.down) k_gated_sum<<<static_cast<unsigned>(std::min(ceil_div(n, 256), kSumGroups)), 256, 0, s>>>(b.down, pl.down.splits, n, a.scale, b.Hs, nullptr);
   }
   FwdParams p{X, {a.w[0].codes, a.w[1].codes}, {scales(a, b, 0), scales(a, b, 1)}, b.Hs, b.Bi, static_cast<__bf16 *>(H),
               static_cast<__bf16 *>(G), static_cast<__bf16 *>(U), a.M, a.N, a.K, pl.rp, pl.tail};
@@ -828,10 +948,19 @@ hipError_t launch_gated_bwd(const GatedArgs &a, const void *dH, const void *X, c
                             void *dX, void *const (&dA)[2], void *const (&dB)[2], void *ws, hipStream_t s) {
   Plan pl = make_plan(a.M, a.N, a.K, a.r, true);
   Buffers b{};
-  carve(ws, pl, a.M, a.N, a.K, true, &b);
+  carve(ws, pl, a.M, a.N, a.K, a.r, true, &b);
   const int64_t n = a.M * a.N;
   run_prep(a, pl, b, true, ActParams{dH, G, U, b.dG, b.dU, n, std::min(ceil_div(n, 2048), kActGroups)}, s);
-  if (pl.rp) {
+  const bool few = few_sums(a.M, a.r);
+  FewParams fp{};
+  if (few) {
+    const auto in = [](const void *p) { return static_cast<const __bf16 *>(p); };
+    fp = {in(dH), in(G), in(U), in(X), in(Hs), {a.B[0], a.B[1]}, {dA[0], dA[1]}, {dB[0], dB[1]}, a.adapter_bf16, a.N, a.K,
+          pl.down.steps_per_split, static_cast<int>(a.M), a.r, pl.rp, b.down, b.wide};
+    k_gated_few_low<<<dim3(static_cast<unsigned>(2 * a.M), static_cast<unsigned>(pl.down.splits)), 256, 0, s>>>(fp);
+    const int64_t count = a.M * 2 * pl.rp;
+    k_gated_sum<<<static_cast<unsigned>(ceil_div(count, 256)), 256, 0, s>>>(b.down, pl.down.splits, count, a.scale, b.low, b.wide);
+  } else if (pl.rp) {
     DownParams d{};
     d.P[0] = b.dG;
     d.P[1] = b.dU;
@@ -851,7 +980,7 @@ hipError_t launch_gated_bwd(const GatedArgs &a, const void *dH, const void *X, c
     d.per = pl.down.steps_per_split;
     k_gated_down<64><<<static_cast<unsigned>(d.tiles * pl.down.splits), 256, 0, s>>>(d);
     const int64_t count = a.M * 2 * pl.rp;
-    if (b.down) k_gated_sum<<<static_cast<unsigned>(std::min(ceil_div(count, 256), kSumGroups)), 256, 0, s>>>(b.down, pl.down.splits, count, a.scale, b.low);
+    if (b.down) k_gated_sum<<<static_cast<unsigned>(std::min(ceil_div(count, 256), kSumGroups)), 256, 0, s>>>(b.down, pl.down.splits, count, a.scale, b.low, nullptr);
   }
   DxParams p{b.dG, b.dU, {a.w[0].codes, a.w[1].codes}, {scales(a, b, 0), scales(a, b, 1)}, b.low, b.At, dX, a.M, a.N, a.K,
              pl.rp, pl.tail};
@@ -865,7 +994,10 @@ hipError_t launch_gated_bwd(const GatedArgs &a, const void *dH, const void *X, c
     default: run(k_gated_dx<256>); break;
   }
   if (pl.tail.rest) k_gated_dx_sum<<<static_cast<unsigned>(pl.tail.bm / 4 * pl.tail.rest), 256, 0, s>>>(p);
-  if (pl.rp) {
+  if (few) {
+    const int64_t threads = 2 * a.r * (a.K / 8) + a.N * ((a.r + 7) / 8);
+    k_gated_few_grad<<<static_cast<unsigned>(ceil_div(threads, 256)), 256, 0, s>>>(fp);
+  } else if (pl.rp) {
     GradParams g{};
     g.X = X;
     g.d[0] = b.dG;

@@ -111,8 +111,9 @@ typedef struct {
  *     dAg = lg^T X,  dBg = dG^T Hs_g,  dAu = lu^T X,  dBu = dU^T Hs_u
  * dH, dX bf16. No output overlaps an input, another output or the workspace.
  * grads NULL without adapters.
- * dG, dU, lg and lu are rounded to bf16, each sum is fp32 in a fixed order and
- * rounded once.
+ * dG, dU, lg and lu are rounded to bf16 (for the adapters' gradients not where
+ * there are few of lg and lu, M <= 16 and M r <= 64), each sum is fp32 in a fixed
+ * order and rounded once.
  */
 int qlora_gated_bwd(const void *dH, const void *X, const void *G, const void *U, const void *Hs, int64_t M,
                     const qlora_nf4_weight *gate, const qlora_nf4_weight *up, const qlora_gated_adapters *adapters,

@@ -572,3 +572,27 @@ def test_most_rows_and_past_32_bits(qb, M, N, K, r):
     # sums over N and over the rows differ in their order: both are the oracle's within its bars, 7e-3 each
     for a, b, label in zip(few, (many[0][-300:], *many[1:]), GRADS):
         near(b, f64(a), 1.4e-2, label)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("M,N,K,r", [(1, 192, 256, 8), (3, 128, 320, 5), (16, 192, 64, 4), (1, 128, 128, 64), (2, 64, 192, 32), (1, 256, 64, 1)])
+def test_few_sums_are_not_rounded(qb, M, N, K, r, bf16):
+    """Gradients of few sums l = s dG B, from the kept G, U and Hs: dG, B and l unrounded, so that only fp32 is left. dG's
+    arithmetic is off by 2^-19 of |dH U| (1 + |G|) (test_gpu_mx_gated.py, with the derivative's four more operations), dU's
+    of |dH G|, a sum of n terms by n 2^-24 of its terms' sizes, and a bf16 gradient by half a step of its own."""
+    gu.announce(f"gated few sums {M}x{N}x{K} r={r} bf16={bf16}")
+    d = Data(qb, M, N, K, r, bf16=bf16)
+    H, G, U, Hs = qb.qlora_gated_fwd_save(d.X, *d.args)
+    out = qb.qlora_gated_bwd(d.dH, d.X, G, U, Hs, *d.args)
+    x, g, u, dh, hs = f64(d.X), f64(G), f64(U), f64(d.dH), f64(Hs)
+    t = 1 / (1 + np.exp(-g))
+    own = STEP if bf16 else 2.0 ** -24
+    for i, (dd, size) in enumerate(((dh * u * t * (1 + g * (1 - t)), np.abs(dh * u) * (1 + np.abs(g))), (dh * g * t, np.abs(dh * g)))):
+        b, h = f64(d.factors[1 + 2 * i]), hs[:, i * hs.shape[1] // 2:i * hs.shape[1] // 2 + r]
+        low = d.scale * dd @ b
+        off = d.scale * (2.0 ** -19 + N * 2.0 ** -24) * (size @ np.abs(b)) + 2.0 ** -23 * np.abs(low)
+        da, db = low.T @ x, dd.T @ h
+        offa = off.T @ np.abs(x) + M * 2.0 ** -24 * (np.abs(low).T @ np.abs(x))
+        offb = (2.0 ** -19 + M * 2.0 ** -24) * (size.T @ np.abs(h))
+        within(out[1 + 2 * i], da, offa + own * (np.abs(da) + offa), GRADS[1 + 2 * i])
+        within(out[2 + 2 * i], db, offb + own * (np.abs(db) + offb), GRADS[2 + 2 * i])
