@@ -119,10 +119,12 @@ def rmsnorm(X, weight, residual=None, eps: float = 1e-6):
 
 class GatedFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, X, Ag, Bg, Au, Bu, gate: NF4Weight, up: NF4Weight, scale: float):
+    def forward(ctx, X, Ag, Bg, Au, Bu, gate: NF4Weight, up: NF4Weight, scale: float, keep: bool):
         X2 = _rows(X, X.shape[-1])
         args = (gate, up, Ag, Bg, Au, Bu, scale)
         shape = (*X.shape[:-1], gate.rows)
+        if not keep:
+            return qlora_gated_fwd(X2, *args).reshape(shape)
         H, G, U, Hs = qlora_gated_fwd_save(X2, *args)
         ctx.save_for_backward(X2, G, U, Hs, Ag, Bg, Au, Bu)
         ctx.weights, ctx.scale, ctx.shape = (gate, up), scale, X.shape
@@ -134,7 +136,7 @@ class GatedFn(torch.autograd.Function):
         X2, G, U, Hs, *factors = ctx.saved_tensors
         dH = _rows(dH.to(torch.bfloat16), G.shape[1])
         dX, *grads = qlora_gated_bwd(dH, X2, G, U, Hs, *ctx.weights, *factors, ctx.scale)
-        return (dX.reshape(ctx.shape), *grads, None, None, None)
+        return (dX.reshape(ctx.shape), *grads, None, None, None, None)
 
 
 def qlora_gated(X, gate: NF4Weight, up: NF4Weight, Ag=None, Bg=None, Au=None, Bu=None, scale: float = 0.0):
@@ -143,9 +145,9 @@ def qlora_gated(X, gate: NF4Weight, up: NF4Weight, Ag=None, Bg=None, Au=None, Bu
     four or none): the feed-forward block up to its down projection in one
     ``qlora_gated_fwd_save`` and one ``qlora_gated_bwd`` call. Where no gradient
     is asked for nothing is kept: ``qlora_gated_fwd``."""
-    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (X, Ag, Bg, Au, Bu))):
-        return qlora_gated_fwd(_rows(X, X.shape[-1]), gate, up, Ag, Bg, Au, Bu, float(scale)).reshape(*X.shape[:-1], gate.rows)
-    return GatedFn.apply(X, Ag, Bg, Au, Bu, gate, up, float(scale))
+    # through the function all the same: torch refuses forward-mode tangents there, which a call past it would drop
+    keep = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (X, Ag, Bg, Au, Bu))
+    return GatedFn.apply(X, Ag, Bg, Au, Bu, gate, up, float(scale), keep)
 
 
 class RopeFn(torch.autograd.Function):

@@ -98,3 +98,41 @@ def test_gradients_have_memory_of_their_own(shape, use):
     y, h = autograd.rmsnorm(x, torch.ones(64), r)
     ((y.float().square().sum() if use != "h" else 0) + (h.float().square().sum() if use != "y" else 0)).backward()
     assert x.grad.untyped_storage().data_ptr() != r.grad.untyped_storage().data_ptr()
+
+
+def _gated_calls(monkeypatch):
+    """The gated block's calls in plain torch; (names of those made, a weight)."""
+    made = []
+
+    def fwd(X, gate, up, Ag, Bg, Au, Bu, scale):
+        made.append("fwd")
+        return torch.ones(X.shape[0], gate.rows, dtype=torch.bfloat16)
+
+    def save(X, gate, up, Ag, Bg, Au, Bu, scale):
+        made.append("save")
+        return (*(torch.ones(X.shape[0], gate.rows, dtype=torch.bfloat16) for _ in range(3)), None)
+    monkeypatch.setattr(autograd, "qlora_gated_fwd", fwd)
+    monkeypatch.setattr(autograd, "qlora_gated_fwd_save", save)
+    return made, qb.NF4Weight(64, 64, *(None,) * 5)
+
+
+@pytest.mark.parametrize("dual", [0, 2])
+@pytest.mark.parametrize("grad", [True, False])
+def test_gated_refuses_forward_mode(monkeypatch, dual, grad):
+    """A tangent of X or of an adapter is refused where no gradient is kept either, and not dropped."""
+    import torch.autograd.forward_ad as fw
+    _, w = _gated_calls(monkeypatch)
+    args = [torch.randn(s).bfloat16() for s in ((3, 64), (8, 64), (64, 8), (8, 64), (64, 8))]
+    with torch.set_grad_enabled(grad), fw.dual_level():
+        args[dual] = fw.make_dual(args[dual], torch.ones_like(args[dual]))
+        with pytest.raises(NotImplementedError):
+            autograd.qlora_gated(args[0], w, w, *args[1:], 0.5)
+
+
+def test_gated_keeps_only_for_gradients(monkeypatch):
+    made, w = _gated_calls(monkeypatch)
+    x, = _leaves((2, 3, 64))
+    assert autograd.qlora_gated(x, w, w).shape == (2, 3, 64) and autograd.qlora_gated(x.detach(), w, w).shape == (2, 3, 64)
+    with torch.no_grad():
+        autograd.qlora_gated(x, w, w)
+    assert made == ["save", "fwd", "fwd"]
