@@ -195,18 +195,21 @@ __device__ __forceinline__ void request_b(const StreamParams &p, int up, int64_t
   }
 }
 
-// acc += the adapters' terms of 32 of their columns: each weight's rows with its own half of Hs.
+// acc += the adapters' terms of 32 of their columns: each weight's rows with its own half of Hs. Both halves meet all
+// rows, and a lane keeps the sums of its own: rows 4 g + 0 .. 3 of the tile are the gate's for g < 2. (Rows of zeros
+// in place of the other weight's would be enough but for an infinity in its half, which zeros make NaN.)
 template <int MT>
-__device__ __forceinline__ void adapt(f32x4 (&acc)[MT], const uint32_t (&b)[8], const u32x4 (&hs)[MT][2], int up, const StreamParams &p, int j0) {
+__device__ __forceinline__ void adapt(f32x4 (&acc)[MT], const uint32_t (&b)[8], const u32x4 (&hs)[MT][2], const StreamParams &p, int j0, int g) {
   float f[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) f[e] = j0 + e < p.r ? __builtin_bit_cast(float, p.bf16 ? b[e] << 16 : b[e]) : 0.0f;
   const bf16x8 v = __builtin_bit_cast(bf16x8, u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])});
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const bf16x8 mine = up == w ? v : bf16x8{};
+  for (int t = 0; t < MT; ++t) {
+    const f32x4 gate = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8, hs[t][0]), acc[t], 0, 0, 0);
+    const f32x4 up = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8, hs[t][1]), acc[t], 0, 0, 0);
 #pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mine, __builtin_bit_cast(bf16x8, hs[t][w]), acc[t], 0, 0, 0);
+    for (int e = 0; e < 4; ++e) acc[t][e] = g < 2 ? gate[e] : up[e];
   }
 }
 
@@ -555,7 +558,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_gated_few(const StreamParams p,
     }
     if (last) {
       if (adapts) {
-        adapt<1>(acc, bc, hs, up, p, 32 * wave + 8 * g);
+        adapt<1>(acc, bc, hs, p, 32 * wave + 8 * g, g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) bc[e] = bn[e];
       }
@@ -672,7 +675,7 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void k_gated_stream(cons
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) request_b(p, up, unit_row + 8 * i + (r & 7), 32 * wave + 8 * g, b[i]);
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) adapt<MT>(acc[i], b[i], hs, up, p, 32 * wave + 8 * g);
+    for (int i = 0; i < kTiles; ++i) adapt<MT>(acc[i], b[i], hs, p, 32 * wave + 8 * g, g);
   }
 #pragma unroll
   for (int i = 0; i < kTiles; ++i) {
