@@ -172,6 +172,7 @@ struct DownParams {
   int64_t M, L;       // L: the reduction, row length of P and Q
   int rows;           // rows of each Q
   int ld;
+  int r, rp;          // the columns of a weight that there are, and with those behind them, which become zeros
   int tiles_n, tiles_m, tiles;   // of one product; of all
   int steps, per;     // 64-deep steps, and those of a split
 };
@@ -211,6 +212,16 @@ __global__ __launch_bounds__(256, 1) void k_gated_down(const DownParams p) {
     mma_step<C>(acc, stage, stage + C::kLdsA, fa, fb);
   }
   RowsP::template wait_copies<0>();
+  // Q's rows of zeros made NaN of an infinity in P
+#pragma unroll
+  for (int j = 0; j < C::TN; ++j) {
+    const int col = j0 + wave % C::WAVES_N * C::WTN + 32 * j + (lane & 31);
+    if ((col < p.rp ? col : col - p.rp) < p.r) continue;
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc.v[i][j][e] = 0.0f;
+  }
   if (p.part) store_f32<C>(acc, p.part + static_cast<int64_t>(z) * p.M * p.ld + w * p.rows, p.ld, p.M, p.rows, m0, j0);
   else store_bf16<C, true>(acc, p.out + w * p.rows, p.ld, p.M, p.rows, m0, j0, p.scale);
 }
@@ -920,6 +931,8 @@ hipError_t launch_gated_fwd(const GatedArgs &a, const void *X, void *H, void *G,
     d.M = a.M;
     d.L = a.K;
     d.rows = d.ld = 2 * pl.rp;
+    d.r = a.r;
+    d.rp = pl.rp;
     d.tiles_n = 2 * pl.rp / 128;
     d.tiles_m = static_cast<int>(ceil_div(a.M, 128));
     d.tiles = d.tiles_m * d.tiles_n;
@@ -971,8 +984,9 @@ hipError_t launch_gated_bwd(const GatedArgs &a, const void *dH, const void *X, c
     d.scale = a.scale;
     d.M = a.M;
     d.L = a.N;
-    d.rows = pl.rp;
+    d.rows = d.rp = pl.rp;
     d.ld = 2 * pl.rp;
+    d.r = a.r;
     d.tiles_n = pl.rp / 64;
     d.tiles_m = static_cast<int>(ceil_div(a.M, 128));
     d.tiles = 2 * d.tiles_m * d.tiles_n;

@@ -1,4 +1,5 @@
-"""Values of the gated block with adapters that random inputs do not reach, at each of its kernels: infinities.
+"""Values of the gated block with adapters that random inputs do not reach, at each of its kernels: infinities and a
+padded rank.
 
 Infinities: a sum with one of them is that one by the sign of its factor, with two of different signs NaN, whatever
 the order; what no infinite term reaches keeps its bits. The formula is taken in fp64 term by term, so that it adds
@@ -8,12 +9,13 @@ import pytest
 
 from oracle import block
 from tests import gpu_util as gu
-from tests.test_gpu_gated import Data, f64, qb  # noqa: F401
+from tests.test_gpu_gated import GRADS, Data, f64, qb  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
-# one row in registers; one that is not; a few in LDS; up to 16, too long for LDS, up to 32; tiles
-PATHS = [(1, 64, 256), (1, 64, 320), (3, 128, 320), (9, 64, 192), (4, 64, 8192), (20, 128, 128), (32, 64, 64), (40, 128, 192)]
+# one row in registers; one that is not; a few in LDS; up to 16, too long for LDS, up to 32; tiles, whole and with split low products
+PATHS = [(1, 64, 256), (1, 64, 320), (3, 128, 320), (9, 64, 192), (4, 64, 8192), (20, 128, 128), (32, 64, 64), (40, 128, 192), (40, 64, 1024),
+         (300, 128, 128)]
 
 
 def product(x, w):
@@ -37,7 +39,7 @@ def equal_rows(a, b, rows):
 
 
 @pytest.mark.parametrize("r", [0, 1, 8, 70])
-@pytest.mark.parametrize("M,N,K", PATHS[:-1])
+@pytest.mark.parametrize("M,N,K", PATHS)
 def test_infinite_inputs(qb, M, N, K, r):  # noqa: F811
     gu.announce(f"gated infinite X {M}x{N}x{K} r={r}")
     d = Data(qb, M, N, K, r)
@@ -62,6 +64,33 @@ def test_infinite_inputs(qb, M, N, K, r):  # noqa: F811
     for got, want, before, label in ((G, sums[0], clean[1], "G"), (U, sums[1], clean[2], "U"), (H, h, clean[0], "H")):
         same_kind(got[rows], want, label)
         assert equal_rows(got, before, rows), label
+
+
+@pytest.mark.parametrize("r", [0, 1, 3, 8, 70])
+@pytest.mark.parametrize("M,N,K", PATHS)
+def test_infinite_gradients(qb, M, N, K, r):  # noqa: F811
+    gu.announce(f"gated infinite dH {M}x{N}x{K} r={r}")
+    d = Data(qb, M, N, K, r)
+    kept = qb.qlora_gated_fwd_save(d.X, *d.args)[1:]
+    clean = qb.qlora_gated_bwd(d.dH, d.X, *kept, *d.args)
+    rows = sorted({0, M - 1})
+    dH = d.dH.clone()
+    for i, m in enumerate(rows):
+        dH[m, (29 * i + 3) % N] = (-1) ** i * float("inf")
+    out = qb.qlora_gated_bwd(dH, d.X, *kept, *d.args)
+    with np.errstate(invalid="ignore"):
+        sides = block.gate_backward(f64(dH), f64(kept[0]), f64(kept[1]))
+        dx = 0.0
+        for i, (dd, w) in enumerate(zip(sides, (d.gate, d.up))):
+            dx = dx + product(dd[rows], f64(qb.qlora_nf4_dequantize(w)).T)
+            if r:
+                a, b, cols = f64(d.factors[2 * i]), f64(d.factors[2 * i + 1]), kept[2].shape[1] // 2
+                low = d.scale * product(dd, b.T)
+                dx = dx + product(low[rows], a.T)
+                same_kind(out[1 + 2 * i], product(low.T, f64(d.X).T), GRADS[1 + 2 * i])
+                same_kind(out[2 + 2 * i], product(dd.T, f64(kept[2])[:, i * cols:i * cols + r].T), GRADS[2 + 2 * i])
+    same_kind(out[0][rows], dx, "dX")
+    assert equal_rows(out[0], clean[0], rows)
 
 
 @pytest.mark.parametrize("side", [0, 1])
