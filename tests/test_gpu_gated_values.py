@@ -1,5 +1,5 @@
-"""Values of the gated block with adapters that random inputs do not reach, at each of its kernels: infinities and a
-padded rank.
+"""Values of the gated block with adapters that random inputs do not reach, at each of its kernels: infinities, a
+padded rank, inputs that have a mean.
 
 Infinities: a sum with one of them is that one by the sign of its factor, with two of different signs NaN, whatever
 the order; what no infinite term reaches keeps its bits. The formula is taken in fp64 term by term, so that it adds
@@ -9,7 +9,7 @@ import pytest
 
 from oracle import block
 from tests import gpu_util as gu
-from tests.test_gpu_gated import GRADS, Data, f64, qb  # noqa: F401
+from tests.test_gpu_gated import GRADS, Data, f64, near, qb  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +107,20 @@ def test_overflow_of_one_adapter(qb, M, N, K, side):  # noqa: F811
     cols = Hs.shape[1] // 2
     assert torch.isinf(Hs[:, side * cols:side * cols + 8]).all() and not torch.isfinite((G, U)[side]).any()
     assert torch.equal((U, G)[side], clean[2 - side])
+
+
+@pytest.mark.parametrize("fmt", [0, 1, 2, 3])
+@pytest.mark.parametrize("mean", [1.0, -4.0])
+@pytest.mark.parametrize("M,N,K", [(1, 1088, 4096), (1, 1088, 4160), (1, 320, 16384), (4, 1088, 4096), (4, 576, 8192), (16, 1088, 4096), (32, 1088, 4096),
+                                   (33, 1088, 4096)])
+def test_inputs_with_a_mean(qb, M, N, K, mean, fmt):  # noqa: F811
+    """A mean of X adds up the mean error of the weights, which is far below the error of one weight: G and U stay
+    within the bar of test_gpu_gated.py, two roundings of 2.26e-3, one a weight's and one the sum's own."""
+    import torch
+    gu.announce(f"gated mean {mean} {M}x{N}x{K} format {fmt}")
+    d = Data(qb, M, N, K, 0, fmt=fmt)
+    d.X.copy_((d.X.float() + mean).to(torch.bfloat16))
+    _, g, u, _ = d.oracle()
+    _, G, U, _ = qb.qlora_gated_fwd_save(d.X, *d.args)
+    near(G, g, 4.5e-3, "G")
+    near(U, u, 4.5e-3, "U")
