@@ -254,3 +254,28 @@ def test_refusals_with_tensors(qb):
         qb.qlora_rope_fwd(q, None, p, f, outs=(torch.empty_like(q), torch.empty_like(q)))
     with pytest.raises(ValueError):
         qb.qlora_rope_fwd(q, None, p, f, outs=(torch.empty(3, 3, 64, device="cuda"), None))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_more_workgroups_than_one_launch_takes(qb, interleaved):
+    """Heads of 1024 elements that begin at an odd one have a workgroup to a token: 2^21 of them to a launch, three
+    launches here, and elements behind 2^32. The rows at the launches' ends are bit for bit what they are in a call of
+    their own, with other outputs and in place, and the others stay zero."""
+    import torch
+    gu.announce(f"rope in three launches {interleaved}")
+    f, _ = qb.qlora_rope_freqs(1024, device="cuda")
+    rows, at = 2 * (1 << 21) + 3, torch.tensor([0, (1 << 21) - 1, 1 << 21, (1 << 22) - 1, 1 << 22, (1 << 22) + 2], device="cuda")
+    flat = torch.zeros(rows * 1024 + 1, dtype=torch.bfloat16, device="cuda")
+    x = flat[1:].view(rows, 1, 1024)
+    x[at] = torch.randn(len(at), 1, 1024, device="cuda").bfloat16()
+    p = torch.arange(rows, device="cuda")
+    few = torch.zeros(len(at) * 1024 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(len(at), 1, 1024)
+    few.copy_(x[at])
+    want = qb.qlora_rope_fwd(few, None, p[at].contiguous(), f, interleaved=interleaved)[0]
+    check(want, few, p[at].cpu().numpy(), host64(f), 1.0, interleaved, False, "few")
+    y, _ = qb.qlora_rope_fwd(x, None, p, f, interleaved=interleaved)
+    qb.qlora_rope_fwd(x, None, p, f, interleaved=interleaved, outs=(x, None))
+    for t in (y, x):
+        assert torch.equal(t[at], want)
+        t[at] = 0
+        assert not t.any()
