@@ -5,15 +5,16 @@
 // the gradient the same with -w. A pair is elements i and i + rot / 2 of the
 // head, or its neighbours 2 i and 2 i + 1; elements from rot on pass through.
 //
-// The angle: t f_i / (2 pi) in fp64, less the nearest whole number, leaves a
-// turn in [-1/2, 1/2] whose error is 2^-53 of t f_i (2^-25 turns at t = 2^31
-// and f = 1); in fp32 the product alone would be off by 2^-24 of it, a tenth
-// of a radian at a million positions. The sine and cosine of that turn and the
-// rotation are fp32, the result is rounded once.
+// The angle: t f_i / (2 pi) in fp64, less the nearest whole number, is a turn
+// in [-1/2, 1/2]. Three roundings of 2^-53 (of 1 / (2 pi), of f_i times that and
+// of t times that) leave it off by 3 * 2^-53 of its turns, 2^-23 turns at t =
+// 2^31 and f = 1; in fp32 the product alone would be off by 2^-24 of t f_i, a
+// tenth of a radian at a million positions. The sine and cosine of that turn
+// and the rotation are fp32, the result is rounded once.
 //
 // Bound by HBM: each element is read and written once. A workgroup has a few
 // tokens, forms their sines and cosines once for all heads in LDS (a head's
-// worth of them per token, which is little beside 40 heads) and then moves 32
+// worth of them per token, which is little beside 40 heads) and then moves 16
 // bytes of each half of a pair run per step and lane.
 #include <algorithm>
 

@@ -166,11 +166,12 @@ typedef struct {
  * Rotate Q and K (K may be NULL) in one launch.
  *   dtype       QLORA_F32 or QLORA_BF16, in and out
  *   dim, rot    even, 2 <= rot <= dim <= 1024; at most 32768 heads together
- *   positions   int32 (wide = 0) or int64 (wide = 1) [rows] on the device
+ *   positions   int32 (wide = 0) or int64 (wide = 1, rounded to fp64) [rows] on the device
  *   freqs       fp64 [rot / 2] on the device
  *   amplitude   finite
- * The angle is formed in fp64 and reduced to a turn there (good to 2^-25 turns
- * at |t| < 2^31); sine, cosine and rotation are fp32, rounded once.
+ * The angle is formed in turns, in fp64, with three roundings, and reduced there:
+ * good to 3 * 2^-53 of its turns, 2^-23 turns at |t| < 2^31 and f <= 1. Sine,
+ * cosine and rotation are fp32, rounded once.
  */
 int qlora_rope_fwd(const qlora_rope_heads *Q, const qlora_rope_heads *K, int dtype, int64_t rows, int32_t dim,
                    int32_t rot, const void *positions, int32_t wide, const double *freqs, double amplitude,

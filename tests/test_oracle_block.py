@@ -104,3 +104,16 @@ def test_rope_freqs():
     for p, t, x in zip(parts, turns, f):
         assert np.isclose(p, x if t >= 32 else x / 4 if t <= 1 else x / 4 + (x - x / 4) * float(t - 1) / 31)
     assert np.isclose(amp, 1 + 0.1 * np.log(4))
+
+
+def test_turns_of_far_positions():
+    """The rotation forms an angle's turns in fp64 as t (f / (2 pi)): three roundings, 2^-23 turns at 2^31, as
+    qlora_block.h states, and more than the 2^-25 of one rounding with a rounded constant left out."""
+    two_pi = 2 * Fraction("3.14159265358979323846264338327950288419716939937510")
+    rng = np.random.default_rng(6)
+    worst = 0
+    for f in [1.0, *rng.uniform(0.5, 1.0, 60)]:
+        for t in rng.integers(2 ** 31 - 2 ** 20, 2 ** 31, 60):
+            got = float(t) * (f * 0.15915494309189533577)
+            worst = max(worst, abs(Fraction(got) - int(t) * Fraction(f) / two_pi))
+    assert Fraction(1, 2 ** 25) < worst < Fraction(1, 2 ** 23)
