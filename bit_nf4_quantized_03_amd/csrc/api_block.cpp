@@ -3,6 +3,7 @@
 // failed check launches nothing.
 #include <cmath>
 #include <cstdint>
+#include <limits>
 
 #include "../../include/qlora_block.h"
 #include "block.h"
@@ -145,7 +146,7 @@ int rope(const char *fn, const qlora_rope_heads *Q, const qlora_rope_heads *K, i
     return api_fail(QLORA_ERR_SHAPE, "%s: dim = %d, rot = %d: needs even 2 <= rot <= dim <= %d", fn, dim, rot, qnf4::kRopeMaxDim);
   if (!aligned(positions, wide ? 8 : 4) || !aligned(freqs, 8))
     return api_fail(QLORA_ERR_ALIGN, "%s: positions and freqs must be aligned to their elements", fn);
-  if (!std::isfinite(amplitude)) return api_fail(QLORA_ERR_SHAPE, "%s: amplitude must be finite", fn);
+  if (!(std::fabs(amplitude) <= std::numeric_limits<float>::max())) return api_fail(QLORA_ERR_SHAPE, "%s: amplitude must be finite in fp32", fn);
   const int size = dtype == QLORA_BF16 ? 2 : 4;
   int st = check_heads(fn, "the first heads", Q, rows, dim, size);
   if (st == QLORA_OK && K) st = check_heads(fn, "the second heads", K, rows, dim, size);

@@ -168,7 +168,7 @@ typedef struct {
  *   dim, rot    even, 2 <= rot <= dim <= 1024; at most 32768 heads together
  *   positions   int32 (wide = 0) or int64 (wide = 1, rounded to fp64) [rows] on the device
  *   freqs       fp64 [rot / 2] on the device
- *   amplitude   finite
+ *   amplitude   finite, in fp32 too
  * The angle is formed in turns, in fp64, with three roundings, and reduced there:
  * good to 3 * 2^-53 of its turns, 2^-23 turns at |t| < 2^31 and f <= 1. Sine,
  * cosine and rotation are fp32, rounded once.

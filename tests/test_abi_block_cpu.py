@@ -214,3 +214,11 @@ def test_refusals_without_gpu_tensors():
                  lambda: qb.qlora_mx_pair(qb.MXMatrix.empty(8, 64, "cpu"), qb.MXMatrix.empty(8, 64, "cpu"))):
         with pytest.raises(TypeError, match="CUDA"):
             call()
+
+
+@pytest.mark.parametrize("name", ["qlora_rope_fwd", "qlora_rope_bwd"])
+def test_rope_rejects_amplitudes_past_fp32(name):
+    for amp in (1e39, -1e300, 3.5e38):
+        q = heads(n=0)   # refused too, behind the amplitude: nothing is launched in any case
+        assert getattr(lib, name)(q, None, BF16, 7, 128, 128, FAKE, 1, FAKE, amp, 0, None) == -2
+        assert "amplitude" in qb.qlora_last_error()
