@@ -92,7 +92,8 @@ def qlora_mx_pair(gate: MXMatrix, up: MXMatrix, out: Optional[MXMatrix] = None) 
 
 
 def _gated_out(X, index, N, mx, out):
-    """H and how the entry point takes it: (result, address of a bf16 H, struct of a microscaled one)"""
+    """H and how the entry point takes it: (result, address of a bf16 H, struct of a microscaled one). A given ``out``
+    decides, whatever ``mx`` is."""
     if N % 32:
         raise ValueError(f"H would have {N} columns: a pair has a multiple of 64 rows")
     if out is None:
@@ -101,8 +102,6 @@ def _gated_out(X, index, N, mx, out):
         else:
             out = MXMatrix.empty(X.rows, N, X.codes.device, mx)
     if isinstance(out, MXMatrix):
-        if mx is not None and mx != out.mx:
-            raise ValueError(f"mx {mx} differs from out.mx {out.mx}")
         return out, None, byref(out.c_struct("out", index))
     return out, _tensor("out", out, torch.bfloat16, (X.rows, N), index), None
 
@@ -119,8 +118,6 @@ def qlora_mx_gated(X: MXMatrix, W: MXMatrix, mx: Optional[int] = QLORA_MX_FP8, o
     sx = X.c_struct("X")
     index = X.codes.get_device()
     sw = W.c_struct("W", index)
-    if out is not None:
-        mx = None
     out, h, hq = _gated_out(X, index, W.rows // 2, mx, out)
     _gated(index, byref(sx), byref(sw), h, hq)
     return out
@@ -145,8 +142,6 @@ def qlora_mx_gated_grouped(X: MXMatrix, W: MXMatrix, offsets, mx: Optional[int] 
     if W.rows % (2 * experts):
         raise ValueError(f"W has {W.rows} rows, not a multiple of two for each of {experts} experts")
     clear = out is None
-    if not clear:
-        mx = None
     out, h, hq = _gated_out(X, index, W.rows // experts // 2, mx, out)
     _gated_grouped(index, byref(sx), byref(sw), off, experts, h, hq, clear)
     return out

@@ -28,8 +28,6 @@ __global__ __launch_bounds__(256) void k_mx_pair(const PairParams p) {
   for (int64_t i = 16 * (threadIdx.x & 63); i < p.pitch; i += 1024) *reinterpret_cast<uint4 *>(ts + i) = *reinterpret_cast<const uint4 *>(s + i);
 }
 
-// Few rows: 16 RT rows of the pair, 8 RT columns of H a workgroup. The waves'
-// sums are added in wave order, then a lane takes eight columns of a row.
 // Zeros in the rows of H in front of the first expert's and behind the last
 // one's, by workgroup `part` of `parts`. These are workgroups of the product's own
 // launch behind its others (a fill in front of 4096 rows over 8 experts 4096 x
@@ -51,7 +49,8 @@ __device__ __forceinline__ void clear_rest(const MxGatedOut &o, const int32_t *o
 }
 constexpr int kClearGroups = 64;
 
-// The sums of a few rows: as mx_linear.hip's, then the gate.
+// Few rows: 16 RT rows of the pair, 8 RT columns of H a workgroup. The waves'
+// sums are added in wave order, then a lane takes eight columns of a row.
 template <int XT, int MT, int RT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_mx_gated_gemv(const MxGemvParams p, const MxGatedOut o) {
   __shared__ float part[WAVES][MT][RT][16][17];

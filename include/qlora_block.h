@@ -63,7 +63,9 @@ int qlora_mx_gated_grouped(const qlora_mx_matrix *X, const qlora_mx_matrix *W, c
  *     G = X Wg^T + s (X Ag^T) Bg^T,  U = X Wu^T + s (X Au^T) Bu^T,  H = silu(G) * U
  *
  * around two frozen 4-bit weights [N, K] of the same shape and format (N and K
- * multiples of 64), each with an adapter of the same rank or both without.
+ * multiples of 64), each with an adapter of the same rank or both without. An
+ * adapter on one of them only has factors of zeros for the other, one of lower
+ * rank rows of A and columns of B that are zero.
  */
 
 /* A [r, K] and B [N, r] of each weight, fp32 or bf16 (dtype), 1 <= r <= 256. */
@@ -144,6 +146,9 @@ typedef enum { QLORA_ROPE_PLAIN = 0, QLORA_ROPE_LINEAR = 1, QLORA_ROPE_NTK = 2, 
  *           makes in the `trained` positions: f_i (k + (1 - k) / factor), k =
  *           (n_i - low) / (high - low) within [0, 1]; amplitude
  *           0.1 ln(factor) + 1 (a model that was trained without it takes 1)
+ *           The ramp goes by the turns. A model whose frequencies ramp over the
+ *           pair's index between two bounds has others, which the rotation takes
+ *           as they are
  * base > 0, factor >= 1, trained >= 1, low < high; finite. Host-only.
  */
 int qlora_rope_freqs(int32_t rot, double base, int32_t scaling, double factor, int64_t trained, double low,
